@@ -392,6 +392,158 @@ MLA_API int sdpa_fp8_decode(const sdpa_plan_t* plan, int total_q, int64_t total_
                     void* workspace, void* stream);
 
 /* ======================================================================= *
+ *  Paged KV cache, and attention over its pages and over whole prompts     *
+ *                                                                          *
+ *  These entry points have no counterpart in the pages. They give the      *
+ *  dense GQA path above a cache that a server can append to, and the       *
+ *  attention of everything before and between its decode steps, with the   *
+ *  same definitions of scores, O, log2 LSE, output casts and amax.         *
+ * ======================================================================= */
+
+/* Element types of Q, K and V (the codes of MLA_OUT_*): bf16, or e4m3 codes that
+ * stand for code * descale. Q, K and V of a call have one type. */
+#define SDPA_BF16 1
+#define SDPA_E4M3 2
+
+/* A paged KV cache: num_pages pages of page_size rows; a row holds one token's
+ * h_kv heads of d elements. Element (page p, row r, head g, dim x) of k and of v
+ * lies p * page_stride + r * row_stride + g * head_stride + x elements from the
+ * base. A slot is p * page_size + r. Contiguous [num_pages][page_size][h_kv][d]
+ * ("row before head") and [num_pages][h_kv][page_size][d] are both strides of
+ * this form. k and v are 16-byte aligned, and the strides are positive multiples
+ * of 16 bytes below 2^40 bytes. */
+typedef struct {
+  void* k;
+  void* v;
+  int32_t dtype;         /* SDPA_BF16 or SDPA_E4M3                          */
+  int32_t num_pages;
+  int32_t page_size;     /* rows a page: a power of two, 16 .. 65536        */
+  int32_t h_kv;
+  int32_t d;             /* 128                                             */
+  int32_t reserved;      /* 0                                               */
+  int64_t page_stride, row_stride, head_stride;   /* in elements            */
+} kv_pages_t;
+
+/* Block tables and slot maps from request lengths, on the GPU, in place and
+ * without a host synchronisation: request b held held_lens[b] cached positions
+ * and shall hold new_lens[b]. With pages(n) = min(ceil(max(n, 0) / page_size),
+ * table_width), F = free_pages and n = free_in[0] (taken as 0 below 0 and as
+ * free_capacity above it):
+ *   1. every table entry of a request that shrinks (b ascending, entries
+ *      pages(new) .. pages(held) - 1 ascending) that is >= 0 is appended to F,
+ *      n growing by one each; the entries themselves are left as they were;
+ *   2. the j-th entry that a growing request lacks (b ascending, entries
+ *      pages(held) .. pages(new) - 1 ascending, j from 0) becomes F[n - 1 - j], or
+ *      -1 once F is used up;
+ *   3. free_out[0] = pages left, free_out[1] = pages that could not be had.
+ * A finished request is new_lens[b] = 0, a rejected draft a smaller new_lens[b].
+ * New tokens: request b has cu_seqlens_q[b + 1] - cu_seqlens_q[b] of them, at its
+ * last positions, as in sdpa_paged: token i sits at position p = new_lens[b] -
+ * (its count) + i. For every row r < total_q of the packed tokens,
+ *   slot_map[r]  = table[b][p / page_size] * page_size + p % page_size, or -1
+ *                  where there is no such page;
+ *   positions[r] = p, or -1 where p < 0 or p / page_size >= table_width.
+ * Rows at and past cu_seqlens_q[batch] (a padded batch) get -1 in both.
+ * The call reads nothing it has not been given lengths for, and leaves F below
+ * free_in[0] as it was, so with free_in and free_out apart the same call gives the
+ * same result again. free_in and free_out may be the same address.
+ *   held_lens, new_lens  int32 [batch]; cu_seqlens_q  int32 [batch + 1] from 0,
+ *       non-decreasing.
+ *   block_table  int32 [batch][table_width]; entries below pages(held) are a
+ *       request's own pages (no page in two requests, none of them in F).
+ *   free_pages   int32 [free_capacity]; entries past free_capacity are not stored.
+ *   free_in int32 [1]; free_out int32 [2]; slot_map int64 [total_q];
+ *   positions    int32 [total_q] or NULL.
+ * MLA_ERR_INVALID_ARG: a NULL or misaligned pointer, batch, page_size,
+ * table_width or free_capacity < 1, total_q < 0. MLA_ERR_UNSUPPORTED: batch >
+ * KV_PAGES_MAX_BATCH. total_q may be 0 (slot_map is then not touched). */
+#define KV_PAGES_MAX_BATCH 16384
+MLA_API int kv_pages_map(int batch, int page_size, const int32_t* held_lens, const int32_t* new_lens,
+                 const int32_t* cu_seqlens_q, int total_q, int32_t* block_table, int table_width,
+                 int32_t* free_pages, int free_capacity, const int32_t* free_in, int32_t* free_out,
+                 int64_t* slot_map, int32_t* positions, void* stream);
+
+/* Appends rows to the cache: row r of k_new and v_new (bf16, h_kv heads of 128,
+ * element (r, g, x) at r * token_stride + g * head_stride + x) goes to slot
+ * slot_map[r]; a bf16 cache takes the bits, an e4m3 cache
+ *   code = e4m3_satfinite_rn(x / descale)      (fp32 division; NaN stays NaN)
+ * with descale_k / descale_v fp32 device scalars (NULL = 1.0; ignored for bf16),
+ * the ones that sdpa_paged multiplies back. A slot outside [0, num_pages *
+ * page_size) is skipped. Two rows with the same slot leave some of each in it.
+ * k_new and v_new are 16-byte aligned and their strides positive multiples of 8
+ * elements, so K and V may be slices of a fused projection's output. rows >= 0. */
+MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, const void* v_new,
+                   int64_t token_stride, int64_t head_stride, const int64_t* slot_map,
+                   const float* descale_k, const float* descale_v, void* stream);
+
+/* Plan of sdpa_paged: what its launches and workspace need, from bounds that the
+ * host knows. Workspace layout as for sdpa_plan_t with rows = total_q_max * h_q. */
+typedef struct {
+  int32_t batch;          /* sequences                                                  */
+  int32_t h_q, h_kv;      /* query and KV heads; h_q % h_kv == 0, group = h_q / h_kv <= 128 */
+  int32_t d;              /* 128                                                        */
+  int32_t dtype;          /* SDPA_BF16 or SDPA_E4M3                                     */
+  int32_t max_q_per_seq;  /* bound on new tokens of one sequence                        */
+  int32_t total_q_max;    /* bound on new tokens of the batch                           */
+  int32_t max_kv;         /* expected bound on keys of one sequence (sizes the split count
+                             only: longer sequences are computed all the same)           */
+  int32_t num_splits;     /* the most splits a sequence gets                            */
+  int32_t num_sms;
+  int32_t adaptive_splits; /* 1: each sequence's split count follows from the lengths, on the GPU */
+  int32_t row_kernel;     /* 1: max_q_per_seq * group <= 16, one 16-row job per sequence and KV head */
+  uint64_t o_acc_bytes;
+  uint64_t lse_acc_offset;
+  uint64_t lse_acc_bytes;
+  uint64_t workspace_bytes;
+} sdpa_paged_plan_t;
+
+MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_per_seq, int total_q_max,
+                    int max_kv, int num_sms, int max_splits, int force_splits, sdpa_paged_plan_t* out);
+
+/* Attention of new tokens over a paged cache that already holds them: one to
+ * thousands of new tokens a sequence (decode, speculative decode, chunked prefill,
+ * a whole prompt, all mixed in one batch). Sequence b has s_b = cu_seqlens_q[b + 1]
+ * - cu_seqlens_q[b] new tokens and kv_lens[b] keys, the new ones included; query i
+ * sits at position kv_lens[b] - s_b + i and sees keys 0 .. that position; query
+ * head j reads KV head j / (h_q / h_kv). Key p of sequence b is row p % page_size
+ * of page block_table[b][p / page_size]; the keys of an entry outside [0,
+ * num_pages) are left out, like masked ones. A query that sees no key gives O = 0
+ * and LSE = -inf. Rows of out and lse_out at and past cu_seqlens_q[batch] are left as they
+ * were, and nothing of the cache outside a sequence's keys reaches a result,
+ * whatever it holds (a non-finite V element below kv_lens[b] may also reach
+ * queries of that sequence before it).
+ *   q  [total_q][h_q][128] of the plan's dtype, element (t, j, x) at t *
+ *      q_token_stride + j * q_head_stride + x; 16-byte aligned, strides positive
+ *      multiples of 16 bytes.
+ *   block_table  int32 [batch][table_width]; kv_lens int32 [batch] (taken as 0
+ *      below 0 and as table_width * page_size above it).
+ *   descale_q/k/v  fp32 device scalars (NULL = 1.0; for bf16 they apply the same).
+ *   out  [total_q][h_q][128] contiguous, fp32 / bf16 / e4m3 (MLA_OUT_*); lse_out
+ *      fp32 [total_q][h_q] or NULL; amax_out fp32 scalar or NULL.
+ *   workspace  plan->workspace_bytes, 256-byte aligned. Calls that overlap on
+ *      the GPU need workspaces of their own. */
+MLA_API int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_t q_token_stride,
+               int64_t q_head_stride, const kv_pages_t* pages, const int32_t* block_table, int table_width,
+               const int32_t* kv_lens, const int32_t* cu_seqlens_q, const float* descale_q, const float* descale_k,
+               const float* descale_v, float sm_scale, int out_dtype, float out_inv_scale, void* out,
+               float* lse_out, float* amax_out, void* workspace, void* stream);
+
+/* Attention over whole prompts, packed one after the other: sequence b has the
+ * queries cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 and the keys cu_seqlens_kv[b]
+ * .. cu_seqlens_kv[b + 1] - 1 (as many for a prompt; more where a prefix precedes
+ * it, fewer leave its first queries without a key), causal and grouped as in
+ * sdpa_paged, same outputs. k and v share their strides; q, k and v may be slices
+ * of one fused projection's output. total_q, total_kv are row counts of q and k/v; nothing
+ * outside them is read, and rows of out and lse_out outside the sequences are left as they
+ * were. Needs no workspace. Same alignment rules as sdpa_paged. */
+MLA_API int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,
+                int64_t q_token_stride, int64_t q_head_stride, const void* k, const void* v,
+                int64_t kv_token_stride, int64_t kv_head_stride, const int32_t* cu_seqlens_q,
+                const int32_t* cu_seqlens_kv, const float* descale_q, const float* descale_k,
+                const float* descale_v, float sm_scale, int out_dtype, float out_inv_scale, void* out,
+                float* lse_out, float* amax_out, void* stream);
+
+/* ======================================================================= *
  *  Status and diagnostics                                                  *
  * ======================================================================= */
 

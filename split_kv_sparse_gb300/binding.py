@@ -23,6 +23,9 @@ MLA_STATUS_BAD_INDEX = 0x10
 MLA_STATUS_BAD_ALIGN = 0x4
 MLA_MAX_SPLITS = 64
 MLA_FORCE_BALANCED = -1
+SDPA_BF16, SDPA_E4M3 = 1, 2
+KV_PAGES_MAX_BATCH = 16384
+MLA_ERR_INVALID_ARG = 1
 OUT_DTYPES = {"f32": MLA_OUT_F32, "bf16": MLA_OUT_BF16, "e4m3": MLA_OUT_E4M3}
 
 # Every symbol the header declares (checked by the library-load test).
@@ -32,6 +35,7 @@ EXPORTS = [
     "sdpa_split_combine", "sdpa_fp8_decode_direct", "sdpa_fp8_decode", "mla_get_status",
     "mla_selftest_wait_timeout", "mla_status_string", "mla_abi_version", "mla_sparse_decode_noalloc",
     "mla_workspace_init", "mla_set_wait_limit_ns", "mla_plan_set_partials_bf16", "mla_set_index_checks",
+    "kv_pages_map", "kv_pages_write", "sdpa_paged_plan", "sdpa_paged", "sdpa_prompt",
 ]
 
 
@@ -56,6 +60,22 @@ class SdpaPlan(ctypes.Structure):
                 ("d", ctypes.c_int32), ("max_q_per_seq", ctypes.c_int32), ("total_q_max", ctypes.c_int32),
                 ("max_kv", ctypes.c_int32), ("key_tile", ctypes.c_int32), ("num_splits", ctypes.c_int32),
                 ("num_sms", ctypes.c_int32), ("adaptive_splits", ctypes.c_int32), ("o_acc_bytes", ctypes.c_uint64),
+                ("lse_acc_offset", ctypes.c_uint64), ("lse_acc_bytes", ctypes.c_uint64),
+                ("workspace_bytes", ctypes.c_uint64)]
+
+
+class KvPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class SdpaPagedPlan(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("h_q", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("max_q_per_seq", ctypes.c_int32), ("total_q_max", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("num_splits", ctypes.c_int32), ("num_sms", ctypes.c_int32),
+                ("adaptive_splits", ctypes.c_int32), ("row_kernel", ctypes.c_int32), ("o_acc_bytes", ctypes.c_uint64),
                 ("lse_acc_offset", ctypes.c_uint64), ("lse_acc_bytes", ctypes.c_uint64),
                 ("workspace_bytes", ctypes.c_uint64)]
 
@@ -91,6 +111,13 @@ _SIGS = {
     "mla_set_wait_limit_ns": [_U64],
     "mla_set_index_checks": [_I],
     "mla_plan_set_partials_bf16": [ctypes.POINTER(MlaPlan), _I],
+    "kv_pages_map": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P],
+    "kv_pages_write": [ctypes.POINTER(KvPages), _I64, _P, _P, _I64, _I64, _P, _P, _P, _P],
+    "sdpa_paged_plan": [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(SdpaPagedPlan)],
+    "sdpa_paged": [ctypes.POINTER(SdpaPagedPlan), _I, _P, _I64, _I64, ctypes.POINTER(KvPages), _P, _I, _P, _P, _P, _P,
+                   _P, _F, _I, _F, _P, _P, _P, _P, _P],
+    "sdpa_prompt": [_I, _I, _I, _I, _I, _I, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _F, _I, _F,
+                    _P, _P, _P, _P],
 }
 
 
@@ -254,6 +281,187 @@ def mla_sparse_decode_noalloc(s_q: int, topk: int, q, kv, n_kv: int, idx, sm_sca
                                            num_splits, _dtype(out_dtype), out_inv_scale, _ptr(out), _ptr(lse_out),
                                            _ptr(amax_out), _stream(stream)),
            "mla_sparse_decode_noalloc")
+
+
+# -------------------------------------------- paged KV cache, prompt attention --
+
+_SDPA_DTYPES = {"bf16": SDPA_BF16, "e4m3": SDPA_E4M3}
+_OUT_TORCH = {MLA_OUT_F32: ("float32",), MLA_OUT_BF16: ("bfloat16",), MLA_OUT_E4M3: ("uint8", "float8_e4m3fn")}
+
+
+def _refuse(where: str, what: str):
+    raise SplitKVError(MLA_ERR_INVALID_ARG, f"{where}: {what}")
+
+
+def _dev(where: str, name: str, x, dtypes, numel: int = 0, contiguous: bool = True, optional: bool = False):
+    """Checks a device tensor (on the current device, of one of `dtypes`, contiguous, of at least `numel`
+    elements) and returns it."""
+    import torch
+    if x is None:
+        if optional:
+            return None
+        _refuse(where, f"{name} is missing")
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index != torch.cuda.current_device():
+        _refuse(where, f"{name} must be a tensor on the current CUDA device")
+    if str(x.dtype)[6:] not in dtypes:
+        _refuse(where, f"{name} has type {x.dtype}, not {' or '.join(dtypes)}")
+    if contiguous and not x.is_contiguous():
+        _refuse(where, f"{name} must be contiguous")
+    if x.numel() < numel:
+        _refuse(where, f"{name} has {x.numel()} elements, fewer than {numel}")
+    return x
+
+
+def _sdpa_dtype(where: str, name: str, x) -> int:
+    t = str(x.dtype)[6:]
+    if t == "bfloat16":
+        return SDPA_BF16
+    if t in ("uint8", "float8_e4m3fn"):
+        return SDPA_E4M3
+    _refuse(where, f"{name} has type {x.dtype}, not bfloat16 or e4m3 codes")
+
+
+def _strided(where: str, name: str, x, dims: int):
+    """The strides of a tensor whose last dimension is contiguous; a dimension of one element, whose stride
+    says nothing, counts as packed."""
+    if x.dim() != dims or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        _refuse(where, f"{name} must have {dims} dimensions, the last one contiguous")
+    st = list(x.stride())
+    packed = 1
+    for i in reversed(range(dims)):
+        if x.shape[i] == 1:
+            st[i] = packed
+        packed *= max(1, x.shape[i])
+    return st
+
+
+def _descales(where: str, **ds):
+    return [_ptr(_dev(where, n, x, ("float32",), 1, optional=True)) for n, x in ds.items()]
+
+
+def _outputs(where: str, out_dtype: int, out, lse_out, amax_out, rows: int, d: int):
+    if out_dtype not in _OUT_TORCH:
+        _refuse(where, f"unknown output type {out_dtype}")
+    _dev(where, "out", out, _OUT_TORCH[out_dtype], rows * d)
+    _dev(where, "lse_out", lse_out, ("float32",), rows, optional=True)
+    _dev(where, "amax_out", amax_out, ("float32",), 1, optional=True)
+
+
+def kv_pages(k_cache, v_cache) -> KvPages:
+    """The C descriptor of a paged cache from views [num_pages, page_size, h_kv, d] of its tensors (bfloat16, or
+    uint8 / float8_e4m3fn codes; any strides over a contiguous d, so a [num_pages, h_kv, page_size, d] cache is
+    passed as its permute(0, 2, 1, 3)). The descriptor keeps the tensors alive."""
+    where = "kv_pages"
+    for n, x in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _dev(where, n, x, ("bfloat16", "uint8", "float8_e4m3fn"), contiguous=False)
+    st = _strided(where, "k_cache", k_cache, 4)
+    dt = _sdpa_dtype(where, "k_cache", k_cache)
+    if tuple(v_cache.shape) != tuple(k_cache.shape) or _sdpa_dtype(where, "v_cache", v_cache) != dt \
+            or _strided(where, "v_cache", v_cache, 4) != st:
+        _refuse(where, "k_cache and v_cache differ in shape, type or strides")
+    n, ps, h, d = k_cache.shape
+    pages = KvPages(k_cache.data_ptr(), v_cache.data_ptr(), dt, n, ps, h, d, 0, st[0], st[1], st[2])
+    pages.tensors = (k_cache, v_cache)
+    return pages
+
+
+def kv_pages_map(page_size: int, held_lens, new_lens, cu_seqlens_q, total_q: int, block_table, free_pages, free_in,
+                 free_out, slot_map=None, positions=None, stream=None):
+    """Block tables and slot maps from request lengths (block_table, free_pages, free_out, slot_map and
+    positions are written in place)."""
+    where, i32 = "kv_pages_map", ("int32",)
+    _dev(where, "held_lens", held_lens, i32, 1)
+    batch = held_lens.numel()
+    _dev(where, "new_lens", new_lens, i32, batch)
+    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, batch + 1)
+    _dev(where, "block_table", block_table, i32, 1)
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
+        _refuse(where, "block_table must be [batch, table_width]")
+    _dev(where, "free_pages", free_pages, i32, 1)
+    _dev(where, "free_in", free_in, i32, 1)
+    _dev(where, "free_out", free_out, i32, 2)
+    _dev(where, "slot_map", slot_map, ("int64",), total_q, optional=total_q == 0)
+    _dev(where, "positions", positions, i32, total_q, optional=True)
+    _check(lib().kv_pages_map(batch, page_size, _ptr(held_lens), _ptr(new_lens), _ptr(cu_seqlens_q), total_q,
+                              _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.numel(),
+                              _ptr(free_in), _ptr(free_out), _ptr(slot_map), _ptr(positions), _stream(stream)), where)
+
+
+def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, descale_v=None, stream=None):
+    """Rows of k_new and v_new (bfloat16 [rows, h_kv, d], any strides over a contiguous d) into their slots."""
+    where = "kv_pages_write"
+    for n, x in (("k_new", k_new), ("v_new", v_new)):
+        _dev(where, n, x, ("bfloat16",), contiguous=False)
+    st = _strided(where, "k_new", k_new, 3)
+    if tuple(v_new.shape) != tuple(k_new.shape) or _strided(where, "v_new", v_new, 3) != st:
+        _refuse(where, "k_new and v_new differ in shape or strides")
+    if tuple(k_new.shape[1:]) != (pages.h_kv, pages.d):
+        _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
+    rows = k_new.shape[0]
+    _dev(where, "slot_map", slot_map, ("int64",), rows)
+    dk, dv = _descales(where, descale_k=descale_k, descale_v=descale_v)
+    _check(lib().kv_pages_write(ctypes.byref(pages), rows, _ptr(k_new), _ptr(v_new), st[0], st[1], _ptr(slot_map), dk,
+                                dv, _stream(stream)), where)
+
+
+def sdpa_paged_plan(batch: int, h_q: int, h_kv: int, d: int, dtype, max_q_per_seq: int, total_q_max: int, max_kv: int,
+                    *, num_sms: int = 0, max_splits: int = 0, force_splits: int = 0) -> SdpaPagedPlan:
+    plan = SdpaPagedPlan()
+    dt = _SDPA_DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    _check(lib().sdpa_paged_plan(batch, h_q, h_kv, d, dt, max_q_per_seq, total_q_max, max_kv, num_sms, max_splits,
+                                 force_splits, ctypes.byref(plan)), "sdpa_paged_plan")
+    return plan
+
+
+def sdpa_paged(plan: SdpaPagedPlan, total_q: int, q, pages: KvPages, block_table, kv_lens, cu_seqlens_q, descale_q,
+               descale_k, descale_v, sm_scale: float, out_dtype, out_inv_scale: float, out, lse_out=None, amax_out=None,
+               workspace=None, stream=None):
+    """Attention of new tokens over a paged cache; q [>= total_q, h_q, d] of the plan's type, any strides over a
+    contiguous d."""
+    where, i32 = "sdpa_paged", ("int32",)
+    _dev(where, "q", q, ("bfloat16",) if plan.dtype == SDPA_BF16 else ("uint8", "float8_e4m3fn"), contiguous=False)
+    st = _strided(where, "q", q, 3)
+    if tuple(q.shape[1:]) != (plan.h_q, plan.d) or q.shape[0] < total_q:
+        _refuse(where, f"q must be [{total_q} or more, {plan.h_q}, {plan.d}]")
+    _dev(where, "block_table", block_table, i32, 1)
+    if block_table.dim() != 2 or block_table.shape[0] < plan.batch:
+        _refuse(where, "block_table must be [batch, table_width]")
+    _dev(where, "kv_lens", kv_lens, i32, plan.batch)
+    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, plan.batch + 1)
+    ds = _descales(where, descale_q=descale_q, descale_k=descale_k, descale_v=descale_v)
+    _outputs(where, _dtype(out_dtype), out, lse_out, amax_out, total_q * plan.h_q, plan.d)
+    if plan.workspace_bytes:
+        _dev(where, "workspace", workspace, ("uint8", "float32"))
+        if workspace.numel() * workspace.element_size() < plan.workspace_bytes:
+            _refuse(where, "workspace is smaller than the plan's")
+    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, _ptr(q), st[0], st[1], ctypes.byref(pages), _ptr(block_table),
+                            block_table.shape[1], _ptr(kv_lens), _ptr(cu_seqlens_q), *ds, sm_scale, _dtype(out_dtype),
+                            out_inv_scale, _ptr(out), _ptr(lse_out), _ptr(amax_out), _ptr(workspace),
+                            _stream(stream)), where)
+
+
+def sdpa_prompt(batch: int, q, k, v, cu_seqlens_q, cu_seqlens_kv, descale_q, descale_k, descale_v, sm_scale: float,
+                out_dtype, out_inv_scale: float, out, lse_out=None, amax_out=None, stream=None):
+    """Causal attention over packed prompts; q [total_q, h_q, d], k and v [total_kv, h_kv, d] of one type, any
+    strides over a contiguous d (k and v the same)."""
+    where, i32 = "sdpa_prompt", ("int32",)
+    for n, x in (("q", q), ("k", k), ("v", v)):
+        _dev(where, n, x, ("bfloat16", "uint8", "float8_e4m3fn"), contiguous=False)
+    dt = _sdpa_dtype(where, "q", q)
+    qs, ks = _strided(where, "q", q, 3), _strided(where, "k", k, 3)
+    if tuple(v.shape) != tuple(k.shape) or _strided(where, "v", v, 3) != ks:
+        _refuse(where, "k and v differ in shape or strides")
+    if _sdpa_dtype(where, "k", k) != dt or _sdpa_dtype(where, "v", v) != dt or k.shape[2] != q.shape[2]:
+        _refuse(where, "q, k and v must have one type and one head dim")
+    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, batch + 1)
+    _dev(where, "cu_seqlens_kv", cu_seqlens_kv, i32, batch + 1)
+    ds = _descales(where, descale_q=descale_q, descale_k=descale_k, descale_v=descale_v)
+    total_q, h_q, d = q.shape
+    _outputs(where, _dtype(out_dtype), out, lse_out, amax_out, total_q * h_q, d)
+    _check(lib().sdpa_prompt(batch, h_q, k.shape[1], d, dt, total_q, k.shape[0], _ptr(q), qs[0], qs[1], _ptr(k),
+                             _ptr(v), ks[0], ks[1], _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv), *ds, sm_scale,
+                             _dtype(out_dtype), out_inv_scale, _ptr(out), _ptr(lse_out), _ptr(amax_out),
+                             _stream(stream)), where)
 
 
 # ------------------------------------------------------------------- status --

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "abi_util.h"
 #include "kernels.h"
 #include "mla_split.h"
 
@@ -67,7 +68,8 @@ int device_state(DeviceState** out) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }
-    if (skv::prepare_mla_kernels() != cudaSuccess || skv::prepare_sdpa_kernels() != cudaSuccess) {
+    if (skv::prepare_mla_kernels() != cudaSuccess || skv::prepare_sdpa_kernels() != cudaSuccess ||
+        skv::prepare_paged_kernels() != cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }
@@ -244,6 +246,22 @@ int mla_q_tensor_map(int s_q, const void* q, CUtensorMap* tq) {
 }
 
 }  // namespace
+
+namespace skv {
+
+int current_device(DeviceInfo* out) {
+  DeviceState* d = nullptr;
+  const int st = device_state(&d);
+  if (st != MLA_OK) return st;
+  out->status = d->status;
+  out->num_sms = d->num_sms;
+  return MLA_OK;
+}
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encoder(); }
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
+uint64_t drain_limit_ns() { return kWaitLimitNs; }
+
+}  // namespace skv
 
 extern "C" {
 

@@ -1,0 +1,284 @@
+// extern "C" entry points of the paged KV cache, of attention over its pages and
+// of attention over packed prompts: planning, argument checks and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "abi_util.h"
+#include "kernels.h"
+#include "mla_split.h"
+
+namespace {
+
+using skv::ptr_aligned;
+
+constexpr int kDim = 128;
+
+uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
+
+int elem_size(int dtype) { return dtype == SDPA_BF16 ? 2 : 1; }
+
+// An element stride that TMA and 16-byte loads can take.
+bool stride_ok(int64_t s, int esz) { return s > 0 && (s * esz) % 16 == 0 && s < (int64_t{1} << 40) / esz; }
+
+bool out_ok(const void* out, int out_dtype, float inv_scale) {
+  if (out == nullptr || !ptr_aligned(out, 16)) return false;
+  if (out_dtype != MLA_OUT_F32 && out_dtype != MLA_OUT_BF16 && out_dtype != MLA_OUT_E4M3) return false;
+  return out_dtype != MLA_OUT_E4M3 || std::isfinite(inv_scale);
+}
+
+// Pointers of fp32 and int32 data that may be null.
+bool words_ok(std::initializer_list<const void*> ps) {
+  for (const void* p : ps)
+    if (!ptr_aligned(p, 4)) return false;
+  return true;
+}
+
+int check_heads(int batch, int h_q, int h_kv, int d, int dtype) {
+  if (d != kDim) return MLA_ERR_UNSUPPORTED;
+  if (dtype != SDPA_BF16 && dtype != SDPA_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (batch < 1 || h_kv < 1 || h_q < 1 || h_q % h_kv != 0) return MLA_ERR_INVALID_ARG;
+  if (h_q / h_kv > 128) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+int check_pages(const kv_pages_t* p) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  if (p->dtype != SDPA_BF16 && p->dtype != SDPA_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (p->d != kDim) return MLA_ERR_UNSUPPORTED;
+  if (p->k == nullptr || p->v == nullptr || !ptr_aligned(p->k, 16) || !ptr_aligned(p->v, 16)) return MLA_ERR_INVALID_ARG;
+  if (p->num_pages < 1 || p->h_kv < 1) return MLA_ERR_INVALID_ARG;
+  if (p->page_size < 16 || p->page_size > 65536 || (p->page_size & (p->page_size - 1)) != 0) return MLA_ERR_UNSUPPORTED;
+  const int e = elem_size(p->dtype);
+  if (!stride_ok(p->page_stride, e) || !stride_ok(p->row_stride, e) || !stride_ok(p->head_stride, e))
+    return MLA_ERR_INVALID_ARG;
+  return MLA_OK;
+}
+
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  cudaGetLastError();
+  return MLA_ERR_CUDA;
+}
+
+int shift_of(int pow2) {
+  int s = 0;
+  while ((1 << s) < pow2) ++s;
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_pages_map(int batch, int page_size, const int32_t* held_lens, const int32_t* new_lens,
+                 const int32_t* cu_seqlens_q, int total_q, int32_t* block_table, int table_width, int32_t* free_pages,
+                 int free_capacity, const int32_t* free_in, int32_t* free_out, int64_t* slot_map, int32_t* positions,
+                 void* stream) {
+  if (batch < 1 || page_size < 1 || table_width < 1 || free_capacity < 1 || total_q < 0) return MLA_ERR_INVALID_ARG;
+  if (held_lens == nullptr || new_lens == nullptr || cu_seqlens_q == nullptr || block_table == nullptr ||
+      free_pages == nullptr || free_in == nullptr || free_out == nullptr || (slot_map == nullptr && total_q > 0))
+    return MLA_ERR_INVALID_ARG;
+  if (!words_ok({held_lens, new_lens, cu_seqlens_q, block_table, free_pages, free_in, free_out, positions}) ||
+      !ptr_aligned(slot_map, 8))
+    return MLA_ERR_INVALID_ARG;
+  if (batch > KV_PAGES_MAX_BATCH) return MLA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * table_width > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;   // page ordinals are int32
+  skv::DeviceInfo dev;
+  const int st = skv::current_device(&dev);
+  if (st != MLA_OK) return st;
+  skv::PagesMapArgs a{};
+  a.batch = batch;
+  a.page_size = page_size;
+  a.held = held_lens;
+  a.lens = new_lens;
+  a.cu_q = cu_seqlens_q;
+  a.total_q = total_q;
+  a.table = block_table;
+  a.width = table_width;
+  a.free_pages = free_pages;
+  a.capacity = free_capacity;
+  a.free_in = free_in;
+  a.free_out = free_out;
+  a.slots = slot_map;
+  a.positions = positions;
+  return cuda_status(skv::launch_pages_map(a, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, const void* v_new, int64_t token_stride,
+                   int64_t head_stride, const int64_t* slot_map, const float* descale_k, const float* descale_v,
+                   void* stream) {
+  int st = check_pages(pages);
+  if (st != MLA_OK) return st;
+  if (rows < 0 || rows > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (rows == 0) return MLA_OK;
+  if (k_new == nullptr || v_new == nullptr || slot_map == nullptr) return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(k_new, 16) || !ptr_aligned(v_new, 16) || !ptr_aligned(slot_map, 8)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(token_stride, 2) || !stride_ok(head_stride, 2)) return MLA_ERR_INVALID_ARG;
+  if (!words_ok({descale_k, descale_v})) return MLA_ERR_INVALID_ARG;
+  if (rows * pages->h_kv > (int64_t{1} << 35)) return MLA_ERR_INVALID_ARG;
+  skv::DeviceInfo dev;
+  st = skv::current_device(&dev);
+  if (st != MLA_OK) return st;
+  skv::PagesWriteArgs a{};
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.token_stride = token_stride;
+  a.head_stride = head_stride;
+  a.slots = slot_map;
+  a.rows = rows;
+  a.k = pages->k;
+  a.v = pages->v;
+  a.page_stride = pages->page_stride;
+  a.row_stride = pages->row_stride;
+  a.cache_head_stride = pages->head_stride;
+  a.num_slots = static_cast<int64_t>(pages->num_pages) * pages->page_size;
+  a.page_shift = shift_of(pages->page_size);
+  a.h_kv = pages->h_kv;
+  a.descale_k = descale_k;
+  a.descale_v = descale_v;
+  return cuda_status(skv::launch_pages_write(a, pages->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_per_seq, int total_q_max, int max_kv,
+                    int num_sms, int max_splits, int force_splits, sdpa_paged_plan_t* out) {
+  if (out == nullptr) return MLA_ERR_INVALID_ARG;
+  std::memset(out, 0, sizeof(*out));
+  int st = check_heads(batch, h_q, h_kv, d, dtype);
+  if (st != MLA_OK) return st;
+  if (max_q_per_seq < 1 || total_q_max < 1 || max_kv < 1 || num_sms < 0) return MLA_ERR_INVALID_ARG;
+  if (max_splits < 0 || max_splits > MLA_MAX_SPLITS || force_splits < 0 || force_splits > MLA_MAX_SPLITS)
+    return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(total_q_max) * h_q > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (num_sms == 0) {
+    skv::DeviceInfo dev;
+    if ((st = skv::current_device(&dev)) != MLA_OK) return st;
+    num_sms = dev.num_sms;
+  }
+  const int S = 1;
+  out->batch = batch;
+  out->h_q = h_q;
+  out->h_kv = h_kv;
+  out->d = d;
+  out->dtype = dtype;
+  out->max_q_per_seq = max_q_per_seq;
+  out->total_q_max = total_q_max;
+  out->max_kv = max_kv;
+  out->num_splits = S;
+  out->num_sms = num_sms;
+  return MLA_OK;
+}
+
+int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_t q_token_stride,
+               int64_t q_head_stride, const kv_pages_t* pages, const int32_t* block_table, int table_width,
+               const int32_t* kv_lens, const int32_t* cu_seqlens_q, const float* descale_q, const float* descale_k,
+               const float* descale_v, float sm_scale, int out_dtype, float out_inv_scale, void* out, float* lse_out,
+               float* amax_out, void* workspace, void* stream) {
+  if (plan == nullptr) return MLA_ERR_INVALID_ARG;
+  int st = check_heads(plan->batch, plan->h_q, plan->h_kv, plan->d, plan->dtype);
+  if (st != MLA_OK) return st;
+  if ((st = check_pages(pages)) != MLA_OK) return st;
+  if (pages->dtype != plan->dtype || pages->h_kv != plan->h_kv || pages->d != plan->d) return MLA_ERR_INVALID_ARG;
+  if (plan->num_splits < 1 || plan->num_splits > MLA_MAX_SPLITS || plan->num_sms < 1) return MLA_ERR_INVALID_ARG;
+  if (total_q < 1 || total_q > plan->total_q_max || table_width < 1) return MLA_ERR_INVALID_ARG;
+  if (q == nullptr || block_table == nullptr || kv_lens == nullptr || cu_seqlens_q == nullptr) return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(q, 16) || !words_ok({block_table, kv_lens, cu_seqlens_q, descale_q, descale_k, descale_v, lse_out, amax_out}))
+    return MLA_ERR_INVALID_ARG;
+  const int e = elem_size(plan->dtype);
+  if (!stride_ok(q_token_stride, e) || !stride_ok(q_head_stride, e)) return MLA_ERR_INVALID_ARG;
+  if (!out_ok(out, out_dtype, out_inv_scale) || !std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
+  if (plan->workspace_bytes > 0 && (workspace == nullptr || !ptr_aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
+  skv::DeviceInfo dev;
+  if ((st = skv::current_device(&dev)) != MLA_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (amax_out != nullptr && (st = cuda_status(cudaMemsetAsync(amax_out, 0, sizeof(float), cs))) != MLA_OK) return st;
+  skv::AttnArgs a{};
+  a.q = q;
+  a.k = pages->k;
+  a.v = pages->v;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.kv_ps = pages->page_stride;
+  a.kv_rs = pages->row_stride;
+  a.kv_hs = pages->head_stride;
+  a.table = block_table;
+  a.table_width = table_width;
+  a.page_shift = shift_of(pages->page_size);
+  a.num_pages = pages->num_pages;
+  a.cu_q = cu_seqlens_q;
+  a.kv_lens = kv_lens;
+  a.descale_q = descale_q;
+  a.descale_k = descale_k;
+  a.descale_v = descale_v;
+  a.batch = plan->batch;
+  a.h_q = plan->h_q;
+  a.h_kv = plan->h_kv;
+  a.group = plan->h_q / plan->h_kv;
+  a.total_q = total_q;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.inv_scale = out_inv_scale;
+  a.lse_out = lse_out;
+  a.amax = amax_out;
+  a.status = dev.status;
+  a.wait_limit_ns = skv::wait_limit_ns();
+  a.drain_limit_ns = skv::drain_limit_ns();
+  return cuda_status(skv::launch_attn_rows(a, plan->dtype, cs));
+}
+
+int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,
+                int64_t q_token_stride, int64_t q_head_stride, const void* k, const void* v, int64_t kv_token_stride,
+                int64_t kv_head_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                const float* descale_q, const float* descale_k, const float* descale_v, float sm_scale, int out_dtype,
+                float out_inv_scale, void* out, float* lse_out, float* amax_out, void* stream) {
+  int st = check_heads(batch, h_q, h_kv, d, dtype);
+  if (st != MLA_OK) return st;
+  if (total_q < 1 || total_kv < 1 || total_kv > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(total_q) * h_q > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (q == nullptr || k == nullptr || v == nullptr || cu_seqlens_q == nullptr || cu_seqlens_kv == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(q, 16) || !ptr_aligned(k, 16) || !ptr_aligned(v, 16) ||
+      !words_ok({cu_seqlens_q, cu_seqlens_kv, descale_q, descale_k, descale_v, lse_out, amax_out}))
+    return MLA_ERR_INVALID_ARG;
+  const int e = elem_size(dtype);
+  if (!stride_ok(q_token_stride, e) || !stride_ok(q_head_stride, e) || !stride_ok(kv_token_stride, e) ||
+      !stride_ok(kv_head_stride, e))
+    return MLA_ERR_INVALID_ARG;
+  if (!out_ok(out, out_dtype, out_inv_scale) || !std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
+  skv::DeviceInfo dev;
+  if ((st = skv::current_device(&dev)) != MLA_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (amax_out != nullptr && (st = cuda_status(cudaMemsetAsync(amax_out, 0, sizeof(float), cs))) != MLA_OK) return st;
+  skv::AttnArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.kv_rs = kv_token_stride;
+  a.kv_hs = kv_head_stride;
+  a.cu_q = cu_seqlens_q;
+  a.cu_kv = cu_seqlens_kv;
+  a.descale_q = descale_q;
+  a.descale_k = descale_k;
+  a.descale_v = descale_v;
+  a.batch = batch;
+  a.h_q = h_q;
+  a.h_kv = h_kv;
+  a.group = h_q / h_kv;
+  a.total_q = total_q;
+  a.total_kv = static_cast<int>(total_kv);
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.out = out;
+  a.out_dtype = out_dtype;
+  a.inv_scale = out_inv_scale;
+  a.lse_out = lse_out;
+  a.amax = amax_out;
+  a.status = dev.status;
+  a.wait_limit_ns = skv::wait_limit_ns();
+  a.drain_limit_ns = skv::drain_limit_ns();
+  return cuda_status(skv::launch_attn_rows(a, dtype, cs));
+}
+
+}  // extern "C"

@@ -146,4 +146,67 @@ int sdpa_decode_smem_bytes();
 cudaError_t launch_sdpa_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const SdpaArgs& a, bool direct, cudaStream_t stream);
 
+// Attention of packed queries over a paged cache or over packed K and V.
+struct AttnArgs {
+  const void* q;                // element (token, head, x) at token * q_ts + head * q_hs + x
+  const void* k;                // paged: element (page, row, head, x) at page * kv_ps + row * kv_rs +
+  const void* v;                // head * kv_hs + x; packed: row = the token, no pages
+  int64_t q_ts, q_hs;
+  int64_t kv_ps, kv_rs, kv_hs;
+  const int32_t* table;         // paged: [batch][table_width]; null: packed
+  int table_width, page_shift, num_pages;
+  const int32_t* cu_q;          // [batch + 1]
+  const int32_t* kv_lens;       // paged: [batch]
+  const int32_t* cu_kv;         // packed: [batch + 1]
+  const float* descale_q;       // device scalars or null
+  const float* descale_k;
+  const float* descale_v;
+  int batch, h_q, h_kv, group, total_q;
+  int total_kv;                 // packed
+  float scale_log2;
+  void* out;                    // [total_q][h_q][128]
+  int out_dtype;
+  float inv_scale;
+  float* lse_out;
+  float* amax;
+  uint32_t* status;
+  uint64_t wait_limit_ns, drain_limit_ns;   // as in MlaArgs
+};
+cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, cudaStream_t stream);
+
+struct PagesMapArgs {
+  int batch, page_size;
+  const int32_t* held;
+  const int32_t* lens;
+  const int32_t* cu_q;
+  int total_q;
+  int32_t* table;
+  int width;
+  int32_t* free_pages;
+  int capacity;
+  const int32_t* free_in;
+  int32_t* free_out;
+  int64_t* slots;
+  int32_t* positions;           // or null
+};
+cudaError_t launch_pages_map(const PagesMapArgs& a, cudaStream_t stream);
+
+struct PagesWriteArgs {
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t token_stride, head_stride;
+  const int64_t* slots;
+  int64_t rows;
+  void* k;
+  void* v;
+  int64_t page_stride, row_stride, cache_head_stride;
+  int64_t num_slots;
+  int page_shift, h_kv;
+  const float* descale_k;
+  const float* descale_v;
+};
+cudaError_t launch_pages_write(const PagesWriteArgs& a, int dtype, cudaStream_t stream);
+
+cudaError_t prepare_paged_kernels();
+
 }  // namespace skv
