@@ -50,7 +50,8 @@ def map_pages(page_size, held, new, cu_q, total_q, table, free_pages, free_in):
 
 def attend(q, keys, values, seen, sm_scale):
     """One sequence: q [n, h_q, d] (fp64), keys and values [m, h_kv, d], seen bool [n, m]. Returns (O [n, h_q, d],
-    LSE2 [n, h_q], A [n, h_q, d]) with A = sum_j softmax_j |v_j|, the scale of rounding errors of P and of the sum."""
+    LSE2 [n, h_q], A [n, h_q, d]) with A = sum_j max(p_j, 2^-14) |v_j| / sum_j p_j, p_j = exp(s_j - max s), the scale of
+    rounding errors of P and of the sum: below 2^-14 an f16 p is subnormal and its error is u 2^-14, not u p."""
     n, h_q, d = q.shape
     group = h_q // max(1, keys.shape[1])
     O, A = np.zeros((n, h_q, d)), np.zeros((n, h_q, d))
@@ -68,7 +69,7 @@ def attend(q, keys, values, seen, sm_scale):
         p = np.exp(s - m[:, None])
         z = np.where(has, p.sum(axis=1), 1.0)
         O[:, j] = (p @ V) / z[:, None]
-        A[:, j] = (p @ np.abs(V)) / z[:, None]
+        A[:, j] = (np.where(seen, np.maximum(p, 2.0 ** -14), 0.0) @ np.abs(V)) / z[:, None]
         L[:, j] = np.where(has, (m + np.log(z)) / LN2, -np.inf)
     return O, L, A
 

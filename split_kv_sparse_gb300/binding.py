@@ -77,7 +77,7 @@ class SdpaPagedPlan(ctypes.Structure):
                 ("max_kv", ctypes.c_int32), ("num_splits", ctypes.c_int32), ("num_sms", ctypes.c_int32),
                 ("adaptive_splits", ctypes.c_int32), ("row_kernel", ctypes.c_int32), ("o_acc_bytes", ctypes.c_uint64),
                 ("lse_acc_offset", ctypes.c_uint64), ("lse_acc_bytes", ctypes.c_uint64),
-                ("workspace_bytes", ctypes.c_uint64)]
+                ("map_offset", ctypes.c_uint64), ("workspace_bytes", ctypes.c_uint64)]
 
 
 _lib = None

@@ -61,6 +61,51 @@ int cuda_status(cudaError_t e) {
   return MLA_ERR_CUDA;
 }
 
+// Q as [total_q][h_q][128] in boxes of one row block: group heads of 128 / group tokens.
+int encode_q(CUtensorMap* m, int dtype, const void* q, int64_t ts, int64_t hs, int h_q, int group, int total_q) {
+  auto enc = skv::tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t e = elem_size(dtype);
+  const cuuint64_t dims[3] = {kDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[2] = {hs * e, ts * e};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / e), static_cast<cuuint32_t>(group),
+                             static_cast<cuuint32_t>(128 / group)};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return enc(m, dtype == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+             const_cast<void*>(q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+// K or V as [heads][pages][rows][128] in boxes of `box_rows` rows of one page and head.
+int encode_kv(CUtensorMap* m, int dtype, const void* base, int64_t rows, int64_t row_stride, int64_t pages,
+              int64_t page_stride, int heads, int64_t head_stride, int box_rows) {
+  auto enc = skv::tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t e = elem_size(dtype);
+  const cuuint64_t dims[4] = {kDim, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(pages),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {row_stride * e, page_stride * e, head_stride * e};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / e), static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, dtype == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+             const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
+// The most (sequence, query tile) pairs of `tokens` tokens that total_q rows of `batch` sequences can make.
+int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / tokens + std::min(total_q, batch); }
+
+// Jobs that one launch may hold: unsplit, forced splits, or counts from the lengths.
+int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int num_sms) {
+  if (!adaptive) return unsplit * num_splits;
+  return unsplit <= num_sms ? num_sms : unsplit + num_sms;
+}
+
 int shift_of(int pow2) {
   int s = 0;
   while ((1 << s) < pow2) ++s;
@@ -155,7 +200,15 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
     if ((st = skv::current_device(&dev)) != MLA_OK) return st;
     num_sms = dev.num_sms;
   }
-  const int S = 1;
+  const int group = h_q / h_kv;
+  int S = force_splits;
+  int adaptive = 0;
+  if (S == 0) {
+    const int cap = max_splits > 0 ? max_splits : MLA_MAX_SPLITS;
+    S = std::min(cap, (max_kv + 127) / 128);
+    adaptive = S > 1 ? 1 : 0;
+  }
+  const int64_t unsplit = tiles_bound(total_q_max, batch, 2 * (128 / group)) * h_kv;
   out->batch = batch;
   out->h_q = h_q;
   out->h_kv = h_kv;
@@ -166,6 +219,21 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->max_kv = max_kv;
   out->num_splits = S;
   out->num_sms = num_sms;
+  out->adaptive_splits = adaptive;
+  if (S > 1) {
+    // split jobs: as many as forced, or at most one wave (the rule keeps to that)
+    const int64_t slots = adaptive ? num_sms : unsplit * S;
+    if (slots * skv::kTileRows > 0x7FFFFFFFll) {
+      std::memset(out, 0, sizeof(*out));
+      return MLA_ERR_UNSUPPORTED;
+    }
+    const uint64_t rows = static_cast<uint64_t>(slots) * skv::kTileRows;
+    out->o_acc_bytes = rows * kDim * 4;
+    out->lse_acc_offset = round_up(out->o_acc_bytes, 256);
+    out->lse_acc_bytes = rows * 4;
+    out->map_offset = round_up(out->lse_acc_offset + out->lse_acc_bytes, 256);
+    out->workspace_bytes = round_up(out->map_offset + static_cast<uint64_t>(total_q_max) * h_kv * 8, 256);
+  }
   return MLA_OK;
 }
 
@@ -221,10 +289,31 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.inv_scale = out_inv_scale;
   a.lse_out = lse_out;
   a.amax = amax_out;
+  a.num_splits = plan->num_splits;
+  a.adaptive = plan->adaptive_splits;
+  a.num_sms = plan->num_sms;
+  if (plan->num_splits > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.o_part = reinterpret_cast<float*>(ws);
+    a.lse_part = reinterpret_cast<float*>(ws + plan->lse_acc_offset);
+    a.row_map = reinterpret_cast<int2*>(ws + plan->map_offset);
+  }
   a.status = dev.status;
   a.wait_limit_ns = skv::wait_limit_ns();
   a.drain_limit_ns = skv::drain_limit_ns();
-  return cuda_status(skv::launch_attn_rows(a, plan->dtype, cs));
+  CUtensorMap tq, tk, tv;
+  const int box = std::min(pages->page_size, 128);
+  if ((st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK ||
+      (st = encode_kv(&tk, plan->dtype, pages->k, pages->page_size, pages->row_stride, pages->num_pages,
+                      pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK ||
+      (st = encode_kv(&tv, plan->dtype, pages->v, pages->page_size, pages->row_stride, pages->num_pages,
+                      pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK)
+    return st;
+  const int64_t unsplit = tiles_bound(total_q, a.batch, 2 * (128 / a.group)) * a.h_kv;
+  const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms);
+  st = cuda_status(skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
+  if (st != MLA_OK || a.num_splits == 1) return st;
+  return cuda_status(skv::launch_attn_combine(a, skv::kTileRows, cs));
 }
 
 int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,
@@ -275,10 +364,18 @@ int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int
   a.inv_scale = out_inv_scale;
   a.lse_out = lse_out;
   a.amax = amax_out;
+  a.num_splits = 1;
+  a.num_sms = dev.num_sms;
   a.status = dev.status;
   a.wait_limit_ns = skv::wait_limit_ns();
   a.drain_limit_ns = skv::drain_limit_ns();
-  return cuda_status(skv::launch_attn_rows(a, dtype, cs));
+  CUtensorMap tq, tk, tv;
+  if ((st = encode_q(&tq, dtype, q, q_token_stride, q_head_stride, h_q, a.group, total_q)) != MLA_OK ||
+      (st = encode_kv(&tk, dtype, k, total_kv, kv_token_stride, 1, kv_token_stride, h_kv, kv_head_stride, 128)) != MLA_OK ||
+      (st = encode_kv(&tv, dtype, v, total_kv, kv_token_stride, 1, kv_token_stride, h_kv, kv_head_stride, 128)) != MLA_OK)
+    return st;
+  const int64_t grid = tiles_bound(total_q, batch, 2 * (128 / a.group)) * h_kv;
+  return cuda_status(skv::launch_attn_tile(tq, tk, tv, a, dtype, grid, cs));
 }
 
 }  // extern "C"

@@ -1,0 +1,199 @@
+// Shared by the kernels of attention over paged or packed K and V: a sequence's
+// lengths, the search for a CTA's job, and waits that can be inlined.
+#pragma once
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "softmax_util.cuh"
+
+namespace skv {
+
+constexpr int kAttnDim = 128;
+constexpr int kAttnKeyTile = 128;   // keys per tile, the unit of a split
+
+struct AttnSeq {
+  int q0, sq;   // first query row and query count
+  int k0, kv;   // packed: first key row; key count
+};
+
+// Lengths of sequence b, cut to what the buffers hold whatever the device arrays say.
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
+  AttnSeq s;
+  s.q0 = min(max(a.cu_q[b], 0), a.total_q);
+  s.sq = max(min(a.cu_q[b + 1], a.total_q) - s.q0, 0);
+  if (a.table != nullptr) {
+    const int64_t most = static_cast<int64_t>(a.table_width) << a.page_shift;
+    s.k0 = 0;
+    s.kv = static_cast<int>(min(static_cast<int64_t>(max(a.kv_lens[b], 0)), most));
+  } else {
+    s.k0 = min(max(a.cu_kv[b], 0), a.total_kv);
+    s.kv = max(min(a.cu_kv[b + 1], a.total_kv) - s.k0, 0);
+  }
+  return s;
+}
+
+__device__ __forceinline__ int warp_scan_incl(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+struct AttnJob {
+  int b;      // sequence, -1: no job
+  int j;      // query tile of the sequence
+  int g;      // KV head
+  int s, S;   // split, and splits of this sequence
+  int slot;   // S > 1: the job's place among the split jobs
+};
+
+// Job `idx` of the batch, found by one warp. Sequence b has n_b = ceil(s_b /
+// tokens) query tiles and S_b splits: num_splits of them where the plan forces a
+// count, else, with T = the key tiles a job should walk, clamp(ceil(tiles_b / T), 1,
+// num_splits). If the unsplit jobs fit the SMs, T is the smallest from ceil(work /
+// num_sms) on (growing by an eighth) whose jobs fit one wave; otherwise only a
+// sequence that walks more than twice its SM's share of the work is split, into
+// shares of two: both bound the split jobs by num_sms. Jobs are listed sequence by
+// sequence; within one the last query tiles first (they see the most keys), then the
+// splits, the KV heads fastest.
+__device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, int idx, int lane) {
+  int T = 0;   // 0: S_b = num_splits
+  const int batches = (a.batch + 31) / 32;
+  auto shape = [&](int b, int& n, int& tiles) {
+    n = tiles = 0;
+    if (b < a.batch) {
+      const AttnSeq q = attn_seq(a, b);
+      n = (q.sq + tokens - 1) / tokens;
+      tiles = (q.kv + kAttnKeyTile - 1) / kAttnKeyTile;
+    }
+  };
+  auto splits = [&](int tiles) { return T == 0 ? a.num_splits : min(a.num_splits, max(1, (tiles + T - 1) / T)); };
+  if (a.adaptive && a.num_splits > 1) {
+    int jobs = 0;
+    long long work = 0;
+    for (int i = 0; i < batches; ++i) {
+      int n, tiles;
+      shape(32 * i + lane, n, tiles);
+      jobs += warp_sum_int(n);
+      long long w = static_cast<long long>(n) * tiles;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      work += w;
+    }
+    const long long share = (work * a.h_kv + a.num_sms - 1) / a.num_sms;
+    T = static_cast<int>(min(max(share, 1ll), 1ll << 24));   // (more tiles than a sequence can have)
+    if (static_cast<int64_t>(jobs) * a.h_kv > a.num_sms) {
+      T *= 2;
+    } else {
+      for (int k = 0; k < 200; ++k) {
+        int total = 0, most = 1;
+        for (int i = 0; i < batches; ++i) {
+          int n, tiles;
+          shape(32 * i + lane, n, tiles);
+          const int s = splits(tiles);
+          total += warp_sum_int(n * s);
+          most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? s : 1));
+        }
+        if (most == 1 || total * a.h_kv <= a.num_sms) break;
+        T += (T + 7) >> 3;
+      }
+    }
+  }
+  AttnJob job = {-1, 0, 0, 0, 1, 0};
+  int base = 0, slots = 0;
+  for (int i = 0; i < batches && job.b < 0; ++i) {
+    int n, tiles;
+    shape(32 * i + lane, n, tiles);
+    const int s = splits(tiles);
+    const int count = n * s * a.h_kv;
+    const int split_count = s > 1 ? count : 0;
+    const int incl = warp_scan_incl(count, lane), sincl = warp_scan_incl(split_count, lane);
+    const int local = idx - base - (incl - count);
+    const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int l = __shfl_sync(0xffffffffu, local, src);
+      const int nn = __shfl_sync(0xffffffffu, n, src);
+      const int first = __shfl_sync(0xffffffffu, slots + sincl - split_count, src);
+      job.b = 32 * i + src;
+      job.S = __shfl_sync(0xffffffffu, s, src);
+      job.g = l % a.h_kv;
+      const int rest = l / a.h_kv;
+      job.s = rest % job.S;
+      job.j = nn - 1 - rest / job.S;
+      job.slot = first + (job.j * a.h_kv + job.g) * job.S + job.s;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    slots += __shfl_sync(0xffffffffu, sincl, 31);
+  }
+  return job;
+}
+
+// wait_bounded without a call, for kernels whose warps share out the registers:
+// gives up after ctx.limit_ns or when another role of the CTA has, and says so.
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const WaitCtx& ctx, uint32_t site) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 15u) == 0) {
+      if (*ctx.abort_flag) return false;
+      if (globaltimer_ns() - t0 > ctx.limit_ns) {
+        *ctx.abort_flag = 1;
+        atomicOr(&ctx.status[0], 1u);
+        atomicCAS(&ctx.status[1], 0u, site);
+        return false;
+      }
+    }
+  }
+}
+
+// One 16-byte piece of an output row: elements c .. c + 3 (fp32), c .. c + 7 (bf16)
+// or c .. c + 15 (e4m3) of values x.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+// 32 consecutive elements at element offset `at` of an output of type out_dtype
+// (MLA_OUT_*: 0 fp32, 1 bf16, 2 e4m3).
+__device__ __forceinline__ void store32(void* out, int out_dtype, int64_t at, const float (&x)[32], float inv_scale) {
+  if (out_dtype == 0) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else if (out_dtype == 1) {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
+                        pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
+  } else {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = pack_e4m3x4(x[16 * i + 4 * k] * inv_scale, x[16 * i + 4 * k + 1] * inv_scale,
+                           x[16 * i + 4 * k + 2] * inv_scale, x[16 * i + 4 * k + 3] * inv_scale);
+      p[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+}  // namespace skv

@@ -1,0 +1,682 @@
+// Attention of many query rows over a paged cache or packed K and V on the tensor
+// cores: S = Q K^T (scaled to log2 units), an online softmax, O += P V.
+//
+// One CTA per job (sequence, KV head, query tile, split). Its rows are tokens x the
+// heads of one group, up to two blocks of 128 rows, so every K and V tile (128
+// keys) is loaded once for the whole group. Two streams run through the tensor
+// pipe in turn, so one stream's softmax overlaps the other's products:
+//   two row blocks: stream i has row block i, both walk the same key tiles;
+//   one row block:  both have it, stream i walks the tiles of parity i, and the two
+//                   results are merged in shared memory.
+//   warps 0-3, 4-7  softmax, rescale and epilogue of stream 0 and 1: a thread is a
+//                   row (a TMEM lane), so no reduction crosses threads.
+//   warp 8          tcgen05 issue: S_i = Q_i K^T; O_i += P_i V with P_i read from
+//                   tensor memory, where it replaces S_i.
+//   warp 9          TMA: Q once, then K and V tiles into a ring of slots, page by page; bf16:
+//                   clears the V rows past the sequence's end (0 * NaN would reach a result).
+//   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0.
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+// P is rounded to V's MMA type (bf16; f16 for e4m3 V, whose values f16 holds exactly);
+// the sums are taken over the unrounded fp32 values. bf16 P costs 2^-8 relative a
+// term at most, as much as the rounding of a bf16 result.
+#include "attn_common.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kD = kAttnDim;
+constexpr int kTile = kAttnKeyTile;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
+
+template <bool kF8>
+struct Cfg {
+  static constexpr int kThreads = kF8 ? 512 : 384;
+  static constexpr int kEsz = kF8 ? 1 : 2;
+  static constexpr int kQBytes = 128 * kD * kEsz;        // one row block
+  static constexpr int kItemBytes = kTile * kD * kEsz;   // one K or V tile
+  static constexpr int kHalves = kF8 ? 1 : 2;            // 128-byte column blocks of a row
+  static constexpr int kSlots = kF8 ? 6 : 5;             // K(t) is item 2t, V(t) item 2t + 1; even for e4m3, so a slot
+                                                         // holds only K or only V tiles
+  static constexpr int kV16Bytes = kF8 ? kTile * kD * 2 : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = 2 * kQBytes;
+  static constexpr int kOffV16 = kOffRing + kSlots * kItemBytes;
+  static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
+  static constexpr int kOffMisc = kOffBars + 256;
+  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  // 128 rows x 128 fp32 of stream 1's result are merged through the ring and V16 area
+  static_assert(kOffBars - kOffRing >= 128 * kD * 4, "merge area");
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+enum {
+  B_Q = 0, B_S0, B_S1, B_P0, B_P1, B_O0, B_O1, B_VFIX, B_DRAIN, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_FULL0,
+  B_EMPTY0 = B_FULL0 + 8, kNumBars = B_EMPTY0 + 8
+};
+static_assert(kNumBars * 8 <= 256, "barrier area");
+
+enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
+
+// Words of the misc area.
+enum { M_TMEM = 0, M_ABORT, M_JOB, M_MASK = 12, kMaskRing = 16 };
+
+template <bool kF8>
+__global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
+    attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+  using C = Cfg<kF8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kOffMisc);
+  auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
+
+  const int tokens = 128 / a.group;   // of one row block
+  grid_dependency_wait();             // the job search reads the lengths
+  if (warp == 9) {
+    const AttnJob job = attn_find_job(a, 2 * tokens, blockIdx.x, lane);
+    if (lane == 0) {
+      misc[M_JOB + 0] = job.b;
+      misc[M_JOB + 1] = job.j;
+      misc[M_JOB + 2] = job.g;
+      misc[M_JOB + 3] = job.s;
+      misc[M_JOB + 4] = job.S;
+      misc[M_JOB + 5] = job.slot;
+    }
+  }
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_Q), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_S0 + i), 1);
+      mbar_init(bar(B_P0 + i), 4);
+      mbar_init(bar(B_O0 + i), 1);
+      mbar_init(bar(B_V16F0 + i), 4);
+      mbar_init(bar(B_V16E0 + i), 1);
+    }
+    mbar_init(bar(B_VFIX), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(bar(B_FULL0 + i), 1);
+      mbar_init(bar(B_EMPTY0 + i), kF8 && (i & 1) ? 4 : 1);   // a V tile of codes is freed by its four converters
+    }
+    misc[M_ABORT] = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  if (misc[M_JOB] < 0) {
+    grid_launch_dependents();
+    return;
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(smem + C::kOffMisc), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_launch_dependents();
+
+  const uint32_t tmem = static_cast<uint32_t>(misc[M_TMEM]);
+  const WaitCtx wc{a.wait_limit_ns, a.status, misc + M_ABORT};
+  const int job_b = misc[M_JOB], job_j = misc[M_JOB + 1], g = misc[M_JOB + 2], split = misc[M_JOB + 3],
+            S = misc[M_JOB + 4], slot0 = misc[M_JOB + 5];
+  const AttnSeq seq = attn_seq(a, job_b);
+  const int tok0 = job_j * 2 * tokens;                    // first token (of the sequence) of row block 0
+  const int tiles_all = (seq.kv + kTile - 1) / kTile;
+  const int base_t = tiles_all / S, rem_t = tiles_all - base_t * S;
+  const int tile0 = split * base_t + min(split, rem_t);
+  const int nt = base_t + (split < rem_t ? 1 : 0);
+  // keys that row block i sees: up to the position of its last token
+  auto tiles_of = [&](int i) {
+    const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
+    if (last < tok0 + i * tokens) return 0;
+    const int keys = seq.kv - seq.sq + last + 1;
+    return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
+  };
+  const bool one = tok0 + tokens >= seq.sq;               // one row block
+  const int n0 = tiles_of(0);
+  const int tiles = one ? n0 : max(n0, tiles_of(1));      // key tiles the job walks
+  const int cnt0 = one ? (tiles + 1) >> 1 : n0;
+  const int cnt1 = one ? tiles >> 1 : tiles_of(1);
+  const int tail = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;   // the
+                                                          // local tile that holds the sequence's ragged end, or -1
+
+  if (warp < 8) {
+    // ================================================= softmax + epilogue ===
+    if constexpr (kF8) regs_inc<176>();
+    else regs_inc<208>();
+    const int i = warp >> 2;
+    const int cnt = i ? cnt1 : cnt0;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + kTmemS + 128 * i, to = tmem + lanes + kTmemO + 128 * i;
+    const int rt = row / a.group;                          // token of the block
+    const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
+    const bool live = rt < tokens && tok < seq.sq;
+    const int lim = live ? seq.kv - seq.sq + tok : -1;     // last key the row sees
+    const float dq = a.descale_q ? *a.descale_q : 1.f, dk = a.descale_k ? *a.descale_k : 1.f,
+                dv = a.descale_v ? *a.descale_v : 1.f;
+    const float sc = dq * dk * a.scale_log2;
+    const bool raw_ok = sc > 0.f;      // then the scale commutes with the maximum and goes into the exponent's FMA
+    const float esc = raw_ok ? sc : 1.f;
+    float m_run = -INFINITY, l = 0.f;
+    bool bad = false;
+#pragma unroll 1
+    for (int u = 0; u < cnt; ++u) {
+      const int t = one ? 2 * u + i : u;
+      if (!wait_inline(bar(B_S0 + i), u & 1, wc, W_T_S)) {
+        bad = true;
+        break;
+      }
+      tc_fence_after();
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, r[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait_ld_x32(r[c]);
+      float(&x)[4][32] = reinterpret_cast<float(&)[4][32]>(r);
+      if (!raw_ok) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k) x[c][k] *= sc;
+      }
+      const int kmax = lim - (tile0 + t) * kTile;          // last visible key of the tile
+      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + (t & (kMaskRing - 1))]);   // 16-key groups with a page
+      if (__any_sync(0xffffffffu, kmax < kTile - 1) || pages != 0xffu) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * c + k > kmax || !((pages >> ((32 * c + k) >> 4)) & 1u)) x[c][k] = -INFINITY;
+      }
+      const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
+      const bool need = mx > m_run + kRescaleThreshold;
+      if (__any_sync(0xffffffffu, need)) {
+        float al = 1.f;
+        if (need) {
+          al = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
+          m_run = mx;
+          l *= al;
+        }
+        if (u > 0) {
+          if (!wait_inline(bar(B_O0 + i), (u - 1) & 1, wc, W_T_O)) {
+            bad = true;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + 16 * c, o);
+            tmem_wait_ld_x16(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al);
+            tmem_st_32x32b_x16(to + 16 * c, o);
+          }
+        }
+      }
+      const float nm = m_run == -INFINITY ? 0.f : -m_run;
+      const uint64_t esc2 = pair_f32(esc, esc), nm2 = pair_f32(nm, nm);
+      uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float e0, e1;
+          unpair_f32(fma_f32x2(pair_f32(x[c][2 * k], x[c][2 * k + 1]), esc2, nm2), e0, e1);
+          e0 = ex2_approx(e0);
+          e1 = ex2_approx(e1);
+          sum[k & 3] = add_f32x2(sum[k & 3], pair_f32(e0, e1));
+          p[k] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+        }
+        tmem_st_32x32b_x16(ts + 16 * c, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_P0 + i));
+      float s0, s1;
+      unpair_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
+      l += s0 + s1;
+    }
+
+    // ---- epilogue
+    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), (cnt - 1) & 1, wc, W_T_FIN);
+    if (one && !bad) {
+      // the merge reuses the ring: both streams' products must be done with it
+      const int oc = i ? cnt0 : cnt1;
+      if (oc > 0) bad = !wait_inline(bar(B_O0 + (1 - i)), (oc - 1) & 1, wc, W_T_MERGE);
+    }
+    tc_fence_after();
+    float4* merge = reinterpret_cast<float4*>(smem + C::kOffRing);           // [32][128 rows] pieces of 4 columns
+    float2* stats = reinterpret_cast<float2*>(smem + C::kOffQ);              // [128 rows] (m, l) of stream 1
+    if (one && i == 1) {
+      if (!bad) {
+        stats[row] = make_float2(m_run, l);
+        if (cnt > 0) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(to + 16 * c, o);
+            tmem_wait_ld_x16(o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              merge[(4 * c + k) * 128 + row] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                           __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+          }
+        }
+      }
+      named_bar_sync(2, 256);
+    } else {
+      float w0 = 1.f, w1 = 0.f;
+      if (one) {
+        named_bar_sync(2, 256);
+        bad = bad || *wc.abort_flag;
+        if (!bad) {
+          const float2 st = stats[row];
+          const float M = fmaxf(m_run, st.x);
+          w0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
+          w1 = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
+          l = l * w0 + st.y * w1;
+          m_run = M;
+        }
+      }
+      if (!bad) {
+        const bool some = l > 0.f || l != l;   // a NaN score stays a NaN result
+        const float inv = some ? dv / l : 0.f;
+        const float lse = some ? m_run + log2f(l) : -INFINITY;
+        const int64_t orow = static_cast<int64_t>(seq.q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
+        const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
+        const bool part = S > 1;
+        if (live) {
+          if (part) a.lse_part[prow] = lse;
+          else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
+          if (a.row_map != nullptr && split == 0 && row == rt * a.group)
+            a.row_map[static_cast<int64_t>(seq.q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
+        }
+        float amax = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float y[32];
+          if (cnt0 > 0 || !one) {
+            uint32_t o[32];
+            if (cnt > 0) {
+              tmem_ld_32x32b_x32(to + 32 * c, o);
+              tmem_wait_ld_x32(o);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = cnt > 0 && some ? __uint_as_float(o[k]) : 0.f;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) y[k] = 0.f;
+          }
+          if (one) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (cnt1 > 0 && w1 != 0.f) v = merge[(8 * c + k) * 128 + row];
+              y[4 * k] = y[4 * k] * w0 + v.x * w1;
+              y[4 * k + 1] = y[4 * k + 1] * w0 + v.y * w1;
+              y[4 * k + 2] = y[4 * k + 2] * w0 + v.z * w1;
+              y[4 * k + 3] = y[4 * k + 3] * w0 + v.w * w1;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            y[k] *= inv;
+            amax = fmaxf(amax, fabsf(y[k]));
+          }
+          if (live) {
+            if (part) store32(a.o_part, 0, prow * kD + 32 * c, y, 1.f);
+            else store32(a.out, a.out_dtype, orow * kD + 32 * c, y, a.inv_scale);
+          }
+        }
+        if (!part && a.amax != nullptr) {
+          if (!live) amax = 0.f;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          if (lane == 0) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
+        }
+      }
+    }
+  } else {
+    if constexpr (kF8) regs_dec<72>();
+    else regs_dec<88>();
+    if (warp == 8) {
+      // ======================================================= MMA issuer ===
+      if (lane == 0 && tiles > 0) {
+        constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
+        constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
+        // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
+        const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(sbase, 16, 1024) >> 32);
+        const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
+        const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffRing, 16, 1024));
+        const uint32_t v_lo = static_cast<uint32_t>(
+            sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffRing), kTile * 128, 1024));
+        auto issue_qk = [&](int i, int t) {
+          const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
+          const uint32_t kb = k_lo + static_cast<uint32_t>((2 * t) % C::kSlots) * (C::kItemBytes >> 4);
+          const uint32_t d = tmem + kTmemS + 128 * i;
+          if constexpr (kF8) {
+            mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
+            mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
+            mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
+            mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
+          } else {
+            mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) {
+              const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
+              mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
+            }
+          }
+        };
+        auto issue_pv = [&](int i, int t, bool acc) {
+          const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
+                                          : static_cast<uint32_t>((2 * t + 1) % C::kSlots) * (C::kItemBytes >> 4));
+          const uint32_t pa = tmem + kTmemS + 128 * i, d = tmem + kTmemO + 128 * i;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
+            mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (acc ? 1u : 0u));
+        };
+        auto tile_at = [&](int i, int u) { return one ? 2 * u + i : u; };
+        auto wait_item = [&](int item, uint32_t site) {
+          return wait_inline(bar(B_FULL0 + item % C::kSlots), (item / C::kSlots) & 1, wc, site);
+        };
+        auto qk_step = [&](int i, int u) {
+          const int t = tile_at(i, u);
+          if (!wait_item(2 * t, W_T_K)) return false;
+          tc_fence_after();
+          issue_qk(i, t);
+          mma_commit(bar(B_S0 + i));
+          if (one || i == 1 || t >= cnt1) mma_commit(bar(B_EMPTY0 + (2 * t) % C::kSlots));
+          return true;
+        };
+        bool ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
+        if (ok && cnt0 > 0) ok = qk_step(0, 0);
+        if (ok && cnt1 > 0) ok = qk_step(1, 0);
+        const int steps = max(cnt0, cnt1);
+#pragma unroll 1
+        for (int u = 0; ok && u < steps; ++u) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int cnt = i ? cnt1 : cnt0;
+            if (!ok || u >= cnt) continue;
+            const int t = tile_at(i, u);
+            if constexpr (kF8) ok = wait_inline(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, wc, W_T_V);
+            else ok = wait_item(2 * t + 1, W_T_V) && (t != tail || wait_inline(bar(B_VFIX), 0, wc, W_T_FIX));
+            ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(i, t, u > 0);
+            mma_commit(bar(B_O0 + i));
+            if (one || i == 1 || t >= cnt1) {
+              if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
+              else mma_commit(bar(B_EMPTY0 + (2 * t + 1) % C::kSlots));
+            }
+            if (u + 1 < cnt) ok = qk_step(i, u + 1);
+          }
+        }
+        if (!ok) {
+          mma_commit(bar(B_DRAIN));
+          if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+        }
+      }
+    } else if (warp == 9) {
+      // ===================================================== TMA producer ===
+      if (tiles > 0) {
+        const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
+        const int boxes = kTile / page_rows;               // of one tile and column block
+        if (lane == 0) {
+          tma_prefetch_desc(&tm_q);
+          tma_prefetch_desc(&tm_k);
+          tma_prefetch_desc(&tm_v);
+          const int blocks = one ? 1 : 2;
+          mbar_arrive_expect_tx(bar(B_Q), blocks * C::kHalves * tokens * a.group * 128);
+          for (int i = 0; i < blocks; ++i)
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_3d(sbase + C::kOffQ + i * C::kQBytes + h * 128 * 128, &tm_q, 64 * h, g * a.group,
+                          seq.q0 + tok0 + i * tokens, bar(B_Q));
+        }
+        // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
+        auto lookup = [&](int t, int& page, int& row) {
+          const int key = (tile0 + t) * kTile + lane * page_rows;
+          if (a.table == nullptr) {
+            page = 0;
+            row = seq.k0 + key;
+            return true;
+          }
+          page = a.num_pages;
+          row = key & ((1 << a.page_shift) - 1);
+          if (lane < boxes && key < seq.kv) {
+            const int p = a.table[static_cast<size_t>(job_b) * a.table_width + (key >> a.page_shift)];
+            if (p >= 0 && p < a.num_pages) page = p;
+          }
+          return page != a.num_pages;
+        };
+        int page, row, page_n = 0, row_n = 0;
+        bool have = lookup(0, page, row), have_n = false;
+        bool ok = true;
+        int item = 0;
+#pragma unroll 1
+        for (int t = 0; ok && t < tiles; ++t) {
+          if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
+          // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
+          const unsigned got = __ballot_sync(0xffffffffu, have);
+          unsigned groups = 0;
+          for (int i = 0; i < 8; ++i)
+            if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            const int sl = item % C::kSlots;
+            if (item >= C::kSlots && !wait_inline(bar(B_EMPTY0 + sl), ((item / C::kSlots) - 1) & 1, wc, W_T_PROD)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              if (kv == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
+              mbar_arrive_expect_tx(bar(B_FULL0 + sl), C::kItemBytes);
+            }
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = sbase + C::kOffRing + sl * C::kItemBytes + lane * page_rows * 128;
+              const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(B_FULL0 + sl));
+            }
+          }
+          page = page_n;
+          row = row_n;
+          have = have_n;
+        }
+        // the ragged end lies in the last tile: clear V's rows past it
+        if (!kF8 && ok && tail >= 0) {
+          const int it = item - 1;
+          if (wait_inline(bar(B_FULL0 + it % C::kSlots), (it / C::kSlots) & 1, wc, W_T_FIX)) {
+            uint8_t* v = smem + C::kOffRing + (it % C::kSlots) * C::kItemBytes;
+            for (int p = (seq.kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
+              *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + kTile * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_VFIX));
+          }
+        }
+        // nothing that was started may still be writing shared memory when the CTA ends
+        __syncwarp();
+        if (lane == 0) {
+          bool done = wait_drain(bar(B_Q), 0, a.drain_limit_ns);
+          for (int k = max(0, item - C::kSlots); k < item; ++k)
+            done = wait_drain(bar(B_FULL0 + k % C::kSlots), (k / C::kSlots) & 1, a.drain_limit_ns) && done;
+          if (!done) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+        }
+      }
+    } else if (kF8 && warp >= 12) {
+      // ================================================== V e4m3 -> f16 ===
+      const int key = threadIdx.x - 32 * 12;               // this thread's row of every tile
+      const int r8 = key & 7;
+#pragma unroll 1
+      for (int t = 0; t < tiles; ++t) {
+        const int it = 2 * t + 1, sl = it % C::kSlots;
+        if (!wait_inline(bar(B_FULL0 + sl), (it / C::kSlots) & 1, wc, W_T_CVT)) break;
+        if (t >= 2 && !wait_inline(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, wc, W_T_CVT)) break;
+        const uint8_t* src = smem + C::kOffRing + sl * C::kItemBytes + key * 128;
+        uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
+        const bool in = (tile0 + t) * kTile + key < seq.kv;
+        uint4 w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          w[c] = in ? *reinterpret_cast<const uint4*>(src + ((c ^ r8) << 4)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {                       // dims 16c .. 16c + 15
+          const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            asm("{\n  .reg .b16 lo, hi;\n  mov.b32 {lo, hi}, %2;\n  cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+                "  cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+                : "=r"(h[2 * k]), "=r"(h[2 * k + 1])
+                : "r"(ws[k]));
+          }
+          uint8_t* blk = dst + (c >> 2) * kTile * 128;      // 64-dim column block
+          const int p = 2 * (c & 3);
+          *reinterpret_cast<uint4*>(blk + ((p ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(blk + (((p + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(B_V16F0 + (t & 1)));
+          mbar_arrive(bar(B_EMPTY0 + sl));
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ combine --
+
+// One warp per (token, head): M = max_s LSE_s, w_s = 2^(LSE_s - M), O = sum_s w_s O_s
+// / sum_s w_s, four columns a lane; a token whose job was not split is left alone.
+__global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a, const int rows_per_slot) {
+  const int lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  const int end = min(max(a.cu_q[a.batch], 0), a.total_q);
+  float amax = 0.f;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+       row < static_cast<int64_t>(end) * a.h_q; row += static_cast<int64_t>(gridDim.x) * 8) {
+    const int tok = static_cast<int>(row / a.h_q), h = static_cast<int>(row - static_cast<int64_t>(tok) * a.h_q);
+    if (tok < max(a.cu_q[0], 0)) continue;
+    const int g = h / a.group;
+    const int2 map = a.row_map[static_cast<int64_t>(tok) * a.h_kv + g];
+    const int S = map.y;
+    if (S < 1) continue;
+    const int64_t p0 = static_cast<int64_t>(map.x) + (h - g * a.group);
+    const float l0 = lane < S ? a.lse_part[p0 + static_cast<int64_t>(lane) * rows_per_slot] : -INFINITY;
+    const float l1 = lane + 32 < S ? a.lse_part[p0 + static_cast<int64_t>(lane + 32) * rows_per_slot] : -INFINITY;
+    float M = fmaxf(l0, l1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float w0 = l0 == -INFINITY ? 0.f : exp2f(l0 - M), w1 = l1 == -INFINITY ? 0.f : exp2f(l1 - M);
+    float z = w0 + w1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < S; s0 += 8) {
+      float4 x[8];
+      float w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int s = s0 + k;
+        w[k] = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31);
+        if (s >= S) w[k] = 0.f;
+        x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (w[k] != 0.f)
+          x[k] = __ldcs(reinterpret_cast<const float4*>(a.o_part + (p0 + static_cast<int64_t>(s) * rows_per_slot) * kD) + lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (w[k] == 0.f) continue;
+        acc.x = fmaf(w[k], x[k].x, acc.x);
+        acc.y = fmaf(w[k], x[k].y, acc.y);
+        acc.z = fmaf(w[k], x[k].z, acc.z);
+        acc.w = fmaf(w[k], x[k].w, acc.w);
+      }
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / z;
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w))));
+    const int64_t at = row * kD + 4 * lane;
+    if (a.out_dtype == 0) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = acc;
+    else if (a.out_dtype == 1)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+          make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + at) =
+          pack_e4m3x4(acc.x * a.inv_scale, acc.y * a.inv_scale, acc.z * a.inv_scale, acc.w * a.inv_scale);
+    if (lane == 0 && a.lse_out != nullptr) a.lse_out[row] = M == -INFINITY ? -INFINITY : M + log2f(z);
+  }
+  if (a.amax != nullptr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (lane == 0 && amax > 0.f) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
+  }
+}
+
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace
+
+cudaError_t prepare_attn_tile() {
+  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<false>::kSmem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attn_tile_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<true>::kSmem);
+}
+
+cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream) {
+  if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(grid);
+  if (dtype == 2) return launch_pdl(attn_tile_kernel<true>, n, Cfg<true>::kThreads, Cfg<true>::kSmem, stream, tm_q, tm_k, tm_v, a);
+  return launch_pdl(attn_tile_kernel<false>, n, Cfg<false>::kThreads, Cfg<false>::kSmem, stream, tm_q, tm_k, tm_v, a);
+}
+
+cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream) {
+  const int64_t blocks = (static_cast<int64_t>(a.total_q) * a.h_q + 7) / 8;
+  const int64_t most = 4ll * a.num_sms;
+  return launch_pdl(attn_combine_kernel, static_cast<unsigned>(blocks < most ? blocks : most), 256, 0, stream, a, rows_per_slot);
+}
+
+}  // namespace skv

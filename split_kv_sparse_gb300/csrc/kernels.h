@@ -169,10 +169,25 @@ struct AttnArgs {
   float inv_scale;
   float* lse_out;
   float* amax;
+  int num_splits;               // the most splits a sequence gets
+  int adaptive;                 // its count follows from the lengths (else: exactly num_splits)
+  int num_sms;                  // SMs that the adaptive rule spreads the work over
+  float* o_part;                // num_splits > 1: partial rows [slot][rows of a job][128], normalised
+  float* lse_part;              // their log2 LSE
+  int2* row_map;                // [total_q][h_kv]: first partial row of the token's group, and its split
+                                // count (0: the final rows were written)
   uint32_t* status;
   uint64_t wait_limit_ns, drain_limit_ns;   // as in MlaArgs
 };
-cudaError_t launch_attn_rows(const AttnArgs& a, int dtype, cudaStream_t stream);
+// Query rows (tokens x group) and partial rows per job of each kernel.
+constexpr int kTileRows = 256;
+constexpr int kRowRows = 16;
+// tm_q: Q as 3-D [total_q][h_q][128], box {128 bytes, group heads, 128 / group tokens}; tm_k / tm_v: K and V as 4-D
+// {128, rows, pages, heads} (packed: one page of total_kv rows), box {128 bytes, min(page, 128) rows, 1, 1}.
+cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
+// Folds the partial rows of every split token; a.num_splits > 1. rows_per_slot: kTileRows or kRowRows.
+cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream);
 
 struct PagesMapArgs {
   int batch, page_size;
@@ -208,5 +223,6 @@ struct PagesWriteArgs {
 cudaError_t launch_pages_write(const PagesWriteArgs& a, int dtype, cudaStream_t stream);
 
 cudaError_t prepare_paged_kernels();
+cudaError_t prepare_attn_tile();
 
 }  // namespace skv

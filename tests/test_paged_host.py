@@ -48,13 +48,12 @@ def test_plan_is_deterministic_and_sizes_its_workspace():
             assert bytes(a) == bytes(z) and 1 <= a.num_splits <= b.MLA_MAX_SPLITS
             for S in (1, 5):
                 p = b.sdpa_paged_plan(batch, 32, 8, 128, "e4m3", max_q, batch * max_q, 16384, num_sms=152, force_splits=S)
-                assert p.num_splits in (1, S)
-                if p.num_splits == 1:
-                    assert p.workspace_bytes == 0
-            if a.num_splits > 1:
-                rows = batch * max_q * 32
-                assert a.o_acc_bytes == a.num_splits * rows * 128 * 4 and a.lse_acc_offset % 256 == 0
-                assert a.workspace_bytes >= a.lse_acc_offset + a.num_splits * rows * 4
+                assert p.num_splits == S and p.adaptive_splits == 0 and (p.workspace_bytes == 0) == (S == 1)
+            rows = 152 * 256              # one wave of split jobs, whatever the tokens
+            assert a.num_splits == 64 and a.adaptive_splits == 1
+            assert a.o_acc_bytes == rows * 128 * 4 and a.lse_acc_bytes == rows * 4 and a.lse_acc_offset % 256 == 0
+            assert a.map_offset >= a.lse_acc_offset + a.lse_acc_bytes
+            assert a.workspace_bytes >= a.map_offset + batch * max_q * 8 * 8
 
 
 def status_of(fn, *args):
