@@ -286,81 +286,116 @@ def mla_sparse_decode_noalloc(s_q: int, topk: int, q, kv, n_kv: int, idx, sm_sca
 # -------------------------------------------- paged KV cache, prompt attention --
 
 _SDPA_DTYPES = {"bf16": SDPA_BF16, "e4m3": SDPA_E4M3}
-_OUT_TORCH = {MLA_OUT_F32: ("float32",), MLA_OUT_BF16: ("bfloat16",), MLA_OUT_E4M3: ("uint8", "float8_e4m3fn")}
+
+
+class _Types:
+    """torch's types that the calls below take, by what they are used for (made on the first call)."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.f32, self.bf16 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
+        self.codes = (torch.uint8, torch.float8_e4m3fn)
+        self.data = self.bf16 + self.codes
+        self.bytes = (torch.uint8, torch.float32)
+        self.sdpa = {torch.bfloat16: SDPA_BF16, torch.uint8: SDPA_E4M3, torch.float8_e4m3fn: SDPA_E4M3}
+        self.out = {MLA_OUT_F32: self.f32, MLA_OUT_BF16: self.bf16, MLA_OUT_E4M3: self.codes}
+        self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.cuda = torch.cuda
+
+
+_types = None
+
+
+def _t() -> _Types:
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types
 
 
 def _refuse(where: str, what: str):
     raise SplitKVError(MLA_ERR_INVALID_ARG, f"{where}: {what}")
 
 
-def _dev(where: str, name: str, x, dtypes, numel: int = 0, contiguous: bool = True, optional: bool = False):
-    """Checks a device tensor (on the current device, of one of `dtypes`, contiguous, of at least `numel`
-    elements) and returns it."""
-    import torch
-    if x is None:
-        if optional:
-            return None
-        _refuse(where, f"{name} is missing")
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.device.index != torch.cuda.current_device():
+def _device(where: str) -> int:
+    """The current CUDA device."""
+    t = _t()
+    if not t.cuda.is_initialized():
+        if not t.cuda.is_available():
+            return -2          # no tensor lies on it
+        t.cuda.init()
+    return t.device()
+
+
+def _dev(where: str, name: str, x, dtypes, dev: int, numel: int = 0, contiguous: bool = True) -> int:
+    """The address of a tensor that lies on the current device, has one of `dtypes`, is contiguous (unless its strides
+    are taken) and holds at least `numel` elements; raises for any other."""
+    try:
+        if x.get_device() == dev and x.dtype in dtypes and x.numel() >= numel and (not contiguous or x.is_contiguous()):
+            return x.data_ptr()
+    except AttributeError:
+        _refuse(where, f"{name} is missing or no tensor")
+    if x.get_device() != dev:
         _refuse(where, f"{name} must be a tensor on the current CUDA device")
-    if str(x.dtype)[6:] not in dtypes:
-        _refuse(where, f"{name} has type {x.dtype}, not {' or '.join(dtypes)}")
-    if contiguous and not x.is_contiguous():
-        _refuse(where, f"{name} must be contiguous")
+    if x.dtype not in dtypes:
+        _refuse(where, f"{name} has type {x.dtype}, not {' or '.join(map(str, dtypes))}")
     if x.numel() < numel:
         _refuse(where, f"{name} has {x.numel()} elements, fewer than {numel}")
-    return x
+    _refuse(where, f"{name} must be contiguous")
 
 
-def _sdpa_dtype(where: str, name: str, x) -> int:
-    t = str(x.dtype)[6:]
-    if t == "bfloat16":
-        return SDPA_BF16
-    if t in ("uint8", "float8_e4m3fn"):
-        return SDPA_E4M3
-    _refuse(where, f"{name} has type {x.dtype}, not bfloat16 or e4m3 codes")
+def _opt(where: str, name: str, x, dtypes, dev: int, numel: int = 0):
+    return None if x is None else _dev(where, name, x, dtypes, dev, numel)
 
 
 def _strided(where: str, name: str, x, dims: int):
     """The strides of a tensor whose last dimension is contiguous; a dimension of one element, whose stride
     says nothing, counts as packed."""
-    if x.dim() != dims or (x.shape[-1] > 1 and x.stride(-1) != 1):
+    st, shape = x.stride(), x.shape
+    if len(shape) != dims or (shape[-1] > 1 and st[-1] != 1):
         _refuse(where, f"{name} must have {dims} dimensions, the last one contiguous")
-    st = list(x.stride())
-    packed = 1
+    if 1 not in shape:
+        return st
+    st, packed = list(st), 1
     for i in reversed(range(dims)):
-        if x.shape[i] == 1:
+        if shape[i] == 1:
             st[i] = packed
-        packed *= max(1, x.shape[i])
-    return st
+        packed *= max(1, shape[i])
+    return tuple(st)
 
 
-def _descales(where: str, **ds):
-    return [_ptr(_dev(where, n, x, ("float32",), 1, optional=True)) for n, x in ds.items()]
+def _table(where: str, block_table, batch: int, dev: int):
+    p = _dev(where, "block_table", block_table, _t().i32, dev, 1)
+    if block_table.dim() != 2 or block_table.shape[0] < batch:
+        _refuse(where, "block_table must be [batch, table_width]")
+    return p, block_table.shape[1]
 
 
-def _outputs(where: str, out_dtype: int, out, lse_out, amax_out, rows: int, d: int):
-    if out_dtype not in _OUT_TORCH:
+def _outputs(where: str, out_dtype: int, out, lse_out, amax_out, rows: int, d: int, dev: int):
+    t = _t()
+    if out_dtype not in t.out:
         _refuse(where, f"unknown output type {out_dtype}")
-    _dev(where, "out", out, _OUT_TORCH[out_dtype], rows * d)
-    _dev(where, "lse_out", lse_out, ("float32",), rows, optional=True)
-    _dev(where, "amax_out", amax_out, ("float32",), 1, optional=True)
+    return (_dev(where, "out", out, t.out[out_dtype], dev, rows * d), _opt(where, "lse_out", lse_out, t.f32, dev, rows),
+            _opt(where, "amax_out", amax_out, t.f32, dev, 1))
+
+
+def _on(stream, dev: int) -> int:
+    return _t().raw_stream(dev) if stream is None else _stream(stream)
 
 
 def kv_pages(k_cache, v_cache) -> KvPages:
     """The C descriptor of a paged cache from views [num_pages, page_size, h_kv, d] of its tensors (bfloat16, or
     uint8 / float8_e4m3fn codes; any strides over a contiguous d, so a [num_pages, h_kv, page_size, d] cache is
     passed as its permute(0, 2, 1, 3)). The descriptor keeps the tensors alive."""
-    where = "kv_pages"
-    for n, x in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _dev(where, n, x, ("bfloat16", "uint8", "float8_e4m3fn"), contiguous=False)
+    where, t = "kv_pages", _t()
+    dev = _device(where)
+    k, v = (_dev(where, n, x, t.data, dev, contiguous=False) for n, x in (("k_cache", k_cache), ("v_cache", v_cache)))
     st = _strided(where, "k_cache", k_cache, 4)
-    dt = _sdpa_dtype(where, "k_cache", k_cache)
-    if tuple(v_cache.shape) != tuple(k_cache.shape) or _sdpa_dtype(where, "v_cache", v_cache) != dt \
-            or _strided(where, "v_cache", v_cache, 4) != st:
+    dt = t.sdpa[k_cache.dtype]
+    if v_cache.shape != k_cache.shape or t.sdpa[v_cache.dtype] != dt or _strided(where, "v_cache", v_cache, 4) != st:
         _refuse(where, "k_cache and v_cache differ in shape, type or strides")
     n, ps, h, d = k_cache.shape
-    pages = KvPages(k_cache.data_ptr(), v_cache.data_ptr(), dt, n, ps, h, d, 0, st[0], st[1], st[2])
+    pages = KvPages(k, v, dt, n, ps, h, d, 0, st[0], st[1], st[2])
     pages.tensors = (k_cache, v_cache)
     return pages
 
@@ -369,39 +404,37 @@ def kv_pages_map(page_size: int, held_lens, new_lens, cu_seqlens_q, total_q: int
                  free_out, slot_map=None, positions=None, stream=None):
     """Block tables and slot maps from request lengths (block_table, free_pages, free_out, slot_map and
     positions are written in place)."""
-    where, i32 = "kv_pages_map", ("int32",)
-    _dev(where, "held_lens", held_lens, i32, 1)
+    where, t = "kv_pages_map", _t()
+    i32, dev = t.i32, _device(where)
+    held = _dev(where, "held_lens", held_lens, i32, dev, 1)
     batch = held_lens.numel()
-    _dev(where, "new_lens", new_lens, i32, batch)
-    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, batch + 1)
-    _dev(where, "block_table", block_table, i32, 1)
-    if block_table.dim() != 2 or block_table.shape[0] < batch:
-        _refuse(where, "block_table must be [batch, table_width]")
-    _dev(where, "free_pages", free_pages, i32, 1)
-    _dev(where, "free_in", free_in, i32, 1)
-    _dev(where, "free_out", free_out, i32, 2)
-    _dev(where, "slot_map", slot_map, ("int64",), total_q, optional=total_q == 0)
-    _dev(where, "positions", positions, i32, total_q, optional=True)
-    _check(lib().kv_pages_map(batch, page_size, _ptr(held_lens), _ptr(new_lens), _ptr(cu_seqlens_q), total_q,
-                              _ptr(block_table), block_table.shape[1], _ptr(free_pages), free_pages.numel(),
-                              _ptr(free_in), _ptr(free_out), _ptr(slot_map), _ptr(positions), _stream(stream)), where)
+    new = _dev(where, "new_lens", new_lens, i32, dev, batch)
+    cu = _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, dev, batch + 1)
+    table, width = _table(where, block_table, batch, dev)
+    free = _dev(where, "free_pages", free_pages, i32, dev, 1)
+    fin, fout = _dev(where, "free_in", free_in, i32, dev, 1), _dev(where, "free_out", free_out, i32, dev, 2)
+    slots = _opt(where, "slot_map", slot_map, t.i64, dev, total_q)
+    pos = _opt(where, "positions", positions, i32, dev, total_q)
+    _check(lib().kv_pages_map(batch, page_size, held, new, cu, total_q, table, width, free, free_pages.numel(), fin, fout,
+                              slots, pos, _on(stream, dev)), where)
 
 
 def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, descale_v=None, stream=None):
     """Rows of k_new and v_new (bfloat16 [rows, h_kv, d], any strides over a contiguous d) into their slots."""
-    where = "kv_pages_write"
-    for n, x in (("k_new", k_new), ("v_new", v_new)):
-        _dev(where, n, x, ("bfloat16",), contiguous=False)
+    where, t = "kv_pages_write", _t()
+    dev = _device(where)
+    k = _dev(where, "k_new", k_new, t.bf16, dev, contiguous=False)
+    v = _dev(where, "v_new", v_new, t.bf16, dev, contiguous=False)
     st = _strided(where, "k_new", k_new, 3)
-    if tuple(v_new.shape) != tuple(k_new.shape) or _strided(where, "v_new", v_new, 3) != st:
+    if v_new.shape != k_new.shape or _strided(where, "v_new", v_new, 3) != st:
         _refuse(where, "k_new and v_new differ in shape or strides")
-    if tuple(k_new.shape[1:]) != (pages.h_kv, pages.d):
+    rows, h, d = k_new.shape
+    if h != pages.h_kv or d != pages.d:
         _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
-    rows = k_new.shape[0]
-    _dev(where, "slot_map", slot_map, ("int64",), rows)
-    dk, dv = _descales(where, descale_k=descale_k, descale_v=descale_v)
-    _check(lib().kv_pages_write(ctypes.byref(pages), rows, _ptr(k_new), _ptr(v_new), st[0], st[1], _ptr(slot_map), dk,
-                                dv, _stream(stream)), where)
+    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
+    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    _check(lib().kv_pages_write(ctypes.byref(pages), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev)), where)
 
 
 def sdpa_paged_plan(batch: int, h_q: int, h_kv: int, d: int, dtype, max_q_per_seq: int, total_q_max: int, max_kv: int,
@@ -418,50 +451,55 @@ def sdpa_paged(plan: SdpaPagedPlan, total_q: int, q, pages: KvPages, block_table
                workspace=None, stream=None):
     """Attention of new tokens over a paged cache; q [>= total_q, h_q, d] of the plan's type, any strides over a
     contiguous d."""
-    where, i32 = "sdpa_paged", ("int32",)
-    _dev(where, "q", q, ("bfloat16",) if plan.dtype == SDPA_BF16 else ("uint8", "float8_e4m3fn"), contiguous=False)
+    where, t = "sdpa_paged", _t()
+    dev = _device(where)
+    batch, h_q, d = plan.batch, plan.h_q, plan.d
+    qp = _dev(where, "q", q, t.bf16 if plan.dtype == SDPA_BF16 else t.codes, dev, contiguous=False)
     st = _strided(where, "q", q, 3)
-    if tuple(q.shape[1:]) != (plan.h_q, plan.d) or q.shape[0] < total_q:
-        _refuse(where, f"q must be [{total_q} or more, {plan.h_q}, {plan.d}]")
-    _dev(where, "block_table", block_table, i32, 1)
-    if block_table.dim() != 2 or block_table.shape[0] < plan.batch:
-        _refuse(where, "block_table must be [batch, table_width]")
-    _dev(where, "kv_lens", kv_lens, i32, plan.batch)
-    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, plan.batch + 1)
-    ds = _descales(where, descale_q=descale_q, descale_k=descale_k, descale_v=descale_v)
-    _outputs(where, _dtype(out_dtype), out, lse_out, amax_out, total_q * plan.h_q, plan.d)
+    n, h, x = q.shape
+    if h != h_q or x != d or n < total_q:
+        _refuse(where, f"q must be [{total_q} or more, {h_q}, {d}]")
+    table, width = _table(where, block_table, batch, dev)
+    lens = _dev(where, "kv_lens", kv_lens, t.i32, dev, batch)
+    cu = _dev(where, "cu_seqlens_q", cu_seqlens_q, t.i32, dev, batch + 1)
+    dq = _opt(where, "descale_q", descale_q, t.f32, dev, 1)
+    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    od = _dtype(out_dtype)
+    o, lse, amax = _outputs(where, od, out, lse_out, amax_out, total_q * h_q, d, dev)
+    ws = None
     if plan.workspace_bytes:
-        _dev(where, "workspace", workspace, ("uint8", "float32"))
-        if workspace.numel() * workspace.element_size() < plan.workspace_bytes:
+        ws = _dev(where, "workspace", workspace, t.bytes, dev)
+        if workspace.nbytes < plan.workspace_bytes:
             _refuse(where, "workspace is smaller than the plan's")
-    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, _ptr(q), st[0], st[1], ctypes.byref(pages), _ptr(block_table),
-                            block_table.shape[1], _ptr(kv_lens), _ptr(cu_seqlens_q), *ds, sm_scale, _dtype(out_dtype),
-                            out_inv_scale, _ptr(out), _ptr(lse_out), _ptr(amax_out), _ptr(workspace),
-                            _stream(stream)), where)
+    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, qp, st[0], st[1], ctypes.byref(pages), table, width, lens, cu, dq,
+                            dk, dv, sm_scale, od, out_inv_scale, o, lse, amax, ws, _on(stream, dev)), where)
 
 
 def sdpa_prompt(batch: int, q, k, v, cu_seqlens_q, cu_seqlens_kv, descale_q, descale_k, descale_v, sm_scale: float,
                 out_dtype, out_inv_scale: float, out, lse_out=None, amax_out=None, stream=None):
     """Causal attention over packed prompts; q [total_q, h_q, d], k and v [total_kv, h_kv, d] of one type, any
     strides over a contiguous d (k and v the same)."""
-    where, i32 = "sdpa_prompt", ("int32",)
-    for n, x in (("q", q), ("k", k), ("v", v)):
-        _dev(where, n, x, ("bfloat16", "uint8", "float8_e4m3fn"), contiguous=False)
-    dt = _sdpa_dtype(where, "q", q)
+    where, t = "sdpa_prompt", _t()
+    dev = _device(where)
+    qp, kp, vp = (_dev(where, n, x, t.data, dev, contiguous=False) for n, x in (("q", q), ("k", k), ("v", v)))
     qs, ks = _strided(where, "q", q, 3), _strided(where, "k", k, 3)
-    if tuple(v.shape) != tuple(k.shape) or _strided(where, "v", v, 3) != ks:
+    if v.shape != k.shape or _strided(where, "v", v, 3) != ks:
         _refuse(where, "k and v differ in shape or strides")
-    if _sdpa_dtype(where, "k", k) != dt or _sdpa_dtype(where, "v", v) != dt or k.shape[2] != q.shape[2]:
-        _refuse(where, "q, k and v must have one type and one head dim")
-    _dev(where, "cu_seqlens_q", cu_seqlens_q, i32, batch + 1)
-    _dev(where, "cu_seqlens_kv", cu_seqlens_kv, i32, batch + 1)
-    ds = _descales(where, descale_q=descale_q, descale_k=descale_k, descale_v=descale_v)
+    dt = t.sdpa[q.dtype]
     total_q, h_q, d = q.shape
-    _outputs(where, _dtype(out_dtype), out, lse_out, amax_out, total_q * h_q, d)
-    _check(lib().sdpa_prompt(batch, h_q, k.shape[1], d, dt, total_q, k.shape[0], _ptr(q), qs[0], qs[1], _ptr(k),
-                             _ptr(v), ks[0], ks[1], _ptr(cu_seqlens_q), _ptr(cu_seqlens_kv), *ds, sm_scale,
-                             _dtype(out_dtype), out_inv_scale, _ptr(out), _ptr(lse_out), _ptr(amax_out),
-                             _stream(stream)), where)
+    total_kv, h_kv, dk_ = k.shape
+    if t.sdpa[k.dtype] != dt or t.sdpa[v.dtype] != dt or dk_ != d:
+        _refuse(where, "q, k and v must have one type and one head dim")
+    cu = _dev(where, "cu_seqlens_q", cu_seqlens_q, t.i32, dev, batch + 1)
+    ck = _dev(where, "cu_seqlens_kv", cu_seqlens_kv, t.i32, dev, batch + 1)
+    dq = _opt(where, "descale_q", descale_q, t.f32, dev, 1)
+    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    od = _dtype(out_dtype)
+    o, lse, amax = _outputs(where, od, out, lse_out, amax_out, total_q * h_q, d, dev)
+    _check(lib().sdpa_prompt(batch, h_q, h_kv, d, dt, total_q, total_kv, qp, qs[0], qs[1], kp, vp, ks[0], ks[1], cu, ck, dq,
+                             dk, dv, sm_scale, od, out_inv_scale, o, lse, amax, _on(stream, dev)), where)
 
 
 # ------------------------------------------------------------------- status --

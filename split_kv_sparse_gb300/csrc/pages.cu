@@ -20,6 +20,8 @@ namespace {
 // few pages, so it is latency, not bandwidth, that counts.
 
 constexpr int kMapThreads = 1024;
+// Rows whose slots the same CTA writes; more get a grid of their own behind it.
+constexpr int kMapFusedRows = 4096;
 
 __device__ __forceinline__ int pages_of(int n, int page_size, int width) {
   const int p = n <= 0 ? 0 : (n - 1) / page_size + 1;
@@ -128,6 +130,10 @@ __global__ void __launch_bounds__(kMapThreads, 1) pages_map_kernel(const PagesMa
     a.free_out[0] = max(n - carry_w, 0);
     a.free_out[1] = max(carry_w - n, 0);
   }
+  if (a.total_q <= kMapFusedRows) {
+    __syncthreads();   // the table entries written above
+    for (int r = threadIdx.x; r < a.total_q; r += blockDim.x) slot_of_row(a, a.cu_q, r);
+  }
 }
 
 __global__ void __launch_bounds__(256) pages_slots_kernel(const PagesMapArgs a) {
@@ -202,7 +208,7 @@ constexpr int kMapMaxBatch = 16384;
 cudaError_t launch_pages_map(const PagesMapArgs& a, cudaStream_t stream) {
   const size_t smem = 2 * (static_cast<size_t>(a.batch) + 1) * sizeof(int);
   const cudaError_t e = launch_dependent(pages_map_kernel, 1, kMapThreads, smem, stream, a);
-  if (e != cudaSuccess || a.total_q == 0) return e;
+  if (e != cudaSuccess || a.total_q <= kMapFusedRows) return e;
   return launch_dependent(pages_slots_kernel, (a.total_q + 255u) / 256u, 256, 0, stream, a);
 }
 
