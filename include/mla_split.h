@@ -477,10 +477,10 @@ MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_
                    const float* descale_k, const float* descale_v, void* stream);
 
 /* Plan of sdpa_paged: what its launches and workspace need, from bounds that the
- * host knows. A job is (sequence, KV head, up to 256 query rows, split), its rows
- * tokens x the heads of one group. Workspace layout (256-byte aligned):
- *   [0, o_acc_bytes)                   fp32 partial rows [split job][256][128]
- *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][256]
+ * host knows. A job is (sequence, KV head, up to R query rows, split), its rows
+ * tokens x the heads of one group, R = 16 with row_kernel, else 256. Workspace layout (256-byte aligned):
+ *   [0, o_acc_bytes)                   fp32 partial rows [split job][R][128]
+ *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][R]
  *   [map_offset, ...)                  per (token, KV head): its first partial row, its splits
  * so its size is bounded by the SMs (one wave of split jobs), not by the tokens,
  * unless a split count is forced. 0 bytes with one split. It needs no clearing. */
@@ -489,14 +489,15 @@ typedef struct {
   int32_t h_q, h_kv;      /* query and KV heads; h_q % h_kv == 0, group = h_q / h_kv <= 128 */
   int32_t d;              /* 128                                                        */
   int32_t dtype;          /* SDPA_BF16 or SDPA_E4M3                                     */
-  int32_t max_q_per_seq;  /* bound on new tokens of one sequence                        */
+  int32_t max_q_per_seq;  /* expected bound on new tokens of one sequence (chooses the kernel) */
   int32_t total_q_max;    /* bound on new tokens of the batch                           */
   int32_t max_kv;         /* expected bound on keys of one sequence (sizes the split count
                              only: longer sequences are computed all the same)           */
   int32_t num_splits;     /* the most splits a sequence gets; exactly that many if forced */
   int32_t num_sms;
   int32_t adaptive_splits; /* 1: each sequence's split count follows from the lengths, on the GPU */
-  int32_t row_kernel;     /* 1: max_q_per_seq * group <= 16, one 16-row job per sequence and KV head */
+  int32_t row_kernel;     /* 1: max_q_per_seq * group <= 16: the kernel of 16-row jobs, two
+                             of them an SM; else the one of 256-row jobs. Either takes any number of tokens */
   uint64_t o_acc_bytes;
   uint64_t lse_acc_offset;
   uint64_t lse_acc_bytes;
@@ -507,9 +508,9 @@ typedef struct {
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
  * max_kv) for each sequence, from the lengths, on the GPU: with T = the key tiles a
- * job should walk, clamp(ceil(tiles / T), 1, bound). If the unsplit jobs fit num_sms SMs, T is
- * the smallest from ceil(work / num_sms) up (growing by an eighth) whose jobs do too;
- * otherwise T = 2 ceil(work / num_sms), so that only a sequence that would hold an SM for
+ * job should walk, clamp(ceil(tiles / T), 1, bound). If the unsplit jobs fit one wave (num_sms jobs, twice that with row_kernel), T is
+ * the smallest from ceil(work / wave) up (growing by an eighth) whose jobs do too;
+ * otherwise T = 2 ceil(work / wave), so that only a sequence that would hold an SM for
  * more than twice its share is split. An unsplit sequence's rows are written at once, those
  * of a split one by a combine kernel launched behind. num_sms 0 = the current device's.
  * Errors as for mla_decode_plan (d must be 128, dtype SDPA_*, group <= 128). */

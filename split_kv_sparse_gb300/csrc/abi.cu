@@ -69,7 +69,8 @@ int device_state(DeviceState** out) {
       return MLA_ERR_CUDA;
     }
     if (skv::prepare_mla_kernels() != cudaSuccess || skv::prepare_sdpa_kernels() != cudaSuccess ||
-        skv::prepare_paged_kernels() != cudaSuccess || skv::prepare_attn_tile() != cudaSuccess) {
+        skv::prepare_paged_kernels() != cudaSuccess || skv::prepare_attn_tile() != cudaSuccess ||
+        skv::prepare_attn_row() != cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }

@@ -100,6 +100,9 @@ int encode_kv(CUtensorMap* m, int dtype, const void* base, int64_t rows, int64_t
 // The most (sequence, query tile) pairs of `tokens` tokens that total_q rows of `batch` sequences can make.
 int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / tokens + std::min(total_q, batch); }
 
+// Tokens of one job's rows.
+int job_tokens(bool rows16, int group) { return rows16 ? skv::kRowRows / group : 2 * (128 / group); }
+
 // Jobs that one launch may hold: unsplit, forced splits, or counts from the lengths.
 int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int num_sms) {
   if (!adaptive) return unsplit * num_splits;
@@ -208,7 +211,11 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
     S = std::min(cap, (max_kv + 127) / 128);
     adaptive = S > 1 ? 1 : 0;
   }
-  const int64_t unsplit = tiles_bound(total_q_max, batch, 2 * (128 / group)) * h_kv;
+  // few rows a sequence: the kernel of 16-row jobs, of which an SM holds two
+  const bool rows16 = static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
+  const int wave = rows16 ? num_sms * skv::kRowCtasPerSm : num_sms;
+  const int job_rows = rows16 ? skv::kRowRows : skv::kTileRows;
+  const int64_t unsplit = tiles_bound(total_q_max, batch, job_tokens(rows16, group)) * h_kv;
   out->batch = batch;
   out->h_q = h_q;
   out->h_kv = h_kv;
@@ -220,14 +227,15 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->num_splits = S;
   out->num_sms = num_sms;
   out->adaptive_splits = adaptive;
+  out->row_kernel = rows16 ? 1 : 0;
   if (S > 1) {
     // split jobs: as many as forced, or at most one wave (the rule keeps to that)
-    const int64_t slots = adaptive ? num_sms : unsplit * S;
-    if (slots * skv::kTileRows > 0x7FFFFFFFll) {
+    const int64_t slots = adaptive ? wave : unsplit * S;
+    if (slots * job_rows > 0x7FFFFFFFll) {
       std::memset(out, 0, sizeof(*out));
       return MLA_ERR_UNSUPPORTED;
     }
-    const uint64_t rows = static_cast<uint64_t>(slots) * skv::kTileRows;
+    const uint64_t rows = static_cast<uint64_t>(slots) * job_rows;
     out->o_acc_bytes = rows * kDim * 4;
     out->lse_acc_offset = round_up(out->o_acc_bytes, 256);
     out->lse_acc_bytes = rows * 4;
@@ -248,6 +256,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if ((st = check_pages(pages)) != MLA_OK) return st;
   if (pages->dtype != plan->dtype || pages->h_kv != plan->h_kv || pages->d != plan->d) return MLA_ERR_INVALID_ARG;
   if (plan->num_splits < 1 || plan->num_splits > MLA_MAX_SPLITS || plan->num_sms < 1) return MLA_ERR_INVALID_ARG;
+  if (plan->row_kernel != 0 && plan->h_q / plan->h_kv > skv::kRowRows) return MLA_ERR_INVALID_ARG;
   if (total_q < 1 || total_q > plan->total_q_max || table_width < 1) return MLA_ERR_INVALID_ARG;
   if (q == nullptr || block_table == nullptr || kv_lens == nullptr || cu_seqlens_q == nullptr) return MLA_ERR_INVALID_ARG;
   if (!ptr_aligned(q, 16) || !words_ok({block_table, kv_lens, cu_seqlens_q, descale_q, descale_k, descale_v, lse_out, amax_out}))
@@ -291,7 +300,8 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.amax = amax_out;
   a.num_splits = plan->num_splits;
   a.adaptive = plan->adaptive_splits;
-  a.num_sms = plan->num_sms;
+  const bool rows16 = plan->row_kernel != 0;
+  a.num_sms = rows16 ? plan->num_sms * skv::kRowCtasPerSm : plan->num_sms;
   if (plan->num_splits > 1) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.o_part = reinterpret_cast<float*>(ws);
@@ -302,18 +312,20 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.wait_limit_ns = skv::wait_limit_ns();
   a.drain_limit_ns = skv::drain_limit_ns();
   CUtensorMap tq, tk, tv;
-  const int box = std::min(pages->page_size, 128);
-  if ((st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK ||
+  const int box = rows16 ? skv::attn_row_box(plan->dtype, pages->page_size) : std::min(pages->page_size, 128);
+  if ((!rows16 &&
+       (st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK) ||
       (st = encode_kv(&tk, plan->dtype, pages->k, pages->page_size, pages->row_stride, pages->num_pages,
                       pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK ||
       (st = encode_kv(&tv, plan->dtype, pages->v, pages->page_size, pages->row_stride, pages->num_pages,
                       pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK)
     return st;
-  const int64_t unsplit = tiles_bound(total_q, a.batch, 2 * (128 / a.group)) * a.h_kv;
+  const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
   const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms);
-  st = cuda_status(skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
+  st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
+                          : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;
-  return cuda_status(skv::launch_attn_combine(a, skv::kTileRows, cs));
+  return cuda_status(skv::launch_attn_combine(a, rows16 ? skv::kRowRows : skv::kTileRows, cs));
 }
 
 int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,

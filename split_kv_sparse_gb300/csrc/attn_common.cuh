@@ -151,8 +151,6 @@ __device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const
   }
 }
 
-// One 16-byte piece of an output row: elements c .. c + 3 (fp32), c .. c + 7 (bf16)
-// or c .. c + 15 (e4m3) of values x.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -169,23 +167,24 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
-// 32 consecutive elements at element offset `at` of an output of type out_dtype
-// (MLA_OUT_*: 0 fp32, 1 bf16, 2 e4m3).
-__device__ __forceinline__ void store32(void* out, int out_dtype, int64_t at, const float (&x)[32], float inv_scale) {
+// N (16 or 32) consecutive elements at element offset `at` of an output of type
+// out_dtype (MLA_OUT_*: 0 fp32, 1 bf16, 2 e4m3).
+template <int N>
+__device__ __forceinline__ void store_row(void* out, int out_dtype, int64_t at, const float (&x)[N], float inv_scale) {
   if (out_dtype == 0) {
     float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < N / 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
   } else if (out_dtype == 1) {
     uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N / 8; ++i)
       p[i] = make_uint4(pack_bf16x2(x[8 * i], x[8 * i + 1]), pack_bf16x2(x[8 * i + 2], x[8 * i + 3]),
                         pack_bf16x2(x[8 * i + 4], x[8 * i + 5]), pack_bf16x2(x[8 * i + 6], x[8 * i + 7]));
   } else {
     uint4* p = reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + at);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N / 16; ++i) {
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -194,6 +193,23 @@ __device__ __forceinline__ void store32(void* out, int out_dtype, int64_t at, co
       p[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
+}
+
+// The kernels here set up while the preceding kernel of the stream ends
+// (grid_dependency_wait before the first read or write of global memory).
+template <typename K, typename... A>
+cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace skv

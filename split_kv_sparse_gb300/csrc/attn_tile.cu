@@ -335,8 +335,8 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             amax = fmaxf(amax, fabsf(y[k]));
           }
           if (live) {
-            if (part) store32(a.o_part, 0, prow * kD + 32 * c, y, 1.f);
-            else store32(a.out, a.out_dtype, orow * kD + 32 * c, y, a.inv_scale);
+            if (part) store_row(a.o_part, 0, prow * kD + 32 * c, y, 1.f);
+            else store_row(a.out, a.out_dtype, orow * kD + 32 * c, y, a.inv_scale);
           }
         }
         if (!part && a.amax != nullptr) {
@@ -640,21 +640,6 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnArgs a, con
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if (lane == 0 && amax > 0.f) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
   }
-}
-
-template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

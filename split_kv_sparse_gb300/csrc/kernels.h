@@ -186,6 +186,12 @@ constexpr int kRowRows = 16;
 // {128, rows, pages, heads} (packed: one page of total_kv rows), box {128 bytes, min(page, 128) rows, 1, 1}.
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
+// Box of tm_k / tm_v: {128 bytes, attn_row_box(dtype, page size) rows, 1, 1}.
+cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
+                            int64_t grid, cudaStream_t stream);
+int attn_row_box(int dtype, int page_size);
+// CTAs of the row kernel that an SM holds.
+constexpr int kRowCtasPerSm = 2;
 // Folds the partial rows of every split token; a.num_splits > 1. rows_per_slot: kTileRows or kRowRows.
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream);
 
@@ -224,5 +230,6 @@ cudaError_t launch_pages_write(const PagesWriteArgs& a, int dtype, cudaStream_t 
 
 cudaError_t prepare_paged_kernels();
 cudaError_t prepare_attn_tile();
+cudaError_t prepare_attn_row();
 
 }  // namespace skv

@@ -5,8 +5,7 @@
 
 #include <algorithm>
 
-#include "kernels.h"
-#include "ptx.cuh"
+#include "attn_common.cuh"
 
 namespace skv {
 namespace {
@@ -185,38 +184,22 @@ __global__ void __launch_bounds__(256) pages_write_kernel(const PagesWriteArgs a
   }
 }
 
-template <typename... A>
-cudaError_t launch_dependent(void (*kernel)(A...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                             const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 constexpr int kMapMaxBatch = 16384;
 
 }  // namespace
 
 cudaError_t launch_pages_map(const PagesMapArgs& a, cudaStream_t stream) {
   const size_t smem = 2 * (static_cast<size_t>(a.batch) + 1) * sizeof(int);
-  const cudaError_t e = launch_dependent(pages_map_kernel, 1, kMapThreads, smem, stream, a);
+  const cudaError_t e = launch_pdl(pages_map_kernel, 1, kMapThreads, smem, stream, a);
   if (e != cudaSuccess || a.total_q <= kMapFusedRows) return e;
-  return launch_dependent(pages_slots_kernel, (a.total_q + 255u) / 256u, 256, 0, stream, a);
+  return launch_pdl(pages_slots_kernel, (a.total_q + 255u) / 256u, 256, 0, stream, a);
 }
 
 cudaError_t launch_pages_write(const PagesWriteArgs& a, int dtype, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const int64_t blocks = (a.rows * a.h_kv * 8 + 255) / 256;
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_dependent(dtype == 2 ? pages_write_kernel<true> : pages_write_kernel<false>,
+  return launch_pdl(dtype == 2 ? pages_write_kernel<true> : pages_write_kernel<false>,
                           static_cast<unsigned>(blocks), 256, 0, stream, a);
 }
 

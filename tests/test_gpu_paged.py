@@ -337,22 +337,12 @@ def test_longer_sequences_than_the_plan_expects():
     go("e4m3", [40, 1], [900, 1500], 8, 2, 16, max_kv=20)
 
 
-def test_more_tokens_than_a_row_plan_holds_are_refused():
-    """A plan for one token of 8 heads a KV head, called with 3 of them (24 rows of a 16-row job)."""
-    c, q, dq, cu = paged_case("bf16", [3, 1], [150, 300], 16, 2, 16, seed=8)
-    plan = b.sdpa_paged_plan(2, 16, 2, D, "bf16", 1, 4, 300)
-    if not plan.row_kernel:
-        pytest.skip("this plan's kernel takes any number of rows")
-    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda") if plan.workspace_bytes else None
-    out = torch.full((4, 16, D), 7.0, device="cuda")
-    b.sdpa_paged(plan, 4, q.cuda(), b.kv_pages(c.k.cuda(), c.v.cuda()), c.table.cuda(), c.kv_lens.cuda(), cu.cuda(), None,
-                 None, None, 0.1, "f32", 1.0, out, None, None, ws)
-    torch.cuda.synchronize()
-    st, _ = b.mla_get_status()
-    assert st & 0x2
-    O, L, A = c.reference(q, dq, cu, 0.1)
-    assert torch.all(out[:3] == 7.0)
-    check(out[3:].cpu(), None, None, (O[3:], L[3:], A[3:]), "bf16")
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_more_tokens_than_the_plan_expects(dtype):
+    """A plan for one token of 8 heads a KV head (16-row jobs), called with 3 to 40 of them."""
+    assert b.sdpa_paged_plan(2, 16, 2, D, dtype, 1, 4, 300).row_kernel == 1
+    go(dtype, [3, 1, 40], [150, 300, 90], 16, 2, 16, max_q=1)
+    go(dtype, [3, 1, 40], [150, 300, 90], 16, 2, 16, max_q=1, force_splits=3)
 
 
 @pytest.mark.parametrize("sq", [[1, 1, 1], [20, 70, 1]])
