@@ -55,13 +55,22 @@ enum {
 };
 static_assert(kNumBars * 8 <= 256, "barrier area");
 
-enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
+enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
-// Words of the misc area.
-enum { M_TMEM = 0, M_ABORT, M_JOB, M_MASK = 12, kMaskRing = 16 };
+// Words of the misc area: what the roles need of the job, worked out once.
+enum {
+  M_TMEM = 0, M_ABORT, M_B, M_G, M_SPLIT, M_S, M_SLOT, M_Q0, M_SQ, M_K0, M_KV,
+  M_TOK0,             // first token (of the sequence) of row block 0
+  M_TILE0, M_TILES,   // first key tile and count that the job walks
+  M_ONE,              // one row block
+  M_CNT0, M_CNT1,     // key tiles of each stream
+  M_TAIL,             // the local tile that holds the sequence's ragged end, or -1
+  M_MASK, kMaskRing = 16
+};
+static_assert((M_MASK + kMaskRing) * 4 <= 256, "misc area");
 
 template <bool kF8>
 __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
@@ -82,12 +91,40 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
   if (warp == 9) {
     const AttnJob job = attn_find_job(a, 2 * tokens, blockIdx.x, lane);
     if (lane == 0) {
-      misc[M_JOB + 0] = job.b;
-      misc[M_JOB + 1] = job.j;
-      misc[M_JOB + 2] = job.g;
-      misc[M_JOB + 3] = job.s;
-      misc[M_JOB + 4] = job.S;
-      misc[M_JOB + 5] = job.slot;
+      misc[M_B] = job.b;
+      if (job.b >= 0) {
+        const AttnSeq seq = attn_seq(a, job.b);
+        const int tok0 = job.j * 2 * tokens;
+        const int tiles_all = (seq.kv + kTile - 1) / kTile;
+        const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
+        const int tile0 = job.s * base_t + min(job.s, rem_t);
+        const int nt = base_t + (job.s < rem_t ? 1 : 0);
+        // key tiles of row block i: up to the position of its last token
+        auto tiles_of = [&](int i) {
+          const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
+          if (last < tok0 + i * tokens) return 0;
+          const int keys = seq.kv - seq.sq + last + 1;
+          return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
+        };
+        const bool one = tok0 + tokens >= seq.sq;
+        const int n0 = tiles_of(0), n1 = tiles_of(1);      // n1 >= n0 where there is a second block
+        const int tiles = one ? n0 : n1;
+        misc[M_G] = job.g;
+        misc[M_SPLIT] = job.s;
+        misc[M_S] = job.S;
+        misc[M_SLOT] = job.slot;
+        misc[M_Q0] = seq.q0;
+        misc[M_SQ] = seq.sq;
+        misc[M_K0] = seq.k0;
+        misc[M_KV] = seq.kv;
+        misc[M_TOK0] = tok0;
+        misc[M_TILE0] = tile0;
+        misc[M_TILES] = tiles;
+        misc[M_ONE] = one;
+        misc[M_CNT0] = one ? (tiles + 1) >> 1 : n0;
+        misc[M_CNT1] = one ? tiles >> 1 : n1;
+        misc[M_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
+      }
     }
   }
   if (threadIdx.x == 0) {
@@ -109,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     mbar_init_fence();
   }
   __syncthreads();
-  if (misc[M_JOB] < 0) {
+  if (misc[M_B] < 0) {
     grid_launch_dependents();
     return;
   }
@@ -124,42 +161,23 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 
   const uint32_t tmem = static_cast<uint32_t>(misc[M_TMEM]);
   const WaitCtx wc{a.wait_limit_ns, a.status, misc + M_ABORT};
-  const int job_b = misc[M_JOB], job_j = misc[M_JOB + 1], g = misc[M_JOB + 2], split = misc[M_JOB + 3],
-            S = misc[M_JOB + 4], slot0 = misc[M_JOB + 5];
-  const AttnSeq seq = attn_seq(a, job_b);
-  const int tok0 = job_j * 2 * tokens;                    // first token (of the sequence) of row block 0
-  const int tiles_all = (seq.kv + kTile - 1) / kTile;
-  const int base_t = tiles_all / S, rem_t = tiles_all - base_t * S;
-  const int tile0 = split * base_t + min(split, rem_t);
-  const int nt = base_t + (split < rem_t ? 1 : 0);
-  // keys that row block i sees: up to the position of its last token
-  auto tiles_of = [&](int i) {
-    const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
-    if (last < tok0 + i * tokens) return 0;
-    const int keys = seq.kv - seq.sq + last + 1;
-    return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
-  };
-  const bool one = tok0 + tokens >= seq.sq;               // one row block
-  const int n0 = tiles_of(0);
-  const int tiles = one ? n0 : max(n0, tiles_of(1));      // key tiles the job walks
-  const int cnt0 = one ? (tiles + 1) >> 1 : n0;
-  const int cnt1 = one ? tiles >> 1 : tiles_of(1);
-  const int tail = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;   // the
-                                                          // local tile that holds the sequence's ragged end, or -1
 
   if (warp < 8) {
     // ================================================= softmax + epilogue ===
-    if constexpr (kF8) regs_inc<176>();
-    else regs_inc<208>();
+    if constexpr (kF8) regs_inc<192>();
+    else regs_inc<200>();
     const int i = warp >> 2;
+    const int g = misc[M_G], split = misc[M_SPLIT], S = misc[M_S], slot0 = misc[M_SLOT], q0 = misc[M_Q0], sq = misc[M_SQ],
+              kv = misc[M_KV], tok0 = misc[M_TOK0], tile0 = misc[M_TILE0], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1];
+    const bool one = misc[M_ONE] != 0;
     const int cnt = i ? cnt1 : cnt0;
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + 128 * i, to = tmem + lanes + kTmemO + 128 * i;
     const int rt = row / a.group;                          // token of the block
     const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
-    const bool live = rt < tokens && tok < seq.sq;
-    const int lim = live ? seq.kv - seq.sq + tok : -1;     // last key the row sees
+    const bool live = rt < tokens && tok < sq;
+    const int lim = live ? kv - sq + tok : -1;     // last key the row sees
     const float dq = a.descale_q ? *a.descale_q : 1.f, dk = a.descale_k ? *a.descale_k : 1.f,
                 dv = a.descale_v ? *a.descale_v : 1.f;
     const float sc = dq * dk * a.scale_log2;
@@ -205,12 +223,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           m_run = mx;
           l *= al;
         }
-        if (u > 0) {
-          if (!wait_inline(bar(B_O0 + i), (u - 1) & 1, wc, W_T_O)) {
-            bad = true;
-            break;
-          }
-          tc_fence_after();
+        if (u > 0) {   // S_i(u) was committed behind O_i's last product, so that is done
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -249,11 +262,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     }
 
     // ---- epilogue
-    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), (cnt - 1) & 1, wc, W_T_FIN);
+    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), 0, wc, W_T_FIN);
     if (one && !bad) {
       // the merge reuses the ring: both streams' products must be done with it
       const int oc = i ? cnt0 : cnt1;
-      if (oc > 0) bad = !wait_inline(bar(B_O0 + (1 - i)), (oc - 1) & 1, wc, W_T_MERGE);
+      if (oc > 0) bad = !wait_inline(bar(B_O0 + (1 - i)), 0, wc, W_T_MERGE);
     }
     tc_fence_after();
     float4* merge = reinterpret_cast<float4*>(smem + C::kOffRing);           // [32][128 rows] pieces of 4 columns
@@ -293,14 +306,14 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const bool some = l > 0.f || l != l;   // a NaN score stays a NaN result
         const float inv = some ? dv / l : 0.f;
         const float lse = some ? m_run + log2f(l) : -INFINITY;
-        const int64_t orow = static_cast<int64_t>(seq.q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
+        const int64_t orow = static_cast<int64_t>(q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
         const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
         const bool part = S > 1;
         if (live) {
           if (part) a.lse_part[prow] = lse;
           else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
           if (a.row_map != nullptr && split == 0 && row == rt * a.group)
-            a.row_map[static_cast<int64_t>(seq.q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
+            a.row_map[static_cast<int64_t>(q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
         }
         float amax = 0.f;
 #pragma unroll 1
@@ -348,11 +361,14 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (kF8) regs_dec<72>();
-    else regs_dec<88>();
+    if constexpr (kF8) regs_dec<64>();
+    else regs_dec<104>();
     if (warp == 8) {
       // ======================================================= MMA issuer ===
-      if (lane == 0 && tiles > 0) {
+      const int tiles = misc[M_TILES], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1], tail = misc[M_TAIL];
+      const bool one = misc[M_ONE] != 0;
+      if (tiles > 0) {
+        // the whole warp walks the loop, so addresses stay uniform; one lane issues
         constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
         constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
         // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
@@ -395,9 +411,12 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           const int t = tile_at(i, u);
           if (!wait_item(2 * t, W_T_K)) return false;
           tc_fence_after();
-          issue_qk(i, t);
-          mma_commit(bar(B_S0 + i));
-          if (one || i == 1 || t >= cnt1) mma_commit(bar(B_EMPTY0 + (2 * t) % C::kSlots));
+          if (elect_one()) {
+            issue_qk(i, t);
+            mma_commit(bar(B_S0 + i));
+            if (one || i == 1) mma_commit(bar(B_EMPTY0 + (2 * t) % C::kSlots));
+          }
+          __syncwarp();
           return true;
         };
         bool ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
@@ -416,22 +435,30 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(i, t, u > 0);
-            mma_commit(bar(B_O0 + i));
-            if (one || i == 1 || t >= cnt1) {
-              if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
-              else mma_commit(bar(B_EMPTY0 + (2 * t + 1) % C::kSlots));
+            if (elect_one()) {
+              issue_pv(i, t, u > 0);
+              // S_i(u + 1) is committed behind this product and says that it is done; the last has its own barrier
+              if (u + 1 == cnt) mma_commit(bar(B_O0 + i));
+              if (one || i == 1) {
+                if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
+                else mma_commit(bar(B_EMPTY0 + (2 * t + 1) % C::kSlots));
+              }
             }
+            __syncwarp();
             if (u + 1 < cnt) ok = qk_step(i, u + 1);
           }
         }
         if (!ok) {
-          mma_commit(bar(B_DRAIN));
+          if (elect_one()) mma_commit(bar(B_DRAIN));
+          __syncwarp();
           if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
         }
       }
     } else if (warp == 9) {
       // ===================================================== TMA producer ===
+      const int job_b = misc[M_B], g = misc[M_G], q0 = misc[M_Q0], k0 = misc[M_K0], kv = misc[M_KV], tok0 = misc[M_TOK0],
+                tile0 = misc[M_TILE0], tiles = misc[M_TILES], tail = misc[M_TAIL];
+      const bool one = misc[M_ONE] != 0;
       if (tiles > 0) {
         const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
         const int boxes = kTile / page_rows;               // of one tile and column block
@@ -444,19 +471,19 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           for (int i = 0; i < blocks; ++i)
             for (int h = 0; h < C::kHalves; ++h)
               tma_load_3d(sbase + C::kOffQ + i * C::kQBytes + h * 128 * 128, &tm_q, 64 * h, g * a.group,
-                          seq.q0 + tok0 + i * tokens, bar(B_Q));
+                          q0 + tok0 + i * tokens, bar(B_Q));
         }
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
           const int key = (tile0 + t) * kTile + lane * page_rows;
           if (a.table == nullptr) {
             page = 0;
-            row = seq.k0 + key;
+            row = k0 + key;
             return true;
           }
           page = a.num_pages;
           row = key & ((1 << a.page_shift) - 1);
-          if (lane < boxes && key < seq.kv) {
+          if (lane < boxes && key < kv) {
             const int p = a.table[static_cast<size_t>(job_b) * a.table_width + (key >> a.page_shift)];
             if (p >= 0 && p < a.num_pages) page = p;
           }
@@ -475,20 +502,20 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           for (int i = 0; i < 8; ++i)
             if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv, ++item) {
+          for (int w = 0; w < 2; ++w, ++item) {
             const int sl = item % C::kSlots;
             if (item >= C::kSlots && !wait_inline(bar(B_EMPTY0 + sl), ((item / C::kSlots) - 1) & 1, wc, W_T_PROD)) {
               ok = false;
               break;
             }
             if (lane == 0) {
-              if (kv == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
+              if (w == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
               mbar_arrive_expect_tx(bar(B_FULL0 + sl), C::kItemBytes);
             }
             __syncwarp();
             if (lane < boxes) {
               const uint32_t dst = sbase + C::kOffRing + sl * C::kItemBytes + lane * page_rows * 128;
-              const CUtensorMap* tm = kv == 0 ? &tm_k : &tm_v;
+              const CUtensorMap* tm = w == 0 ? &tm_k : &tm_v;
               for (int h = 0; h < C::kHalves; ++h)
                 tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(B_FULL0 + sl));
             }
@@ -502,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           const int it = item - 1;
           if (wait_inline(bar(B_FULL0 + it % C::kSlots), (it / C::kSlots) & 1, wc, W_T_FIX)) {
             uint8_t* v = smem + C::kOffRing + (it % C::kSlots) * C::kItemBytes;
-            for (int p = (seq.kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
+            for (int p = (kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
               *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(v + kTile * 128 + p * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -523,6 +550,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     } else if (kF8 && warp >= 12) {
       // ================================================== V e4m3 -> f16 ===
       const int key = threadIdx.x - 32 * 12;               // this thread's row of every tile
+      const int kv = misc[M_KV], tile0 = misc[M_TILE0], tiles = misc[M_TILES];
       const int r8 = key & 7;
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
@@ -531,7 +559,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         if (t >= 2 && !wait_inline(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, wc, W_T_CVT)) break;
         const uint8_t* src = smem + C::kOffRing + sl * C::kItemBytes + key * 128;
         uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
-        const bool in = (tile0 + t) * kTile + key < seq.kv;
+        const bool in = (tile0 + t) * kTile + key < kv;
         uint4 w[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c)
