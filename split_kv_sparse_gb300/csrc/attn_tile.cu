@@ -10,12 +10,14 @@
 //                   results are merged in shared memory.
 //   warps 0-3, 4-7  softmax, rescale and epilogue of stream 0 and 1: a thread is a
 //                   row (a TMEM lane), so no reduction crosses threads.
-//   warp 8          tcgen05 issue: S_i = Q_i K^T; O_i += P_i V with P_i read from
-//                   tensor memory, where it replaces S_i.
-//   warp 9          TMA: Q once, then K and V tiles into a ring of slots, page by page; bf16:
+//   warps 8, 10     tcgen05 issue: S = Q_i K^T; O_i += P_i V with P_i read from tensor
+//                   memory. Two warps, since waits and commits cost the issuing thread as
+//                   much as the products cost the pipe.
+//   warp 9          TMA: Q once, then K and V tiles into two rings of slots, page by page; bf16:
 //                   clears the V rows past the sequence's end (0 * NaN would reach a result).
 //   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0.
-// TMEM: S_0, S_1, O_0, O_1, 128 columns each.
+// TMEM: S (128 columns, one buffer for both streams: a stream's scores leave it for
+// registers as soon as they are there), P_0, P_1 (64 each), O_0, O_1 (128 each).
 // P is rounded to V's MMA type (bf16; f16 for e4m3 V, whose values f16 holds exactly);
 // the sums are taken over the unrounded fp32 values. bf16 P costs 2^-8 relative a
 // term at most, as much as the rounding of a bf16 result.
@@ -35,30 +37,31 @@ struct Cfg {
   static constexpr int kQBytes = 128 * kD * kEsz;        // one row block
   static constexpr int kItemBytes = kTile * kD * kEsz;   // one K or V tile
   static constexpr int kHalves = kF8 ? 1 : 2;            // 128-byte column blocks of a row
-  static constexpr int kSlots = kF8 ? 6 : 5;             // K(t) is item 2t, V(t) item 2t + 1; even for e4m3, so a slot
-                                                         // holds only K or only V tiles
+  static constexpr int kKSlots = kF8 ? 4 : 3;            // K(t) in slot t % kKSlots of its ring, V(t) in t % kVSlots
+  static constexpr int kVSlots = kF8 ? 4 : 2;
   static constexpr int kV16Bytes = kF8 ? kTile * kD * 2 : 0;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffRing = 2 * kQBytes;
-  static constexpr int kOffV16 = kOffRing + kSlots * kItemBytes;
+  static constexpr int kOffK = 2 * kQBytes;
+  static constexpr int kOffV = kOffK + kKSlots * kItemBytes;
+  static constexpr int kOffV16 = kOffV + kVSlots * kItemBytes;
   static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
   static constexpr int kOffMisc = kOffBars + 256;
   static constexpr int kSmem = kOffMisc + 256 + 1024;
-  // 128 rows x 128 fp32 of stream 1's result are merged through the ring and V16 area
-  static_assert(kOffBars - kOffRing >= 128 * kD * 4, "merge area");
+  // 128 rows x 128 fp32 of stream 1's result are merged through the rings
+  static_assert(kOffBars - kOffK >= 128 * kD * 4, "merge area");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 enum {
-  B_Q = 0, B_S0, B_S1, B_P0, B_P1, B_O0, B_O1, B_VFIX, B_DRAIN, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_FULL0,
-  B_EMPTY0 = B_FULL0 + 8, kNumBars = B_EMPTY0 + 8
+  B_Q = 0, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_VFIX, B_END, B_DRAIN, B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_KFULL,
+  B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
 static_assert(kNumBars * 8 <= 256, "barrier area");
 
-enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
+enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_SFREE, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
 
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 0, kTmemO = 256;
+constexpr uint32_t kTmemS = 0, kTmemP = 128, kTmemO = 256;   // S; P_0, P_1 (64 each); O_0, O_1 (128 each)
 
 // Words of the misc area: what the roles need of the job, worked out once.
 enum {
@@ -137,10 +140,17 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       mbar_init(bar(B_V16E0 + i), 1);
     }
     mbar_init(bar(B_VFIX), 1);
+    mbar_init(bar(B_END), 1);
     mbar_init(bar(B_DRAIN), 1);
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(bar(B_FULL0 + i), 1);
-      mbar_init(bar(B_EMPTY0 + i), kF8 && (i & 1) ? 4 : 1);   // a V tile of codes is freed by its four converters
+    mbar_init(bar(B_DRAIN2), 1);
+    mbar_init(bar(B_SFREE), 4);
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::kVSlots; ++i) {
+      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VEMPTY + i), kF8 ? 4 : 1);   // a V tile of codes is freed by its four converter warps
     }
     misc[M_ABORT] = 0;
     mbar_init_fence();
@@ -173,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     const int cnt = i ? cnt1 : cnt0;
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lanes + kTmemS + 128 * i, to = tmem + lanes + kTmemO + 128 * i;
+    const uint32_t ts = tmem + lanes + kTmemS, tp = tmem + lanes + kTmemP + 64 * i, to = tmem + lanes + kTmemO + 128 * i;
     const int rt = row / a.group;                          // token of the block
     const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
     const bool live = rt < tokens && tok < sq;
@@ -198,6 +208,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, r[c]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_wait_ld_x32(r[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_SFREE));   // the other stream's scores may come
       float(&x)[4][32] = reinterpret_cast<float(&)[4][32]>(r);
       if (!raw_ok) {
 #pragma unroll
@@ -216,6 +229,12 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       }
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
       const bool need = mx > m_run + kRescaleThreshold;
+      // O_i's last product is done: P_i may be written again, O_i rescaled
+      if (u > 0 && !wait_inline(bar(B_O0 + i), (u - 1) & 1, wc, W_T_O)) {
+        bad = true;
+        break;
+      }
+      tc_fence_after();
       if (__any_sync(0xffffffffu, need)) {
         float al = 1.f;
         if (need) {
@@ -223,7 +242,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           m_run = mx;
           l *= al;
         }
-        if (u > 0) {   // S_i(u) was committed behind O_i's last product, so that is done
+        if (u > 0) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
@@ -250,7 +269,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           sum[k & 3] = add_f32x2(sum[k & 3], pair_f32(e0, e1));
           p[k] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
         }
-        tmem_st_32x32b_x16(ts + 16 * c, p);
+        tmem_st_32x32b_x16(tp + 16 * c, p);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -262,14 +281,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     }
 
     // ---- epilogue
-    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), 0, wc, W_T_FIN);
-    if (one && !bad) {
-      // the merge reuses the ring: both streams' products must be done with it
-      const int oc = i ? cnt0 : cnt1;
-      if (oc > 0) bad = !wait_inline(bar(B_O0 + (1 - i)), 0, wc, W_T_MERGE);
-    }
+    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), (cnt - 1) & 1, wc, W_T_FIN);
+    // the merge reuses the rings: both streams' products must be done with them
+    if (one && cnt0 > 0 && !bad) bad = !wait_inline(bar(B_END), 0, wc, W_T_MERGE);
     tc_fence_after();
-    float4* merge = reinterpret_cast<float4*>(smem + C::kOffRing);           // [32][128 rows] pieces of 4 columns
+    float4* merge = reinterpret_cast<float4*>(smem + C::kOffK);              // [32][128 rows] pieces of 4 columns
     float2* stats = reinterpret_cast<float2*>(smem + C::kOffQ);              // [128 rows] (m, l) of stream 1
     if (one && i == 1) {
       if (!bad) {
@@ -363,96 +379,98 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
   } else {
     if constexpr (kF8) regs_dec<64>();
     else regs_dec<104>();
-    if (warp == 8) {
-      // ======================================================= MMA issuer ===
+    if (warp == 8 || warp == 10) {
+      // ====================================================== MMA issuers ===
+      // The whole warp walks its loop, so addresses stay uniform; one elected lane issues. S is one buffer: QK_1(u)
+      // waits until stream 0 has S_0(u) in registers, and PV_i(u) until P_i(u) is written, so a stream's scores are ready
+      // while its last product still runs.
       const int tiles = misc[M_TILES], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1], tail = misc[M_TAIL];
       const bool one = misc[M_ONE] != 0;
-      if (tiles > 0) {
-        // the whole warp walks the loop, so addresses stay uniform; one lane issues
+      // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
+      const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(sbase, 16, 1024) >> 32);
+      const int steps = max(cnt0, cnt1);
+      auto tile_at = [&](int i, int u) { return one ? 2 * u + i : u; };
+      bool ok = true;
+      if (warp == 8 && tiles > 0) {
         constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
-        constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
-        // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
-        const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(sbase, 16, 1024) >> 32);
         const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
-        const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffRing, 16, 1024));
-        const uint32_t v_lo = static_cast<uint32_t>(
-            sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffRing), kTile * 128, 1024));
-        auto issue_qk = [&](int i, int t) {
-          const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
-          const uint32_t kb = k_lo + static_cast<uint32_t>((2 * t) % C::kSlots) * (C::kItemBytes >> 4);
-          const uint32_t d = tmem + kTmemS + 128 * i;
-          if constexpr (kF8) {
-            mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
-            mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
-            mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
-            mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
-          } else {
-            mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
-#pragma unroll
-            for (int k = 1; k < 8; ++k) {
-              const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
-              mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
-            }
-          }
-        };
-        auto issue_pv = [&](int i, int t, bool acc) {
-          const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
-                                          : static_cast<uint32_t>((2 * t + 1) % C::kSlots) * (C::kItemBytes >> 4));
-          const uint32_t pa = tmem + kTmemS + 128 * i, d = tmem + kTmemO + 128 * i;
-#pragma unroll
-          for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
-            mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (acc ? 1u : 0u));
-        };
-        auto tile_at = [&](int i, int u) { return one ? 2 * u + i : u; };
-        auto wait_item = [&](int item, uint32_t site) {
-          return wait_inline(bar(B_FULL0 + item % C::kSlots), (item / C::kSlots) & 1, wc, site);
-        };
-        auto qk_step = [&](int i, int u) {
-          const int t = tile_at(i, u);
-          if (!wait_item(2 * t, W_T_K)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_qk(i, t);
-            mma_commit(bar(B_S0 + i));
-            if (one || i == 1) mma_commit(bar(B_EMPTY0 + (2 * t) % C::kSlots));
-          }
-          __syncwarp();
-          return true;
-        };
-        bool ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
-        if (ok && cnt0 > 0) ok = qk_step(0, 0);
-        if (ok && cnt1 > 0) ok = qk_step(1, 0);
-        const int steps = max(cnt0, cnt1);
+        const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
+        const uint32_t d = tmem + kTmemS;
+        ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
+        int scores = 0;   // S tiles issued
 #pragma unroll 1
         for (int u = 0; ok && u < steps; ++u) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int cnt = i ? cnt1 : cnt0;
-            if (!ok || u >= cnt) continue;
+            if (!ok || u >= (i ? cnt1 : cnt0)) continue;
+            const int t = tile_at(i, u);
+            ok = wait_inline(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, wc, W_T_K) &&
+                 (scores == 0 || wait_inline(bar(B_SFREE), (scores - 1) & 1, wc, W_T_SFREE));
+            if (!ok) break;
+            ++scores;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
+              const uint32_t kb = k_lo + static_cast<uint32_t>(t % C::kKSlots) * (C::kItemBytes >> 4);
+              if constexpr (kF8) {
+                mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
+                mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
+                mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
+                mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
+              } else {
+                mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                  const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
+                  mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
+                }
+              }
+              mma_commit(bar(B_S0 + i));
+              if (one || i == 1) mma_commit(bar(B_KEMPTY + t % C::kKSlots));
+            }
+            __syncwarp();
+          }
+        }
+      } else if (warp == 10 && tiles > 0) {
+        constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
+        const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), kTile * 128, 1024));
+#pragma unroll 1
+        for (int u = 0; ok && u < steps; ++u) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || u >= (i ? cnt1 : cnt0)) continue;
             const int t = tile_at(i, u);
             if constexpr (kF8) ok = wait_inline(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, wc, W_T_V);
-            else ok = wait_item(2 * t + 1, W_T_V) && (t != tail || wait_inline(bar(B_VFIX), 0, wc, W_T_FIX));
+            else
+              ok = wait_inline(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, wc, W_T_V) &&
+                   (t != tail || wait_inline(bar(B_VFIX), 0, wc, W_T_FIX));
             ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              issue_pv(i, t, u > 0);
-              // S_i(u + 1) is committed behind this product and says that it is done; the last has its own barrier
-              if (u + 1 == cnt) mma_commit(bar(B_O0 + i));
+              const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
+                                              : static_cast<uint32_t>(t % C::kVSlots) * (C::kItemBytes >> 4));
+              const uint32_t pa = tmem + kTmemP + 64 * i, d = tmem + kTmemO + 128 * i;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
+                mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
+              mma_commit(bar(B_O0 + i));
               if (one || i == 1) {
                 if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
-                else mma_commit(bar(B_EMPTY0 + (2 * t + 1) % C::kSlots));
+                else mma_commit(bar(B_VEMPTY + t % C::kVSlots));
               }
             }
             __syncwarp();
-            if (u + 1 < cnt) ok = qk_step(i, u + 1);
           }
         }
-        if (!ok) {
-          if (elect_one()) mma_commit(bar(B_DRAIN));
-          __syncwarp();
-          if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
-        }
+        if (ok && elect_one()) mma_commit(bar(B_END));
+        __syncwarp();
+      }
+      if (!ok) {
+        const int drain = warp == 8 ? B_DRAIN : B_DRAIN2;
+        if (elect_one()) mma_commit(bar(drain));
+        __syncwarp();
+        if (!wait_drain(bar(drain), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
       }
     } else if (warp == 9) {
       // ===================================================== TMA producer ===
@@ -489,46 +507,63 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
           return page != a.num_pages;
         };
-        int page, row, page_n = 0, row_n = 0;
-        bool have = lookup(0, page, row), have_n = false;
+        // K runs ahead of V by as many tiles as the products do: K(0) .. K(lag - 1), then K(t), V(t - lag) in turn
+        const int lag = one ? 2 : 1;
+        int kpage[3], krow[3];                               // the pages of K(t), K(t - 1), K(t - 2)
         bool ok = true;
-        int item = 0;
+        bool have = lookup(0, kpage[0], krow[0]);
+        auto load = [&](int base_off, int full, int slot, const CUtensorMap* tm, int page, int row) {
+          if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), C::kItemBytes);
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = sbase + base_off + slot * C::kItemBytes + lane * page_rows * 128;
+            for (int h = 0; h < C::kHalves; ++h)
+              tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + slot));
+          }
+        };
+        int kdone = 0, vdone = 0;                            // tiles whose loads were started
 #pragma unroll 1
-        for (int t = 0; ok && t < tiles; ++t) {
+        for (int t = 0; t < tiles + lag; ++t) {
+          int page_n = 0, row_n = 0;
+          bool have_n = false;
           if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
-          // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
-          const unsigned got = __ballot_sync(0xffffffffu, have);
-          unsigned groups = 0;
-          for (int i = 0; i < 8; ++i)
-            if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
-#pragma unroll
-          for (int w = 0; w < 2; ++w, ++item) {
-            const int sl = item % C::kSlots;
-            if (item >= C::kSlots && !wait_inline(bar(B_EMPTY0 + sl), ((item / C::kSlots) - 1) & 1, wc, W_T_PROD)) {
+          if (t < tiles) {
+            const int sl = t % C::kKSlots;
+            if (t >= C::kKSlots && !wait_inline(bar(B_KEMPTY + sl), ((t / C::kKSlots) - 1) & 1, wc, W_T_PROD)) {
               ok = false;
               break;
             }
-            if (lane == 0) {
-              if (w == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
-              mbar_arrive_expect_tx(bar(B_FULL0 + sl), C::kItemBytes);
-            }
-            __syncwarp();
-            if (lane < boxes) {
-              const uint32_t dst = sbase + C::kOffRing + sl * C::kItemBytes + lane * page_rows * 128;
-              const CUtensorMap* tm = w == 0 ? &tm_k : &tm_v;
-              for (int h = 0; h < C::kHalves; ++h)
-                tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(B_FULL0 + sl));
-            }
+            // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
+            const unsigned got = __ballot_sync(0xffffffffu, have);
+            unsigned groups = 0;
+            for (int i = 0; i < 8; ++i)
+              if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
+            if (lane == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
+            load(C::kOffK, B_KFULL, sl, &tm_k, kpage[0], krow[0]);
+            kdone = t + 1;
           }
-          page = page_n;
-          row = row_n;
+          if (t >= lag) {
+            const int tv = t - lag, sl = tv % C::kVSlots;
+            if (tv >= C::kVSlots && !wait_inline(bar(B_VEMPTY + sl), ((tv / C::kVSlots) - 1) & 1, wc, W_T_PROD)) {
+              ok = false;
+              break;
+            }
+            load(C::kOffV, B_VFULL, sl, &tm_v, one ? kpage[2] : kpage[1], one ? krow[2] : krow[1]);
+            vdone = tv + 1;
+          }
+          kpage[2] = kpage[1];
+          krow[2] = krow[1];
+          kpage[1] = kpage[0];
+          krow[1] = krow[0];
+          kpage[0] = page_n;
+          krow[0] = row_n;
           have = have_n;
         }
         // the ragged end lies in the last tile: clear V's rows past it
         if (!kF8 && ok && tail >= 0) {
-          const int it = item - 1;
-          if (wait_inline(bar(B_FULL0 + it % C::kSlots), (it / C::kSlots) & 1, wc, W_T_FIX)) {
-            uint8_t* v = smem + C::kOffRing + (it % C::kSlots) * C::kItemBytes;
+          const int sl = tail % C::kVSlots;
+          if (wait_inline(bar(B_VFULL + sl), (tail / C::kVSlots) & 1, wc, W_T_FIX)) {
+            uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
             for (int p = (kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
               *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(v + kTile * 128 + p * 16) = make_uint4(0, 0, 0, 0);
@@ -542,8 +577,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           bool done = wait_drain(bar(B_Q), 0, a.drain_limit_ns);
-          for (int k = max(0, item - C::kSlots); k < item; ++k)
-            done = wait_drain(bar(B_FULL0 + k % C::kSlots), (k / C::kSlots) & 1, a.drain_limit_ns) && done;
+          for (int k = max(0, kdone - C::kKSlots); k < kdone; ++k)
+            done = wait_drain(bar(B_KFULL + k % C::kKSlots), (k / C::kKSlots) & 1, a.drain_limit_ns) && done;
+          for (int k = max(0, vdone - C::kVSlots); k < vdone; ++k)
+            done = wait_drain(bar(B_VFULL + k % C::kVSlots), (k / C::kVSlots) & 1, a.drain_limit_ns) && done;
           if (!done) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
         }
       }
@@ -554,10 +591,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       const int r8 = key & 7;
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
-        const int it = 2 * t + 1, sl = it % C::kSlots;
-        if (!wait_inline(bar(B_FULL0 + sl), (it / C::kSlots) & 1, wc, W_T_CVT)) break;
+        const int sl = t % C::kVSlots;
+        if (!wait_inline(bar(B_VFULL + sl), (t / C::kVSlots) & 1, wc, W_T_CVT)) break;
         if (t >= 2 && !wait_inline(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, wc, W_T_CVT)) break;
-        const uint8_t* src = smem + C::kOffRing + sl * C::kItemBytes + key * 128;
+        const uint8_t* src = smem + C::kOffV + sl * C::kItemBytes + key * 128;
         uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
         const bool in = (tile0 + t) * kTile + key < kv;
         uint4 w[8];
@@ -584,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(B_V16F0 + (t & 1)));
-          mbar_arrive(bar(B_EMPTY0 + sl));
+          mbar_arrive(bar(B_VEMPTY + sl));
         }
       }
     }
