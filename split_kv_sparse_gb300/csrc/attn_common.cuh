@@ -50,63 +50,79 @@ struct AttnJob {
   int slot;   // S > 1: the job's place among the split jobs
 };
 
-// Job `idx` of the batch, found by one warp. Sequence b has n_b = ceil(s_b /
-// tokens) query tiles and S_b splits: num_splits of them where the plan forces a
-// count, else, with T = the key tiles a job should walk, clamp(ceil(tiles_b / T), 1,
-// num_splits). If the unsplit jobs fit the SMs, T is the smallest from ceil(work /
-// num_sms) on (growing by an eighth) whose jobs fit one wave; otherwise only a
-// sequence that walks more than twice its SM's share of the work is split, into
-// shares of two: both bound the split jobs by num_sms. Jobs are listed sequence by
-// sequence; within one the last query tiles first (they see the most keys), then the
-// splits, the KV heads fastest.
+// Job `idx` of the batch, found by one warp (lane by lane a sequence). Sequence b has
+// n_b = ceil(s_b / tokens) query tiles and S_b splits: num_splits of them where the plan
+// forces a count, else, with T = the key tiles a job should walk, clamp(ceil(tiles_b / T),
+// 1, num_splits). If the unsplit jobs fit one wave of num_sms, T is the smallest whose
+// jobs do too; otherwise only a sequence that walks more than twice its SM's share of
+// the work is split, into shares of two: both bound the split jobs by num_sms. Jobs are
+// listed sequence by sequence; within one the last query tiles first (they see the most
+// keys), then the splits, the KV heads fastest.
 __device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, int idx, int lane) {
-  int T = 0;   // 0: S_b = num_splits
-  const int batches = (a.batch + 31) / 32;
-  auto shape = [&](int b, int& n, int& tiles) {
+  const int groups = (a.batch + 31) / 32;
+  auto load = [&](int i, int& n, int& tiles) {
     n = tiles = 0;
+    const int b = 32 * i + lane;
     if (b < a.batch) {
       const AttnSeq q = attn_seq(a, b);
       n = (q.sq + tokens - 1) / tokens;
       tiles = (q.kv + kAttnKeyTile - 1) / kAttnKeyTile;
     }
   };
+  int n_first, tiles_first;   // the first 32 sequences stay in registers
+  load(0, n_first, tiles_first);
+  auto shape = [&](int i, int& n, int& tiles) {
+    if (i == 0) {
+      n = n_first;
+      tiles = tiles_first;
+    } else {
+      load(i, n, tiles);
+    }
+  };
+  int T = 0;   // 0: S_b = num_splits
   auto splits = [&](int tiles) { return T == 0 ? a.num_splits : min(a.num_splits, max(1, (tiles + T - 1) / T)); };
   if (a.adaptive && a.num_splits > 1) {
-    int jobs = 0;
+    int jobs = 0, most = 1;
     long long work = 0;
-    for (int i = 0; i < batches; ++i) {
+    for (int i = 0; i < groups; ++i) {
       int n, tiles;
-      shape(32 * i + lane, n, tiles);
+      shape(i, n, tiles);
       jobs += warp_sum_int(n);
+      most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? tiles : 0));
       long long w = static_cast<long long>(n) * tiles;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       work += w;
     }
-    const long long share = (work * a.h_kv + a.num_sms - 1) / a.num_sms;
-    T = static_cast<int>(min(max(share, 1ll), 1ll << 24));   // (more tiles than a sequence can have)
-    if (static_cast<int64_t>(jobs) * a.h_kv > a.num_sms) {
-      T *= 2;
+    work *= a.h_kv;
+    const long long unsplit = static_cast<long long>(jobs) * a.h_kv;
+    const int share = static_cast<int>(min((work + a.num_sms - 1) / a.num_sms, 1ll << 24));   // (above any sequence's tiles)
+    if (unsplit > a.num_sms) {
+      T = 2 * max(share, 1);
     } else {
-      for (int k = 0; k < 200; ++k) {
-        int total = 0, most = 1;
-        for (int i = 0; i < batches; ++i) {
+      // jobs(T) <= work / T + unsplit, so from work / (num_sms - unsplit) on they fit
+      int lo = max(share, 1);
+      int hi = unsplit < a.num_sms ? static_cast<int>(min(work / (a.num_sms - unsplit) + 1, static_cast<long long>(most))) : most;
+      hi = max(hi, lo);
+      while (lo < hi) {
+        T = (lo + hi) >> 1;
+        int total = 0;
+        for (int i = 0; i < groups; ++i) {
           int n, tiles;
-          shape(32 * i + lane, n, tiles);
-          const int s = splits(tiles);
-          total += warp_sum_int(n * s);
-          most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? s : 1));
+          shape(i, n, tiles);
+          total += warp_sum_int(n * splits(tiles));
         }
-        if (most == 1 || total * a.h_kv <= a.num_sms) break;
-        T += (T + 7) >> 3;
+        if (static_cast<long long>(total) * a.h_kv <= a.num_sms) hi = T;
+        else lo = T + 1;
       }
+      T = hi;
     }
   }
   AttnJob job = {-1, 0, 0, 0, 1, 0};
   int base = 0, slots = 0;
-  for (int i = 0; i < batches && job.b < 0; ++i) {
+  for (int i = 0; i < groups && job.b < 0; ++i) {
     int n, tiles;
-    shape(32 * i + lane, n, tiles);
+    shape(i, n, tiles);
     const int s = splits(tiles);
     const int count = n * s * a.h_kv;
     const int split_count = s > 1 ? count : 0;
@@ -120,10 +136,11 @@ __device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, 
       const int first = __shfl_sync(0xffffffffu, slots + sincl - split_count, src);
       job.b = 32 * i + src;
       job.S = __shfl_sync(0xffffffffu, s, src);
-      job.g = l % a.h_kv;
       const int rest = l / a.h_kv;
-      job.s = rest % job.S;
-      job.j = nn - 1 - rest / job.S;
+      job.g = l - rest * a.h_kv;
+      const int tile = rest / job.S;
+      job.s = rest - tile * job.S;
+      job.j = nn - 1 - tile;
       job.slot = first + (job.j * a.h_kv + job.g) * job.S + job.s;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);

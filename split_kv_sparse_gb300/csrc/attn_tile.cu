@@ -10,9 +10,8 @@
 //                   results are merged in shared memory.
 //   warps 0-3, 4-7  softmax, rescale and epilogue of stream 0 and 1: a thread is a
 //                   row (a TMEM lane), so no reduction crosses threads.
-//   warps 8, 10     tcgen05 issue: S = Q_i K^T; O_i += P_i V with P_i read from tensor
-//                   memory. Two warps, since waits and commits cost the issuing thread as
-//                   much as the products cost the pipe.
+//   warps 8, 10     tcgen05 issue, in turn: S = Q_i K^T; O_i += P_i V with P_i read from
+//                   tensor memory.
 //   warp 9          TMA: Q once, then K and V tiles into two rings of slots, page by page; bf16:
 //                   clears the V rows past the sequence's end (0 * NaN would reach a result).
 //   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0.
@@ -45,20 +44,20 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kKSlots * kItemBytes;
   static constexpr int kOffV16 = kOffV + kVSlots * kItemBytes;
   static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
-  static constexpr int kOffMisc = kOffBars + 256;
+  static constexpr int kOffMisc = kOffBars + 320;
   static constexpr int kSmem = kOffMisc + 256 + 1024;
   // 128 rows x 128 fp32 of stream 1's result are merged through the rings
-  static_assert(kOffBars - kOffK >= 128 * kD * 4, "merge area");
+  static_assert(kOffBars - kOffK >= 128 * kD * 4 + 128 * 8, "merge area");
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 enum {
-  B_Q = 0, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_VFIX, B_END, B_DRAIN, B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_KFULL,
+  B_Q = 0, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VFIX, B_END, B_DRAIN, B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_KFULL,
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
-static_assert(kNumBars * 8 <= 256, "barrier area");
+static_assert(kNumBars * 8 <= 320, "barrier area");
 
-enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_SFREE, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
+enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_SFREE, W_T_TURN, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemP = 128, kTmemO = 256;   // S; P_0, P_1 (64 each); O_0, O_1 (128 each)
@@ -90,10 +89,44 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
   auto bar = [&](int i) -> uint32_t { return sbase + C::kOffBars + 8 * i; };
 
   const int tokens = 128 / a.group;   // of one row block
+  if (threadIdx.x == 0) {
+    mbar_init(bar(B_Q), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(B_S0 + i), 1);
+      mbar_init(bar(B_P0 + i), 4);
+      mbar_init(bar(B_O0 + i), 1);
+      mbar_init(bar(B_V16F0 + i), 4);
+      mbar_init(bar(B_V16E0 + i), 1);
+    }
+    mbar_init(bar(B_TURN_QK), 1);
+    mbar_init(bar(B_TURN_PV), 1);
+    mbar_init(bar(B_VFIX), 1);
+    mbar_init(bar(B_END), 1);
+    mbar_init(bar(B_DRAIN), 1);
+    mbar_init(bar(B_DRAIN2), 1);
+    mbar_init(bar(B_SFREE), 4);
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::kVSlots; ++i) {
+      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VEMPTY + i), kF8 ? 4 : 1);   // a V tile of codes is freed by its four converter warps
+    }
+    misc[M_ABORT] = 0;
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(smem + C::kOffMisc), kTmemCols);
+    tmem_relinquish();
+  }
   grid_dependency_wait();             // the job search reads the lengths
   if (warp == 9) {
     const AttnJob job = attn_find_job(a, 2 * tokens, blockIdx.x, lane);
     if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
       misc[M_B] = job.b;
       if (job.b >= 0) {
         const AttnSeq seq = attn_seq(a, job.b);
@@ -130,47 +163,16 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       }
     }
   }
-  if (threadIdx.x == 0) {
-    mbar_init(bar(B_Q), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(B_S0 + i), 1);
-      mbar_init(bar(B_P0 + i), 4);
-      mbar_init(bar(B_O0 + i), 1);
-      mbar_init(bar(B_V16F0 + i), 4);
-      mbar_init(bar(B_V16E0 + i), 1);
-    }
-    mbar_init(bar(B_VFIX), 1);
-    mbar_init(bar(B_END), 1);
-    mbar_init(bar(B_DRAIN), 1);
-    mbar_init(bar(B_DRAIN2), 1);
-    mbar_init(bar(B_SFREE), 4);
-    for (int i = 0; i < C::kKSlots; ++i) {
-      mbar_init(bar(B_KFULL + i), 1);
-      mbar_init(bar(B_KEMPTY + i), 1);
-    }
-    for (int i = 0; i < C::kVSlots; ++i) {
-      mbar_init(bar(B_VFULL + i), 1);
-      mbar_init(bar(B_VEMPTY + i), kF8 ? 4 : 1);   // a V tile of codes is freed by its four converter warps
-    }
-    misc[M_ABORT] = 0;
-    mbar_init_fence();
-  }
-  __syncthreads();
-  if (misc[M_B] < 0) {
-    grid_launch_dependents();
-    return;
-  }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(smem + C::kOffMisc), kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   grid_launch_dependents();
-
   const uint32_t tmem = static_cast<uint32_t>(misc[M_TMEM]);
   const WaitCtx wc{a.wait_limit_ns, a.status, misc + M_ABORT};
+  if (misc[M_B] < 0) {   // no job
+    if (warp == 8) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   if (warp < 8) {
     // ================================================= softmax + epilogue ===
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     const int rt = row / a.group;                          // token of the block
     const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
     const bool live = rt < tokens && tok < sq;
-    const int lim = live ? kv - sq + tok : -1;     // last key the row sees
+    const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
     const float dq = a.descale_q ? *a.descale_q : 1.f, dk = a.descale_k ? *a.descale_k : 1.f,
                 dv = a.descale_v ? *a.descale_v : 1.f;
     const float sc = dq * dk * a.scale_log2;
@@ -219,13 +221,21 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           for (int k = 0; k < 32; ++k) x[c][k] *= sc;
       }
       const int kmax = lim - (tile0 + t) * kTile;          // last visible key of the tile
-      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + (t & (kMaskRing - 1))]);   // 16-key groups with a page
-      if (__any_sync(0xffffffffu, kmax < kTile - 1) || pages != 0xffu) {
+      if (__any_sync(0xffffffffu, kmax < kTile - 1)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * c + k > kmax || !((pages >> ((32 * c + k) >> 4)) & 1u)) x[c][k] = -INFINITY;
+            if (32 * c + k > kmax) x[c][k] = -INFINITY;
+      }
+      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + (t & (kMaskRing - 1))]);   // 16-key groups with a page
+      if (pages != 0xffu) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (!((pages >> c) & 1u)) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) x[c >> 1][16 * (c & 1) + k] = -INFINITY;
+          }
       }
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
       const bool need = mx > m_run + kRescaleThreshold;
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     if (one && cnt0 > 0 && !bad) bad = !wait_inline(bar(B_END), 0, wc, W_T_MERGE);
     tc_fence_after();
     float4* merge = reinterpret_cast<float4*>(smem + C::kOffK);              // [32][128 rows] pieces of 4 columns
-    float2* stats = reinterpret_cast<float2*>(smem + C::kOffQ);              // [128 rows] (m, l) of stream 1
+    float2* stats = reinterpret_cast<float2*>(smem + C::kOffK + 128 * kD * 4);   // [128 rows] (m, l) of stream 1
     if (one && i == 1) {
       if (!bad) {
         stats[row] = make_float2(m_run, l);
@@ -331,27 +341,32 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           if (a.row_map != nullptr && split == 0 && row == rt * a.group)
             a.row_map[static_cast<int64_t>(q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
         }
+        // Rows go out through 4 KB a warp of its row block's Q (its products are done): 128 bytes of each of the 32 rows,
+        // 16-byte pieces swizzled by the row, then 8 lanes a row write whole lines.
+        uint8_t* stage = smem + C::kOffQ + i * C::kQBytes + (warp & 3) * 4096;
+        const int dst_type = part ? 0 : a.out_dtype;
+        void* dst = part ? static_cast<void*>(a.o_part) : a.out;
+        const int dst_row = live ? static_cast<int>(part ? prow : orow) : -1;
+        const int row_bytes = dst_type == 0 ? kD * 4 : dst_type == 1 ? kD * 2 : kD;
         float amax = 0.f;
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
           float y[32];
-          if (cnt0 > 0 || !one) {
+          if (cnt > 0) {
             uint32_t o[32];
-            if (cnt > 0) {
-              tmem_ld_32x32b_x32(to + 32 * c, o);
-              tmem_wait_ld_x32(o);
-            }
+            tmem_ld_32x32b_x32(to + 32 * c, o);
+            tmem_wait_ld_x32(o);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) y[k] = cnt > 0 && some ? __uint_as_float(o[k]) : 0.f;
+            for (int k = 0; k < 32; ++k) y[k] = some ? __uint_as_float(o[k]) : 0.f;
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) y[k] = 0.f;
           }
-          if (one) {
+          if (one && cnt1 > 0) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (cnt1 > 0 && w1 != 0.f) v = merge[(8 * c + k) * 128 + row];
+              if (w1 != 0.f) v = merge[(8 * c + k) * 128 + row];
               y[4 * k] = y[4 * k] * w0 + v.x * w1;
               y[4 * k + 1] = y[4 * k + 1] * w0 + v.y * w1;
               y[4 * k + 2] = y[4 * k + 2] * w0 + v.z * w1;
@@ -363,9 +378,41 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             y[k] *= inv;
             amax = fmaxf(amax, fabsf(y[k]));
           }
-          if (live) {
-            if (part) store_row(a.o_part, 0, prow * kD + 32 * c, y, 1.f);
-            else store_row(a.out, a.out_dtype, orow * kD + 32 * c, y, a.inv_scale);
+          auto piece = [&](int p) { return reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)); };
+          if (dst_type == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *piece(k) = make_uint4(__float_as_uint(y[4 * k]), __float_as_uint(y[4 * k + 1]), __float_as_uint(y[4 * k + 2]),
+                                     __float_as_uint(y[4 * k + 3]));
+          } else if (dst_type == 1) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *piece(4 * (c & 1) + k) = make_uint4(pack_bf16x2(y[8 * k], y[8 * k + 1]), pack_bf16x2(y[8 * k + 2], y[8 * k + 3]),
+                                                   pack_bf16x2(y[8 * k + 4], y[8 * k + 5]), pack_bf16x2(y[8 * k + 6], y[8 * k + 7]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_e4m3x4(y[16 * k + 4 * e] * a.inv_scale, y[16 * k + 4 * e + 1] * a.inv_scale,
+                                   y[16 * k + 4 * e + 2] * a.inv_scale, y[16 * k + 4 * e + 3] * a.inv_scale);
+              *piece(2 * c + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          // 128 bytes of every row are there: after each group of 32 columns (fp32), two (bf16) or four (e4m3)
+          if (dst_type == 0 || (dst_type == 1 && (c & 1)) || c == 3) {
+            const int line = dst_type == 0 ? c : dst_type == 1 ? c >> 1 : 0;
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = 4 * k + (lane >> 3), p = lane & 7;
+              const int at = __shfl_sync(0xffffffffu, dst_row, r);
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+              if (at >= 0)
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(dst) + static_cast<int64_t>(at) * row_bytes + line * 128 + p * 16) = v;
+            }
+            __syncwarp();
           }
         }
         if (!part && a.amax != nullptr) {
@@ -381,9 +428,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     else regs_dec<104>();
     if (warp == 8 || warp == 10) {
       // ====================================================== MMA issuers ===
-      // The whole warp walks its loop, so addresses stay uniform; one elected lane issues. S is one buffer: QK_1(u)
-      // waits until stream 0 has S_0(u) in registers, and PV_i(u) until P_i(u) is written, so a stream's scores are ready
-      // while its last product still runs.
+      // The whole warp walks its loop, so addresses stay uniform; one elected lane issues. The pipe takes the order
+      // QK_0(u), PV_0(u - 1), QK_1(u), PV_1(u - 1): S is one buffer, and stream 0 takes S_0(u) into registers while PV_0(u - 1)
+      // runs; a stream has the time of four products for its softmax. An issue blocks until the pipe is two MMAs
+      // from idle, so a wait on one warp alone would be idle time, and two warps in no order would stretch both
+      // products: each warp waits for its own operands ahead, then for its turn. PV number m follows QK number m + 2.
       const int tiles = misc[M_TILES], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1], tail = misc[M_TAIL];
       const bool one = misc[M_ONE] != 0;
       // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
@@ -397,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
         const uint32_t d = tmem + kTmemS;
         ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
-        int scores = 0;   // S tiles issued
+        int n = 0;   // products issued
 #pragma unroll 1
         for (int u = 0; ok && u < steps; ++u) {
 #pragma unroll
@@ -405,9 +454,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             if (!ok || u >= (i ? cnt1 : cnt0)) continue;
             const int t = tile_at(i, u);
             ok = wait_inline(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, wc, W_T_K) &&
-                 (scores == 0 || wait_inline(bar(B_SFREE), (scores - 1) & 1, wc, W_T_SFREE));
+                 (n < 3 || wait_inline(bar(B_TURN_QK), (n - 3) & 1, wc, W_T_TURN)) &&
+                 (n == 0 || wait_inline(bar(B_SFREE), (n - 1) & 1, wc, W_T_SFREE));
             if (!ok) break;
-            ++scores;
+            ++n;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
@@ -425,6 +475,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                   mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
                 }
               }
+              mbar_arrive(bar(B_TURN_PV));
               mma_commit(bar(B_S0 + i));
               if (one || i == 1) mma_commit(bar(B_KEMPTY + t % C::kKSlots));
             }
@@ -434,6 +485,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       } else if (warp == 10 && tiles > 0) {
         constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
         const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), kTile * 128, 1024));
+        int m = 0;   // products issued
 #pragma unroll 1
         for (int u = 0; ok && u < steps; ++u) {
 #pragma unroll
@@ -444,8 +496,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             else
               ok = wait_inline(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, wc, W_T_V) &&
                    (t != tail || wait_inline(bar(B_VFIX), 0, wc, W_T_FIX));
-            ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P);
+            ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P) &&
+                 wait_inline(bar(B_TURN_PV), min(m + 2, cnt0 + cnt1 - 1) & 1, wc, W_T_TURN);
             if (!ok) break;
+            ++m;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
@@ -454,6 +508,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
                 mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
+              mbar_arrive(bar(B_TURN_QK));
               mma_commit(bar(B_O0 + i));
               if (one || i == 1) {
                 if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
@@ -481,9 +536,6 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
         const int boxes = kTile / page_rows;               // of one tile and column block
         if (lane == 0) {
-          tma_prefetch_desc(&tm_q);
-          tma_prefetch_desc(&tm_k);
-          tma_prefetch_desc(&tm_v);
           const int blocks = one ? 1 : 2;
           mbar_arrive_expect_tx(bar(B_Q), blocks * C::kHalves * tokens * a.group * 128);
           for (int i = 0; i < blocks; ++i)
