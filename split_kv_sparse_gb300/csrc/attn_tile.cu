@@ -649,25 +649,27 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const uint8_t* src = smem + C::kOffV + sl * C::kItemBytes + key * 128;
         uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
         const bool in = (tile0 + t) * kTile + key < kv;
-        uint4 w[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          w[c] = in ? *reinterpret_cast<const uint4*>(src + ((c ^ r8) << 4)) : make_uint4(0, 0, 0, 0);
+        for (int half = 0; half < 2; ++half) {               // 64 dims
+          uint4 w[4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {                       // dims 16c .. 16c + 15
-          const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-          uint32_t h[8];
+          for (int c = 0; c < 4; ++c)
+            w[c] = in ? *reinterpret_cast<const uint4*>(src + (((4 * half + c) ^ r8) << 4)) : make_uint4(0, 0, 0, 0);
+          uint8_t* blk = dst + half * kTile * 128;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            asm("{\n  .reg .b16 lo, hi;\n  mov.b32 {lo, hi}, %2;\n  cvt.rn.f16x2.e4m3x2 %0, lo;\n"
-                "  cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
-                : "=r"(h[2 * k]), "=r"(h[2 * k + 1])
-                : "r"(ws[k]));
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              asm("{\n  .reg .b16 lo, hi;\n  mov.b32 {lo, hi}, %2;\n  cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+                  "  cvt.rn.f16x2.e4m3x2 %1, hi;\n}\n"
+                  : "=r"(h[2 * k]), "=r"(h[2 * k + 1])
+                  : "r"(ws[k]));
+            }
+            *reinterpret_cast<uint4*>(blk + (((2 * c) ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(blk + (((2 * c + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-          uint8_t* blk = dst + (c >> 2) * kTile * 128;      // 64-dim column block
-          const int p = 2 * (c & 3);
-          *reinterpret_cast<uint4*>(blk + ((p ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(blk + (((p + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
