@@ -103,10 +103,12 @@ int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / token
 // Tokens of one job's rows.
 int job_tokens(bool rows16, int group) { return rows16 ? skv::kRowRows / group : 2 * (128 / group); }
 
+int split_waves(bool rows16) { return rows16 ? skv::kRowSplitWaves : skv::kTileSplitWaves; }
+
 // Jobs that one launch may hold: unsplit, forced splits, or counts from the lengths.
-int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int num_sms) {
+int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int wave, int split_waves) {
   if (!adaptive) return unsplit * num_splits;
-  return unsplit <= num_sms ? num_sms : unsplit + num_sms;
+  return unsplit <= wave ? wave : unsplit + split_waves * wave;
 }
 
 int shift_of(int pow2) {
@@ -229,8 +231,8 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->adaptive_splits = adaptive;
   out->row_kernel = rows16 ? 1 : 0;
   if (S > 1) {
-    // split jobs: as many as forced, or at most one wave (the rule keeps to that)
-    const int64_t slots = adaptive ? wave : unsplit * S;
+    // split jobs: as many as forced, or at most so many waves (the rule keeps to that)
+    const int64_t slots = adaptive ? static_cast<int64_t>(wave) * split_waves(rows16) : unsplit * S;
     if (slots * job_rows > 0x7FFFFFFFll) {
       std::memset(out, 0, sizeof(*out));
       return MLA_ERR_UNSUPPORTED;
@@ -302,6 +304,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.adaptive = plan->adaptive_splits;
   const bool rows16 = plan->row_kernel != 0;
   a.num_sms = rows16 ? plan->num_sms * skv::kRowCtasPerSm : plan->num_sms;
+  a.max_slots = a.num_sms * split_waves(rows16);
   if (plan->num_splits > 1) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.o_part = reinterpret_cast<float*>(ws);
@@ -321,7 +324,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
                       pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK)
     return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
-  const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms);
+  const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms, split_waves(rows16));
   st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
                           : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;

@@ -50,17 +50,20 @@ struct AttnJob {
   int slot;   // S > 1: the job's place among the split jobs
 };
 
-// Job `idx` of the batch, found by one warp (lane by lane a sequence). Sequence b has
-// n_b = ceil(s_b / tokens) query tiles and S_b splits: num_splits of them where the plan
+// The batch's jobs, found by one warp (lane by lane a sequence). Sequence b has n_b =
+// ceil(s_b / tokens) query tiles and S_b splits: num_splits of them where the plan
 // forces a count, else, with T = the key tiles a job should walk, clamp(ceil(tiles_b / T),
 // 1, num_splits). If the unsplit jobs fit one wave of num_sms, T is the smallest whose
-// jobs do too; otherwise only a sequence that walks more than twice its SM's share of
-// the work is split, into shares of two: both bound the split jobs by num_sms. Jobs are
-// listed sequence by sequence; within one the last query tiles first (they see the most
-// keys), then the splits, the KV heads fastest.
-__device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, int idx, int lane) {
-  const int groups = (a.batch + 31) / 32;
-  auto load = [&](int i, int& n, int& tiles) {
+// jobs do too; otherwise T is thirds / 3 of an SM's share of the work, or the next (by
+// quarters) whose split jobs fit the workspace's max_slots.
+// Jobs are listed sequence by sequence; within one the last query tiles first (they
+// see the most keys), then the splits, the KV heads fastest.
+struct AttnJobs {
+  int tokens, groups;
+  int n_first, tiles_first;   // the first 32 sequences stay in registers
+  int T;                      // 0: S_b = num_splits
+
+  __device__ __forceinline__ void load(const AttnArgs& a, int i, int lane, int& n, int& tiles) const {
     n = tiles = 0;
     const int b = 32 * i + lane;
     if (b < a.batch) {
@@ -68,25 +71,30 @@ __device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, 
       n = (q.sq + tokens - 1) / tokens;
       tiles = (q.kv + kAttnKeyTile - 1) / kAttnKeyTile;
     }
-  };
-  int n_first, tiles_first;   // the first 32 sequences stay in registers
-  load(0, n_first, tiles_first);
-  auto shape = [&](int i, int& n, int& tiles) {
+  }
+  __device__ __forceinline__ void shape(const AttnArgs& a, int i, int lane, int& n, int& tiles) const {
     if (i == 0) {
       n = n_first;
       tiles = tiles_first;
     } else {
-      load(i, n, tiles);
+      load(a, i, lane, n, tiles);
     }
-  };
-  int T = 0;   // 0: S_b = num_splits
-  auto splits = [&](int tiles) { return T == 0 ? a.num_splits : min(a.num_splits, max(1, (tiles + T - 1) / T)); };
-  if (a.adaptive && a.num_splits > 1) {
+  }
+  __device__ __forceinline__ int splits(const AttnArgs& a, int tiles) const {
+    return T == 0 ? a.num_splits : min(a.num_splits, max(1, (tiles + T - 1) / T));
+  }
+
+  __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int thirds, int lane) {
+    tokens = job_tokens;
+    groups = (a.batch + 31) / 32;
+    T = 0;
+    load(a, 0, lane, n_first, tiles_first);
+    if (!a.adaptive || a.num_splits <= 1) return;
     int jobs = 0, most = 1;
     long long work = 0;
     for (int i = 0; i < groups; ++i) {
       int n, tiles;
-      shape(i, n, tiles);
+      shape(a, i, lane, n, tiles);
       jobs += warp_sum_int(n);
       most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? tiles : 0));
       long long w = static_cast<long long>(n) * tiles;
@@ -96,75 +104,97 @@ __device__ __forceinline__ AttnJob attn_find_job(const AttnArgs& a, int tokens, 
     }
     work *= a.h_kv;
     const long long unsplit = static_cast<long long>(jobs) * a.h_kv;
-    const int share = static_cast<int>(min((work + a.num_sms - 1) / a.num_sms, 1ll << 24));   // (above any sequence's tiles)
     if (unsplit > a.num_sms) {
-      T = 2 * max(share, 1);
-    } else {
-      // jobs(T) <= work / T + unsplit, so from work / (num_sms - unsplit) on they fit
-      int lo = max(share, 1);
-      int hi = unsplit < a.num_sms ? static_cast<int>(min(work / (a.num_sms - unsplit) + 1, static_cast<long long>(most))) : most;
-      hi = max(hi, lo);
-      while (lo < hi) {
-        T = (lo + hi) >> 1;
-        int total = 0;
+      const long long t = (work * thirds + 3ll * a.num_sms - 1) / (3ll * a.num_sms);
+      T = static_cast<int>(min(max(t, 1ll), 1ll << 24));   // (above any sequence's tiles)
+      for (;;) {
+        int split_jobs = 0;
         for (int i = 0; i < groups; ++i) {
           int n, tiles;
-          shape(i, n, tiles);
-          total += warp_sum_int(n * splits(tiles));
+          shape(a, i, lane, n, tiles);
+          const int s = splits(a, tiles);
+          split_jobs += warp_sum_int(s > 1 ? n * s : 0);
         }
-        if (static_cast<long long>(total) * a.h_kv <= a.num_sms) hi = T;
-        else lo = T + 1;
+        if (static_cast<long long>(split_jobs) * a.h_kv <= a.max_slots) return;
+        T += (T + 3) >> 2;
       }
-      T = hi;
     }
-  }
-  AttnJob job = {-1, 0, 0, 0, 1, 0};
-  int base = 0, slots = 0;
-  for (int i = 0; i < groups && job.b < 0; ++i) {
-    int n, tiles;
-    shape(i, n, tiles);
-    const int s = splits(tiles);
-    const int count = n * s * a.h_kv;
-    const int split_count = s > 1 ? count : 0;
-    const int incl = warp_scan_incl(count, lane), sincl = warp_scan_incl(split_count, lane);
-    const int local = idx - base - (incl - count);
-    const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
-    if (hit != 0) {
-      const int src = __ffs(hit) - 1;
-      const int l = __shfl_sync(0xffffffffu, local, src);
-      const int nn = __shfl_sync(0xffffffffu, n, src);
-      const int first = __shfl_sync(0xffffffffu, slots + sincl - split_count, src);
-      job.b = 32 * i + src;
-      job.S = __shfl_sync(0xffffffffu, s, src);
-      const int rest = l / a.h_kv;
-      job.g = l - rest * a.h_kv;
-      const int tile = rest / job.S;
-      job.s = rest - tile * job.S;
-      job.j = nn - 1 - tile;
-      job.slot = first + (job.j * a.h_kv + job.g) * job.S + job.s;
+    // jobs(T) <= work / T + unsplit, so from work / (num_sms - unsplit) on they fit
+    int lo = max(static_cast<int>((work + a.num_sms - 1) / a.num_sms), 1);
+    int hi = unsplit < a.num_sms ? static_cast<int>(min(work / (a.num_sms - unsplit) + 1, static_cast<long long>(most))) : most;
+    hi = max(hi, lo);
+    while (lo < hi) {
+      T = (lo + hi) >> 1;
+      int total = 0;
+      for (int i = 0; i < groups; ++i) {
+        int n, tiles;
+        shape(a, i, lane, n, tiles);
+        total += warp_sum_int(n * splits(a, tiles));
+      }
+      if (static_cast<long long>(total) * a.h_kv <= a.num_sms) hi = T;
+      else lo = T + 1;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-    slots += __shfl_sync(0xffffffffu, sincl, 31);
+    T = hi;
   }
-  return job;
-}
 
-// wait_bounded without a call, for kernels whose warps share out the registers:
-// gives up after ctx.limit_ns or when another role of the CTA has, and says so.
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, const WaitCtx& ctx, uint32_t site) {
-  if (mbar_test_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 15u) == 0) {
-      if (*ctx.abort_flag) return false;
-      if (globaltimer_ns() - t0 > ctx.limit_ns) {
-        *ctx.abort_flag = 1;
-        atomicOr(&ctx.status[0], 1u);
-        atomicCAS(&ctx.status[1], 0u, site);
-        return false;
+  __device__ __forceinline__ AttnJob find(const AttnArgs& a, int idx, int lane) const {
+    AttnJob job = {-1, 0, 0, 0, 1, 0};
+    int base = 0, slots = 0;
+    for (int i = 0; i < groups && job.b < 0; ++i) {
+      int n, tiles;
+      shape(a, i, lane, n, tiles);
+      const int s = splits(a, tiles);
+      const int count = n * s * a.h_kv;
+      const int split_count = s > 1 ? count : 0;
+      const int incl = warp_scan_incl(count, lane), sincl = warp_scan_incl(split_count, lane);
+      const int local = idx - base - (incl - count);
+      const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
+      if (hit != 0) {
+        const int src = __ffs(hit) - 1;
+        const int l = __shfl_sync(0xffffffffu, local, src);
+        const int nn = __shfl_sync(0xffffffffu, n, src);
+        const int first = __shfl_sync(0xffffffffu, slots + sincl - split_count, src);
+        job.b = 32 * i + src;
+        job.S = __shfl_sync(0xffffffffu, s, src);
+        const int rest = l / a.h_kv;
+        job.g = l - rest * a.h_kv;
+        const int tile = rest / job.S;
+        job.s = rest - tile * job.S;
+        job.j = nn - 1 - tile;
+        job.slot = first + (job.j * a.h_kv + job.g) * job.S + job.s;
       }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+      slots += __shfl_sync(0xffffffffu, sincl, 31);
     }
+    return job;
+  }
+};
+
+// Waits for the phase with the given parity of `bar`, at most `limit` ns. All lanes of
+// a converged warp call it and leave it together (one barrier word, one timer). It
+// is kept this small because it is inlined at some thirty places: with the status
+// word and the CTA's abort flag handled in its loop, or with a vote behind it, these
+// kernels lose up to 40 % (e4m3 prompt of 16,384 tokens: 1.2 -> 2.0 ms). A role that gives up
+// says so once (give_up); the others run into their own limit.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t limit) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const uint32_t t0 = globaltimer_lo();
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (globaltimer_lo() - t0 <= limit);
+  return false;
+}
+// The limit of wait_for: the caller's (mla_set_wait_limit_ns), at most what 32 bits of
+// nanoseconds can tell apart.
+__device__ __forceinline__ uint32_t wait_limit(const AttnArgs& a) {
+  return a.wait_limit_ns < 4000000000ull ? static_cast<uint32_t>(a.wait_limit_ns) : 4000000000u;
+}
+// Records that a role's wait ran out.
+__device__ __forceinline__ void give_up(const AttnArgs& a, volatile int* abort_flag, uint32_t site) {
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    atomicOr(&a.status[0], 1u);
+    atomicCAS(&a.status[1], 0u, site);
   }
 }
 

@@ -31,6 +31,8 @@ constexpr int kSmem = kOffAbort + 16 + 1024;
 constexpr int kMergeStride = kD + 4;                    // floats a row of a warp's result (16 rows in its ring)
 static_assert(16 * kMergeStride * 4 <= kWarpBytes, "merge area");
 constexpr float kRescaleThreshold = 8.0f;
+// More jobs than a wave: a sequence is split from twice its share of the work on.
+constexpr int kRowThirds = 6;
 
 enum : uint32_t { W_R_FULL = 301, W_R_DRAIN };
 
@@ -98,7 +100,9 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   grid_dependency_wait();
 
   const int tokens = kRowRows / a.group;
-  const AttnJob job = attn_find_job(a, tokens, blockIdx.x, lane);   // every warp for itself
+  AttnJobs jobs;                      // every warp for itself
+  jobs.init(a, tokens, kRowThirds, lane);
+  const AttnJob job = jobs.find(a, blockIdx.x, lane);
   grid_launch_dependents();
   if (job.b < 0) return;
   const AttnSeq seq = attn_seq(a, job.b);
@@ -196,13 +200,13 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  const WaitCtx wc{a.wait_limit_ns, a.status, abort_flag};
+  const uint32_t limit = wait_limit(a);
   bool ok = true;
   int n = 0;
 #pragma unroll 1
   for (; n < cnt; ++n) {
     const int st = n % kStages;
-    if (!wait_inline(bar(st), (n / kStages) & 1, wc, W_R_FULL)) {
+    if (!wait_for(bar(st), (n / kStages) & 1, limit)) {
       ok = false;
       break;
     }
@@ -347,6 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     if (n + kStages < cnt) issue(n + kStages);
   }
   if (!ok) {
+    give_up(a, abort_flag, W_R_FULL);
     // nothing that was started may still be writing shared memory when the CTA ends
     bool done = true;
     for (int k = n; k < min(n + kStages, cnt); ++k)

@@ -27,6 +27,8 @@ namespace {
 
 constexpr int kD = kAttnDim;
 constexpr int kTile = kAttnKeyTile;
+// More jobs than a wave: sequences are cut into jobs of a third of an SM's share.
+constexpr int kTileThirds = 1;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
 
 template <bool kF8>
@@ -44,35 +46,39 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kKSlots * kItemBytes;
   static constexpr int kOffV16 = kOffV + kVSlots * kItemBytes;
   static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
-  static constexpr int kOffMisc = kOffBars + 320;
-  static constexpr int kSmem = kOffMisc + 256 + 1024;
-  // 128 rows x 128 fp32 of stream 1's result are merged through the rings
-  static_assert(kOffBars - kOffK >= 128 * kD * 4 + 128 * 8, "merge area");
+  static constexpr int kOffMisc = kOffBars + 352;
+  static constexpr int kOffStats = kOffMisc + 384;       // float2 [128 rows]: m, l of stream 1
+  static constexpr int kSmem = kOffStats + 1024 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
+  static constexpr int kConsumers = kF8 ? 15 : 11;       // warps that read a job's description
 };
 
 enum {
-  B_Q = 0, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VFIX, B_END, B_DRAIN, B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_KFULL,
+  B_Q = 0, B_QFREE0, B_QFREE1, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VFIX, B_END, B_DRAIN,
+  B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_NEXT, B_CLC, B_STAT,
+  B_OREAD, B_KFULL,
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
-static_assert(kNumBars * 8 <= 320, "barrier area");
+static_assert(kNumBars * 8 <= 352, "barrier area");
 
-enum : uint32_t { W_T_PROD = 201, W_T_Q, W_T_K, W_T_V, W_T_P, W_T_S, W_T_SFREE, W_T_TURN, W_T_O, W_T_FIN, W_T_CVT, W_T_FIX, W_T_MERGE, W_T_DRAIN };
+enum : uint32_t { W_T_SOFTMAX = 201, W_T_MMA, W_T_LOAD, W_T_SCHED, W_T_CONVERT, W_T_DRAIN };   // whose wait ran out
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemP = 128, kTmemO = 256;   // S; P_0, P_1 (64 each); O_0, O_1 (128 each)
 
-// Words of the misc area: what the roles need of the job, worked out once.
+// What the roles need of a job, worked out once by the scheduler warp; two of them are
+// in flight.
 enum {
-  M_TMEM = 0, M_ABORT, M_B, M_G, M_SPLIT, M_S, M_SLOT, M_Q0, M_SQ, M_K0, M_KV,
-  M_TOK0,             // first token (of the sequence) of row block 0
-  M_TILE0, M_TILES,   // first key tile and count that the job walks
-  M_ONE,              // one row block
-  M_CNT0, M_CNT1,     // key tiles of each stream
-  M_TAIL,             // the local tile that holds the sequence's ragged end, or -1
-  M_MASK, kMaskRing = 16
+  J_B, J_G, J_SPLIT, J_S, J_SLOT, J_Q0, J_SQ, J_K0, J_KV,
+  J_TOK0,             // first token (of the sequence) of row block 0
+  J_TILE0, J_TILES,   // first key tile and count that the job walks
+  J_ONE,              // one row block
+  J_CNT0, J_CNT1,     // key tiles of each stream
+  J_TAIL,             // the local tile that holds the sequence's ragged end, or -1
+  kJobWords
 };
-static_assert((M_MASK + kMaskRing) * 4 <= 256, "misc area");
+enum { M_TMEM = 0, M_ABORT, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
+static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
 template <bool kF8>
 __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
@@ -90,28 +96,13 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 
   const int tokens = 128 / a.group;   // of one row block
   if (threadIdx.x == 0) {
-    mbar_init(bar(B_Q), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(B_S0 + i), 1);
-      mbar_init(bar(B_P0 + i), 4);
-      mbar_init(bar(B_O0 + i), 1);
-      mbar_init(bar(B_V16F0 + i), 4);
-      mbar_init(bar(B_V16E0 + i), 1);
-    }
-    mbar_init(bar(B_TURN_QK), 1);
-    mbar_init(bar(B_TURN_PV), 1);
-    mbar_init(bar(B_VFIX), 1);
-    mbar_init(bar(B_END), 1);
-    mbar_init(bar(B_DRAIN), 1);
-    mbar_init(bar(B_DRAIN2), 1);
-    mbar_init(bar(B_SFREE), 4);
-    for (int i = 0; i < C::kKSlots; ++i) {
-      mbar_init(bar(B_KFULL + i), 1);
-      mbar_init(bar(B_KEMPTY + i), 1);
-    }
-    for (int i = 0; i < C::kVSlots; ++i) {
-      mbar_init(bar(B_VFULL + i), 1);
-      mbar_init(bar(B_VEMPTY + i), kF8 ? 4 : 1);   // a V tile of codes is freed by its four converter warps
+    for (int i = 0; i < kNumBars; ++i) {
+      const int n = i == B_STAT || i == B_OREAD || i == B_QFREE0 || i == B_QFREE1 || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 ||
+                            (kF8 && i >= B_VEMPTY)   // a V tile of codes is freed by its four converter warps
+                        ? 4
+                    : i == B_READ0 || i == B_READ1 ? C::kConsumers
+                                                   : 1;
+      mbar_init(bar(i), n);
     }
     misc[M_ABORT] = 0;
     mbar_init_fence();
@@ -120,87 +111,57 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     tmem_alloc(smem_u32(smem + C::kOffMisc), kTmemCols);
     tmem_relinquish();
   }
-  grid_dependency_wait();             // the job search reads the lengths
-  if (warp == 9) {
-    const AttnJob job = attn_find_job(a, 2 * tokens, blockIdx.x, lane);
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-      misc[M_B] = job.b;
-      if (job.b >= 0) {
-        const AttnSeq seq = attn_seq(a, job.b);
-        const int tok0 = job.j * 2 * tokens;
-        const int tiles_all = (seq.kv + kTile - 1) / kTile;
-        const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
-        const int tile0 = job.s * base_t + min(job.s, rem_t);
-        const int nt = base_t + (job.s < rem_t ? 1 : 0);
-        // key tiles of row block i: up to the position of its last token
-        auto tiles_of = [&](int i) {
-          const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
-          if (last < tok0 + i * tokens) return 0;
-          const int keys = seq.kv - seq.sq + last + 1;
-          return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
-        };
-        const bool one = tok0 + tokens >= seq.sq;
-        const int n0 = tiles_of(0), n1 = tiles_of(1);      // n1 >= n0 where there is a second block
-        const int tiles = one ? n0 : n1;
-        misc[M_G] = job.g;
-        misc[M_SPLIT] = job.s;
-        misc[M_S] = job.S;
-        misc[M_SLOT] = job.slot;
-        misc[M_Q0] = seq.q0;
-        misc[M_SQ] = seq.sq;
-        misc[M_K0] = seq.k0;
-        misc[M_KV] = seq.kv;
-        misc[M_TOK0] = tok0;
-        misc[M_TILE0] = tile0;
-        misc[M_TILES] = tiles;
-        misc[M_ONE] = one;
-        misc[M_CNT0] = one ? (tiles + 1) >> 1 : n0;
-        misc[M_CNT1] = one ? tiles >> 1 : n1;
-        misc[M_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
-      }
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dependency_wait();
   grid_launch_dependents();
   const uint32_t tmem = static_cast<uint32_t>(misc[M_TMEM]);
-  const WaitCtx wc{a.wait_limit_ns, a.status, misc + M_ABORT};
-  if (misc[M_B] < 0) {   // no job
-    if (warp == 8) tmem_dealloc(tmem, kTmemCols);
-    return;
-  }
+  const uint32_t limit = wait_limit(a);
+  // Job number k of this CTA: waits until the scheduler has described it and returns its words (negative J_B: no more).
+  auto job_at = [&](int k, volatile int*& words) {
+    words = misc + M_JOBS + (k & 1) * kJobWords;
+    return wait_for(bar(B_JOB0 + (k & 1)), (k >> 1) & 1, limit);
+  };
+  // The words have been copied.
+  auto job_read = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B_READ0 + (k & 1)));
+  };
 
   if (warp < 8) {
     // ================================================= softmax + epilogue ===
     if constexpr (kF8) regs_inc<192>();
-    else regs_inc<200>();
+    else regs_inc<208>();
     const int i = warp >> 2;
-    const int g = misc[M_G], split = misc[M_SPLIT], S = misc[M_S], slot0 = misc[M_SLOT], q0 = misc[M_Q0], sq = misc[M_SQ],
-              kv = misc[M_KV], tok0 = misc[M_TOK0], tile0 = misc[M_TILE0], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1];
-    const bool one = misc[M_ONE] != 0;
-    const int cnt = i ? cnt1 : cnt0;
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS, tp = tmem + lanes + kTmemP + 64 * i, to = tmem + lanes + kTmemO + 128 * i;
     const int rt = row / a.group;                          // token of the block
-    const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
-    const bool live = rt < tokens && tok < sq;
-    const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
     const float dq = a.descale_q ? *a.descale_q : 1.f, dk = a.descale_k ? *a.descale_k : 1.f,
                 dv = a.descale_v ? *a.descale_v : 1.f;
     const float sc = dq * dk * a.scale_log2;
     const bool raw_ok = sc > 0.f;      // then the scale commutes with the maximum and goes into the exponent's FMA
     const float esc = raw_ok ? sc : 1.f;
+    int su = 0, ends = 0, ones = 0, mask0 = 0;   // this stream's tiles, jobs with tiles, jobs of one row block, all tiles
+#pragma unroll 1
+    for (int job = 0;; ++job) {
+    volatile int* w;
+    if (!job_at(job, w) || w[J_B] < 0) break;
+    const int g = w[J_G], split = w[J_SPLIT], S = w[J_S], slot0 = w[J_SLOT], q0 = w[J_Q0], sq = w[J_SQ], kv = w[J_KV],
+              tok0 = w[J_TOK0], tile0 = w[J_TILE0], tiles = w[J_TILES], cnt0 = w[J_CNT0], cnt1 = w[J_CNT1];
+    const bool one = w[J_ONE] != 0;
+    job_read(job);
+    const int cnt = i ? cnt1 : cnt0;
+    const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
+    const bool live = rt < tokens && tok < sq;
+    const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
     float m_run = -INFINITY, l = 0.f;
     bool bad = false;
 #pragma unroll 1
     for (int u = 0; u < cnt; ++u) {
       const int t = one ? 2 * u + i : u;
-      if (!wait_inline(bar(B_S0 + i), u & 1, wc, W_T_S)) {
+      if (!wait_for(bar(B_S0 + i), (su + u) & 1, limit)) {
         bad = true;
         break;
       }
@@ -228,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           for (int k = 0; k < 32; ++k)
             if (32 * c + k > kmax) x[c][k] = -INFINITY;
       }
-      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + (t & (kMaskRing - 1))]);   // 16-key groups with a page
+      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
       if (pages != 0xffu) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -240,7 +201,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
       const bool need = mx > m_run + kRescaleThreshold;
       // O_i's last product is done: P_i may be written again, O_i rescaled
-      if (u > 0 && !wait_inline(bar(B_O0 + i), (u - 1) & 1, wc, W_T_O)) {
+      if (u > 0 && !wait_for(bar(B_O0 + i), (su + u - 1) & 1, limit)) {
         bad = true;
         break;
       }
@@ -291,42 +252,28 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     }
 
     // ---- epilogue
-    if (!bad && cnt > 0) bad = !wait_inline(bar(B_O0 + i), (cnt - 1) & 1, wc, W_T_FIN);
-    // the merge reuses the rings: both streams' products must be done with them
-    if (one && cnt0 > 0 && !bad) bad = !wait_inline(bar(B_END), 0, wc, W_T_MERGE);
+    if (!bad && cnt > 0) bad = !wait_for(bar(B_O0 + i), (su + cnt - 1) & 1, limit);
+    // rows that see no key of a job that loads Q all the same: not before that load has left Q's place
+    if (!bad && cnt == 0 && tiles > 0) bad = !wait_for(bar(B_Q), ends & 1, limit);
+    // one row block: stream 0 takes both results from tensor memory (they lie in the same lanes)
+    if (one && tiles > 0 && !bad) bad = !wait_for(bar(B_END), ends & 1, limit);
     tc_fence_after();
-    float4* merge = reinterpret_cast<float4*>(smem + C::kOffK);              // [32][128 rows] pieces of 4 columns
-    float2* stats = reinterpret_cast<float2*>(smem + C::kOffK + 128 * kD * 4);   // [128 rows] (m, l) of stream 1
+    float2* stats = reinterpret_cast<float2*>(smem + C::kOffStats);
     if (one && i == 1) {
-      if (!bad) {
-        stats[row] = make_float2(m_run, l);
-        if (cnt > 0) {
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(to + 16 * c, o);
-            tmem_wait_ld_x16(o);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              merge[(4 * c + k) * 128 + row] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                           __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-          }
-        }
-      }
-      named_bar_sync(2, 256);
+      stats[row] = make_float2(m_run, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_STAT));
+      bad = !wait_for(bar(B_OREAD), ones & 1, limit) || bad;   // stream 0 has read O_1
     } else {
       float w0 = 1.f, w1 = 0.f;
       if (one) {
-        named_bar_sync(2, 256);
-        bad = bad || *wc.abort_flag;
-        if (!bad) {
-          const float2 st = stats[row];
-          const float M = fmaxf(m_run, st.x);
-          w0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
-          w1 = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
-          l = l * w0 + st.y * w1;
-          m_run = M;
-        }
+        bad = !wait_for(bar(B_STAT), ones & 1, limit) || bad;
+        const float2 st = stats[row];
+        const float M = fmaxf(m_run, st.x);
+        w0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
+        w1 = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
+        l = l * w0 + st.y * w1;
+        m_run = M;
       }
       if (!bad) {
         const bool some = l > 0.f || l != l;   // a NaN score stays a NaN result
@@ -363,15 +310,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             for (int k = 0; k < 32; ++k) y[k] = 0.f;
           }
           if (one && cnt1 > 0) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 128 + 32 * c, o);
+            tmem_wait_ld_x32(o);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (w1 != 0.f) v = merge[(8 * c + k) * 128 + row];
-              y[4 * k] = y[4 * k] * w0 + v.x * w1;
-              y[4 * k + 1] = y[4 * k + 1] * w0 + v.y * w1;
-              y[4 * k + 2] = y[4 * k + 2] * w0 + v.z * w1;
-              y[4 * k + 3] = y[4 * k + 3] * w0 + v.w * w1;
-            }
+            for (int k = 0; k < 32; ++k) y[k] = y[k] * w0 + (w1 != 0.f ? __uint_as_float(o[k]) * w1 : 0.f);
           }
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
@@ -422,10 +365,28 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           if (lane == 0) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
         }
       }
+      if (one) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_OREAD));
+      }
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();                              // Q's place was read and written here; TMA writes it next
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B_QFREE0 + i));
+    su += cnt;
+    mask0 += tiles;
+    ends += tiles > 0 ? 1 : 0;
+    ones += one ? 1 : 0;
+    if (bad) {
+      give_up(a, misc + M_ABORT, W_T_SOFTMAX);
+      break;
+    }
     }
   } else {
     if constexpr (kF8) regs_dec<64>();
-    else regs_dec<104>();
+    else regs_dec<88>();
     if (warp == 8 || warp == 10) {
       // ====================================================== MMA issuers ===
       // The whole warp walks its loop, so addresses stay uniform; one elected lane issues. The pipe takes the order
@@ -433,115 +394,145 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       // runs; a stream has the time of four products for its softmax. An issue blocks until the pipe is two MMAs
       // from idle, so a wait on one warp alone would be idle time, and two warps in no order would stretch both
       // products: each warp waits for its own operands ahead, then for its turn. PV number m follows QK number m + 2.
-      const int tiles = misc[M_TILES], cnt0 = misc[M_CNT0], cnt1 = misc[M_CNT1], tail = misc[M_TAIL];
-      const bool one = misc[M_ONE] != 0;
       // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
       const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(sbase, 16, 1024) >> 32);
-      const int steps = max(cnt0, cnt1);
-      auto tile_at = [&](int i, int u) { return one ? 2 * u + i : u; };
+      const bool is_qk = warp == 8;
+      constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
+      constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
+      const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
+      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
+      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), kTile * 128, 1024));
       bool ok = true;
-      if (warp == 8 && tiles > 0) {
-        constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
-        const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
-        const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
-        const uint32_t d = tmem + kTmemS;
-        ok = wait_inline(bar(B_Q), 0, wc, W_T_Q);
-        int n = 0;   // products issued
+      int tile_base = 0;     // tiles of earlier jobs
+      int n = 0;             // this warp's products so far
+      int with_tiles = 0;    // jobs that had any
+      int seen0 = 0, seen1 = 0, fixes = 0;
 #pragma unroll 1
-        for (int u = 0; ok && u < steps; ++u) {
+      for (int job = 0; ok; ++job) {
+        volatile int* w;
+        ok = job_at(job, w);
+        if (!ok || w[J_B] < 0) break;
+        const int tiles = w[J_TILES], cnt0 = w[J_CNT0], cnt1 = w[J_CNT1], tail = w[J_TAIL];
+        const bool one = w[J_ONE] != 0;
+        job_read(job);
+        if (tiles == 0) continue;
+        const int steps = max(cnt0, cnt1);
+        auto tile_at = [&](int i, int u) { return one ? 2 * u + i : u; };
+        if (is_qk) {
+          const uint32_t d = tmem + kTmemS;
+          const int first = n;   // (a job's first products have none of its own to follow)
+          ok = wait_for(bar(B_Q), with_tiles & 1, limit);
+#pragma unroll 1
+          for (int u = 0; ok && u < steps; ++u) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok || u >= (i ? cnt1 : cnt0)) continue;
-            const int t = tile_at(i, u);
-            ok = wait_inline(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, wc, W_T_K) &&
-                 (n < 3 || wait_inline(bar(B_TURN_QK), (n - 3) & 1, wc, W_T_TURN)) &&
-                 (n == 0 || wait_inline(bar(B_SFREE), (n - 1) & 1, wc, W_T_SFREE));
-            if (!ok) break;
-            ++n;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
-              const uint32_t kb = k_lo + static_cast<uint32_t>(t % C::kKSlots) * (C::kItemBytes >> 4);
-              if constexpr (kF8) {
-                mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
-                mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
-                mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
-                mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
-              } else {
-                mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || u >= (i ? cnt1 : cnt0)) continue;
+              const int t = tile_base + tile_at(i, u);
+              ok = wait_for(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, limit) &&
+                   (n < first + 3 || wait_for(bar(B_TURN_QK), (n - 3) & 1, limit)) &&
+                   (n == 0 || wait_for(bar(B_SFREE), (n - 1) & 1, limit));
+              if (!ok) break;
+              ++n;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
+                const uint32_t kb = k_lo + static_cast<uint32_t>(t % C::kKSlots) * (C::kItemBytes >> 4);
+                if constexpr (kF8) {
+                  mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
+                  mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
+                  mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
+                  mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
+                } else {
+                  mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
 #pragma unroll
-                for (int k = 1; k < 8; ++k) {
-                  const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
-                  mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
+                  for (int k = 1; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
+                    mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
+                  }
+                }
+                mbar_arrive(bar(B_TURN_PV));
+                mma_commit(bar(B_S0 + i));
+                if (one || i == 1) mma_commit(bar(B_KEMPTY + t % C::kKSlots));
+              }
+              __syncwarp();
+            }
+          }
+        } else {
+          const int last = n + cnt0 + cnt1 - 1;   // the job's last product
+#pragma unroll 1
+          for (int u = 0; ok && u < steps; ++u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!ok || u >= (i ? cnt1 : cnt0)) continue;
+              const int t = tile_base + tile_at(i, u);
+              if constexpr (kF8) ok = wait_for(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
+              else
+                ok = wait_for(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit) &&
+                     (t - tile_base != tail || wait_for(bar(B_VFIX), fixes & 1, limit));
+              // (the job's last two products have no later QK to follow; the turn is an order, P is the dependency)
+              ok = ok && wait_for(bar(B_P0 + i), (i ? seen1 : seen0) & 1, limit) &&
+                   (n + 2 > last || wait_for(bar(B_TURN_PV), (n + 2) & 1, limit));
+              if (!ok) break;
+              ++n;
+              if (i) ++seen1;
+              else ++seen0;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
+                                                : static_cast<uint32_t>(t % C::kVSlots) * (C::kItemBytes >> 4));
+                const uint32_t pa = tmem + kTmemP + 64 * i, d = tmem + kTmemO + 128 * i;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
+                  mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
+                mbar_arrive(bar(B_TURN_QK));
+                mma_commit(bar(B_O0 + i));
+                if (one || i == 1) {
+                  if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
+                  else mma_commit(bar(B_VEMPTY + t % C::kVSlots));
                 }
               }
-              mbar_arrive(bar(B_TURN_PV));
-              mma_commit(bar(B_S0 + i));
-              if (one || i == 1) mma_commit(bar(B_KEMPTY + t % C::kKSlots));
+              __syncwarp();
             }
-            __syncwarp();
           }
+          if (ok && elect_one()) mma_commit(bar(B_END));
+          __syncwarp();
+          if (tail >= 0) ++fixes;
         }
-      } else if (warp == 10 && tiles > 0) {
-        constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
-        const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), kTile * 128, 1024));
-        int m = 0;   // products issued
-#pragma unroll 1
-        for (int u = 0; ok && u < steps; ++u) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok || u >= (i ? cnt1 : cnt0)) continue;
-            const int t = tile_at(i, u);
-            if constexpr (kF8) ok = wait_inline(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, wc, W_T_V);
-            else
-              ok = wait_inline(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, wc, W_T_V) &&
-                   (t != tail || wait_inline(bar(B_VFIX), 0, wc, W_T_FIX));
-            ok = ok && wait_inline(bar(B_P0 + i), u & 1, wc, W_T_P) &&
-                 wait_inline(bar(B_TURN_PV), min(m + 2, cnt0 + cnt1 - 1) & 1, wc, W_T_TURN);
-            if (!ok) break;
-            ++m;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
-                                              : static_cast<uint32_t>(t % C::kVSlots) * (C::kItemBytes >> 4));
-              const uint32_t pa = tmem + kTmemP + 64 * i, d = tmem + kTmemO + 128 * i;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
-                mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
-              mbar_arrive(bar(B_TURN_QK));
-              mma_commit(bar(B_O0 + i));
-              if (one || i == 1) {
-                if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
-                else mma_commit(bar(B_VEMPTY + t % C::kVSlots));
-              }
-            }
-            __syncwarp();
-          }
-        }
-        if (ok && elect_one()) mma_commit(bar(B_END));
-        __syncwarp();
+        tile_base += tiles;
+        ++with_tiles;
       }
       if (!ok) {
-        const int drain = warp == 8 ? B_DRAIN : B_DRAIN2;
+        give_up(a, misc + M_ABORT, W_T_MMA);
+        const int drain = is_qk ? B_DRAIN : B_DRAIN2;
         if (elect_one()) mma_commit(bar(drain));
         __syncwarp();
         if (!wait_drain(bar(drain), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
       }
     } else if (warp == 9) {
       // ===================================================== TMA producer ===
-      const int job_b = misc[M_B], g = misc[M_G], q0 = misc[M_Q0], k0 = misc[M_K0], kv = misc[M_KV], tok0 = misc[M_TOK0],
-                tile0 = misc[M_TILE0], tiles = misc[M_TILES], tail = misc[M_TAIL];
-      const bool one = misc[M_ONE] != 0;
-      if (tiles > 0) {
-        const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
-        const int boxes = kTile / page_rows;               // of one tile and column block
-        if (lane == 0) {
-          const int blocks = one ? 1 : 2;
-          mbar_arrive_expect_tx(bar(B_Q), blocks * C::kHalves * tokens * a.group * 128);
-          for (int i = 0; i < blocks; ++i)
-            for (int h = 0; h < C::kHalves; ++h)
-              tma_load_3d(sbase + C::kOffQ + i * C::kQBytes + h * 128 * 128, &tm_q, 64 * h, g * a.group,
-                          q0 + tok0 + i * tokens, bar(B_Q));
+      const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
+      const int boxes = kTile / page_rows;                 // of one tile and column block
+      bool ok = true;
+      int kdone = 0, vdone = 0;                            // tiles whose loads were started
+      int with_tiles = 0;
+#pragma unroll 1
+      for (int job = 0; ok; ++job) {
+        volatile int* w;
+        ok = job_at(job, w);
+        if (!ok || w[J_B] < 0) break;
+        const int job_b = w[J_B], g = w[J_G], q0 = w[J_Q0], k0 = w[J_K0], kv = w[J_KV], tok0 = w[J_TOK0], tile0 = w[J_TILE0],
+                  tiles = w[J_TILES], tail = w[J_TAIL];
+        const bool one = w[J_ONE] != 0;
+        job_read(job);
+        // Q's place once the rows of the job before (which go through it, tiles or not) have left it
+        auto q_free = [&]() {
+          return job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) &&
+                              wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
+        };
+        if (tiles == 0) {
+          if (lane == 0) mbar_arrive(bar(B_NEXT));
+          ok = q_free();
+          continue;
         }
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
@@ -559,11 +550,6 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
           return page != a.num_pages;
         };
-        // K runs ahead of V by as many tiles as the products do: K(0) .. K(lag - 1), then K(t), V(t - lag) in turn
-        const int lag = one ? 2 : 1;
-        int kpage[3], krow[3];                               // the pages of K(t), K(t - 1), K(t - 2)
-        bool ok = true;
-        bool have = lookup(0, kpage[0], krow[0]);
         auto load = [&](int base_off, int full, int slot, const CUtensorMap* tm, int page, int row) {
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), C::kItemBytes);
           __syncwarp();
@@ -573,15 +559,18 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + slot));
           }
         };
-        int kdone = 0, vdone = 0;                            // tiles whose loads were started
+        // K runs ahead of V by as many tiles as the products do: K(0) .. K(lag - 1), then K(t), V(t - lag) in turn
+        const int lag = one ? 2 : 1;
+        int kpage[3], krow[3];                               // the pages of K(t), K(t - 1), K(t - 2)
+        bool have = lookup(0, kpage[0], krow[0]);
 #pragma unroll 1
         for (int t = 0; t < tiles + lag; ++t) {
           int page_n = 0, row_n = 0;
           bool have_n = false;
           if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
           if (t < tiles) {
-            const int sl = t % C::kKSlots;
-            if (t >= C::kKSlots && !wait_inline(bar(B_KEMPTY + sl), ((t / C::kKSlots) - 1) & 1, wc, W_T_PROD)) {
+            const int sl = kdone % C::kKSlots;
+            if (kdone >= C::kKSlots && !wait_for(bar(B_KEMPTY + sl), ((kdone / C::kKSlots) - 1) & 1, limit)) {
               ok = false;
               break;
             }
@@ -590,18 +579,30 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             unsigned groups = 0;
             for (int i = 0; i < 8; ++i)
               if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
-            if (lane == 0) misc[M_MASK + (t & (kMaskRing - 1))] = static_cast<int>(groups);
+            if (lane == 0) misc[M_MASK + (kdone & (kMaskRing - 1))] = static_cast<int>(groups);
             load(C::kOffK, B_KFULL, sl, &tm_k, kpage[0], krow[0]);
-            kdone = t + 1;
+            ++kdone;
+          }
+          if (t == 0) {
+            if (!(ok = q_free())) break;
+            if (lane == 0) {
+              const int blocks = one ? 1 : 2;
+              mbar_arrive_expect_tx(bar(B_Q), blocks * C::kHalves * tokens * a.group * 128);
+              for (int i = 0; i < blocks; ++i)
+                for (int h = 0; h < C::kHalves; ++h)
+                  tma_load_3d(sbase + C::kOffQ + i * C::kQBytes + h * 128 * 128, &tm_q, 64 * h, g * a.group,
+                              q0 + tok0 + i * tokens, bar(B_Q));
+            }
+            ++with_tiles;
           }
           if (t >= lag) {
-            const int tv = t - lag, sl = tv % C::kVSlots;
-            if (tv >= C::kVSlots && !wait_inline(bar(B_VEMPTY + sl), ((tv / C::kVSlots) - 1) & 1, wc, W_T_PROD)) {
+            const int sl = vdone % C::kVSlots;
+            if (vdone >= C::kVSlots && !wait_for(bar(B_VEMPTY + sl), ((vdone / C::kVSlots) - 1) & 1, limit)) {
               ok = false;
               break;
             }
             load(C::kOffV, B_VFULL, sl, &tm_v, one ? kpage[2] : kpage[1], one ? krow[2] : krow[1]);
-            vdone = tv + 1;
+            ++vdone;
           }
           kpage[2] = kpage[1];
           krow[2] = krow[1];
@@ -611,10 +612,13 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           krow[0] = row_n;
           have = have_n;
         }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(B_NEXT));             // the next job may be looked for
         // the ragged end lies in the last tile: clear V's rows past it
-        if (!kF8 && ok && tail >= 0) {
-          const int sl = tail % C::kVSlots;
-          if (wait_inline(bar(B_VFULL + sl), (tail / C::kVSlots) & 1, wc, W_T_FIX)) {
+        if (!kF8 && tail >= 0) {
+          const int sl = (vdone - 1) % C::kVSlots;
+          ok = wait_for(bar(B_VFULL + sl), ((vdone - 1) / C::kVSlots) & 1, limit);
+          if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
             for (int p = (kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
               *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
@@ -625,30 +629,128 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             if (lane == 0) mbar_arrive(bar(B_VFIX));
           }
         }
-        // nothing that was started may still be writing shared memory when the CTA ends
-        __syncwarp();
-        if (lane == 0) {
-          bool done = wait_drain(bar(B_Q), 0, a.drain_limit_ns);
-          for (int k = max(0, kdone - C::kKSlots); k < kdone; ++k)
-            done = wait_drain(bar(B_KFULL + k % C::kKSlots), (k / C::kKSlots) & 1, a.drain_limit_ns) && done;
-          for (int k = max(0, vdone - C::kVSlots); k < vdone; ++k)
-            done = wait_drain(bar(B_VFULL + k % C::kVSlots), (k / C::kVSlots) & 1, a.drain_limit_ns) && done;
-          if (!done) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
-        }
       }
+      if (!ok) give_up(a, misc + M_ABORT, W_T_LOAD);
+      // nothing that was started may still be writing shared memory when the CTA ends
+      __syncwarp();
+      if (lane == 0) {
+        bool done = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
+        for (int k = max(0, kdone - C::kKSlots); k < kdone; ++k)
+          done = wait_drain(bar(B_KFULL + k % C::kKSlots), (k / C::kKSlots) & 1, a.drain_limit_ns) && done;
+        for (int k = max(0, vdone - C::kVSlots); k < vdone; ++k)
+          done = wait_drain(bar(B_VFULL + k % C::kVSlots), (k / C::kVSlots) & 1, a.drain_limit_ns) && done;
+        if (!done) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+      }
+    } else if (warp == 11) {
+      // ======================================================== scheduler ===
+      // Describes this CTA's own job, then, each time the loads of one have all been started, takes over a CTA that
+      // was not launched yet, and describes its job while the products of the last tiles run.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      AttnJobs jobs;
+      jobs.init(a, 2 * tokens, kTileThirds, lane);
+      int idx = blockIdx.x, asked = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int k = 0; ok; ++k) {
+        AttnJob job = {-1, 0, 0, 0, 1, 0};
+        while (idx >= 0) {
+          job = jobs.find(a, idx, lane);
+          if (job.b >= 0) break;
+          // (an index past the batch's jobs; the grid is sized by a bound)
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(B_CLC), 16);
+            try_cancel_cta(sbase + C::kOffMisc + 4 * M_CLC, bar(B_CLC));
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, wait_drain(bar(B_CLC), asked & 1, a.drain_limit_ns));
+          ++asked;
+          idx = ok ? canceled_cta(sbase + C::kOffMisc + 4 * M_CLC) : -1;
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ok = ok && (k < 2 || wait_for(bar(B_READ0 + (k & 1)), ((k >> 1) - 1) & 1, limit));
+        if (!ok) break;
+        if (lane == 0) {
+          volatile int* w = misc + M_JOBS + (k & 1) * kJobWords;
+          w[J_B] = job.b;
+          if (job.b >= 0) {
+            const AttnSeq seq = attn_seq(a, job.b);
+            const int tok0 = job.j * 2 * tokens;
+            const int tiles_all = (seq.kv + kTile - 1) / kTile;
+            const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
+            const int tile0 = job.s * base_t + min(job.s, rem_t);
+            const int nt = base_t + (job.s < rem_t ? 1 : 0);
+            // key tiles of row block i: up to the position of its last token
+            auto tiles_of = [&](int i) {
+              const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
+              if (last < tok0 + i * tokens) return 0;
+              const int keys = seq.kv - seq.sq + last + 1;
+              return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
+            };
+            const bool one = tok0 + tokens >= seq.sq;
+            const int n0 = tiles_of(0), n1 = tiles_of(1);    // n1 >= n0 where there is a second block
+            const int tiles = one ? n0 : n1;
+            w[J_G] = job.g;
+            w[J_SPLIT] = job.s;
+            w[J_S] = job.S;
+            w[J_SLOT] = job.slot;
+            w[J_Q0] = seq.q0;
+            w[J_SQ] = seq.sq;
+            w[J_K0] = seq.k0;
+            w[J_KV] = seq.kv;
+            w[J_TOK0] = tok0;
+            w[J_TILE0] = tile0;
+            w[J_TILES] = tiles;
+            w[J_ONE] = one;
+            w[J_CNT0] = one ? (tiles + 1) >> 1 : n0;
+            w[J_CNT1] = one ? tiles >> 1 : n1;
+            w[J_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
+          }
+          mbar_arrive(bar(B_JOB0 + (k & 1)));
+        }
+        __syncwarp();
+        if (job.b < 0) break;
+        ok = wait_for(bar(B_NEXT), k & 1, limit);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_CLC), 16);
+          try_cancel_cta(sbase + C::kOffMisc + 4 * M_CLC, bar(B_CLC));
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_drain(bar(B_CLC), asked & 1, a.drain_limit_ns));
+        ++asked;
+        idx = ok ? canceled_cta(sbase + C::kOffMisc + 4 * M_CLC) : -1;
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!ok) give_up(a, misc + M_ABORT, W_T_SCHED);
     } else if (kF8 && warp >= 12) {
       // ================================================== V e4m3 -> f16 ===
       const int key = threadIdx.x - 32 * 12;               // this thread's row of every tile
-      const int kv = misc[M_KV], tile0 = misc[M_TILE0], tiles = misc[M_TILES];
       const int r8 = key & 7;
+      int tile_base = 0;
+      bool ok = true;
 #pragma unroll 1
-      for (int t = 0; t < tiles; ++t) {
+      for (int job = 0; ok; ++job) {
+      volatile int* jw;
+      ok = job_at(job, jw);
+      if (!ok || jw[J_B] < 0) break;
+      const int kv = jw[J_KV], tile0 = jw[J_TILE0], tiles = jw[J_TILES];
+      job_read(job);
+#pragma unroll 1
+      for (int tl = 0; tl < tiles; ++tl) {
+        const int t = tile_base + tl;
         const int sl = t % C::kVSlots;
-        if (!wait_inline(bar(B_VFULL + sl), (t / C::kVSlots) & 1, wc, W_T_CVT)) break;
-        if (t >= 2 && !wait_inline(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, wc, W_T_CVT)) break;
+        ok = wait_for(bar(B_VFULL + sl), (t / C::kVSlots) & 1, limit) &&
+             (t < 2 || wait_for(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, limit));
+        if (!ok) break;
         const uint8_t* src = smem + C::kOffV + sl * C::kItemBytes + key * 128;
         uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
-        const bool in = (tile0 + t) * kTile + key < kv;
+        const bool in = (tile0 + tl) * kTile + key < kv;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {               // 64 dims
           uint4 w[4];
@@ -678,6 +780,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           mbar_arrive(bar(B_VEMPTY + sl));
         }
       }
+      tile_base += tiles;
+      }
+      if (!ok) give_up(a, misc + M_ABORT, W_T_CONVERT);
     }
   }
 

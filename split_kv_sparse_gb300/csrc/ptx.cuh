@@ -18,6 +18,13 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// Its low word (wraps after 4.29 s).
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
+
 // ---------------------------------------------------------------- mbarrier --
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
@@ -159,6 +166,36 @@ __device__ __forceinline__ void grid_launch_dependents() {
 // (returns at once when the kernel was not launched as a dependent).
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------- taking over pending CTAs --
+
+// Asks for a CTA of this grid that has not been launched: its answer (16 bytes) lands
+// at `dst`, completion counted on `bar` in bytes. Not to be called again once an
+// answer was negative.
+__device__ __forceinline__ void try_cancel_cta(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst), "r"(bar)
+      : "memory");
+}
+// The blockIdx.x that an answer grants, or -1.
+__device__ __forceinline__ int canceled_cta(uint32_t answer) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  .reg .b128 h;\n"
+      "  .reg .b32 y, z, w;\n"
+      "  ld.shared.b128 h, [%2];\n"
+      "  clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n"
+      "  selp.u32 %0, 1, 0, p;\n"
+      "  mov.u32 %1, 0;\n"
+      "  @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n"
+      "}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return ok ? static_cast<int>(x) : -1;
 }
 
 // ---------------------------------------------------------------------- TMA --
