@@ -97,6 +97,25 @@ int encode_kv(CUtensorMap* m, int dtype, const void* base, int64_t rows, int64_t
              : MLA_ERR_CUDA;
 }
 
+// bf16 K or V pages as {64 dims, 8 rows, column blocks, row groups, pages}: a box takes both 64-dim column blocks of
+// its rows, so a page of 16 rows is one copy of 4 KB. `wide` as in AttnArgs.
+int encode_kv_wide(CUtensorMap* m, const kv_pages_t* p, const void* base, int wide, int box_rows) {
+  auto enc = skv::tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t heads = static_cast<cuuint64_t>(p->h_kv), groups = static_cast<cuuint64_t>(p->page_size / 8);
+  const cuuint64_t dims[5] = {64, 8, wide == 1 ? 2 * heads : 2, wide == 1 ? groups : groups * heads,
+                              static_cast<cuuint64_t>(p->num_pages)};
+  const cuuint64_t row = static_cast<cuuint64_t>(p->row_stride) * 2;
+  const cuuint64_t strides[4] = {row, 128, 8 * row, static_cast<cuuint64_t>(p->page_stride) * 2};
+  const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(box_rows / 8), 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
 // The most (sequence, query tile) pairs of `tokens` tokens that total_q rows of `batch` sequences can make.
 int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / tokens + std::min(total_q, batch); }
 
@@ -316,13 +335,19 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.drain_limit_ns = skv::drain_limit_ns();
   CUtensorMap tq, tk, tv;
   const int box = rows16 ? skv::attn_row_box(plan->dtype, pages->page_size) : std::min(pages->page_size, 128);
-  if ((!rows16 &&
-       (st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK) ||
-      (st = encode_kv(&tk, plan->dtype, pages->k, pages->page_size, pages->row_stride, pages->num_pages,
-                      pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK ||
-      (st = encode_kv(&tv, plan->dtype, pages->v, pages->page_size, pages->row_stride, pages->num_pages,
-                      pages->page_stride, pages->h_kv, pages->head_stride, box)) != MLA_OK)
+  if (!rows16 && plan->dtype == SDPA_BF16) {
+    // (with one head its stride says nothing)
+    if (pages->h_kv == 1 || pages->head_stride == kDim) a.kv_wide = 1;
+    else if (pages->head_stride == pages->page_size * pages->row_stride) a.kv_wide = 2;
+  }
+  auto encode = [&](CUtensorMap* m, const void* base) {
+    if (a.kv_wide) return encode_kv_wide(m, pages, base, a.kv_wide, box);
+    return encode_kv(m, plan->dtype, base, pages->page_size, pages->row_stride, pages->num_pages, pages->page_stride,
+                     pages->h_kv, pages->head_stride, box);
+  };
+  if (!rows16 && (st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK)
     return st;
+  if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
   const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms, split_waves(rows16));
   st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)

@@ -401,7 +401,13 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
       const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
       const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
-      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), kTile * 128, 1024));
+      // K and V tiles: the 64-dim column blocks one after the other (8-row atoms 1024 bytes apart), or with kv_wide
+      // beside one another (atoms 2048 bytes apart, the second block 1024 bytes on)
+      const bool wide = !kF8 && a.kv_wide != 0;
+      const uint32_t block = wide ? 1024 : kTile * 128;
+      const uint32_t kv_hi = wide ? static_cast<uint32_t>(sdesc_sw128(sbase, 16, 2048) >> 32) : hi;
+      const uint32_t v_step = (wide ? 4096 : 2048) >> 4;   // 16 keys
+      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), block, 1024));
       bool ok = true;
       int tile_base = 0;     // tiles of earlier jobs
       int n = 0;             // this warp's products so far
@@ -443,12 +449,12 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                   mma_f8_wc<1>(d, qa + 4, kb + 4, hi, kIdescQK);
                   mma_f8_wc<1>(d, qa + 6, kb + 6, hi, kIdescQK);
                 } else {
-                  mma_f16_wc<0>(d, qa, kb, hi, kIdescQK);
+                  const uint32_t kb2 = kb + (block >> 4);   // 64 dims a column block, 16 an MMA
+                  mma_f16_wc2<0>(d, qa, hi, kb, kv_hi, kIdescQK);
 #pragma unroll
-                  for (int k = 1; k < 8; ++k) {
-                    const uint32_t off = (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2;   // 64 dims a column block, 16 an MMA
-                    mma_f16_wc<1>(d, qa + off, kb + off, hi, kIdescQK);
-                  }
+                  for (int k = 1; k < 8; ++k)
+                    mma_f16_wc2<1>(d, qa + (k >> 2) * (128 * 128 >> 4) + (k & 3) * 2, hi, (k < 4 ? kb : kb2) + (k & 3) * 2, kv_hi,
+                                   kIdescQK);
                 }
                 mbar_arrive(bar(B_TURN_PV));
                 mma_commit(bar(B_S0 + i));
@@ -483,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 const uint32_t pa = tmem + kTmemP + 64 * i, d = tmem + kTmemO + 128 * i;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
-                  mma_f16_ts(d, pa + 8 * k, vb + k * (2048 >> 4), hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
+                  mma_f16_ts(d, pa + 8 * k, vb + k * v_step, kv_hi, kIdescPV, k > 0 ? 1u : (u > 0 ? 1u : 0u));
                 mbar_arrive(bar(B_TURN_QK));
                 mma_commit(bar(B_O0 + i));
                 if (one || i == 1) {
@@ -554,9 +560,15 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), C::kItemBytes);
           __syncwarp();
           if (lane < boxes) {
-            const uint32_t dst = sbase + base_off + slot * C::kItemBytes + lane * page_rows * 128;
-            for (int h = 0; h < C::kHalves; ++h)
-              tma_load_4d(dst + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + slot));
+            const uint32_t dst = sbase + base_off + slot * C::kItemBytes;
+            if (!kF8 && a.kv_wide != 0) {
+              const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
+              tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
+                          bar(full + slot));
+            } else {
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + slot));
+            }
           }
         };
         // K runs ahead of V by as many tiles as the products do: K(0) .. K(lag - 1), then K(t), V(t - lag) in turn
@@ -620,9 +632,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           ok = wait_for(bar(B_VFULL + sl), ((vdone - 1) / C::kVSlots) & 1, limit);
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
+            const bool wide = a.kv_wide != 0;
             for (int p = (kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
-              *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
-              *reinterpret_cast<uint4*>(v + kTile * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+              uint8_t* at = v + (wide ? (p >> 6) * 2048 + (p & 63) * 16 : p * 16);   // 64 pieces an 8-row atom
+              *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(at + (wide ? 1024 : kTile * 128)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
             __syncwarp();

@@ -161,6 +161,8 @@ struct AttnArgs {
   const float* descale_q;       // device scalars or null
   const float* descale_k;
   const float* descale_v;
+  int kv_wide;                  // tile kernel, bf16 pages: tm_k / tm_v take both 64-dim column blocks of a row in one box
+                                // (1: heads beside one another in a row, 2: pages of one head after the other)
   int batch, h_q, h_kv, group, total_q;
   int total_kv;                 // packed
   float scale_log2;
@@ -187,7 +189,8 @@ constexpr int kRowRows = 16;
 constexpr int kTileSplitWaves = 3;
 constexpr int kRowSplitWaves = 1;
 // tm_q: Q as 3-D [total_q][h_q][128], box {128 bytes, group heads, 128 / group tokens}; tm_k / tm_v: K and V as 4-D
-// {128, rows, pages, heads} (packed: one page of total_kv rows), box {128 bytes, min(page, 128) rows, 1, 1}.
+// {128, rows, pages, heads} (packed: one page of total_kv rows), box {128 bytes, min(page, 128) rows, 1, 1}; with
+// kv_wide as 5-D {64, 8 rows, column blocks, row groups, pages}, box {64, 8, 2, min(page, 128) / 8, 1}.
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
 // Box of tm_k / tm_v: {128 bytes, attn_row_box(dtype, page size) rows, 1, 1}.

@@ -239,6 +239,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int x
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* map, int x, int y, int z, int w, int v,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cta.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(bar)
+      : "memory");
+}
+
 // Bulk shared -> global copy (async proxy), bytes a multiple of 16, both addresses
 // 16-byte aligned; tracked by the issuing thread's bulk groups.
 __device__ __forceinline__ void bulk_store(void* gdst, uint32_t ssrc, uint32_t bytes) {
@@ -367,6 +376,23 @@ __device__ __forceinline__ void mma_f16_w(uint32_t d_tmem, uint32_t a_lo, uint32
       "  tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n"
       "}\n" ::"r"(d_tmem),
       "r"(a_lo), "r"(b_lo), "r"(ab_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same with a high word for each operand (atom strides that differ).
+template <int kAccumulate>
+__device__ __forceinline__ void mma_f16_wc2(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                            uint32_t idesc) {
+  asm volatile(
+      "{\n"
+      "  .reg .pred p;\n"
+      "  .reg .b64 da, db;\n"
+      "  setp.ne.b32 p, %6, 0;\n"
+      "  mov.b64 da, {%1, %2};\n"
+      "  mov.b64 db, {%3, %4};\n"
+      "  tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n"
+      "}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(kAccumulate)
       : "memory");
 }
 

@@ -289,6 +289,33 @@ def test_head_major_pages_and_no_lse(sq):
         go(dtype, sq, [150, 300], 8, 2, 32, lse=False, amax=False)
 
 
+@pytest.mark.parametrize("sq", [[1, 1], [30, 200]])
+@pytest.mark.parametrize("page", [16, 128])
+def test_page_strides(sq, page):
+    """Caches of one head, head-major pages, and pages inside a wider allocation (heads, rows and pages apart)."""
+    for dtype in ("bf16", "e4m3"):
+        go(dtype, sq, [150, 300], 4, 1, page, seed=page)
+        go(dtype, sq, [150, 300], 8, 2, page, seed=page, layout="head")
+        c, q, dq, cu = paged_case(dtype, sq, [150, 300], 8, 2, page, seed=page)
+        ref = c.reference(q, dq, cu, 1 / math.sqrt(D))
+        for x in ("k", "v"):
+            t = getattr(c, x)
+            wide = torch.empty((t.shape[0], page + 3, 2, 256), dtype=t.dtype)
+            garbage(wide)
+            wide[:, :page, :, :D] = t
+            setattr(c, x, wide)
+
+        class View:     # keeps the strides on the device
+            def __init__(self, x):
+                self.x, self.shape = x, (x.shape[0], page, 2, D)
+
+            def to(self, dev):
+                return self.x.to(dev)[:, :page, :, :D]
+
+        c.k, c.v = View(c.k), View(c.v)
+        check(*run_paged(c, q, dq, cu, 8), ref, dtype)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 @pytest.mark.parametrize("sq", [[1, 1], [30, 200]])
 def test_scales(scale, sq):
