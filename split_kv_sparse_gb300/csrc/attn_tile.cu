@@ -12,8 +12,9 @@
 //                   row (a TMEM lane), so no reduction crosses threads.
 //   warps 8, 10     tcgen05 issue, in turn: S = Q_i K^T; O_i += P_i V with P_i read from
 //                   tensor memory.
-//   warp 9          TMA: Q once, then K and V tiles into two rings of slots, page by page; bf16:
-//                   clears the V rows past the sequence's end (0 * NaN would reach a result).
+//   warps 9, 11     TMA: Q and the K tiles, the V tiles, each into a ring of slots, page by page;
+//                   warp 11 also looks for the CTA's jobs and (bf16) clears the V rows past
+//                   a sequence's end (0 * NaN would reach a result).
 //   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0.
 // TMEM: S (128 columns, one buffer for both streams: a stream's scores leave it for
 // registers as soon as they are there), P_0, P_1 (64 each), O_0, O_1 (128 each).
@@ -50,18 +51,18 @@ struct Cfg {
   static constexpr int kOffStats = kOffMisc + 384;       // float2 [128 rows]: m, l of stream 1
   static constexpr int kSmem = kOffStats + 1024 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static constexpr int kConsumers = kF8 ? 15 : 11;       // warps that read a job's description
+  static constexpr int kConsumers = kF8 ? 16 : 12;       // warps that read a job's description
 };
 
 enum {
   B_Q = 0, B_QFREE0, B_QFREE1, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VFIX, B_END, B_DRAIN,
-  B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_NEXT, B_CLC, B_STAT,
+  B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_CLC, B_STAT,
   B_OREAD, B_KFULL,
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
 static_assert(kNumBars * 8 <= 352, "barrier area");
 
-enum : uint32_t { W_T_SOFTMAX = 201, W_T_MMA, W_T_LOAD, W_T_SCHED, W_T_CONVERT, W_T_DRAIN };   // whose wait ran out
+enum : uint32_t { W_T_SOFTMAX = 201, W_T_MMA, W_T_LOAD, W_T_CONVERT, W_T_DRAIN };   // whose wait ran out
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0, kTmemP = 128, kTmemO = 256;   // S; P_0, P_1 (64 each); O_0, O_1 (128 each)
@@ -514,32 +515,101 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         __syncwarp();
         if (!wait_drain(bar(drain), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
       }
-    } else if (warp == 9) {
-      // ===================================================== TMA producer ===
+    } else if (warp == 9 || warp == 11) {
+      // ============================================ loads (K and Q; V) and jobs ===
+      // Warp 9 loads Q and the K tiles, warp 11 the V tiles: with pages of 16 rows a tile is eight boxes, and one warp's
+      // issue of K and V would bound the kernel. Warp 11 also describes the jobs: this CTA's own, then, each time the
+      // loads of one have all been started, that of a CTA that was not launched yet and that it takes over.
+      const bool is_k = warp == 9;
       const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
-      const int boxes = kTile / page_rows;                 // of one tile and column block
+      const int boxes = kTile / page_rows;                 // of one tile (and column block)
       bool ok = true;
-      int kdone = 0, vdone = 0;                            // tiles whose loads were started
+      int done = 0;                                        // tiles whose loads were started
       int with_tiles = 0;
+      AttnJobs jobs;
+      int idx = blockIdx.x, asked = 0;
+      auto take_over = [&]() {                             // the index of a CTA that was pending, or -1
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_CLC), 16);
+          try_cancel_cta(sbase + C::kOffMisc + 4 * M_CLC, bar(B_CLC));
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_drain(bar(B_CLC), asked & 1, a.drain_limit_ns));
+        ++asked;
+        const int x = ok ? canceled_cta(sbase + C::kOffMisc + 4 * M_CLC) : -1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        return x;
+      };
+      if (!is_k) {
+        if (lane == 0) {
+          tma_prefetch_desc(&tm_q);
+          tma_prefetch_desc(&tm_k);
+          tma_prefetch_desc(&tm_v);
+        }
+        jobs.init(a, 2 * tokens, kTileThirds, lane);
+      }
 #pragma unroll 1
       for (int job = 0; ok; ++job) {
         volatile int* w;
-        ok = job_at(job, w);
+        if (is_k) {
+          ok = job_at(job, w);
+        } else {
+          // ---- the next job
+          AttnJob next = {-1, 0, 0, 0, 1, 0};
+          if (job > 0) idx = take_over();
+          while (ok && idx >= 0) {
+            next = jobs.find(a, idx, lane);
+            if (next.b >= 0) break;
+            idx = take_over();   // (an index past the batch's jobs; the grid is sized by a bound)
+          }
+          w = misc + M_JOBS + (job & 1) * kJobWords;
+          ok = ok && (job < 2 || wait_for(bar(B_READ0 + (job & 1)), ((job >> 1) - 1) & 1, limit));
+          if (!ok) break;
+          if (lane == 0) {
+            w[J_B] = next.b;
+            if (next.b >= 0) {
+              const AttnSeq seq = attn_seq(a, next.b);
+              const int tok0 = next.j * 2 * tokens;
+              const int tiles_all = (seq.kv + kTile - 1) / kTile;
+              const int base_t = tiles_all / next.S, rem_t = tiles_all - base_t * next.S;
+              const int tile0 = next.s * base_t + min(next.s, rem_t);
+              const int nt = base_t + (next.s < rem_t ? 1 : 0);
+              // key tiles of row block i: up to the position of its last token
+              auto tiles_of = [&](int i) {
+                const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
+                if (last < tok0 + i * tokens) return 0;
+                const int keys = seq.kv - seq.sq + last + 1;
+                return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
+              };
+              const bool one = tok0 + tokens >= seq.sq;
+              const int n0 = tiles_of(0), n1 = tiles_of(1);  // n1 >= n0 where there is a second block
+              const int tiles = one ? n0 : n1;
+              w[J_G] = next.g;
+              w[J_SPLIT] = next.s;
+              w[J_S] = next.S;
+              w[J_SLOT] = next.slot;
+              w[J_Q0] = seq.q0;
+              w[J_SQ] = seq.sq;
+              w[J_K0] = seq.k0;
+              w[J_KV] = seq.kv;
+              w[J_TOK0] = tok0;
+              w[J_TILE0] = tile0;
+              w[J_TILES] = tiles;
+              w[J_ONE] = one;
+              w[J_CNT0] = one ? (tiles + 1) >> 1 : n0;
+              w[J_CNT1] = one ? tiles >> 1 : n1;
+              w[J_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
+            }
+            mbar_arrive(bar(B_JOB0 + (job & 1)));
+          }
+          __syncwarp();
+        }
         if (!ok || w[J_B] < 0) break;
         const int job_b = w[J_B], g = w[J_G], q0 = w[J_Q0], k0 = w[J_K0], kv = w[J_KV], tok0 = w[J_TOK0], tile0 = w[J_TILE0],
                   tiles = w[J_TILES], tail = w[J_TAIL];
         const bool one = w[J_ONE] != 0;
         job_read(job);
-        // Q's place once the rows of the job before (which go through it, tiles or not) have left it
-        auto q_free = [&]() {
-          return job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) &&
-                              wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
-        };
-        if (tiles == 0) {
-          if (lane == 0) mbar_arrive(bar(B_NEXT));
-          ok = q_free();
-          continue;
-        }
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
           const int key = (tile0 + t) * kTile + lane * page_rows;
@@ -556,47 +626,48 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
           return page != a.num_pages;
         };
-        auto load = [&](int base_off, int full, int slot, const CUtensorMap* tm, int page, int row) {
-          if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), C::kItemBytes);
-          __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = sbase + base_off + slot * C::kItemBytes;
-            if (!kF8 && a.kv_wide != 0) {
-              const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
-              tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
-                          bar(full + slot));
-            } else {
-              for (int h = 0; h < C::kHalves; ++h)
-                tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + slot));
-            }
-          }
-        };
-        // K runs ahead of V by as many tiles as the products do: K(0) .. K(lag - 1), then K(t), V(t - lag) in turn
-        const int lag = one ? 2 : 1;
-        int kpage[3], krow[3];                               // the pages of K(t), K(t - 1), K(t - 2)
-        bool have = lookup(0, kpage[0], krow[0]);
+        int page = 0, row = 0;
+        bool have = tiles > 0 && lookup(0, page, row);
+        const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL, empty = is_k ? B_KEMPTY : B_VEMPTY;
+        const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
 #pragma unroll 1
-        for (int t = 0; t < tiles + lag; ++t) {
+        for (int t = 0; t < tiles; ++t, ++done) {
           int page_n = 0, row_n = 0;
           bool have_n = false;
           if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
-          if (t < tiles) {
-            const int sl = kdone % C::kKSlots;
-            if (kdone >= C::kKSlots && !wait_for(bar(B_KEMPTY + sl), ((kdone / C::kKSlots) - 1) & 1, limit)) {
-              ok = false;
-              break;
-            }
+          const int sl = done % slots;
+          if (done >= slots && !wait_for(bar(empty + sl), ((done / slots) - 1) & 1, limit)) {
+            ok = false;
+            break;
+          }
+          if (is_k) {
             // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
             const unsigned got = __ballot_sync(0xffffffffu, have);
             unsigned groups = 0;
             for (int i = 0; i < 8; ++i)
               if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
-            if (lane == 0) misc[M_MASK + (kdone & (kMaskRing - 1))] = static_cast<int>(groups);
-            load(C::kOffK, B_KFULL, sl, &tm_k, kpage[0], krow[0]);
-            ++kdone;
+            if (lane == 0) misc[M_MASK + (done & (kMaskRing - 1))] = static_cast<int>(groups);
           }
-          if (t == 0) {
-            if (!(ok = q_free())) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full + sl), C::kItemBytes);
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
+            if (!kF8 && a.kv_wide != 0) {
+              const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
+              tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
+                          bar(full + sl));
+            } else {
+              for (int h = 0; h < C::kHalves; ++h)
+                tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + sl));
+            }
+          }
+          page = page_n;
+          row = row_n;
+          have = have_n;
+          if (is_k && t == 0) {
+            // Q once the rows of the job before (which go through it, tiles or not) have left its place
+            ok = job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
+            if (!ok) break;
             if (lane == 0) {
               const int blocks = one ? 1 : 2;
               mbar_arrive_expect_tx(bar(B_Q), blocks * C::kHalves * tokens * a.group * 128);
@@ -607,29 +678,14 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             }
             ++with_tiles;
           }
-          if (t >= lag) {
-            const int sl = vdone % C::kVSlots;
-            if (vdone >= C::kVSlots && !wait_for(bar(B_VEMPTY + sl), ((vdone / C::kVSlots) - 1) & 1, limit)) {
-              ok = false;
-              break;
-            }
-            load(C::kOffV, B_VFULL, sl, &tm_v, one ? kpage[2] : kpage[1], one ? krow[2] : krow[1]);
-            ++vdone;
-          }
-          kpage[2] = kpage[1];
-          krow[2] = krow[1];
-          kpage[1] = kpage[0];
-          krow[1] = krow[0];
-          kpage[0] = page_n;
-          krow[0] = row_n;
-          have = have_n;
         }
         if (!ok) break;
-        if (lane == 0) mbar_arrive(bar(B_NEXT));             // the next job may be looked for
+        if (is_k && tiles == 0)
+          ok = job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
         // the ragged end lies in the last tile: clear V's rows past it
-        if (!kF8 && tail >= 0) {
-          const int sl = (vdone - 1) % C::kVSlots;
-          ok = wait_for(bar(B_VFULL + sl), ((vdone - 1) / C::kVSlots) & 1, limit);
+        if (!kF8 && !is_k && tail >= 0) {
+          const int sl = (done - 1) % C::kVSlots;
+          ok = wait_for(bar(B_VFULL + sl), ((done - 1) / C::kVSlots) & 1, limit);
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
             const bool wide = a.kv_wide != 0;
@@ -648,100 +704,12 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       // nothing that was started may still be writing shared memory when the CTA ends
       __syncwarp();
       if (lane == 0) {
-        bool done = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
-        for (int k = max(0, kdone - C::kKSlots); k < kdone; ++k)
-          done = wait_drain(bar(B_KFULL + k % C::kKSlots), (k / C::kKSlots) & 1, a.drain_limit_ns) && done;
-        for (int k = max(0, vdone - C::kVSlots); k < vdone; ++k)
-          done = wait_drain(bar(B_VFULL + k % C::kVSlots), (k / C::kVSlots) & 1, a.drain_limit_ns) && done;
-        if (!done) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+        const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL;
+        bool landed = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
+        for (int k = max(0, done - slots); k < done; ++k)
+          landed = wait_drain(bar(full + k % slots), (k / slots) & 1, a.drain_limit_ns) && landed;
+        if (!landed) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
       }
-    } else if (warp == 11) {
-      // ======================================================== scheduler ===
-      // Describes this CTA's own job, then, each time the loads of one have all been started, takes over a CTA that
-      // was not launched yet, and describes its job while the products of the last tiles run.
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-      }
-      AttnJobs jobs;
-      jobs.init(a, 2 * tokens, kTileThirds, lane);
-      int idx = blockIdx.x, asked = 0;
-      bool ok = true;
-#pragma unroll 1
-      for (int k = 0; ok; ++k) {
-        AttnJob job = {-1, 0, 0, 0, 1, 0};
-        while (idx >= 0) {
-          job = jobs.find(a, idx, lane);
-          if (job.b >= 0) break;
-          // (an index past the batch's jobs; the grid is sized by a bound)
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(B_CLC), 16);
-            try_cancel_cta(sbase + C::kOffMisc + 4 * M_CLC, bar(B_CLC));
-          }
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, wait_drain(bar(B_CLC), asked & 1, a.drain_limit_ns));
-          ++asked;
-          idx = ok ? canceled_cta(sbase + C::kOffMisc + 4 * M_CLC) : -1;
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        ok = ok && (k < 2 || wait_for(bar(B_READ0 + (k & 1)), ((k >> 1) - 1) & 1, limit));
-        if (!ok) break;
-        if (lane == 0) {
-          volatile int* w = misc + M_JOBS + (k & 1) * kJobWords;
-          w[J_B] = job.b;
-          if (job.b >= 0) {
-            const AttnSeq seq = attn_seq(a, job.b);
-            const int tok0 = job.j * 2 * tokens;
-            const int tiles_all = (seq.kv + kTile - 1) / kTile;
-            const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
-            const int tile0 = job.s * base_t + min(job.s, rem_t);
-            const int nt = base_t + (job.s < rem_t ? 1 : 0);
-            // key tiles of row block i: up to the position of its last token
-            auto tiles_of = [&](int i) {
-              const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
-              if (last < tok0 + i * tokens) return 0;
-              const int keys = seq.kv - seq.sq + last + 1;
-              return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
-            };
-            const bool one = tok0 + tokens >= seq.sq;
-            const int n0 = tiles_of(0), n1 = tiles_of(1);    // n1 >= n0 where there is a second block
-            const int tiles = one ? n0 : n1;
-            w[J_G] = job.g;
-            w[J_SPLIT] = job.s;
-            w[J_S] = job.S;
-            w[J_SLOT] = job.slot;
-            w[J_Q0] = seq.q0;
-            w[J_SQ] = seq.sq;
-            w[J_K0] = seq.k0;
-            w[J_KV] = seq.kv;
-            w[J_TOK0] = tok0;
-            w[J_TILE0] = tile0;
-            w[J_TILES] = tiles;
-            w[J_ONE] = one;
-            w[J_CNT0] = one ? (tiles + 1) >> 1 : n0;
-            w[J_CNT1] = one ? tiles >> 1 : n1;
-            w[J_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
-          }
-          mbar_arrive(bar(B_JOB0 + (k & 1)));
-        }
-        __syncwarp();
-        if (job.b < 0) break;
-        ok = wait_for(bar(B_NEXT), k & 1, limit);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(B_CLC), 16);
-          try_cancel_cta(sbase + C::kOffMisc + 4 * M_CLC, bar(B_CLC));
-        }
-        __syncwarp();
-        ok = __all_sync(0xffffffffu, wait_drain(bar(B_CLC), asked & 1, a.drain_limit_ns));
-        ++asked;
-        idx = ok ? canceled_cta(sbase + C::kOffMisc + 4 * M_CLC) : -1;
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (!ok) give_up(a, misc + M_ABORT, W_T_SCHED);
     } else if (kF8 && warp >= 12) {
       // ================================================== V e4m3 -> f16 ===
       const int key = threadIdx.x - 32 * 12;               // this thread's row of every tile
