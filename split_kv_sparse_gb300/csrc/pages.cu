@@ -19,6 +19,7 @@ namespace {
 // few pages, so it is latency, not bandwidth, that counts.
 
 constexpr int kMapThreads = 1024;
+constexpr int kMapRun = 8;
 // Rows whose slots the same CTA writes; more get a grid of their own behind it.
 constexpr int kMapFusedRows = 4096;
 
@@ -38,25 +39,30 @@ __device__ __forceinline__ int segment_of(const int* off, int n, int x) {
   return lo;
 }
 
-// Exclusive prefix sum of v over the CTA; *total = the sum. `part` holds one int a warp.
-__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+// Exclusive prefix sum of v over the CTA; *total = the sum. `part` holds a word a warp and
+// alternates between two places, so one barrier a call is enough.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T (*part)[kMapThreads / 32], int& turn, T* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  T x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const T y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) part[warp] = x;
+  T* p = part[turn];
+  turn ^= 1;
+  if (lane == 31) p[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    if (w < warp) before += part[w];
-    all += part[w];
+  T s = p[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  __syncthreads();   // part may be written again
-  *total = all;
-  return before + x - v;
+  *total = __shfl_sync(0xffffffffu, s, 31);
+  const T before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + x - v;
 }
 
 __device__ __forceinline__ void slot_of_row(const PagesMapArgs& a, const int32_t* cu, int r) {
@@ -79,55 +85,79 @@ __global__ void __launch_bounds__(kMapThreads, 1) pages_map_kernel(const PagesMa
   extern __shared__ int dyn[];
   int* freed = dyn;                   // [batch + 1] exclusive prefix sums
   int* wanted = dyn + a.batch + 1;    // [batch + 1]
-  __shared__ int part[kMapThreads / 32];
+  __shared__ uint64_t part[2][kMapThreads / 32];
+  int turn = 0;
   grid_dependency_wait();
   const int n0 = min(max(a.free_in[0], 0), a.capacity);
-  int carry_f = 0, carry_w = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
+  uint64_t carry = 0;                 // freed pages in the high word, wanted ones in the low
+  for (int b0 = 0; b0 < a.batch; b0 += kMapThreads) {
     const int b = b0 + threadIdx.x;
-    int f = 0, w = 0;
+    uint64_t v = 0;
     if (b < a.batch) {
       const int h = pages_of(a.held[b], a.page_size, a.width), p = pages_of(a.lens[b], a.page_size, a.width);
-      f = max(h - p, 0);
-      w = max(p - h, 0);
+      v = (static_cast<uint64_t>(max(h - p, 0)) << 32) | static_cast<uint64_t>(max(p - h, 0));
     }
-    int tf, tw;
-    const int xf = block_scan(f, part, &tf), xw = block_scan(w, part, &tw);
+    uint64_t total;
+    const uint64_t x = carry + block_scan(v, part, turn, &total);
     if (b < a.batch) {
-      freed[b] = carry_f + xf;
-      wanted[b] = carry_w + xw;
+      freed[b] = static_cast<int>(x >> 32);
+      wanted[b] = static_cast<int>(x & 0xffffffffu);
     }
-    carry_f += tf;
-    carry_w += tw;
+    carry += total;
   }
+  const int all_freed = static_cast<int>(carry >> 32), all_wanted = static_cast<int>(carry & 0xffffffffu);
   __syncthreads();
 
-  // push: the freed entries in order, without those that hold no page
+  // push: the freed entries in order, without those that hold no page; kMapRun consecutive ones a thread, all loads
+  // in flight at once
   int n = n0;
-  for (int i0 = 0; i0 < carry_f; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x;
-    int page = -1;
-    if (i < carry_f) {
-      const int b = segment_of(freed, a.batch, i);
-      page = a.table[static_cast<size_t>(b) * a.width + pages_of(a.lens[b], a.page_size, a.width) + (i - freed[b])];
+  for (int i0 = 0; i0 < all_freed; i0 += kMapThreads * kMapRun) {
+    const int first = i0 + threadIdx.x * kMapRun;
+    int page[kMapRun], held = 0;
+    int b = first < all_freed ? segment_of(freed, a.batch, first) : 0;
+#pragma unroll
+    for (int k = 0; k < kMapRun; ++k) {
+      const int i = first + k;
+      page[k] = -1;
+      if (i < all_freed) {
+        while (b + 1 < a.batch && freed[b + 1] <= i) ++b;
+        page[k] = a.table[static_cast<size_t>(b) * a.width + pages_of(a.lens[b], a.page_size, a.width) + (i - freed[b])];
+      }
     }
-    int t;
-    const int at = n + block_scan(page >= 0 ? 1 : 0, part, &t);
-    if (page >= 0 && at < a.capacity) a.free_pages[at] = page;
-    n += t;
+#pragma unroll
+    for (int k = 0; k < kMapRun; ++k) held += page[k] >= 0 ? 1 : 0;
+    uint64_t t;
+    int at = n + static_cast<int>(block_scan(static_cast<uint64_t>(held), part, turn, &t));
+#pragma unroll
+    for (int k = 0; k < kMapRun; ++k)
+      if (page[k] >= 0) {
+        if (at < a.capacity) a.free_pages[at] = page[k];
+        ++at;
+      }
+    n += static_cast<int>(t);
   }
   n = min(n, a.capacity);
   __syncthreads();   // the pushed pages are read below
 
   // pop
-  for (int j = threadIdx.x; j < carry_w; j += blockDim.x) {
-    const int b = segment_of(wanted, a.batch, j);
-    a.table[static_cast<size_t>(b) * a.width + pages_of(a.held[b], a.page_size, a.width) + (j - wanted[b])] =
-        j < n ? a.free_pages[n - 1 - j] : -1;
+  for (int j0 = threadIdx.x; j0 < all_wanted; j0 += kMapThreads * 4) {
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + k * kMapThreads;
+      page[k] = j < all_wanted && j < n ? a.free_pages[n - 1 - j] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = j0 + k * kMapThreads;
+      if (j >= all_wanted) break;
+      const int b = segment_of(wanted, a.batch, j);
+      a.table[static_cast<size_t>(b) * a.width + pages_of(a.held[b], a.page_size, a.width) + (j - wanted[b])] = page[k];
+    }
   }
   if (threadIdx.x == 0) {
-    a.free_out[0] = max(n - carry_w, 0);
-    a.free_out[1] = max(carry_w - n, 0);
+    a.free_out[0] = max(n - all_wanted, 0);
+    a.free_out[1] = max(all_wanted - n, 0);
   }
   if (a.total_q <= kMapFusedRows) {
     __syncthreads();   // the table entries written above
