@@ -32,6 +32,22 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return s;
 }
 
+// Brings the lengths and this CTA's share of the block table towards L2, by one warp,
+// before grid_dependency_wait: a prefetch returns nothing, so it may run ahead of the
+// kernel that writes them, and the first loads after the wait are L2 hits.
+__device__ __forceinline__ void attn_prefetch(const AttnArgs& a, int lane) {
+  for (int b = 32 * lane; b <= a.batch && b < 32 * 32; b += 32 * 32) {
+    prefetch_l2_line(a.cu_q + b);
+    if (b < a.batch) prefetch_l2_line(a.table != nullptr ? a.kv_lens + b : a.cu_kv + b);
+  }
+  if (a.table != nullptr) {
+    const int64_t lines = (static_cast<int64_t>(a.batch) * a.table_width + 31) / 32;
+    const int64_t each = (lines + gridDim.x - 1) / gridDim.x;
+    const int64_t first = each * blockIdx.x;
+    if (lane < each && each <= 32 && first + lane < lines) prefetch_l2_line(a.table + 32 * (first + lane));
+  }
+}
+
 __device__ __forceinline__ int warp_scan_incl(int v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -41,6 +57,14 @@ __device__ __forceinline__ int warp_scan_incl(int v, int lane) {
   return v;
 }
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// ceil(x / y) for 0 <= x < 2^23, 1 <= y < 2^24 (exact: the float quotient is off by one at most).
+__device__ __forceinline__ int ceil_div(int x, int y) {
+  int q = __float2int_rz(__fdividef(static_cast<float>(x), static_cast<float>(y)));
+  const int r = x - q * y;
+  q += r > y ? 2 : r > 0 ? 1 : r <= -y ? -1 : 0;
+  return q;
+}
 
 struct AttnJob {
   int b;      // sequence, -1: no job
@@ -81,32 +105,37 @@ struct AttnJobs {
     }
   }
   __device__ __forceinline__ int splits(const AttnArgs& a, int tiles) const {
-    return T == 0 ? a.num_splits : min(a.num_splits, max(1, (tiles + T - 1) / T));
+    return T == 0 ? a.num_splits : min(a.num_splits, max(1, ceil_div(tiles, T)));
   }
 
+  // kSplits: false where no job is ever split.
+  template <bool kSplits>
   __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int thirds, int lane) {
     tokens = job_tokens;
     groups = (a.batch + 31) / 32;
     T = 0;
     load(a, 0, lane, n_first, tiles_first);
-    if (!a.adaptive || a.num_splits <= 1) return;
+    if (!kSplits || !a.adaptive || a.num_splits <= 1) return;
+    // The sums are floats (exact to 2^-23), and the bounds below give way by more than that. (64-bit integers cost a
+    // microsecond at the start of every launch.)
     int jobs = 0, most = 1;
-    long long work = 0;
+    float work = 0.f;
     for (int i = 0; i < groups; ++i) {
       int n, tiles;
       shape(a, i, lane, n, tiles);
       jobs += warp_sum_int(n);
       most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? tiles : 0));
-      long long w = static_cast<long long>(n) * tiles;
+      float w = static_cast<float>(n) * static_cast<float>(tiles);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       work += w;
     }
-    work *= a.h_kv;
-    const long long unsplit = static_cast<long long>(jobs) * a.h_kv;
-    if (unsplit > a.num_sms) {
-      const long long t = (work * thirds + 3ll * a.num_sms - 1) / (3ll * a.num_sms);
-      T = static_cast<int>(min(max(t, 1ll), 1ll << 24));   // (above any sequence's tiles)
+    work *= static_cast<float>(a.h_kv);
+    const float unsplit = static_cast<float>(jobs) * static_cast<float>(a.h_kv);
+    const float wave = static_cast<float>(a.num_sms);
+    if (unsplit > wave) {
+      T = max(1, static_cast<int>(fminf(ceilf(work * static_cast<float>(thirds) / (3.f * wave)), 16777216.f)));   // (above any
+                                                                                             // sequence's tiles)
       for (;;) {
         int split_jobs = 0;
         for (int i = 0; i < groups; ++i) {
@@ -119,9 +148,10 @@ struct AttnJobs {
         T += (T + 3) >> 2;
       }
     }
-    // jobs(T) <= work / T + unsplit, so from work / (num_sms - unsplit) on they fit
-    int lo = max(static_cast<int>((work + a.num_sms - 1) / a.num_sms), 1);
-    int hi = unsplit < a.num_sms ? static_cast<int>(min(work / (a.num_sms - unsplit) + 1, static_cast<long long>(most))) : most;
+    // jobs(T) <= work / T + unsplit, so from work / (wave - unsplit) on they fit
+    int lo = max(1, static_cast<int>(work * 0.9999f / wave));
+    int hi = most;
+    if (unsplit < wave) hi = min(hi, static_cast<int>(fminf(work * 1.0001f / (wave - unsplit), 16777216.f)) + 2);
     hi = max(hi, lo);
     while (lo < hi) {
       T = (lo + hi) >> 1;

@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  if (warp == 1) attn_prefetch(a, lane);
   __syncthreads();
   grid_dependency_wait();
 
   const int tokens = kRowRows / a.group;
   AttnJobs jobs;                      // every warp for itself
-  jobs.init(a, tokens, kRowThirds, lane);
+  jobs.init<true>(a, tokens, kRowThirds, lane);
   const AttnJob job = jobs.find(a, blockIdx.x, lane);
   grid_launch_dependents();
   if (job.b < 0) return;

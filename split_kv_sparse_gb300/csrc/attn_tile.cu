@@ -81,7 +81,9 @@ enum {
 enum { M_TMEM = 0, M_ABORT, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
 static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
-template <bool kF8>
+// kPaged: K and V in pages, split jobs; else packed and whole (a kernel of its own, since
+// the loops' code has to stay near in the instruction caches).
+template <bool kF8, bool kPaged>
 __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           for (int k = 0; k < 32; ++k)
             if (32 * c + k > kmax) x[c][k] = -INFINITY;
       }
-      const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
+      const uint32_t pages = !kPaged ? 0xffu : static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
       if (pages != 0xffu) {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -282,11 +284,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const float lse = some ? m_run + log2f(l) : -INFINITY;
         const int64_t orow = static_cast<int64_t>(q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
         const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
-        const bool part = S > 1;
+        const bool part = kPaged && S > 1;
         if (live) {
           if (part) a.lse_part[prow] = lse;
           else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
-          if (a.row_map != nullptr && split == 0 && row == rt * a.group)
+          if (kPaged && a.row_map != nullptr && split == 0 && row == rt * a.group)
             a.row_map[static_cast<int64_t>(q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
         }
         // Rows go out through 4 KB a warp of its row block's Q (its products are done): 128 bytes of each of the 32 rows,
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
       // K and V tiles: the 64-dim column blocks one after the other (8-row atoms 1024 bytes apart), or with kv_wide
       // beside one another (atoms 2048 bytes apart, the second block 1024 bytes on)
-      const bool wide = !kF8 && a.kv_wide != 0;
+      const bool wide = kPaged && !kF8 && a.kv_wide != 0;
       const uint32_t block = wide ? 1024 : kTile * 128;
       const uint32_t kv_hi = wide ? static_cast<uint32_t>(sdesc_sw128(sbase, 16, 2048) >> 32) : hi;
       const uint32_t v_step = (wide ? 4096 : 2048) >> 4;   // 16 keys
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       // issue of K and V would bound the kernel. Warp 11 also describes the jobs: this CTA's own, then, each time the
       // loads of one have all been started, that of a CTA that was not launched yet and that it takes over.
       const bool is_k = warp == 9;
-      const int page_rows = a.table != nullptr ? min(1 << a.page_shift, kTile) : kTile;
+      const int page_rows = kPaged ? min(1 << a.page_shift, kTile) : kTile;
       const int boxes = kTile / page_rows;                 // of one tile (and column block)
       bool ok = true;
       int done = 0;                                        // tiles whose loads were started
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           tma_prefetch_desc(&tm_k);
           tma_prefetch_desc(&tm_v);
         }
-        jobs.init(a, 2 * tokens, kTileThirds, lane);
+        jobs.init<kPaged>(a, 2 * tokens, kTileThirds, lane);
       }
 #pragma unroll 1
       for (int job = 0; ok; ++job) {
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
           const int key = (tile0 + t) * kTile + lane * page_rows;
-          if (a.table == nullptr) {
+          if (!kPaged) {
             page = 0;
             row = k0 + key;
             return true;
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             ok = false;
             break;
           }
-          if (is_k) {
+          if (kPaged && is_k) {
             // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
             const unsigned got = __ballot_sync(0xffffffffu, have);
             unsigned groups = 0;
@@ -652,7 +654,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           __syncwarp();
           if (lane < boxes) {
             const uint32_t dst = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
-            if (!kF8 && a.kv_wide != 0) {
+            if (kPaged && !kF8 && a.kv_wide != 0) {
               const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
               tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
                           bar(full + sl));
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           ok = wait_for(bar(B_VFULL + sl), ((done - 1) / C::kVSlots) & 1, limit);
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
-            const bool wide = a.kv_wide != 0;
+            const bool wide = kPaged && a.kv_wide != 0;
             for (int p = (kv & (kTile - 1)) * 8 + lane; p < kTile * 8; p += 32) {
               uint8_t* at = v + (wide ? (p >> 6) * 2048 + (p & 63) * 16 : p * 16);   // 64 pieces an 8-row atom
               *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
@@ -879,17 +881,26 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
 }  // namespace
 
 cudaError_t prepare_attn_tile() {
-  cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<false>::kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_tile_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<true>::kSmem);
+  cudaError_t e = cudaSuccess;
+  auto set = [&](const void* kernel, int smem) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  set(reinterpret_cast<const void*>(attn_tile_kernel<false, false>), Cfg<false>::kSmem);
+  set(reinterpret_cast<const void*>(attn_tile_kernel<false, true>), Cfg<false>::kSmem);
+  set(reinterpret_cast<const void*>(attn_tile_kernel<true, false>), Cfg<true>::kSmem);
+  set(reinterpret_cast<const void*>(attn_tile_kernel<true, true>), Cfg<true>::kSmem);
+  return e;
 }
 
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream) {
   if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   const unsigned n = static_cast<unsigned>(grid);
-  if (dtype == 2) return launch_pdl(attn_tile_kernel<true>, n, Cfg<true>::kThreads, Cfg<true>::kSmem, stream, tm_q, tm_k, tm_v, a);
-  return launch_pdl(attn_tile_kernel<false>, n, Cfg<false>::kThreads, Cfg<false>::kSmem, stream, tm_q, tm_k, tm_v, a);
+  if (dtype == 2)
+    return launch_pdl(a.table != nullptr ? attn_tile_kernel<true, true> : attn_tile_kernel<true, false>, n, Cfg<true>::kThreads,
+                      Cfg<true>::kSmem, stream, tm_q, tm_k, tm_v, a);
+  return launch_pdl(a.table != nullptr ? attn_tile_kernel<false, true> : attn_tile_kernel<false, false>, n,
+                    Cfg<false>::kThreads, Cfg<false>::kSmem, stream, tm_q, tm_k, tm_v, a);
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream) {
