@@ -528,7 +528,8 @@ MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int 
  * and LSE = -inf. Rows of out and lse_out at and past cu_seqlens_q[batch] are left as they
  * were, and nothing of the cache outside a sequence's keys reaches a result,
  * whatever it holds (a non-finite V element below kv_lens[b] may also reach
- * queries of that sequence before it).
+ * queries of that sequence before it). cu_seqlens_q starts at 0 and does not decrease;
+ * offsets that do leave rows undefined, but nothing outside the buffers is touched.
  *   q  [total_q][h_q][128] of the plan's dtype, element (t, j, x) at t *
  *      q_token_stride + j * q_head_stride + x; 16-byte aligned, strides positive
  *      multiples of 16 bytes.

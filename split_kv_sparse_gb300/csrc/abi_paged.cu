@@ -323,7 +323,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.adaptive = plan->adaptive_splits;
   const bool rows16 = plan->row_kernel != 0;
   a.num_sms = rows16 ? plan->num_sms * skv::kRowCtasPerSm : plan->num_sms;
-  a.max_slots = a.num_sms * split_waves(rows16);
+  a.max_slots = static_cast<int>(plan->o_acc_bytes / ((rows16 ? skv::kRowRows : skv::kTileRows) * kDim * 4ull));
   if (plan->num_splits > 1) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.o_part = reinterpret_cast<float*>(ws);

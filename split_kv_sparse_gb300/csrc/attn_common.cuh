@@ -22,12 +22,12 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   s.q0 = min(max(a.cu_q[b], 0), a.total_q);
   s.sq = max(min(a.cu_q[b + 1], a.total_q) - s.q0, 0);
   if (a.table != nullptr) {
-    const int64_t most = static_cast<int64_t>(a.table_width) << a.page_shift;
+    const int64_t most = min(static_cast<int64_t>(a.table_width) << a.page_shift, int64_t{0x7fff0000});
     s.k0 = 0;
     s.kv = static_cast<int>(min(static_cast<int64_t>(max(a.kv_lens[b], 0)), most));
   } else {
     s.k0 = min(max(a.cu_kv[b], 0), a.total_kv);
-    s.kv = max(min(a.cu_kv[b + 1], a.total_kv) - s.k0, 0);
+    s.kv = min(max(min(a.cu_kv[b + 1], a.total_kv) - s.k0, 0), 0x7fff0000);
   }
   return s;
 }
@@ -206,11 +206,16 @@ struct AttnJobs {
 // word and the CTA's abort flag handled in its loop, or with a vote behind it, these
 // kernels lose up to 40 % (e4m3 prompt of 16,384 tokens: 1.2 -> 2.0 ms). A role that gives up
 // says so once (give_up); the others run into their own limit.
+// kPoll: test_wait, for limits below kSuspendNs: the hardware suspends a try_wait for
+// longer than a load from memory takes, so such a limit could never run out. Limits
+// that short are for tests of the way out, and have kernels of their own.
+constexpr uint64_t kSuspendNs = 20000;
+template <bool kPoll>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, uint32_t limit) {
   if (mbar_test_wait(bar, parity)) return true;
   const uint32_t t0 = globaltimer_lo();
   do {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (kPoll ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
   } while (globaltimer_lo() - t0 <= limit);
   return false;
 }

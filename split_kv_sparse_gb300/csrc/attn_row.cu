@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t f16x2_of_e4m3x2(uint32_t w, bool high) {
   return h;
 }
 
-template <bool kF8>
+template <bool kF8, bool kPoll>
 __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     attn_row_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a,
                     const int box_rows) {
@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   jobs.init<true>(a, tokens, kRowThirds, lane);
   const AttnJob job = jobs.find(a, blockIdx.x, lane);
   grid_launch_dependents();
-  if (job.b < 0) return;
+  // (offsets that decrease can name more split jobs than the workspace holds)
+  if (job.b < 0 || (job.S > 1 && job.slot >= a.max_slots)) return;
   const AttnSeq seq = attn_seq(a, job.b);
   const int tok0 = job.j * tokens;
   const int ntok = min(tokens, seq.sq - tok0);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll 1
   for (; n < cnt; ++n) {
     const int st = n % kStages;
-    if (!wait_for(bar(st), (n / kStages) & 1, limit)) {
+    if (!wait_for<kPoll>(bar(st), (n / kStages) & 1, limit)) {
       ok = false;
       break;
     }
@@ -448,18 +449,27 @@ int attn_row_box(int dtype, int page_size) {
   return page_size < block ? page_size : block;
 }
 
+namespace {
+using RowKernel = void (*)(CUtensorMap, CUtensorMap, AttnArgs, int);
+// [e4m3][polling waits]
+constexpr RowKernel kRowKernels[2][2] = {{attn_row_kernel<false, false>, attn_row_kernel<false, true>},
+                                         {attn_row_kernel<true, false>, attn_row_kernel<true, true>}};
+}  // namespace
+
 cudaError_t prepare_attn_row() {
-  const cudaError_t e = cudaFuncSetAttribute(attn_row_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(attn_row_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  for (int k = 0; k < 4; ++k) {
+    const cudaError_t e = cudaFuncSetAttribute(kRowKernels[k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
                             int64_t grid, cudaStream_t stream) {
   if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   const int box = attn_row_box(dtype, 1 << a.page_shift);
-  return launch_pdl(dtype == 2 ? attn_row_kernel<true> : attn_row_kernel<false>, static_cast<unsigned>(grid), kWarps * 32,
-                    kSmem, stream, tm_k, tm_v, a, box);
+  return launch_pdl(kRowKernels[dtype == 2][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid), kWarps * 32, kSmem,
+                    stream, tm_k, tm_v, a, box);
 }
 
 }  // namespace skv

@@ -83,7 +83,7 @@ static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
 // kPaged: K and V in pages, split jobs; else packed and whole (a kernel of its own, since
 // the loops' code has to stay near in the instruction caches).
-template <bool kF8, bool kPaged>
+template <bool kF8, bool kPaged, bool kPoll>
 __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
   // Job number k of this CTA: waits until the scheduler has described it and returns its words (negative J_B: no more).
   auto job_at = [&](int k, volatile int*& words) {
     words = misc + M_JOBS + (k & 1) * kJobWords;
-    return wait_for(bar(B_JOB0 + (k & 1)), (k >> 1) & 1, limit);
+    return wait_for<kPoll>(bar(B_JOB0 + (k & 1)), (k >> 1) & 1, limit);
   };
   // The words have been copied.
   auto job_read = [&](int k) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 #pragma unroll 1
     for (int u = 0; u < cnt; ++u) {
       const int t = one ? 2 * u + i : u;
-      if (!wait_for(bar(B_S0 + i), (su + u) & 1, limit)) {
+      if (!wait_for<kPoll>(bar(B_S0 + i), (su + u) & 1, limit)) {
         bad = true;
         break;
       }
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
       const bool need = mx > m_run + kRescaleThreshold;
       // O_i's last product is done: P_i may be written again, O_i rescaled
-      if (u > 0 && !wait_for(bar(B_O0 + i), (su + u - 1) & 1, limit)) {
+      if (u > 0 && !wait_for<kPoll>(bar(B_O0 + i), (su + u - 1) & 1, limit)) {
         bad = true;
         break;
       }
@@ -255,22 +255,22 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     }
 
     // ---- epilogue
-    if (!bad && cnt > 0) bad = !wait_for(bar(B_O0 + i), (su + cnt - 1) & 1, limit);
+    if (!bad && cnt > 0) bad = !wait_for<kPoll>(bar(B_O0 + i), (su + cnt - 1) & 1, limit);
     // rows that see no key of a job that loads Q all the same: not before that load has left Q's place
-    if (!bad && cnt == 0 && tiles > 0) bad = !wait_for(bar(B_Q), ends & 1, limit);
+    if (!bad && cnt == 0 && tiles > 0) bad = !wait_for<kPoll>(bar(B_Q), ends & 1, limit);
     // one row block: stream 0 takes both results from tensor memory (they lie in the same lanes)
-    if (one && tiles > 0 && !bad) bad = !wait_for(bar(B_END), ends & 1, limit);
+    if (one && tiles > 0 && !bad) bad = !wait_for<kPoll>(bar(B_END), ends & 1, limit);
     tc_fence_after();
     float2* stats = reinterpret_cast<float2*>(smem + C::kOffStats);
     if (one && i == 1) {
       stats[row] = make_float2(m_run, l);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_STAT));
-      bad = !wait_for(bar(B_OREAD), ones & 1, limit) || bad;   // stream 0 has read O_1
+      bad = !wait_for<kPoll>(bar(B_OREAD), ones & 1, limit) || bad;   // stream 0 has read O_1
     } else {
       float w0 = 1.f, w1 = 0.f;
       if (one) {
-        bad = !wait_for(bar(B_STAT), ones & 1, limit) || bad;
+        bad = !wait_for<kPoll>(bar(B_STAT), ones & 1, limit) || bad;
         const float2 st = stats[row];
         const float M = fmaxf(m_run, st.x);
         w0 = m_run == -INFINITY ? 0.f : ex2_approx(m_run - M);
@@ -430,16 +430,16 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         if (is_qk) {
           const uint32_t d = tmem + kTmemS;
           const int first = n;   // (a job's first products have none of its own to follow)
-          ok = wait_for(bar(B_Q), with_tiles & 1, limit);
+          ok = wait_for<kPoll>(bar(B_Q), with_tiles & 1, limit);
 #pragma unroll 1
           for (int u = 0; ok && u < steps; ++u) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (!ok || u >= (i ? cnt1 : cnt0)) continue;
               const int t = tile_base + tile_at(i, u);
-              ok = wait_for(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, limit) &&
-                   (n < first + 3 || wait_for(bar(B_TURN_QK), (n - 3) & 1, limit)) &&
-                   (n == 0 || wait_for(bar(B_SFREE), (n - 1) & 1, limit));
+              ok = wait_for<kPoll>(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, limit) &&
+                   (n < first + 3 || wait_for<kPoll>(bar(B_TURN_QK), (n - 3) & 1, limit)) &&
+                   (n == 0 || wait_for<kPoll>(bar(B_SFREE), (n - 1) & 1, limit));
               if (!ok) break;
               ++n;
               tc_fence_after();
@@ -474,13 +474,13 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             for (int i = 0; i < 2; ++i) {
               if (!ok || u >= (i ? cnt1 : cnt0)) continue;
               const int t = tile_base + tile_at(i, u);
-              if constexpr (kF8) ok = wait_for(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
+              if constexpr (kF8) ok = wait_for<kPoll>(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
               else
-                ok = wait_for(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit) &&
-                     (t - tile_base != tail || wait_for(bar(B_VFIX), fixes & 1, limit));
+                ok = wait_for<kPoll>(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit) &&
+                     (t - tile_base != tail || wait_for<kPoll>(bar(B_VFIX), fixes & 1, limit));
               // (the job's last two products have no later QK to follow; the turn is an order, P is the dependency)
-              ok = ok && wait_for(bar(B_P0 + i), (i ? seen1 : seen0) & 1, limit) &&
-                   (n + 2 > last || wait_for(bar(B_TURN_PV), (n + 2) & 1, limit));
+              ok = ok && wait_for<kPoll>(bar(B_P0 + i), (i ? seen1 : seen0) & 1, limit) &&
+                   (n + 2 > last || wait_for<kPoll>(bar(B_TURN_PV), (n + 2) & 1, limit));
               if (!ok) break;
               ++n;
               if (i) ++seen1;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             idx = take_over();   // (an index past the batch's jobs; the grid is sized by a bound)
           }
           w = misc + M_JOBS + (job & 1) * kJobWords;
-          ok = ok && (job < 2 || wait_for(bar(B_READ0 + (job & 1)), ((job >> 1) - 1) & 1, limit));
+          ok = ok && (job < 2 || wait_for<kPoll>(bar(B_READ0 + (job & 1)), ((job >> 1) - 1) & 1, limit));
           if (!ok) break;
           if (lane == 0) {
             w[J_B] = next.b;
@@ -584,15 +584,17 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 const int keys = seq.kv - seq.sq + last + 1;
                 return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
               };
-              const bool one = tok0 + tokens >= seq.sq;
+              // (offsets that decrease can name more split jobs than the workspace holds: such a job has no rows)
+              const bool over = kPaged && next.S > 1 && next.slot >= a.max_slots;
+              const bool one = over || tok0 + tokens >= seq.sq;
               const int n0 = tiles_of(0), n1 = tiles_of(1);  // n1 >= n0 where there is a second block
-              const int tiles = one ? n0 : n1;
+              const int tiles = over ? 0 : one ? n0 : n1;
               w[J_G] = next.g;
               w[J_SPLIT] = next.s;
               w[J_S] = next.S;
               w[J_SLOT] = next.slot;
               w[J_Q0] = seq.q0;
-              w[J_SQ] = seq.sq;
+              w[J_SQ] = over ? 0 : seq.sq;
               w[J_K0] = seq.k0;
               w[J_KV] = seq.kv;
               w[J_TOK0] = tok0;
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           bool have_n = false;
           if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
           const int sl = done % slots;
-          if (done >= slots && !wait_for(bar(empty + sl), ((done / slots) - 1) & 1, limit)) {
+          if (done >= slots && !wait_for<kPoll>(bar(empty + sl), ((done / slots) - 1) & 1, limit)) {
             ok = false;
             break;
           }
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           have = have_n;
           if (is_k && t == 0) {
             // Q once the rows of the job before (which go through it, tiles or not) have left its place
-            ok = job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
+            ok = job == 0 || (wait_for<kPoll>(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for<kPoll>(bar(B_QFREE1), (job - 1) & 1, limit));
             if (!ok) break;
             if (lane == 0) {
               const int blocks = one ? 1 : 2;
@@ -683,11 +685,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         }
         if (!ok) break;
         if (is_k && tiles == 0)
-          ok = job == 0 || (wait_for(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for(bar(B_QFREE1), (job - 1) & 1, limit));
+          ok = job == 0 || (wait_for<kPoll>(bar(B_QFREE0), (job - 1) & 1, limit) && wait_for<kPoll>(bar(B_QFREE1), (job - 1) & 1, limit));
         // the ragged end lies in the last tile: clear V's rows past it
         if (!kF8 && !is_k && tail >= 0) {
           const int sl = (done - 1) % C::kVSlots;
-          ok = wait_for(bar(B_VFULL + sl), ((done - 1) / C::kVSlots) & 1, limit);
+          ok = wait_for<kPoll>(bar(B_VFULL + sl), ((done - 1) / C::kVSlots) & 1, limit);
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
             const bool wide = kPaged && a.kv_wide != 0;
@@ -729,8 +731,8 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       for (int tl = 0; tl < tiles; ++tl) {
         const int t = tile_base + tl;
         const int sl = t % C::kVSlots;
-        ok = wait_for(bar(B_VFULL + sl), (t / C::kVSlots) & 1, limit) &&
-             (t < 2 || wait_for(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, limit));
+        ok = wait_for<kPoll>(bar(B_VFULL + sl), (t / C::kVSlots) & 1, limit) &&
+             (t < 2 || wait_for<kPoll>(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, limit));
         if (!ok) break;
         const uint8_t* src = smem + C::kOffV + sl * C::kItemBytes + key * 128;
         uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
@@ -803,7 +805,10 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
     if (tok < begin) continue;
     const int2 map = a.row_map[static_cast<int64_t>(tok) * a.h_kv + g];
     const int S = map.y;
-    if (S < 1) continue;
+    // (a token of no job, which only offsets that decrease can leave, has no entry: nothing outside the partials is read)
+    if (S < 1 || S > a.num_splits || map.x < 0 ||
+        map.x + (S - 1ll) * rows_per_slot + a.group > static_cast<int64_t>(a.max_slots) * rows_per_slot)
+      continue;
     {
       const int64_t p0 = static_cast<int64_t>(map.x) + h0;
       const int heads = min(kHeads, a.group - h0);
@@ -880,27 +885,33 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
 
 }  // namespace
 
+namespace {
+using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
+// [e4m3][paged][polling waits]
+constexpr TileKernel kTileKernels[2][2][2] = {
+    {{attn_tile_kernel<false, false, false>, attn_tile_kernel<false, false, true>},
+     {attn_tile_kernel<false, true, false>, attn_tile_kernel<false, true, true>}},
+    {{attn_tile_kernel<true, false, false>, attn_tile_kernel<true, false, true>},
+     {attn_tile_kernel<true, true, false>, attn_tile_kernel<true, true, true>}}};
+}  // namespace
+
 cudaError_t prepare_attn_tile() {
-  cudaError_t e = cudaSuccess;
-  auto set = [&](const void* kernel, int smem) {
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  };
-  set(reinterpret_cast<const void*>(attn_tile_kernel<false, false>), Cfg<false>::kSmem);
-  set(reinterpret_cast<const void*>(attn_tile_kernel<false, true>), Cfg<false>::kSmem);
-  set(reinterpret_cast<const void*>(attn_tile_kernel<true, false>), Cfg<true>::kSmem);
-  set(reinterpret_cast<const void*>(attn_tile_kernel<true, true>), Cfg<true>::kSmem);
-  return e;
+  for (int f8 = 0; f8 < 2; ++f8)
+    for (int k = 0; k < 4; ++k) {
+      const cudaError_t e = cudaFuncSetAttribute(kTileKernels[f8][k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem);
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
 }
 
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream) {
   if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned n = static_cast<unsigned>(grid);
-  if (dtype == 2)
-    return launch_pdl(a.table != nullptr ? attn_tile_kernel<true, true> : attn_tile_kernel<true, false>, n, Cfg<true>::kThreads,
-                      Cfg<true>::kSmem, stream, tm_q, tm_k, tm_v, a);
-  return launch_pdl(a.table != nullptr ? attn_tile_kernel<false, true> : attn_tile_kernel<false, false>, n,
-                    Cfg<false>::kThreads, Cfg<false>::kSmem, stream, tm_q, tm_k, tm_v, a);
+  const bool f8 = dtype == 2;
+  return launch_pdl(kTileKernels[f8][a.table != nullptr][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid),
+                    f8 ? Cfg<true>::kThreads : Cfg<false>::kThreads, f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem, stream, tm_q,
+                    tm_k, tm_v, a);
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream) {

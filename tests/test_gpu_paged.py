@@ -419,12 +419,57 @@ def test_two_streams_with_workspaces_of_their_own(sq):
         check(s[8].cpu(), None, None, c.reference(q, dq, cu, 0.1), "bf16")
 
 
+@pytest.mark.parametrize("S", [0, 2])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [4, 9, 2, 12], [0, 200, 10, 250], [-5, 7, 1 << 20, 3], [0, 0, 0, 0]])
+def test_offsets_that_decrease_touch_nothing_outside(cu, S):
+    """Rows are undefined then, but every write stays inside the buffers and every wait ends."""
+    for dtype in ("bf16", "e4m3"):
+        c, q, dq, _ = paged_case(dtype, [80, 80, 100], [500, 300, 64], 8, 2, 16, seed=6)
+        total = 260
+        plan = b.sdpa_paged_plan(3, 8, 2, D, dtype, 1 if max(cu) < 50 else 100, total, 500, force_splits=S)
+        ws = torch.empty(max(16, plan.workspace_bytes) + 4096, dtype=torch.uint8, device="cuda")
+        ws.fill_(0x5A)
+        out = torch.full((total + 8, 8, D), 7.0, device="cuda")
+        b.sdpa_paged(plan, total, q.cuda(), b.kv_pages(c.k.cuda(), c.v.cuda()), c.table.cuda(), c.kv_lens.cuda(),
+                     torch.tensor(cu, dtype=torch.int32, device="cuda"), scalar(dq, dtype), scalar(c.dk, dtype),
+                     scalar(c.dv, dtype), 0.1, "f32", 1.0, out, None, None, ws)
+        torch.cuda.synchronize()
+        status_clear()
+        assert torch.all(out[total:] == 7.0) and torch.all(ws[-4096:] == 0x5A)
+
+
 def test_repeated_calls_give_the_same_bits():
     for dtype, sq in (("bf16", [1, 1, 1]), ("e4m3", [1, 1, 1]), ("bf16", [20, 70, 1]), ("e4m3", [20, 70, 1])):
         c, q, dq, cu = paged_case(dtype, sq, [1500, 300, 64], 8, 2, 16, seed=3)
         a = run_paged(c, q, dq, cu, 8)
         z = run_paged(c, q, dq, cu, 8)
         assert torch.equal(a[0], z[0]) and torch.equal(a[1], z[1]) and a[2] == z[2]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("sq", [[1, 1, 1], [20, 300, 1]])
+def test_waits_that_run_out_end_the_call_with_a_status(dtype, sq):
+    """With a limit far below a step's latency the kernels' waits run out: the call ends, says so, and the next one is
+    right again. (200 ns: the shortest load from memory takes longer.)"""
+    c, q, dq, cu = paged_case(dtype, sq, [1500, 900, 64], 8, 2, 16, seed=3)
+    ref = c.reference(q, dq, cu, 1 / math.sqrt(D))
+    n = int(cu[-1])
+    plan = b.sdpa_paged_plan(3, 8, 2, D, dtype, max(sq), n, 1500)
+    ws = torch.empty(max(16, plan.workspace_bytes), dtype=torch.uint8, device="cuda")
+    out = torch.empty((n, 8, D), device="cuda")
+    args = [q.cuda(), b.kv_pages(c.k.cuda(), c.v.cuda()), c.table.cuda(), c.kv_lens.cuda(), cu.cuda()]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    try:
+        b.mla_set_wait_limit_ns(200)
+        flush.fill_(1)          # the keys are not in the cache
+        b.sdpa_paged(plan, n, *args, scalar(dq, dtype), scalar(c.dk, dtype), scalar(c.dv, dtype), 0.1, "f32", 1.0, out, None,
+                     None, ws)
+        torch.cuda.synchronize()
+        st, site = b.mla_get_status()
+        assert st & b.MLA_STATUS_TIMEOUT and site != 0
+    finally:
+        b.mla_set_wait_limit_ns(0)
+    check(*run_paged(c, q, dq, cu, 8), ref, dtype)
 
 
 # ------------------------------------------------------------------------- prompt --
@@ -507,6 +552,24 @@ def test_prompt_values_of_the_next_sequence_do_not_leak():
     ref = op.prompt_attention(q[:100].double().numpy(), k[:100].double().numpy(), v[:100].double().numpy(),
                               np.array([0, 100]), np.array([0, 100]), 0.1)
     check(out[:100].cpu(), None, None, ref, "bf16")
+
+
+def test_prompt_on_another_stream_and_repeated():
+    g = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn((900, h, D), generator=g).to(torch.bfloat16) for h in (8, 2, 2))
+    cu = cu_of([300, 17, 583])
+    ref = op.prompt_attention(q.double().numpy(), k.double().numpy(), v.double().numpy(), cu.numpy(), cu.numpy(), 0.1)
+    qd, kd, vd, cd = q.cuda(), k.cuda(), v.cuda(), cu.cuda()
+    outs = [torch.empty((900, 8, D), device="cuda") for _ in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        with torch.cuda.stream(streams[i % 2]):
+            b.sdpa_prompt(3, qd, kd, vd, cd, cd, None, None, None, 0.1, "f32", 1.0, o)
+    torch.cuda.synchronize()
+    status_clear()
+    check(outs[0].cpu(), None, None, ref, "bf16")
+    assert all(torch.equal(o, outs[0]) for o in outs)
 
 
 def test_prompt_in_a_graph():
