@@ -482,8 +482,9 @@ MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_
  *   [0, o_acc_bytes)                   fp32 partial rows [split job][R][128]
  *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][R]
  *   [map_offset, ...)                  per (token, KV head): its first partial row, its splits
- * so its size is bounded by the SMs (one wave of split jobs), not by the tokens,
- * unless a split count is forced. 0 bytes with one split. It needs no clearing. */
+ * so its size is bounded by the SMs (one wave of split jobs with row_kernel, three
+ * otherwise: 60 MB on 152 SMs), not by the tokens, unless a split count is forced. 0
+ * bytes with one split. It needs no clearing. */
 typedef struct {
   int32_t batch;          /* sequences                                                  */
   int32_t h_q, h_kv;      /* query and KV heads; h_q % h_kv == 0, group = h_q / h_kv <= 128 */
@@ -508,11 +509,13 @@ typedef struct {
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
  * max_kv) for each sequence, from the lengths, on the GPU: with T = the key tiles a
- * job should walk, clamp(ceil(tiles / T), 1, bound). If the unsplit jobs fit one wave (num_sms jobs, twice that with row_kernel), T is
- * the smallest from ceil(work / wave) up (growing by an eighth) whose jobs do too;
- * otherwise T = 2 ceil(work / wave), so that only a sequence that would hold an SM for
- * more than twice its share is split. An unsplit sequence's rows are written at once, those
- * of a split one by a combine kernel launched behind. num_sms 0 = the current device's.
+ * job should walk, clamp(ceil(tiles / T), 1, bound). If the unsplit jobs fit one wave
+ * (num_sms jobs, twice that with row_kernel), T is the smallest whose jobs do too.
+ * Otherwise T is twice an SM's share of the work with row_kernel (only a sequence that
+ * would hold its SM for long is split) and a third of it without (its SMs take the jobs
+ * one after the other), or more where the split jobs would not fit the workspace. An
+ * unsplit sequence's rows are written at once, those of a split one by a combine kernel
+ * launched behind. num_sms 0 = the current device's.
  * Errors as for mla_decode_plan (d must be 128, dtype SDPA_*, group <= 128). */
 MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_per_seq, int total_q_max,
                     int max_kv, int num_sms, int max_splits, int force_splits, sdpa_paged_plan_t* out);
