@@ -155,10 +155,10 @@ struct AttnJobs {
     hi = max(hi, lo);
     while (lo < hi) {
       T = (lo + hi) >> 1;
-      int total = 0;
-      for (int i = 0; i < groups; ++i) {
+      int total = warp_sum_int(n_first * splits(a, tiles_first));
+      for (int i = 1; i < groups; ++i) {
         int n, tiles;
-        shape(a, i, lane, n, tiles);
+        load(a, i, lane, n, tiles);
         total += warp_sum_int(n * splits(a, tiles));
       }
       if (static_cast<long long>(total) * a.h_kv <= a.num_sms) hi = T;

@@ -159,6 +159,25 @@ def test_write_special_values_to_e4m3():
     assert int(got[1, 0]) & 0x7F == 0x7F and int(got[1, 1]) == 0x38
 
 
+@pytest.mark.parametrize("descale", [0.013, 1.0, 3.0, 1.9999999, 1e-20, 7e30, 2.0 ** -126, 1e-39, 0.0, float("inf")])
+def test_write_divides_as_a_division_does(descale):
+    """Every bf16 value (all 65,536 bit patterns) against e4m3 of the rounded fp32 quotient, at descales whose quotients
+    fall on ties and outside the range of e4m3, of fp32, and of a reciprocal."""
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).reshape(512, 1, D)
+    kc, vc = (torch.zeros((32, 16, 1, D), dtype=torch.uint8, device="cuda") for _ in range(2))
+    d = torch.tensor([descale], dtype=torch.float32, device="cuda")
+    b.kv_pages_write(b.kv_pages(kc, vc), x.cuda(), x.cuda(), torch.arange(512, device="cuda"), d, d)
+    with np.errstate(all="ignore"):
+        q = x.reshape(-1).float().numpy() / np.float32(descale)      # IEEE division, subnormals and all
+    got = kc.cpu().reshape(-1).numpy()
+    nan = np.isnan(q)
+    assert np.all((got[nan] & 0x7F) == 0x7F)
+    want = codecs.e4m3_encode(np.clip(q[~nan], -448.0, 448.0).astype(np.float64))
+    same = (got[~nan] == want) | (((got[~nan] | want) & 0x7F) == 0)   # either zero
+    assert same.all(), (x.reshape(-1)[torch.from_numpy(~nan)][torch.from_numpy(~same)][:5], q[~nan][~same][:5])
+    assert torch.equal(kc, vc)
+
+
 def test_write_and_read_behind_32_bit_offsets():
     """Pages that lie more than 2^32 bytes from the base."""
     page, h_kv = 16, 1
