@@ -456,8 +456,10 @@ typedef struct {
  *   positions    int32 [total_q] or NULL.
  * MLA_ERR_INVALID_ARG: a NULL or misaligned pointer, batch, page_size,
  * table_width or free_capacity < 1, total_q < 0. MLA_ERR_UNSUPPORTED: batch >
- * KV_PAGES_MAX_BATCH. total_q may be 0 (slot_map is then not touched). */
+ * KV_PAGES_MAX_BATCH, or batch * table_width or free_capacity > KV_PAGES_MAX_ENTRIES.
+ * total_q may be 0 (slot_map is then not touched). */
 #define KV_PAGES_MAX_BATCH 16384
+#define KV_PAGES_MAX_ENTRIES 0x3FFFFFFF
 MLA_API int kv_pages_map(int batch, int page_size, const int32_t* held_lens, const int32_t* new_lens,
                  const int32_t* cu_seqlens_q, int total_q, int32_t* block_table, int table_width,
                  int32_t* free_pages, int free_capacity, const int32_t* free_in, int32_t* free_out,

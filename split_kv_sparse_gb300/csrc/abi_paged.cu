@@ -152,7 +152,9 @@ int kv_pages_map(int batch, int page_size, const int32_t* held_lens, const int32
       !ptr_aligned(slot_map, 8))
     return MLA_ERR_INVALID_ARG;
   if (batch > KV_PAGES_MAX_BATCH) return MLA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(batch) * table_width > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;   // page ordinals are int32
+  // (the kernel's page ordinals, and their sum with the list's count, are int32)
+  if (static_cast<int64_t>(batch) * table_width > KV_PAGES_MAX_ENTRIES || free_capacity > KV_PAGES_MAX_ENTRIES)
+    return MLA_ERR_UNSUPPORTED;
   skv::DeviceInfo dev;
   const int st = skv::current_device(&dev);
   if (st != MLA_OK) return st;

@@ -73,6 +73,13 @@ def test_map_refusals():
         assert status_of("kv_pages_map", *(ok | kw).values()) == code, kw
 
 
+def test_map_refuses_ordinals_past_32_bits():
+    """A list's count and every page of a table freed at once have to add up to an int32."""
+    for batch, width, cap, code in [(16384, 1 << 17, 8, 2), (1, 1 << 30, 8, 2), (2, 4, 1 << 30, 2), (2, 4, (1 << 31) - 1, 2)]:
+        assert status_of("kv_pages_map", batch, 16, FAKE, FAKE, FAKE, 3, FAKE, width, FAKE, cap, FAKE, FAKE, FAKE, FAKE,
+                         None) == code, (batch, width, cap)
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(k=None), 1), (dict(v=FAKE + 8), 1), (dict(dtype=0), 2), (dict(dtype=3), 2), (dict(num_pages=0), 1),
     (dict(page_size=8), 2), (dict(page_size=48), 2), (dict(page_size=131072), 2), (dict(h_kv=0), 1), (dict(d=64), 2),
