@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   const AttnJob job = jobs.find(a, blockIdx.x, lane);
   grid_launch_dependents();
   // (offsets that decrease can name more split jobs than the workspace holds)
-  if (job.b < 0 || (job.S > 1 && job.slot >= a.max_slots)) return;
+  if (job.b < 0 || (job.S > 1 && static_cast<unsigned>(job.slot) >= static_cast<unsigned>(a.max_slots))) return;
   const AttnSeq seq = attn_seq(a, job.b);
   const int tok0 = job.j * tokens;
   const int ntok = min(tokens, seq.sq - tok0);

@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
               };
               // (offsets that decrease can name more split jobs than the workspace holds: such a job has no rows)
-              const bool over = kPaged && next.S > 1 && next.slot >= a.max_slots;
+              const bool over = kPaged && next.S > 1 && static_cast<unsigned>(next.slot) >= static_cast<unsigned>(a.max_slots);
               const bool one = over || tok0 + tokens >= seq.sq;
               const int n0 = tiles_of(0), n1 = tiles_of(1);  // n1 >= n0 where there is a second block
               const int tiles = over ? 0 : one ? n0 : n1;
@@ -858,8 +858,8 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
       for (int o = kLanes / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       const int64_t row0 = static_cast<int64_t>(tok) * a.h_q + g * a.group + h0;
       if (sl == 0 && hl < heads && a.lse_out != nullptr)
-        a.lse_out[row0 + hl] = M == -INFINITY ? -INFINITY : M + log2f(z);
-      const float inv_l = M == -INFINITY ? 0.f : 1.f / z;
+        a.lse_out[row0 + hl] = z == 0.f ? -INFINITY : M + log2f(z);   // (a NaN partial's weight, and so z, is NaN)
+      const float inv_l = z == 0.f ? 0.f : 1.f / z;
 #pragma unroll
       for (int h = 0; h < kHeads; ++h) {
         const float inv = __shfl_sync(0xffffffffu, inv_l, kLanes * h);

@@ -285,6 +285,21 @@ def test_pages_that_are_missing(dtype, sq):
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("sq", [[1, 1], [30, 45]])
+@pytest.mark.parametrize("S", [1, 3])
+def test_nan_scores_give_nan_rows_and_touch_no_other(dtype, sq, S):
+    """Sequence 1's keys are NaN: its O and LSE are NaN however it is split, sequence 0's are what they were."""
+    c, q, dq, cu = paged_case(dtype, sq, [150, 500], 8, 2, 16, seed=9)
+    O, L, A = c.reference(q, dq, cu, 1 / math.sqrt(D))
+    held = c.table[1][c.table[1] >= 0].long()
+    c.k[held] = float("nan") if dtype == "bf16" else 0x7F
+    out, lse, _ = run_paged(c, q, dq, cu, 8, force_splits=S, amax=False)
+    n = sq[0]
+    check(out[:n], lse[:n], None, (O[:n], L[:n], A[:n]), dtype)
+    assert torch.isnan(out[n:]).all() and torch.isnan(lse[n:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("sq", [[1, 1], [30, 45]])
 @pytest.mark.parametrize("S", [0, 1, 3])
 def test_padded_batch_rows_are_left_alone(dtype, sq, S):
     c, q, dq, cu = paged_case(dtype, sq, [150, 300], 8, 2, 16, seed=4)
