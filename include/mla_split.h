@@ -484,8 +484,8 @@ MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_
  *   [0, o_acc_bytes)                   fp32 partial rows [split job][R][128]
  *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][R]
  *   [map_offset, ...)                  per (token, KV head): its first partial row, its splits
- * so its size is bounded by the SMs (one wave of split jobs with row_kernel, three
- * otherwise: 60 MB on 152 SMs), not by the tokens, unless a split count is forced. 0
+ * so its size is bounded by the SMs and KV heads (two split jobs a CTA with row_kernel: 5 MB
+ * on 152 SMs; three waves otherwise: 60 MB), not by the tokens, unless a split count is forced. 0
  * bytes with one split. It needs no clearing. */
 typedef struct {
   int32_t batch;          /* sequences                                                  */
@@ -510,12 +510,13 @@ typedef struct {
 
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
- * max_kv) for each sequence, from the lengths, on the GPU: with T = the key tiles a
- * job should walk, clamp(ceil(tiles / T), 1, bound). If the unsplit jobs fit one wave
- * (num_sms jobs, twice that with row_kernel), T is the smallest whose jobs do too.
- * Otherwise T is twice an SM's share of the work with row_kernel (only a sequence that
- * would hold its SM for long is split) and a third of it without (its SMs take the jobs
- * one after the other), or more where the split jobs would not fit the workspace. An
+ * max_kv) for each sequence, from the lengths, on the GPU. With row_kernel one wave of CTAs
+ * (two an SM) takes equal shares of the key tiles of all sequences, laid one after the
+ * other, and a sequence is split where a share ends (shares are larger where it would
+ * be split into more than the bound). Otherwise, with T = the key tiles a job should walk, it
+ * gets clamp(ceil(tiles / T), 1, bound) splits: if the unsplit jobs fit one wave (num_sms
+ * jobs), T is the smallest whose jobs do too, else a third of an SM's share of the work (its
+ * SMs take the jobs one after the other), or more where the split jobs would not fit the workspace. An
  * unsplit sequence's rows are written at once, those of a split one by a combine kernel
  * launched behind. num_sms 0 = the current device's.
  * Errors as for mla_decode_plan (d must be 128, dtype SDPA_*, group <= 128). */

@@ -122,12 +122,13 @@ int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / token
 // Tokens of one job's rows.
 int job_tokens(bool rows16, int group) { return rows16 ? skv::kRowRows / group : 2 * (128 / group); }
 
-int split_waves(bool rows16) { return rows16 ? skv::kRowSplitWaves : skv::kTileSplitWaves; }
+// CTAs of the row kernel with equal shares: as many for each KV head, one wave of them.
+int64_t row_ctas(int wave, int h_kv) { return static_cast<int64_t>(std::max(1, wave / h_kv)) * h_kv; }
 
 // Jobs that one launch may hold: unsplit, forced splits, or counts from the lengths.
-int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int wave, int split_waves) {
+int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int wave) {
   if (!adaptive) return unsplit * num_splits;
-  return unsplit <= wave ? wave : unsplit + split_waves * wave;
+  return unsplit <= wave ? wave : unsplit + skv::kTileSplitWaves * wave;
 }
 
 int shift_of(int pow2) {
@@ -253,7 +254,9 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->row_kernel = rows16 ? 1 : 0;
   if (S > 1) {
     // split jobs: as many as forced, or at most so many waves (the rule keeps to that)
-    const int64_t slots = adaptive ? static_cast<int64_t>(wave) * split_waves(rows16) : unsplit * S;
+    const int64_t slots = !adaptive ? unsplit * S
+                          : rows16  ? 2 * row_ctas(wave, h_kv)   // two pieces of cut jobs a CTA
+                                    : static_cast<int64_t>(wave) * skv::kTileSplitWaves;
     if (slots * job_rows > 0x7FFFFFFFll) {
       std::memset(out, 0, sizeof(*out));
       return MLA_ERR_UNSUPPORTED;
@@ -279,6 +282,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if ((st = check_pages(pages)) != MLA_OK) return st;
   if (pages->dtype != plan->dtype || pages->h_kv != plan->h_kv || pages->d != plan->d) return MLA_ERR_INVALID_ARG;
   if (plan->num_splits < 1 || plan->num_splits > MLA_MAX_SPLITS || plan->num_sms < 1) return MLA_ERR_INVALID_ARG;
+  if (plan->adaptive_splits != 0 && plan->num_splits < 2) return MLA_ERR_INVALID_ARG;
   if (plan->row_kernel != 0 && plan->h_q / plan->h_kv > skv::kRowRows) return MLA_ERR_INVALID_ARG;
   if (total_q < 1 || total_q > plan->total_q_max || table_width < 1) return MLA_ERR_INVALID_ARG;
   if (q == nullptr || block_table == nullptr || kv_lens == nullptr || cu_seqlens_q == nullptr) return MLA_ERR_INVALID_ARG;
@@ -351,7 +355,16 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     return st;
   if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
-  const int64_t grid = jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms, split_waves(rows16));
+  if (rows16 && a.adaptive) {
+    // the units of all jobs have to add up to an int32
+    const int64_t tiles = (static_cast<int64_t>(table_width) << a.page_shift) / 128 + 1;
+    while (unsplit / a.h_kv * ((std::min<int64_t>(tiles, 1 << 24) >> a.share_shift) + 4) > 0x7FFFFFFFll) {
+      if (++a.share_shift > 24) return MLA_ERR_UNSUPPORTED;
+    }
+    a.part_gap = static_cast<int>(row_ctas(a.num_sms, a.h_kv)) * skv::kRowRows;
+  }
+  const int64_t grid = rows16 && a.adaptive ? row_ctas(a.num_sms, a.h_kv)
+                                            : jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms);
   st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
                           : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;

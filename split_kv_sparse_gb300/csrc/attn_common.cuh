@@ -78,8 +78,9 @@ struct AttnJob {
 // ceil(s_b / tokens) query tiles and S_b splits: num_splits of them where the plan
 // forces a count, else, with T = the key tiles a job should walk, clamp(ceil(tiles_b / T),
 // 1, num_splits). If the unsplit jobs fit one wave of num_sms, T is the smallest whose
-// jobs do too; otherwise T is thirds / 3 of an SM's share of the work, or the next (by
-// quarters) whose split jobs fit the workspace's max_slots.
+// jobs do too; otherwise T is a third of an SM's share of the work (ragged chunks and e4m3
+// chunks both lose with two thirds or a whole one: fewer jobs to even out), or the next
+// (by quarters) whose split jobs fit the workspace's max_slots.
 // Jobs are listed sequence by sequence; within one the last query tiles first (they
 // see the most keys), then the splits, the KV heads fastest.
 struct AttnJobs {
@@ -110,7 +111,7 @@ struct AttnJobs {
 
   // kSplits: false where no job is ever split.
   template <bool kSplits>
-  __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int thirds, int lane) {
+  __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int lane) {
     tokens = job_tokens;
     groups = (a.batch + 31) / 32;
     T = 0;
@@ -134,8 +135,7 @@ struct AttnJobs {
     const float unsplit = static_cast<float>(jobs) * static_cast<float>(a.h_kv);
     const float wave = static_cast<float>(a.num_sms);
     if (unsplit > wave) {
-      T = max(1, static_cast<int>(fminf(ceilf(work * static_cast<float>(thirds) / (3.f * wave)), 16777216.f)));   // (above any
-                                                                                             // sequence's tiles)
+      T = max(1, static_cast<int>(fminf(ceilf(work / (3.f * wave)), 16777216.f)));   // (above any sequence's tiles)
       for (;;) {
         int split_jobs = 0;
         for (int i = 0; i < groups; ++i) {
@@ -197,6 +197,109 @@ struct AttnJobs {
       slots += __shfl_sync(0xffffffffu, sincl, 31);
     }
     return job;
+  }
+};
+
+// Equal shares of the batch's work (the kernel of 16-row jobs). Its jobs (sequence, query tile)
+// lie one after the other on a line, each as kShareHead units for its start and end and
+// then a unit for every 2^share_shift key tiles (one at least). Range r of R = num_sms /
+// h_kv takes the units [r U, (r + 1) U), by one CTA for each KV head: the heads of a row lie
+// side by side in memory, and read at one time they share DRAM rows (128 sequences of 2,048
+// e4m3 keys, 8 KV heads: 98 us, with the heads one after the other on the line 141; one job a CTA
+// 118). A job that crosses no boundary is written at once; the pieces of one that does are partials: a CTA
+// has at most one piece that begins its job (slot R h_kv + g R + r) and one that goes on with
+// it (slot g R + r), so the pieces of a job that begins in range r lie at R h_kv + g R + r, then
+// g R + r + 1, g R + r + 2, ..
+constexpr int kShareHead = 2;
+struct AttnPiece {
+  int b, j, g;       // sequence (-1: none), query tile, KV head
+  int tile0, tiles;  // key tiles
+  int slot;          // -1: the whole job
+  int S;             // pieces of the job where this is its first, else 0
+};
+struct AttnShares {
+  int tokens;
+  int n_first, units_first;   // the first 32 sequences: query tiles, units of a job
+  int ranges, r, g;
+  int U, pos, end;
+
+  __device__ __forceinline__ void load(const AttnArgs& a, int i, int lane, int& n, int& units) const {
+    n = units = 0;
+    const int b = 32 * i + lane;
+    if (b < a.batch) {
+      const AttnSeq q = attn_seq(a, b);
+      n = (q.sq + tokens - 1) / tokens;
+      units = (max((q.kv + kAttnKeyTile - 1) / kAttnKeyTile - 1, 0) >> a.share_shift) + 1 + kShareHead;
+    }
+  }
+  __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int lane) {
+    tokens = job_tokens;
+    ranges = gridDim.x / a.h_kv;
+    r = blockIdx.x / a.h_kv;
+    g = blockIdx.x - r * a.h_kv;
+    load(a, 0, lane, n_first, units_first);
+    int total = warp_sum_int(n_first * units_first);
+    int most = __reduce_max_sync(0xffffffffu, n_first > 0 ? units_first : 0);
+    for (int i = 1; 32 * i < a.batch; ++i) {
+      int n, units;
+      load(a, i, lane, n, units);
+      total += warp_sum_int(n * units);
+      most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? units : 0));
+    }
+    // (a job of num_splits - 1 shares touches num_splits ranges at most)
+    U = max(max(ceil_share(total, ranges), ceil_share(most - kShareHead, a.num_splits - 1)), 1);
+    const long long first = static_cast<long long>(U) * r;
+    pos = static_cast<int>(first < total ? first : total);
+    end = total - pos < U ? total : pos + U;
+  }
+  static __device__ __forceinline__ int ceil_share(int x, int y) { return x > 0 ? (x - 1) / y + 1 : 0; }
+
+  // The next piece of this CTA.
+  __device__ __forceinline__ AttnPiece next(const AttnArgs& a, int lane) {
+    AttnPiece p = {-1, 0, 0, 0, 0, -1, 0};
+    while (pos < end) {
+      int base = 0, b = -1, l = 0, off = 0, n = 0, units = 0;
+      for (int i = 0; 32 * i < a.batch; ++i) {
+        int nl = n_first, ul = units_first;
+        if (i > 0) load(a, i, lane, nl, ul);
+        const int count = nl * ul;
+        const int incl = warp_scan_incl(count, lane);
+        const int local = pos - base - (incl - count);
+        const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
+        if (hit != 0) {
+          const int src = __ffs(hit) - 1;
+          b = 32 * i + src;
+          n = __shfl_sync(0xffffffffu, nl, src);
+          units = __shfl_sync(0xffffffffu, ul, src);
+          const int at = __shfl_sync(0xffffffffu, local, src);
+          l = at / units;
+          off = at - l * units;
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      if (b < 0) {                     // (offsets that decrease)
+        pos = end;
+        break;
+      }
+      const int start = pos - off, stop = min(end, start + units);
+      const int k0 = max(off - kShareHead, 0), k1 = stop - start - kShareHead, k_all = units - kShareHead;
+      pos = start + units;
+      if (k1 <= k0) continue;          // the job's first key tile is the next range's
+      p.b = b;
+      p.g = g;
+      p.j = n - 1 - l;
+      p.tile0 = k0 << a.share_shift;
+      p.tiles = (k1 - k0) << a.share_shift;   // (of the last piece perhaps more than there are)
+      if (k0 > 0) {
+        p.slot = g * ranges + r;
+      } else if (k1 < k_all) {
+        p.slot = gridDim.x + g * ranges + r;
+        p.S = (start + units - 1) / U - r + 1;
+      }
+      return p;
+    }
+    return p;
   }
 };
 

@@ -4,7 +4,8 @@
 // head, split) a CTA of four warps, two CTAs an SM; each warp walks key blocks of
 // its own (every fourth of the job's), with a ring of its own that TMA fills page by
 // page, and its own running maximum and sum, so no warp waits for another until the four
-// results are merged at the end.
+// results are merged at the end. Where the plan forces no split count, a CTA takes an equal
+// share of the batch's work (AttnShares): parts of one or more jobs, one after the other.
 //
 // The products are mma.sync with the 16 rows as M: a tcgen05 tile has at least 64, and
 // the tensor work of 16 rows is far below either pipe's rate. bf16: blocks of 16 keys
@@ -27,12 +28,10 @@ constexpr int kWarpBytes = kStages * kStageBytes;
 constexpr int kOffBars = kWarps * kWarpBytes;
 constexpr int kOffStats = kOffBars + kWarps * kStages * 8;   // float2 [kWarps][16]: m, l
 constexpr int kOffAbort = kOffStats + kWarps * 16 * 8;
-constexpr int kSmem = kOffAbort + 16 + 1024;
-constexpr int kMergeStride = kD + 4;                    // floats a row of a warp's result (16 rows in its ring)
-static_assert(16 * kMergeStride * 4 <= kWarpBytes, "merge area");
+constexpr int kOffStage = kOffAbort + 16;               // int [kWarps]: the stage that holds a warp's result
+constexpr int kSmem = kOffStage + 16 + 1024;
+static_assert(16 * kD * 4 <= kStageBytes, "a warp's result goes through one stage");
 constexpr float kRescaleThreshold = 8.0f;
-// More jobs than a wave: a sequence is split from twice its share of the work on.
-constexpr int kRowThirds = 6;
 
 enum : uint32_t { W_R_FULL = 301, W_R_DRAIN };
 
@@ -101,67 +100,127 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   grid_dependency_wait();
 
   const int tokens = kRowRows / a.group;
-  AttnJobs jobs;                      // every warp for itself
-  jobs.init<true>(a, tokens, kRowThirds, lane);
-  const AttnJob job = jobs.find(a, blockIdx.x, lane);
+  // every warp for itself: the pieces of an equal share, or one job where the split count is given
+  AttnShares shares;
+  AttnPiece next;
+  if (a.adaptive) {
+    shares.init(a, tokens, lane);
+    next = shares.next(a, lane);
+  } else {
+    AttnJobs jobs;
+    jobs.init<false>(a, tokens, lane);
+    const AttnJob job = jobs.find(a, blockIdx.x, lane);
+    next = {job.b, job.j, job.g, 0, 0, job.S > 1 ? job.slot : -1, job.s == 0 ? job.S : 0};
+    if (job.b >= 0) {
+      const int tiles_all = (attn_seq(a, job.b).kv + kTile - 1) / kTile;
+      const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
+      next.tile0 = job.s * base_t + min(job.s, rem_t);
+      next.tiles = base_t + (job.s < rem_t ? 1 : 0);
+      // (offsets that decrease can name more split jobs than the workspace holds)
+      if (job.S > 1 && static_cast<unsigned>(job.slot) >= static_cast<unsigned>(a.max_slots)) next.b = -1;
+    }
+  }
   grid_launch_dependents();
-  // (offsets that decrease can name more split jobs than the workspace holds)
-  if (job.b < 0 || (job.S > 1 && static_cast<unsigned>(job.slot) >= static_cast<unsigned>(a.max_slots))) return;
-  const AttnSeq seq = attn_seq(a, job.b);
-  const int tok0 = job.j * tokens;
-  const int ntok = min(tokens, seq.sq - tok0);
-  const int tiles_all = (seq.kv + kTile - 1) / kTile;
-  const int base_t = tiles_all / job.S, rem_t = tiles_all - base_t * job.S;
-  const int tile0 = job.s * base_t + min(job.s, rem_t);
-  const int nt = base_t + (job.s < rem_t ? 1 : 0);
-  const int key0 = tile0 * kTile;
-  const int key_end = min((tile0 + nt) * kTile, seq.kv - seq.sq + tok0 + ntok);   // the last token's keys
-  const int blocks = key_end > key0 ? (key_end - key0 + kBlock - 1) / kBlock : 0;
-  const int cnt = blocks > warp ? (blocks - warp + kWarps - 1) / kWarps : 0;      // this warp's
 
-  // ---- this warp's loads
+  // ---- this warp's loads: they run ahead of its products, into the next piece
   const int boxes = kBlock / box_rows;                   // pages (or parts of one) of a block: 1 or 2
-  const int32_t* table = a.table + static_cast<size_t>(job.b) * a.table_width;
+  struct Loads {                      // a piece: the warp's first key, its blocks, the sequence's keys, KV head, table
+    int key, cnt, kv, g;
+    const int32_t* table;
+  };
+  auto loads_of = [&](const AttnPiece& p) {
+    const AttnSeq seq = attn_seq(a, p.b);
+    const int key0 = p.tile0 * kTile;
+    // up to the last token's keys
+    const int key_end = static_cast<int>(min(key0 + static_cast<int64_t>(p.tiles) * kTile,
+                                             static_cast<int64_t>(seq.kv - seq.sq + min((p.j + 1) * tokens, seq.sq))));
+    const int blocks = key_end > key0 ? (key_end - key0 + kBlock - 1) / kBlock : 0;
+    Loads x;
+    x.key = key0 + warp * kBlock;
+    x.cnt = blocks > warp ? (blocks - warp + kWarps - 1) / kWarps : 0;
+    x.kv = seq.kv;
+    x.g = p.g;
+    x.table = a.table + static_cast<size_t>(p.b) * a.table_width;
+    return x;
+  };
   // lane's (block, box) of a group of 32: the page, or num_pages (zeros) where there is none
-  auto lookup = [&](int first) {
+  auto lookup = [&](const Loads& x, int first) {
     const int e = first + lane;
-    const int key = key0 + (warp + kWarps * (e / boxes)) * kBlock + (e % boxes) * box_rows;
+    const int key = x.key + kWarps * kBlock * (e / boxes) + (e % boxes) * box_rows;
     int page = a.num_pages;
-    if (e < cnt * boxes && key < seq.kv) {
-      const int p = table[key >> a.page_shift];
+    if (e < x.cnt * boxes && key < x.kv) {
+      const int p = x.table[key >> a.page_shift];
       if (p >= 0 && p < a.num_pages) page = p;
     }
     return page;
   };
-  int pages = lookup(0), pages_next = lookup(32);
-  int group0 = 0;                                        // first (block, box) of `pages`
-  uint32_t have = 0;                                     // two bits a block in flight: its boxes' pages exist
-  auto issue = [&](int n) {
-    if (n * boxes - group0 >= 32) {
-      pages = pages_next;
-      group0 += 32;
-      pages_next = lookup(group0 + 32);
-    }
-    const int page = __shfl_sync(0xffffffffu, pages, (n * boxes - group0 + (lane & (boxes - 1))) & 31);
-    const unsigned got = __ballot_sync(0xffffffffu, lane < boxes && page != a.num_pages);
-    const uint32_t two = boxes == 1 ? (got & 1u) * 3u : (got & 3u);
-    have = (have & ~(3u << (2 * (n & 7)))) | (two << (2 * (n & 7)));
-    const int st = n % kStages;
-    if (lane == 0) mbar_arrive_expect_tx(bar(st), kStageBytes);
-    __syncwarp();
-    if (lane < boxes) {
-      const int key = key0 + (warp + kWarps * n) * kBlock + lane * box_rows;
-      const int row = key & ((1 << a.page_shift) - 1);
-      const uint32_t dst = ring + st * kStageBytes + lane * box_rows * 128;
-      tma_load_4d(dst, &tm_k, 0, row, page, job.g, bar(st));
-      if constexpr (!kF8) tma_load_4d(dst + kBlock * 128, &tm_k, 64, row, page, job.g, bar(st));
-      tma_load_4d(dst + kStageBytes / 2, &tm_v, 0, row, page, job.g, bar(st));
-      if constexpr (!kF8) tma_load_4d(dst + kStageBytes / 2 + kBlock * 128, &tm_v, 64, row, page, job.g, bar(st));
+  int loaded = 0, issued = 0;         // blocks of earlier pieces; blocks whose loads were started
+  uint32_t have = 0;                  // two bits a block in flight: its boxes' pages exist
+  Loads in = {0, 0, 0, 0, nullptr}, then = in;   // the piece that the loads are in, the next one
+  bool more = false;                  // `then` is there and not entered yet
+  int at = 0, group0 = 0;             // next block of `in`; first (block, box) of `pages`
+  int pages = 0, pages_next = 0, pages_then = 0;
+  auto announce = [&](const AttnPiece& p) {   // `then` = p
+    more = p.b >= 0;
+    if (more) {
+      then = loads_of(p);
+      pages_then = lookup(then, 0);
     }
   };
-#pragma unroll
-  for (int n = 0; n < kStages; ++n)
-    if (n < cnt) issue(n);
+  auto load_ahead = [&](int seen) {   // until every stage is in flight
+    while (issued - seen < kStages) {
+      if (at == in.cnt) {
+        if (!more) break;
+        more = false;
+        in = then;
+        at = group0 = 0;
+        pages = pages_then;
+        pages_next = lookup(in, 32);
+        continue;
+      }
+      if (at * boxes - group0 >= 32) {
+        pages = pages_next;
+        group0 += 32;
+        pages_next = lookup(in, group0 + 32);
+      }
+      const int page = __shfl_sync(0xffffffffu, pages, (at * boxes - group0 + (lane & (boxes - 1))) & 31);
+      const unsigned got = __ballot_sync(0xffffffffu, lane < boxes && page != a.num_pages);
+      const uint32_t two = boxes == 1 ? (got & 1u) * 3u : (got & 3u);
+      have = (have & ~(3u << (2 * (issued & 7)))) | (two << (2 * (issued & 7)));
+      const int st = issued % kStages;
+      if (lane == 0) mbar_arrive_expect_tx(bar(st), kStageBytes);
+      __syncwarp();
+      if (lane < boxes) {
+        const int key = in.key + kWarps * kBlock * at + lane * box_rows;
+        const int row = key & ((1 << a.page_shift) - 1);
+        const uint32_t dst = ring + st * kStageBytes + lane * box_rows * 128;
+        tma_load_4d(dst, &tm_k, 0, row, page, in.g, bar(st));
+        if constexpr (!kF8) tma_load_4d(dst + kBlock * 128, &tm_k, 64, row, page, in.g, bar(st));
+        tma_load_4d(dst + kStageBytes / 2, &tm_v, 0, row, page, in.g, bar(st));
+        if constexpr (!kF8) tma_load_4d(dst + kStageBytes / 2 + kBlock * 128, &tm_v, 64, row, page, in.g, bar(st));
+      }
+      ++at;
+      ++issued;
+    }
+  };
+  auto drain = [&](int seen) {        // what was started may not be writing shared memory any more when the CTA ends
+    bool done = true;
+    for (int k = seen; k < issued; ++k)
+      done = wait_drain(bar(k % kStages), (k / kStages) & 1, a.drain_limit_ns) && done;
+    if (!done && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
+  };
+  announce(next);
+#pragma unroll 1
+  while (next.b >= 0) {
+  const AttnPiece job = next;
+  const AttnSeq seq = attn_seq(a, job.b);
+  const int tok0 = job.j * tokens;
+  const int ntok = min(tokens, seq.sq - tok0);
+  load_ahead(loaded);                 // (every earlier block has been used, so the loads are in this piece now)
+  const int first_key = in.key, cnt = in.cnt;   // this warp's
+  next.b = -1;
+  if (a.adaptive) next = shares.next(a, lane);
+  announce(next);
 
   // ---- Q fragments: rows quad and quad + 8 (token r / group, head r % group)
   constexpr int kKs = kF8 ? 4 : 8;                       // MMA steps over the 128 dims
@@ -207,13 +266,14 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   int n = 0;
 #pragma unroll 1
   for (; n < cnt; ++n) {
-    const int st = n % kStages;
-    if (!wait_for<kPoll>(bar(st), (n / kStages) & 1, limit)) {
+    load_ahead(loaded + n);
+    const int st = (loaded + n) % kStages;
+    if (!wait_for<kPoll>(bar(st), ((loaded + n) / kStages) & 1, limit)) {
       ok = false;
       break;
     }
     const uint32_t ks = ring + st * kStageBytes, vs = ks + kStageBytes / 2;
-    const int key = key0 + (warp + kWarps * n) * kBlock;
+    const int key = first_key + kWarps * kBlock * n;
     if (key + kBlock > seq.kv) {
       // rows past the sequence's end: 0 * NaN would reach the result
       uint8_t* v = smem + warp * kWarpBytes + st * kStageBytes + kStageBytes / 2;
@@ -221,6 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
         *reinterpret_cast<uint4*>(v + p * 16) = make_uint4(0, 0, 0, 0);
         if constexpr (!kF8) *reinterpret_cast<uint4*>(v + kBlock * 128 + p * 16) = make_uint4(0, 0, 0, 0);
       }
+      fence_proxy_async_smem();        // (a later load writes the stage)
       __syncwarp();
     }
     float s[kNt][4];
@@ -256,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[i][k] *= sc;
     }
-    const uint32_t two = (have >> (2 * (n & 7))) & 3u;
+    const uint32_t two = (have >> (2 * ((loaded + n) & 7))) & 3u;
     if (key + kBlock - 1 > lim_min || two != 3u) {
 #pragma unroll
       for (int i = 0; i < kNt; ++i)
@@ -350,15 +411,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       }
     }
     __syncwarp();                                          // every lane has read the stage
-    if (n + kStages < cnt) issue(n + kStages);
   }
   if (!ok) {
     give_up(a, abort_flag, W_R_FULL);
-    // nothing that was started may still be writing shared memory when the CTA ends
-    bool done = true;
-    for (int k = n; k < min(n + kStages, cnt); ++k)
-      done = wait_drain(bar(k % kStages), (k / kStages) & 1, a.drain_limit_ns) && done;
-    if (!done && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
+    drain(loaded + n);
   }
 
   // ---- merge of the four warps' results
@@ -367,27 +423,35 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
   }
-  float* mine = reinterpret_cast<float*>(smem + warp * kWarpBytes);
+  // A warp's 16 x 128 fp32 go through the stage that the next load will take (at most two are in flight now). Row r's
+  // 16-byte piece c lies at c ^ c / 8 ^ 4 (r % 2) ^ r & 2 within its eight: no bank conflicts on either side.
+  auto piece_at = [](int row, int c) { return row * 512 + (((c & 24) | ((c ^ (c >> 3) ^ ((row & 1) << 2) ^ (row & 2)) & 7)) << 4); };
+  volatile int* stage_of = reinterpret_cast<volatile int*>(smem + kOffStage);
+  uint8_t* mine = smem + warp * kWarpBytes + (issued % kStages) * kStageBytes;
+  if (lane == 0) stage_of[warp] = issued % kStages;
   float2* stats = reinterpret_cast<float2*>(smem + kOffStats);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float* r = mine + (quad + 8 * h) * kMergeStride;
+    const int r = quad + 8 * h;
     if constexpr (kF8) {
 #pragma unroll
       for (int c = 0; c < 2; ++c)                          // dims 32 q4 + 16 c .. + 15
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<float4*>(r + 32 * q4 + 16 * c + 4 * j) =
+          *reinterpret_cast<float4*>(mine + piece_at(r, 8 * q4 + 4 * c + j)) =
               make_float4(o[4 * j][2 * h + c], o[4 * j + 1][2 * h + c], o[4 * j + 2][2 * h + c], o[4 * j + 3][2 * h + c]);
     } else {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        *reinterpret_cast<float2*>(r + 8 * i + 2 * q4) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+        *reinterpret_cast<float2*>(mine + piece_at(r, 2 * i + (q4 >> 1)) + 8 * (q4 & 1)) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
     }
     if (q4 == 0) stats[warp * 16 + quad + 8 * h] = make_float2(m[h], l[h]);
   }
   __syncthreads();
-  if (*abort_flag) return;
+  if (*abort_flag) {
+    if (ok) drain(loaded + cnt);
+    return;
+  }
   const int row = threadIdx.x >> 3, x0 = (threadIdx.x & 7) * 16;
   const int rt = row / a.group;
   float M = -INFINITY;
@@ -401,10 +465,10 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     const float2 st = stats[w * 16 + row];
     const float f = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
     tot = fmaf(st.y, f, tot);
-    const float4* r = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * kWarpBytes) + row * kMergeStride + x0);
+    const uint8_t* r = smem + w * kWarpBytes + stage_of[w] * kStageBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = r[i];
+      const float4 v = *reinterpret_cast<const float4*>(r + piece_at(row, (x0 >> 2) + i));
       y[4 * i] = fmaf(v.x, f, y[4 * i]);
       y[4 * i + 1] = fmaf(v.y, f, y[4 * i + 1]);
       y[4 * i + 2] = fmaf(v.z, f, y[4 * i + 2]);
@@ -421,7 +485,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     amax = fmaxf(amax, fabsf(y[i]));
   }
   const bool live = rt < ntok;
-  const bool part = job.S > 1;
+  const bool part = job.slot >= 0;
   const int64_t orow = static_cast<int64_t>(seq.q0 + tok0 + rt) * a.h_q + job.g * a.group + (row - rt * a.group);
   const int64_t prow = static_cast<int64_t>(job.slot) * kRowRows + row;
   if (live) {
@@ -430,7 +494,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     if (x0 == 0) {
       if (part) a.lse_part[prow] = lse;
       else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
-      if (a.row_map != nullptr && job.s == 0 && row == rt * a.group)
+      if (a.row_map != nullptr && (job.S > 0 || !part) && row == rt * a.group)
         a.row_map[static_cast<int64_t>(seq.q0 + tok0 + rt) * a.h_kv + job.g] = make_int2(static_cast<int>(prow), part ? job.S : 0);
     }
   }
@@ -439,6 +503,11 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
     if (lane == 0) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
+  }
+  if (next.b < 0) break;
+  loaded += cnt;
+  fence_proxy_async_smem();            // stages were read and written here; TMA writes them next
+  __syncthreads();
   }
 }
 

@@ -28,8 +28,6 @@ namespace {
 
 constexpr int kD = kAttnDim;
 constexpr int kTile = kAttnKeyTile;
-// More jobs than a wave: sequences are cut into jobs of a third of an SM's share.
-constexpr int kTileThirds = 1;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
 
 template <bool kF8>
@@ -549,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           tma_prefetch_desc(&tm_k);
           tma_prefetch_desc(&tm_v);
         }
-        jobs.init<kPaged>(a, 2 * tokens, kTileThirds, lane);
+        jobs.init<kPaged>(a, 2 * tokens, lane);
       }
 #pragma unroll 1
       for (int job = 0; ok; ++job) {
@@ -807,15 +805,19 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
     const int S = map.y;
     // (a token of no job, which only offsets that decrease can leave, has no entry: nothing outside the partials is read)
     if (S < 1 || S > a.num_splits || map.x < 0 ||
-        map.x + (S - 1ll) * rows_per_slot + a.group > static_cast<int64_t>(a.max_slots) * rows_per_slot)
+        map.x + a.group > static_cast<int64_t>(a.max_slots) * rows_per_slot ||
+        map.x + (S - 1ll) * rows_per_slot - a.part_gap + a.group > static_cast<int64_t>(a.max_slots) * rows_per_slot ||
+        (S > 1 && map.x + rows_per_slot - a.part_gap < 0))
       continue;
     {
+      // split s > 0 lies at the first one's place + s slots - part_gap rows
       const int64_t p0 = static_cast<int64_t>(map.x) + h0;
+      auto row_of = [&](int s) { return p0 + static_cast<int64_t>(s) * rows_per_slot - (s > 0 ? a.part_gap : 0); };
       const int heads = min(kHeads, a.group - h0);
       const int hl = lane / kLanes, sl = lane & (kLanes - 1);
       auto lse_at = [&](int s0) {
         const int s = s0 + sl;
-        return hl < heads && s < S ? a.lse_part[p0 + hl + static_cast<int64_t>(s) * rows_per_slot] : -INFINITY;
+        return hl < heads && s < S ? a.lse_part[row_of(s) + hl] : -INFINITY;
       };
       const float first = lse_at(0);
       float M = first, z = 0.f;
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
               x[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (ws[h][k] != 0.f)
                 x[h][k] = __ldcs(reinterpret_cast<const float4*>(
-                                     a.o_part + (p0 + h + static_cast<int64_t>(s0 + s1 + k) * rows_per_slot) * kD) + lane);
+                                     a.o_part + (row_of(s0 + s1 + k) + h) * kD) + lane);
             }
 #pragma unroll
           for (int h = 0; h < kHeads; ++h)

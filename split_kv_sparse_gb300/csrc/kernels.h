@@ -175,6 +175,8 @@ struct AttnArgs {
   int adaptive;                 // its count follows from the lengths (else: exactly num_splits)
   int num_sms;                  // jobs of one wave, over which the adaptive rule spreads the work
   int max_slots;                // split jobs that the workspace holds
+  int share_shift;              // adaptive row kernel: log2 of the key tiles of a unit of work
+  int part_gap;                 // rows that a sequence's splits after its first lie nearer to the front
   float* o_part;                // num_splits > 1: partial rows [slot][rows of a job][128], normalised
   float* lse_part;              // their log2 LSE
   int2* row_map;                // [total_q][h_kv]: first partial row of the token's group, and its split
@@ -185,9 +187,8 @@ struct AttnArgs {
 // Query rows (tokens x group) and partial rows per job of each kernel.
 constexpr int kTileRows = 256;
 constexpr int kRowRows = 16;
-// Split jobs that an automatic plan's workspace holds, in waves.
+// Split jobs of the tile kernel that an automatic plan's workspace holds, in waves.
 constexpr int kTileSplitWaves = 3;
-constexpr int kRowSplitWaves = 1;
 // tm_q: Q as 3-D [total_q][h_q][128], box {128 bytes, group heads, 128 / group tokens}; tm_k / tm_v: K and V as 4-D
 // {128, rows, pages, heads} (packed: one page of total_kv rows), box {128 bytes, min(page, 128) rows, 1, 1}; with
 // kv_wide as 5-D {64, 8 rows, column blocks, row groups, pages}, box {64, 8, 2, min(page, 128) / 8, 1}.

@@ -1,6 +1,7 @@
 """GPU tests of the paged KV cache (kv_pages_map, kv_pages_write), of attention over its pages (sdpa_paged) and over
 packed prompts (sdpa_prompt), against the integer / fp64 oracle in oracle/paged.py. Tolerances: _paged_util."""
 import math
+import types
 
 import numpy as np
 import pytest
@@ -260,6 +261,36 @@ def test_split_counts_from_the_lengths(num_sms):
     """Fewer SMs in the plan, fewer splits: same results."""
     go("e4m3", [1] * 6, [1900, 100, 700, 1, 1500, 33], 8, 2, 16, seed=1, num_sms=num_sms)
     go("bf16", [9, 30, 1], [1900, 100, 700], 8, 2, 16, seed=2, num_sms=num_sms)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("num_sms", [1, 3, 20])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_shares_that_cross_sequences(dtype, num_sms, page):
+    """CTAs that take the end of one sequence, several whole ones and the start of another; more KV heads than CTAs."""
+    rng = np.random.default_rng(num_sms)
+    kv = [int(x) for x in rng.integers(0, 700, 45)]
+    sq = [int(x) for x in rng.integers(0, 4, 45)]
+    go(dtype, sq, kv, 8, 2, page, seed=num_sms, num_sms=num_sms, max_q=2)
+    go(dtype, sq[:9], kv[:9], 10, 5, page, seed=num_sms, num_sms=num_sms, max_q=2)
+
+
+def test_decode_work_counted_in_coarser_units():
+    """Tables so wide that the key tiles of all sequences could pass 32 bits: a unit of work is several tiles."""
+    g = torch.Generator().manual_seed(5)
+    batch, page, width = 600, 65536, 1 << 15
+    c = types.SimpleNamespace(dtype="bf16", dk=1.0, dv=1.0)
+    c.k, c.v = (torch.randn((2, page, 1, D), generator=g).to(torch.bfloat16) for _ in range(2))
+    c.table = torch.full((batch, width), -1, dtype=torch.int32)
+    c.table[:, 0] = torch.arange(batch) % 2
+    c.kv_lens = torch.randint(0, 3000, (batch,), generator=g, dtype=torch.int32)
+    c.kv_lens[7], c.kv_lens[500] = 60000, 20000
+    q, dq = values(g, (batch, 4, D), "bf16")
+    cu = cu_of([1] * batch)
+    scale = 1 / math.sqrt(D)
+    k, v = c.k.double().numpy(), c.v.double().numpy()
+    ref = op.paged_attention(q.double().numpy(), k, v, c.table.numpy(), c.kv_lens.numpy(), cu.numpy(), scale)
+    check(*run_paged(c, q, dq, cu, 4), ref, "bf16")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])

@@ -50,8 +50,8 @@ def test_plan_is_deterministic_and_sizes_its_workspace():
                 p = b.sdpa_paged_plan(batch, 32, 8, 128, "e4m3", max_q, batch * max_q, 16384, num_sms=152, force_splits=S)
                 assert p.num_splits == S and p.adaptive_splits == 0 and (p.workspace_bytes == 0) == (S == 1)
             assert a.row_kernel == (max_q * 4 <= 16)
-            # one wave of split jobs (two an SM) or three (one an SM), whatever the tokens
-            rows = 304 * 16 if a.row_kernel else 3 * 152 * 256
+            # two pieces of split jobs for each of two CTAs an SM, or three waves of split jobs, whatever the tokens
+            rows = 2 * 304 * 16 if a.row_kernel else 3 * 152 * 256
             assert a.num_splits == 64 and a.adaptive_splits == 1
             assert a.o_acc_bytes == rows * 128 * 4 and a.lse_acc_bytes == rows * 4 and a.lse_acc_offset % 256 == 0
             assert a.map_offset >= a.lse_acc_offset + a.lse_acc_bytes
