@@ -510,13 +510,14 @@ typedef struct {
 
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
- * max_kv) for each sequence, from the lengths, on the GPU. With row_kernel one wave of CTAs
- * (two an SM) takes equal shares of the key tiles of all sequences, laid one after the
- * other, and a sequence is split where a share ends (shares are larger where it would
- * be split into more than the bound). Otherwise, with T = the key tiles a job should walk, it
- * gets clamp(ceil(tiles / T), 1, bound) splits: if the unsplit jobs fit one wave (num_sms
- * jobs), T is the smallest whose jobs do too, else a third of an SM's share of the work (its
- * SMs take the jobs one after the other), or more where the split jobs would not fit the workspace. An
+ * max_kv) for each sequence, from the lengths, on the GPU. With row_kernel (two CTAs an SM), and
+ * for e4m3 where the unsplit jobs pass one wave (num_sms jobs) and max_kv >= 6144, one wave of
+ * CTAs takes equal shares of the key tiles of all jobs, laid one after the other, and a job
+ * is split where a share ends (shares are larger where it would be split into more than the
+ * bound). Otherwise, with T = the key tiles a job should walk, a sequence gets
+ * clamp(ceil(tiles / T), 1, bound) splits: if the unsplit jobs fit one wave, T is the smallest whose
+ * jobs do too, else a third of an SM's share of the work (its SMs take the jobs
+ * one after the other), or more where the split jobs would not fit the workspace. An
  * unsplit sequence's rows are written at once, those of a split one by a combine kernel
  * launched behind. num_sms 0 = the current device's.
  * Errors as for mla_decode_plan (d must be 128, dtype SDPA_*, group <= 128). */

@@ -122,13 +122,16 @@ int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / token
 // Tokens of one job's rows.
 int job_tokens(bool rows16, int group) { return rows16 ? skv::kRowRows / group : 2 * (128 / group); }
 
-// CTAs of the row kernel with equal shares: as many for each KV head, one wave of them.
-int64_t row_ctas(int wave, int h_kv) { return static_cast<int64_t>(std::max(1, wave / h_kv)) * h_kv; }
-
-// Jobs that one launch may hold: unsplit, forced splits, or counts from the lengths.
-int64_t jobs_bound(int64_t unsplit, int num_splits, bool adaptive, int wave) {
-  if (!adaptive) return unsplit * num_splits;
-  return unsplit <= wave ? wave : unsplit + skv::kTileSplitWaves * wave;
+// Equal shares: of a wave's CTAs as many for each of `side` KV heads, the largest divisor of h_kv that leaves at most
+// one in sixteen without work.
+int heads_side(int wave, int h_kv) {
+  for (int side = std::min(wave, h_kv); side > 1; --side)
+    if (h_kv % side == 0 && wave % side <= wave / 16) return side;
+  return 1;
+}
+int64_t share_ctas(int wave, int h_kv) {
+  const int side = heads_side(wave, h_kv);
+  return static_cast<int64_t>(wave / side) * side;
 }
 
 int shift_of(int pow2) {
@@ -253,9 +256,9 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->adaptive_splits = adaptive;
   out->row_kernel = rows16 ? 1 : 0;
   if (S > 1) {
-    // split jobs: as many as forced, or at most so many waves (the rule keeps to that)
+    // split jobs: as many as forced; two pieces of cut jobs a CTA; at most so many waves (the rule keeps to that)
     const int64_t slots = !adaptive ? unsplit * S
-                          : rows16  ? 2 * row_ctas(wave, h_kv)   // two pieces of cut jobs a CTA
+                          : rows16  ? 2 * share_ctas(wave, h_kv)
                                     : static_cast<int64_t>(wave) * skv::kTileSplitWaves;
     if (slots * job_rows > 0x7FFFFFFFll) {
       std::memset(out, 0, sizeof(*out));
@@ -326,7 +329,6 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.lse_out = lse_out;
   a.amax = amax_out;
   a.num_splits = plan->num_splits;
-  a.adaptive = plan->adaptive_splits;
   const bool rows16 = plan->row_kernel != 0;
   a.num_sms = rows16 ? plan->num_sms * skv::kRowCtasPerSm : plan->num_sms;
   a.max_slots = static_cast<int>(plan->o_acc_bytes / ((rows16 ? skv::kRowRows : skv::kTileRows) * kDim * 4ull));
@@ -355,16 +357,29 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     return st;
   if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
-  if (rows16 && a.adaptive) {
-    // the units of all jobs have to add up to an int32
-    const int64_t tiles = (static_cast<int64_t>(table_width) << a.page_shift) / 128 + 1;
-    while (unsplit / a.h_kv * ((std::min<int64_t>(tiles, 1 << 24) >> a.share_shift) + 4) > 0x7FFFFFFFll) {
-      if (++a.share_shift > 24) return MLA_ERR_UNSUPPORTED;
-    }
-    a.part_gap = static_cast<int>(row_ctas(a.num_sms, a.h_kv)) * skv::kRowRows;
+  int64_t grid = unsplit * a.num_splits;
+  // Equal shares balance best, but let query tiles of one sequence read the same keys at different times. Decode has one
+  // query tile a sequence. With more rows, the keys of e4m3 still come from DRAM fast enough (32 KB a tile and SM in
+  // 1.4 us: 3.5 TB/s), those of bf16 do not (1,024 tokens over 65,536 keys: 641 -> 729 us); unsplit jobs that fit one
+  // wave have no second one to even out (8 x 16 over 8,192 e4m3 keys: 40.5 -> 44.6 us); and the two cut jobs of
+  // every CTA (256 rows each, and their combine) have to be small beside a sequence (e4m3, 2 x 2,048 tokens over 4,096 keys 145 ->
+  // 157 us, 8,192 308 -> 296, 16,384 638 -> 579; 4 x 300 over 9,000 169 -> 129; 40 x 16 over 9,000 185 -> 144).
+  constexpr int kLongKeys = 6144;
+  if (plan->adaptive_splits) {
+    const bool shares = rows16 || (plan->dtype == SDPA_E4M3 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);
+    a.adaptive = shares ? skv::kShares : skv::kByLength;
   }
-  const int64_t grid = rows16 && a.adaptive ? row_ctas(a.num_sms, a.h_kv)
-                                            : jobs_bound(unsplit, a.num_splits, a.adaptive != 0, a.num_sms);
+  if (a.adaptive == skv::kByLength) {
+    grid = unsplit <= a.num_sms ? a.num_sms : unsplit + static_cast<int64_t>(skv::kTileSplitWaves) * a.num_sms;
+  } else if (a.adaptive == skv::kShares) {
+    // the units of all jobs have to add up to an int32
+    const int64_t tiles = std::min<int64_t>((static_cast<int64_t>(table_width) << a.page_shift) / 128, 1 << 24);
+    a.side = heads_side(a.num_sms, a.h_kv);
+    while (unsplit / a.side * (2 * (tiles >> a.share_shift) + 32) > 0x7FFFFFFFll)
+      if (++a.share_shift > 24) return MLA_ERR_UNSUPPORTED;
+    grid = share_ctas(a.num_sms, a.h_kv);
+    a.part_gap = static_cast<int>(grid) * (rows16 ? skv::kRowRows : skv::kTileRows);
+  }
   st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
                           : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;

@@ -66,12 +66,11 @@ __device__ __forceinline__ int ceil_div(int x, int y) {
   return q;
 }
 
-struct AttnJob {
-  int b;      // sequence, -1: no job
-  int j;      // query tile of the sequence
-  int g;      // KV head
-  int s, S;   // split, and splits of this sequence
-  int slot;   // S > 1: the job's place among the split jobs
+struct AttnPiece {
+  int b, j, g;       // sequence (-1: none), query tile, KV head
+  int tile0, tiles;  // key tiles (perhaps more than the sequence has)
+  int slot;          // the piece's place among the partials, or -1: the whole job
+  int S;             // pieces of the job where this is its first, else 0
 };
 
 // The batch's jobs, found by one warp (lane by lane a sequence). Sequence b has n_b =
@@ -87,6 +86,7 @@ struct AttnJobs {
   int tokens, groups;
   int n_first, tiles_first;   // the first 32 sequences stay in registers
   int T;                      // 0: S_b = num_splits
+  int from, from_base, from_slots;   // the group of 32 sequences of the last job found, jobs and slots before it
 
   __device__ __forceinline__ void load(const AttnArgs& a, int i, int lane, int& n, int& tiles) const {
     n = tiles = 0;
@@ -115,8 +115,9 @@ struct AttnJobs {
     tokens = job_tokens;
     groups = (a.batch + 31) / 32;
     T = 0;
+    from = from_base = from_slots = 0;
     load(a, 0, lane, n_first, tiles_first);
-    if (!kSplits || !a.adaptive || a.num_splits <= 1) return;
+    if (!kSplits || a.adaptive != kByLength || a.num_splits <= 1) return;
     // The sums are floats (exact to 2^-23), and the bounds below give way by more than that. (64-bit integers cost a
     // microsecond at the start of every launch.)
     int jobs = 0, most = 1;
@@ -167,137 +168,215 @@ struct AttnJobs {
     T = hi;
   }
 
-  __device__ __forceinline__ AttnJob find(const AttnArgs& a, int idx, int lane) const {
-    AttnJob job = {-1, 0, 0, 0, 1, 0};
-    int base = 0, slots = 0;
-    for (int i = 0; i < groups && job.b < 0; ++i) {
+  // (a CTA's jobs come in rising order, as a rule)
+  template <bool kSplits>
+  __device__ __forceinline__ AttnPiece find(const AttnArgs& a, int idx, int lane) {
+    AttnPiece job = {-1, 0, 0, 0, 0, -1, 0};
+    if (idx < from_base) from = from_base = from_slots = 0;
+    int base = from_base, slots = from_slots;
+    for (int i = from; i < groups; ++i) {
       int n, tiles;
       shape(a, i, lane, n, tiles);
-      const int s = splits(a, tiles);
+      const int s = kSplits ? splits(a, tiles) : 1;
       const int count = n * s * a.h_kv;
       const int split_count = s > 1 ? count : 0;
-      const int incl = warp_scan_incl(count, lane), sincl = warp_scan_incl(split_count, lane);
+      const int incl = warp_scan_incl(count, lane), sincl = kSplits ? warp_scan_incl(split_count, lane) : 0;
       const int local = idx - base - (incl - count);
       const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
       if (hit != 0) {
+        from = i;
+        from_base = base;
+        from_slots = slots;
         const int src = __ffs(hit) - 1;
         const int l = __shfl_sync(0xffffffffu, local, src);
         const int nn = __shfl_sync(0xffffffffu, n, src);
-        const int first = __shfl_sync(0xffffffffu, slots + sincl - split_count, src);
-        job.b = 32 * i + src;
-        job.S = __shfl_sync(0xffffffffu, s, src);
+        const int all = __shfl_sync(0xffffffffu, tiles, src);
+        const int first = kSplits ? __shfl_sync(0xffffffffu, slots + sincl - split_count, src) : 0;
+        const int S = kSplits ? __shfl_sync(0xffffffffu, s, src) : 1;
         const int rest = l / a.h_kv;
+        job.b = 32 * i + src;
         job.g = l - rest * a.h_kv;
-        const int tile = rest / job.S;
-        job.s = rest - tile * job.S;
-        job.j = nn - 1 - tile;
-        job.slot = first + (job.j * a.h_kv + job.g) * job.S + job.s;
+        job.j = nn - 1 - rest;
+        job.tiles = all;
+        if (S > 1) {
+          const int tile = rest / S, at = rest - tile * S;
+          job.j = nn - 1 - tile;
+          const int each = all / S, more = all - each * S;
+          job.tile0 = at * each + min(at, more);
+          job.tiles = each + (at < more ? 1 : 0);
+          job.slot = first + (job.j * a.h_kv + job.g) * S + at;
+          job.S = at == 0 ? S : 0;
+          // (offsets that decrease can name more split jobs than the workspace holds)
+          if (static_cast<unsigned>(job.slot) >= static_cast<unsigned>(a.max_slots)) job.b = -1;
+        }
+        break;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
-      slots += __shfl_sync(0xffffffffu, sincl, 31);
+      if (kSplits) slots += __shfl_sync(0xffffffffu, sincl, 31);
     }
     return job;
   }
 };
 
-// Equal shares of the batch's work (the kernel of 16-row jobs). Its jobs (sequence, query tile)
-// lie one after the other on a line, each as kShareHead units for its start and end and
-// then a unit for every 2^share_shift key tiles (one at least). Range r of R = num_sms /
-// h_kv takes the units [r U, (r + 1) U), by one CTA for each KV head: the heads of a row lie
-// side by side in memory, and read at one time they share DRAM rows (128 sequences of 2,048
-// e4m3 keys, 8 KV heads: 98 us, with the heads one after the other on the line 141; one job a CTA
-// 118). A job that crosses no boundary is written at once; the pieces of one that does are partials: a CTA
-// has at most one piece that begins its job (slot R h_kv + g R + r) and one that goes on with
-// it (slot g R + r), so the pieces of a job that begins in range r lie at R h_kv + g R + r, then
-// g R + r + 1, g R + r + 2, ..
-constexpr int kShareHead = 2;
-struct AttnPiece {
-  int b, j, g;       // sequence (-1: none), query tile, KV head
-  int tile0, tiles;  // key tiles
-  int slot;          // -1: the whole job
-  int S;             // pieces of the job where this is its first, else 0
-};
+// Equal shares of the batch's work for one wave of CTAs. Its jobs (sequence, query tile,
+// group of side heads) lie one after the other on a line, each as kHead units for its start
+// and end and then kWeight units for every 2^share_shift key tiles that its tokens see (or
+// one more; half as many where a job of the tile kernel has one row block only). Range r of R
+// takes the units [r U, (r + 1) U), by one CTA for each of the side heads: the heads of a row
+// lie side by side in memory, and read at one time they share DRAM rows (decode of 128 sequences of
+// 2,048 e4m3 keys, 8 KV heads: 98 us, with the heads one after the other on the line 141; one
+// job a CTA 118). A job that crosses no boundary is written at once; the pieces of one
+// that does are partials. A CTA has at most one piece that begins a cut job (slot R side + h R +
+// r, h its head of the group) and one that goes on with one (slot h R + r), so the pieces of a
+// job lie at R side + h R + r, then h R + r + 1, h R + r + 2, ..
+template <int kWeight, int kHead>
 struct AttnShares {
-  int tokens;
-  int n_first, units_first;   // the first 32 sequences: query tiles, units of a job
-  int ranges, r, g;
-  int U, pos, end;
+  int tokens;               // of a job
+  int R, r, h;              // ranges; this CTA's range and head of a group
+  int U, pos, end;          // units of a range; the next one of this CTA, its last
+  int b, n, sq, kv;         // the sequence at pos: query tiles, tokens, keys
+  int job, group, off;      // in it: the job (its last query tile is job 0), head group, units before pos
+  uint32_t frac;            // running sum of the key tiles before the job: what was rounded off
 
-  __device__ __forceinline__ void load(const AttnArgs& a, int i, int lane, int& n, int& units) const {
-    n = units = 0;
-    const int b = 32 * i + lane;
+  // Job i of a sequence sees ceil(x_i / 128) key tiles, x_i = kv - sq + (n - i) tokens (all of the sequence's where
+  // it has fewer keys than tokens). The running sum of (x_i + 127) / 128, rounded down, gives each job at least as many.
+  // (kWeight 1: a job has at most 16 tokens, and counts all of its sequence's tiles.)
+  __device__ __forceinline__ uint32_t keys_up(const AttnArgs& a, int i) const {
+    if constexpr (kWeight == 1) {
+      const uint32_t up = (1u << (7 + a.share_shift)) - 1u;
+      return (max(kv, 1) + up) & ~up;
+    }
+    const bool behind = kv >= sq && kv > 0;
+    const uint32_t x = (behind ? kv - sq : max(kv, 1)) + (1u << (7 + a.share_shift)) - 1u;
+    return x + (behind ? static_cast<uint32_t>(tokens * (n - i)) : 0u);
+  }
+  // 128 << share_shift times the key tiles of the jobs before i.
+  __device__ __forceinline__ unsigned long long sum_before(const AttnArgs& a, int i) const {
+    const unsigned long long first = keys_up(a, 0), step = kv >= sq && kv > 0 ? tokens : 0, m = i;
+    return m * first - step * (m * (m - (i > 0)) / 2);
+  }
+  // (kWeight 2: a job of at most tokens / 2 tokens has one row block)
+  __device__ __forceinline__ int weight_of(int i) const {
+    return kWeight == 2 && i == 0 && sq - (n - 1) * tokens <= tokens / 2 ? 1 : kWeight;
+  }
+  __device__ __forceinline__ int units_before(const AttnArgs& a, int i) const {
+    const int sh = 7 + a.share_shift;
+    if constexpr (kWeight == 1) return i * (kHead + static_cast<int>(keys_up(a, 0) >> sh));
+    const int one = i > 0 && weight_of(0) < kWeight ? static_cast<int>(keys_up(a, 0) >> sh) : 0;
+    return i * kHead + kWeight * static_cast<int>(sum_before(a, i) >> sh) - one;
+  }
+  __device__ __forceinline__ void load(const AttnArgs& a, int seq) {
+    b = seq;
+    n = sq = kv = 0;
     if (b < a.batch) {
       const AttnSeq q = attn_seq(a, b);
-      n = (q.sq + tokens - 1) / tokens;
-      units = (max((q.kv + kAttnKeyTile - 1) / kAttnKeyTile - 1, 0) >> a.share_shift) + 1 + kShareHead;
+      sq = q.sq;
+      kv = q.kv;
+      n = (sq + tokens - 1) / tokens;
     }
   }
+
   __device__ __forceinline__ void init(const AttnArgs& a, int job_tokens, int lane) {
     tokens = job_tokens;
-    ranges = gridDim.x / a.h_kv;
-    r = blockIdx.x / a.h_kv;
-    g = blockIdx.x - r * a.h_kv;
-    load(a, 0, lane, n_first, units_first);
-    int total = warp_sum_int(n_first * units_first);
-    int most = __reduce_max_sync(0xffffffffu, n_first > 0 ? units_first : 0);
-    for (int i = 1; 32 * i < a.batch; ++i) {
-      int n, units;
-      load(a, i, lane, n, units);
-      total += warp_sum_int(n * units);
-      most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? units : 0));
+    const int groups = a.h_kv / a.side;
+    R = gridDim.x / a.side;
+    r = blockIdx.x / a.side;
+    h = blockIdx.x - r * a.side;
+    int total = 0, most = 0, count = 0;
+    for (int i = (a.batch - 1) / 32; i >= 0; --i) {   // (the first 32 sequences last: they stay for the search)
+      load(a, 32 * i + lane);
+      count = groups * units_before(a, n);
+      total += warp_sum_int(count);
+      most = max(most, __reduce_max_sync(0xffffffffu, n > 0 ? (max(kv, 1) + tokens) >> (7 + a.share_shift) : 0));
     }
-    // (a job of num_splits - 1 shares touches num_splits ranges at most)
-    U = max(max(ceil_share(total, ranges), ceil_share(most - kShareHead, a.num_splits - 1)), 1);
+    // (a job of num_splits - 1 shares touches num_splits ranges at most; a share has a key tile of every job in it)
+    U = max(max((total + R - 1) / R, kWeight * (most + 2) / (a.num_splits - 1) + 1), kWeight);
     const long long first = static_cast<long long>(U) * r;
     pos = static_cast<int>(first < total ? first : total);
     end = total - pos < U ? total : pos + U;
-  }
-  static __device__ __forceinline__ int ceil_share(int x, int y) { return x > 0 ? (x - 1) / y + 1 : 0; }
-
-  // The next piece of this CTA.
-  __device__ __forceinline__ AttnPiece next(const AttnArgs& a, int lane) {
-    AttnPiece p = {-1, 0, 0, 0, 0, -1, 0};
-    while (pos < end) {
-      int base = 0, b = -1, l = 0, off = 0, n = 0, units = 0;
-      for (int i = 0; 32 * i < a.batch; ++i) {
-        int nl = n_first, ul = units_first;
-        if (i > 0) load(a, i, lane, nl, ul);
-        const int count = nl * ul;
-        const int incl = warp_scan_incl(count, lane);
-        const int local = pos - base - (incl - count);
-        const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
-        if (hit != 0) {
-          const int src = __ffs(hit) - 1;
-          b = 32 * i + src;
-          n = __shfl_sync(0xffffffffu, nl, src);
-          units = __shfl_sync(0xffffffffu, ul, src);
-          const int at = __shfl_sync(0xffffffffu, local, src);
-          l = at / units;
-          off = at - l * units;
-          break;
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
+    if (pos >= end) return;
+    int base = 0, at = -1;
+    for (int i = 0; 32 * i < a.batch; ++i) {
+      if (i > 0) {
+        load(a, 32 * i + lane);
+        count = groups * units_before(a, n);
       }
-      if (b < 0) {                     // (offsets that decrease)
-        pos = end;
+      const int incl = warp_scan_incl(count, lane);
+      const int local = pos - base - (incl - count);
+      const unsigned hit = __ballot_sync(0xffffffffu, local >= 0 && local < count);
+      if (hit != 0) {
+        const int src = __ffs(hit) - 1;
+        b = 32 * i + src;
+        n = __shfl_sync(0xffffffffu, n, src);
+        sq = __shfl_sync(0xffffffffu, sq, src);
+        kv = __shfl_sync(0xffffffffu, kv, src);
+        at = __shfl_sync(0xffffffffu, local, src);
         break;
       }
-      const int start = pos - off, stop = min(end, start + units);
-      const int k0 = max(off - kShareHead, 0), k1 = stop - start - kShareHead, k_all = units - kShareHead;
-      pos = start + units;
-      if (k1 <= k0) continue;          // the job's first key tile is the next range's
-      p.b = b;
-      p.g = g;
-      p.j = n - 1 - l;
-      p.tile0 = k0 << a.share_shift;
-      p.tiles = (k1 - k0) << a.share_shift;   // (of the last piece perhaps more than there are)
-      if (k0 > 0) {
-        p.slot = g * ranges + r;
-      } else if (k1 < k_all) {
-        p.slot = gridDim.x + g * ranges + r;
-        p.S = (start + units - 1) / U - r + 1;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (at < 0) {                    // (offsets that decrease)
+      pos = end;
+      return;
+    }
+    job = 0;
+    if constexpr (kWeight == 1) {
+      if (n > 1) job = at / (groups * units_before(a, 1));
+    } else {
+      for (int hi = n; hi - job > 1;) {
+        const int mid = (job + hi) >> 1;
+        if (groups * units_before(a, mid) <= at) job = mid;
+        else hi = mid;
       }
-      return p;
+    }
+    const int before = units_before(a, job);
+    off = at - groups * before;
+    group = 0;
+    if (groups > 1) {
+      const int units = units_before(a, job + 1) - before;
+      group = off / units;
+      off -= group * units;
+    }
+    frac = kWeight == 1 ? 0u : static_cast<uint32_t>(sum_before(a, job)) & ((128u << a.share_shift) - 1u);
+  }
+
+  // The next piece of this CTA.
+  __device__ __forceinline__ AttnPiece next(const AttnArgs& a) {
+    AttnPiece p = {-1, 0, 0, 0, 0, -1, 0};
+    while (pos < end && p.b < 0) {
+      const uint32_t sum = frac + keys_up(a, job);
+      const int weight = weight_of(job), k_all = static_cast<int>(sum >> (7 + a.share_shift));
+      const int units = kHead + weight * k_all;
+      const int start = pos - off, stop = min(end, start + units);
+      // key tile k (of 2^share_shift) is the unit start + kHead + weight k
+      auto ceil_w = [&](int x) { return x <= 0 ? 0 : kWeight == 2 && weight == 2 ? (x + 1) >> 1 : x; };
+      const int k0 = ceil_w(off - kHead), k1 = ceil_w(stop - start - kHead);
+      if (k1 > k0) {                   // (else the job's first key tile is the next range's)
+        p.b = b;
+        p.g = group * a.side + h;
+        p.j = n - 1 - job;
+        p.tile0 = k0 << a.share_shift;
+        p.tiles = (k1 - k0) << a.share_shift;
+        if (k0 > 0) {
+          p.slot = h * R + r;
+        } else if (k1 < k_all) {
+          p.slot = gridDim.x + h * R + r;
+          p.S = (start + kHead + weight * (k_all - 1)) / U - r + 1;
+        }
+      }
+      pos = start + units;
+      off = 0;
+      if (pos < end && (++group) * a.side == a.h_kv) {
+        group = 0;
+        frac = sum & ((128u << a.share_shift) - 1u);
+        if (++job == n) {
+          job = 0;
+          frac = 0;
+          do load(a, b + 1);
+          while (n == 0 && b < a.batch);
+          if (b >= a.batch) pos = end;   // (offsets that decrease)
+        }
+      }
     }
     return p;
   }

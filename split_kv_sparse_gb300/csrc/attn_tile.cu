@@ -29,6 +29,8 @@ namespace {
 constexpr int kD = kAttnDim;
 constexpr int kTile = kAttnKeyTile;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
+// A piece's start and end, in halves of a key tile of an equal share (2 to 12 measure alike).
+constexpr int kTileHead = 4;
 
 template <bool kF8>
 struct Cfg {
@@ -47,7 +49,8 @@ struct Cfg {
   static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
   static constexpr int kOffMisc = kOffBars + 352;
   static constexpr int kOffStats = kOffMisc + 384;       // float2 [128 rows]: m, l of stream 1
-  static constexpr int kSmem = kOffStats + 1024 + 1024;
+  static constexpr int kOffShares = kOffStats + 1024;
+  static constexpr int kSmem = kOffShares + 128 + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
   static constexpr int kConsumers = kF8 ? 16 : 12;       // warps that read a job's description
 };
@@ -68,7 +71,7 @@ constexpr uint32_t kTmemS = 0, kTmemP = 128, kTmemO = 256;   // S; P_0, P_1 (64 
 // What the roles need of a job, worked out once by the scheduler warp; two of them are
 // in flight.
 enum {
-  J_B, J_G, J_SPLIT, J_S, J_SLOT, J_Q0, J_SQ, J_K0, J_KV,
+  J_B, J_G, J_S, J_SLOT, J_Q0, J_SQ, J_K0, J_KV,
   J_TOK0,             // first token (of the sequence) of row block 0
   J_TILE0, J_TILES,   // first key tile and count that the job walks
   J_ONE,              // one row block
@@ -79,13 +82,14 @@ enum {
 enum { M_TMEM = 0, M_ABORT, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
 static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
-// kPaged: K and V in pages, split jobs; else packed and whole (a kernel of its own, since
-// the loops' code has to stay near in the instruction caches).
-template <bool kF8, bool kPaged, bool kPoll>
+// kPages: 0 packed K and V, jobs never split; 1 pages; 2 pages in equal shares (kernels of their
+// own, since the loops' code has to stay near in the instruction caches).
+template <bool kF8, int kPages, bool kPoll>
 __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
   using C = Cfg<kF8>;
+  constexpr bool kPaged = kPages > 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     for (int job = 0;; ++job) {
     volatile int* w;
     if (!job_at(job, w) || w[J_B] < 0) break;
-    const int g = w[J_G], split = w[J_SPLIT], S = w[J_S], slot0 = w[J_SLOT], q0 = w[J_Q0], sq = w[J_SQ], kv = w[J_KV],
+    const int g = w[J_G], S = w[J_S], slot0 = w[J_SLOT], q0 = w[J_Q0], sq = w[J_SQ], kv = w[J_KV],
               tok0 = w[J_TOK0], tile0 = w[J_TILE0], tiles = w[J_TILES], cnt0 = w[J_CNT0], cnt1 = w[J_CNT1];
     const bool one = w[J_ONE] != 0;
     job_read(job);
@@ -280,11 +284,11 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const float lse = some ? m_run + log2f(l) : -INFINITY;
         const int64_t orow = static_cast<int64_t>(q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
         const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
-        const bool part = kPaged && S > 1;
+        const bool part = kPaged && slot0 >= 0;
         if (live) {
           if (part) a.lse_part[prow] = lse;
           else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
-          if (kPaged && a.row_map != nullptr && split == 0 && row == rt * a.group)
+          if (kPaged && a.row_map != nullptr && (S > 0 || !part) && row == rt * a.group)
             a.row_map[static_cast<int64_t>(q0 + tok) * a.h_kv + g] = make_int2(static_cast<int>(prow), part ? S : 0);
         }
         // A thread stores its own row, whole 32-byte sectors at a time: no place in shared memory is needed, so the next
@@ -517,6 +521,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       int done = 0;                                        // tiles whose loads were started
       int with_tiles = 0;
       AttnJobs jobs;
+      // (in shared memory between the jobs: the loads' loop needs the registers)
+      auto shares_at = reinterpret_cast<AttnShares<2, kTileHead>*>(smem + C::kOffShares);
+      static_assert(sizeof(AttnShares<2, kTileHead>) <= 128, "shares area");
+      constexpr bool shared = kPages == 2;
       int idx = blockIdx.x, asked = 0;
       auto take_over = [&]() {                             // the index of a CTA that was pending, or -1
         if (lane == 0) {
@@ -537,66 +545,76 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           tma_prefetch_desc(&tm_k);
           tma_prefetch_desc(&tm_v);
         }
-        jobs.init<kPaged>(a, 2 * tokens, lane);
-      }
-#pragma unroll 1
-      for (int job = 0; ok; ++job) {
-        volatile int* w;
-        if (is_k) {
-          ok = job_at(job, w);
+        if constexpr (shared) {
+          AttnShares<2, kTileHead> shares;
+          shares.init(a, 2 * tokens, lane);
+          if (lane == 0) *shares_at = shares;
+          __syncwarp();
         } else {
-          // ---- the next job
-          AttnJob next = {-1, 0, 0, 0, 1, 0};
+          jobs.init<kPaged>(a, 2 * tokens, lane);
+        }
+      }
+      // Works out job number `job` and writes its words.
+      auto describe = [&](int job) {
+        AttnPiece next = {-1, 0, 0, 0, 0, -1, 0};
+        if constexpr (shared) {
+          AttnShares<2, kTileHead> shares = *shares_at;
+          next = shares.next(a);
+          __syncwarp();
+          if (lane == 0) *shares_at = shares;
+          __syncwarp();
+        } else {
           if (job > 0) idx = take_over();
           while (ok && idx >= 0) {
-            next = jobs.find(a, idx, lane);
+            next = jobs.find<kPaged>(a, idx, lane);
             if (next.b >= 0) break;
             idx = take_over();   // (an index past the batch's jobs; the grid is sized by a bound)
           }
-          w = misc + M_JOBS + (job & 1) * kJobWords;
-          ok = ok && (job < 2 || wait_for<kPoll>(bar(B_READ0 + (job & 1)), ((job >> 1) - 1) & 1, limit));
-          if (!ok) break;
-          if (lane == 0) {
-            w[J_B] = next.b;
-            if (next.b >= 0) {
-              const AttnSeq seq = attn_seq(a, next.b);
-              const int tok0 = next.j * 2 * tokens;
-              const int tiles_all = (seq.kv + kTile - 1) / kTile;
-              const int base_t = tiles_all / next.S, rem_t = tiles_all - base_t * next.S;
-              const int tile0 = next.s * base_t + min(next.s, rem_t);
-              const int nt = base_t + (next.s < rem_t ? 1 : 0);
-              // key tiles of row block i: up to the position of its last token
-              auto tiles_of = [&](int i) {
-                const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
-                if (last < tok0 + i * tokens) return 0;
-                const int keys = seq.kv - seq.sq + last + 1;
-                return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
-              };
-              // (offsets that decrease can name more split jobs than the workspace holds: such a job has no rows)
-              const bool over = kPaged && next.S > 1 && static_cast<unsigned>(next.slot) >= static_cast<unsigned>(a.max_slots);
-              const bool one = over || tok0 + tokens >= seq.sq;
-              const int n0 = tiles_of(0), n1 = tiles_of(1);  // n1 >= n0 where there is a second block
-              const int tiles = over ? 0 : one ? n0 : n1;
-              w[J_G] = next.g;
-              w[J_SPLIT] = next.s;
-              w[J_S] = next.S;
-              w[J_SLOT] = next.slot;
-              w[J_Q0] = seq.q0;
-              w[J_SQ] = over ? 0 : seq.sq;
-              w[J_K0] = seq.k0;
-              w[J_KV] = seq.kv;
-              w[J_TOK0] = tok0;
-              w[J_TILE0] = tile0;
-              w[J_TILES] = tiles;
-              w[J_ONE] = one;
-              w[J_CNT0] = one ? (tiles + 1) >> 1 : n0;
-              w[J_CNT1] = one ? tiles >> 1 : n1;
-              w[J_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
-            }
-            mbar_arrive(bar(B_JOB0 + (job & 1)));
-          }
-          __syncwarp();
         }
+        volatile int* w = misc + M_JOBS + (job & 1) * kJobWords;
+        ok = ok && (job < 2 || wait_for<kPoll>(bar(B_READ0 + (job & 1)), ((job >> 1) - 1) & 1, limit));
+        if (!ok) return;
+        if (lane == 0) {
+          w[J_B] = next.b;
+          if (next.b >= 0) {
+            const AttnSeq seq = attn_seq(a, next.b);
+            const int tok0 = next.j * 2 * tokens;
+            const int tiles_all = (seq.kv + kTile - 1) / kTile;
+            const int tile0 = next.tile0, nt = max(min(next.tiles, tiles_all - tile0), 0);
+            // key tiles of row block i: up to the position of its last token
+            auto tiles_of = [&](int i) {
+              const int last = min(tok0 + (i + 1) * tokens, seq.sq) - 1;
+              if (last < tok0 + i * tokens) return 0;
+              const int keys = seq.kv - seq.sq + last + 1;
+              return min(max((keys + kTile - 1) / kTile - tile0, 0), nt);
+            };
+            const bool one = tok0 + tokens >= seq.sq;
+            const int n0 = tiles_of(0), n1 = tiles_of(1);  // n1 >= n0 where there is a second block
+            const int tiles = one ? n0 : n1;
+            w[J_G] = next.g;
+            w[J_S] = next.S;
+            w[J_SLOT] = next.slot;
+            w[J_Q0] = seq.q0;
+            w[J_SQ] = seq.sq;
+            w[J_K0] = seq.k0;
+            w[J_KV] = seq.kv;
+            w[J_TOK0] = tok0;
+            w[J_TILE0] = tile0;
+            w[J_TILES] = tiles;
+            w[J_ONE] = one;
+            w[J_CNT0] = one ? (tiles + 1) >> 1 : n0;
+            w[J_CNT1] = one ? tiles >> 1 : n1;
+            w[J_TAIL] = (seq.kv & (kTile - 1)) != 0 && tiles_all - 1 - tile0 < tiles ? tiles_all - 1 - tile0 : -1;
+          }
+          mbar_arrive(bar(B_JOB0 + (job & 1)));
+        }
+        __syncwarp();
+      };
+#pragma unroll 1
+      for (int job = 0; ok; ++job) {
+        if (!is_k) describe(job);
+        volatile int* w;
+        ok = ok && job_at(job, w);
         if (!ok || w[J_B] < 0) break;
         const int job_b = w[J_B], g = w[J_G], q0 = w[J_Q0], k0 = w[J_K0], kv = w[J_KV], tok0 = w[J_TOK0], tile0 = w[J_TILE0],
                   tiles = w[J_TILES], tail = w[J_TAIL];
@@ -877,17 +895,20 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
 
 namespace {
 using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
-// [e4m3][paged][polling waits]
-constexpr TileKernel kTileKernels[2][2][2] = {
-    {{attn_tile_kernel<false, false, false>, attn_tile_kernel<false, false, true>},
-     {attn_tile_kernel<false, true, false>, attn_tile_kernel<false, true, true>}},
-    {{attn_tile_kernel<true, false, false>, attn_tile_kernel<true, false, true>},
-     {attn_tile_kernel<true, true, false>, attn_tile_kernel<true, true, true>}}};
+// [e4m3][pages][polling waits]; bf16 takes no equal shares
+constexpr TileKernel kTileKernels[2][3][2] = {
+    {{attn_tile_kernel<false, 0, false>, attn_tile_kernel<false, 0, true>},
+     {attn_tile_kernel<false, 1, false>, attn_tile_kernel<false, 1, true>},
+     {nullptr, nullptr}},
+    {{attn_tile_kernel<true, 0, false>, attn_tile_kernel<true, 0, true>},
+     {attn_tile_kernel<true, 1, false>, attn_tile_kernel<true, 1, true>},
+     {attn_tile_kernel<true, 2, false>, attn_tile_kernel<true, 2, true>}}};
 }  // namespace
 
 cudaError_t prepare_attn_tile() {
   for (int f8 = 0; f8 < 2; ++f8)
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 6; ++k) {
+      if (kTileKernels[f8][k >> 1][k & 1] == nullptr) continue;
       const cudaError_t e = cudaFuncSetAttribute(kTileKernels[f8][k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem);
       if (e != cudaSuccess) return e;
@@ -899,7 +920,9 @@ cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, c
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream) {
   if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
   const bool f8 = dtype == 2;
-  return launch_pdl(kTileKernels[f8][a.table != nullptr][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid),
+  const int pages = a.table == nullptr ? 0 : a.adaptive == kShares ? 2 : 1;
+  if (kTileKernels[f8][pages][0] == nullptr) return cudaErrorInvalidValue;
+  return launch_pdl(kTileKernels[f8][pages][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid),
                     f8 ? Cfg<true>::kThreads : Cfg<false>::kThreads, f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem, stream, tm_q,
                     tm_k, tm_v, a);
 }

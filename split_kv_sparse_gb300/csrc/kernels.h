@@ -147,6 +147,7 @@ cudaError_t launch_sdpa_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const SdpaArgs& a, bool direct, cudaStream_t stream);
 
 // Attention of packed queries over a paged cache or over packed K and V.
+constexpr int kByLength = 1, kShares = 2;   // rules of AttnArgs::adaptive
 struct AttnArgs {
   const void* q;                // element (token, head, x) at token * q_ts + head * q_hs + x
   const void* k;                // paged: element (page, row, head, x) at page * kv_ps + row * kv_rs +
@@ -172,11 +173,12 @@ struct AttnArgs {
   float* lse_out;
   float* amax;
   int num_splits;               // the most splits a sequence gets
-  int adaptive;                 // its count follows from the lengths (else: exactly num_splits)
-  int num_sms;                  // jobs of one wave, over which the adaptive rule spreads the work
+  int adaptive;                 // its count follows from the lengths: kByLength or kShares (0: exactly num_splits)
+  int num_sms;                  // jobs of one wave, over which the adaptive rules spread the work
   int max_slots;                // split jobs that the workspace holds
-  int share_shift;              // adaptive row kernel: log2 of the key tiles of a unit of work
-  int part_gap;                 // rows that a sequence's splits after its first lie nearer to the front
+  int side;                     // kShares: KV heads whose CTAs walk the same keys side by side
+  int share_shift;              // kShares: log2 of the key tiles of a unit of work
+  int part_gap;                 // kShares: rows that a sequence's splits after its first lie nearer to the front
   float* o_part;                // num_splits > 1: partial rows [slot][rows of a job][128], normalised
   float* lse_part;              // their log2 LSE
   int2* row_map;                // [total_q][h_kv]: first partial row of the token's group, and its split

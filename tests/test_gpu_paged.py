@@ -275,6 +275,16 @@ def test_decode_shares_that_cross_sequences(dtype, num_sms, page):
     go(dtype, sq[:9], kv[:9], 10, 5, page, seed=num_sms, num_sms=num_sms, max_q=2)
 
 
+@pytest.mark.parametrize("num_sms", [1, 3, 20])
+@pytest.mark.parametrize("h_q,h_kv", [(8, 2), (10, 5), (96, 1)])
+def test_chunk_shares_that_cross_sequences(num_sms, h_q, h_kv):
+    """e4m3 over long tables: ranges that end in a sequence's query tiles, rows that see no key, one row block or two."""
+    rng = np.random.default_rng(num_sms + h_q)
+    kv = [int(x) for x in rng.integers(0, 900, 12)] + [0, 40, 1000]
+    sq = [int(x) for x in rng.integers(0, 260, 12)] + [9, 90, 0]
+    go("e4m3", sq, kv, h_q, h_kv, 32, seed=num_sms, num_sms=num_sms, max_kv=9000)
+
+
 def test_decode_work_counted_in_coarser_units():
     """Tables so wide that the key tiles of all sequences could pass 32 bits: a unit of work is several tiles."""
     g = torch.Generator().manual_seed(5)
