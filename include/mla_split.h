@@ -584,14 +584,15 @@ MLA_API int mla_get_status(uint32_t* status_out, uint32_t* site_out);
 MLA_API int mla_selftest_wait_timeout(uint64_t limit_ns, void* stream);
 
 /* Sets the time limit of the decode kernels' pipeline waits (every mbarrier
- * wait of the sparse-MLA and the dense kernels' roles) for the calls launched
+ * wait of the sparse-MLA, dense, paged and prompt kernels' roles) for the calls launched
  * after it, process wide. limit_ns = 0 restores the default of 2 s; otherwise
  * 100 ns .. 10 s, else MLA_ERR_INVALID_ARG. A wait that runs out records
  * MLA_STATUS_TIMEOUT and the wait's site in the status word (mla_get_status) and
  * aborts its CTA: the other roles stop at their next wait, the CTA waits (up to
  * 2 s, whatever this limit) for its own copies and MMAs in flight, frees its
  * tensor memory and exits; the call's outputs are then undefined. For tests of
- * that abort path: a limit far below a step's latency makes real waits run out.
+ * that abort path: a limit far below a step's latency makes real waits run out. The
+ * paged and prompt kernels wait 4 s at most, and below 20 us take instances that poll.
  * The pages have no counterpart (failure handling of this library). */
 MLA_API int mla_set_wait_limit_ns(uint64_t limit_ns);
 

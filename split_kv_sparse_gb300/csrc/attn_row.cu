@@ -1,11 +1,13 @@
 // Attention of few query rows (at most 16: the tokens x the heads of one group) over
 // a paged cache: decode. Every K and V element is read once and used for 16 rows, so
-// HBM bounds it, and the kernel is built around bytes in flight: one job (sequence, KV
-// head, split) a CTA of four warps, two CTAs an SM; each warp walks key blocks of
-// its own (every fourth of the job's), with a ring of its own that TMA fills page by
-// page, and its own running maximum and sum, so no warp waits for another until the four
-// results are merged at the end. Where the plan forces no split count, a CTA takes an equal
-// share of the batch's work (AttnShares): parts of one or more jobs, one after the other.
+// HBM bounds it, and the kernel is built around bytes in flight (196 KB an SM): four warps a CTA,
+// two CTAs an SM; each warp walks key blocks of its own (every fourth of a job's), with a
+// ring of its own that TMA fills page by page, and its own running maximum and sum, so no
+// warp waits for another until the four results of a job are merged. Where the plan forces
+// no split count, a CTA takes an equal share of the batch's work (AttnShares): pieces of one or more
+// jobs, one after the other, the loads running ahead into the next. Measured with 32 query and 8
+// KV heads: 96 sequences of 100 to 12,000 bf16 keys 334 us (6.5 TB/s; one job a CTA 367),
+// 256 of 500 106 us (148), 8 of 65,536 e4m3 keys 167 us (6.4 TB/s), 8 of 1,024 to 16,384 35.5 us.
 //
 // The products are mma.sync with the 16 rows as M: a tcgen05 tile has at least 64, and
 // the tensor work of 16 rows is far below either pipe's rate. bf16: blocks of 16 keys
