@@ -301,13 +301,8 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if (amax_out != nullptr && (st = cuda_status(cudaMemsetAsync(amax_out, 0, sizeof(float), cs))) != MLA_OK) return st;
   skv::AttnArgs a{};
   a.q = q;
-  a.k = pages->k;
-  a.v = pages->v;
   a.q_ts = q_token_stride;
   a.q_hs = q_head_stride;
-  a.kv_ps = pages->page_stride;
-  a.kv_rs = pages->row_stride;
-  a.kv_hs = pages->head_stride;
   a.table = block_table;
   a.table_width = table_width;
   a.page_shift = shift_of(pages->page_size);
@@ -376,7 +371,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     const int64_t tiles = std::min<int64_t>((static_cast<int64_t>(table_width) << a.page_shift) / 128, 1 << 24);
     a.side = heads_side(a.num_sms, a.h_kv);
     while (unsplit / a.side * (2 * (tiles >> a.share_shift) + 32) > 0x7FFFFFFFll)
-      if (++a.share_shift > 24) return MLA_ERR_UNSUPPORTED;
+      if (++a.share_shift > 16) return MLA_ERR_UNSUPPORTED;   // (four million jobs)
     grid = share_ctas(a.num_sms, a.h_kv);
     a.part_gap = static_cast<int>(grid) * (rows16 ? skv::kRowRows : skv::kTileRows);
   }
@@ -411,12 +406,8 @@ int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int
   if (amax_out != nullptr && (st = cuda_status(cudaMemsetAsync(amax_out, 0, sizeof(float), cs))) != MLA_OK) return st;
   skv::AttnArgs a{};
   a.q = q;
-  a.k = k;
-  a.v = v;
   a.q_ts = q_token_stride;
   a.q_hs = q_head_stride;
-  a.kv_rs = kv_token_stride;
-  a.kv_hs = kv_head_stride;
   a.cu_q = cu_seqlens_q;
   a.cu_kv = cu_seqlens_kv;
   a.descale_q = descale_q;

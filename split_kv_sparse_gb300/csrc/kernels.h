@@ -150,10 +150,7 @@ cudaError_t launch_sdpa_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
 constexpr int kByLength = 1, kShares = 2;   // rules of AttnArgs::adaptive
 struct AttnArgs {
   const void* q;                // element (token, head, x) at token * q_ts + head * q_hs + x
-  const void* k;                // paged: element (page, row, head, x) at page * kv_ps + row * kv_rs +
-  const void* v;                // head * kv_hs + x; packed: row = the token, no pages
-  int64_t q_ts, q_hs;
-  int64_t kv_ps, kv_rs, kv_hs;
+  int64_t q_ts, q_hs;           // (K and V are read through tensor maps)
   const int32_t* table;         // paged: [batch][table_width]; null: packed
   int table_width, page_shift, num_pages;
   const int32_t* cu_q;          // [batch + 1]
