@@ -285,6 +285,19 @@ def test_chunk_shares_that_cross_sequences(num_sms, h_q, h_kv):
     go("e4m3", sq, kv, h_q, h_kv, 32, seed=num_sms, num_sms=num_sms, max_kv=9000)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("max_q,max_kv", [(2, 60), (2, 500), (40, 60), (40, 500), (40, 9000)])
+def test_hundreds_of_short_sequences(dtype, max_q, max_kv):
+    """Job searches over many groups of sequences, empty ones among them."""
+    rng = np.random.default_rng(max_q + max_kv)
+    sq = [int(x) for x in rng.integers(0, 4, 700)]
+    kv = [int(x) for x in rng.integers(0, 60, 700)]
+    sq[300], kv[300] = (3, 400) if max_q == 2 else (150, 480)
+    go(dtype, sq, kv, 8, 2, 16, seed=7, max_q=max_q, max_kv=max_kv)
+    if max_kv == 60:
+        run_prompt(dtype, sq, [max(n, m) for n, m in zip(sq, kv)], 8, 2, seed=7)
+
+
 def test_decode_work_counted_in_coarser_units():
     """Tables so wide that the key tiles of all sequences could pass 32 bits: a unit of work is several tiles."""
     g = torch.Generator().manual_seed(5)
@@ -593,6 +606,39 @@ def test_prompt(dtype, lens):
 @pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (64, 1), (128, 1)])
 def test_prompt_groups(dtype, h_q, h_kv):
     run_prompt(dtype, [200, 3, 97], [200, 3, 97], h_q, h_kv, seed=h_q)
+
+
+@pytest.mark.parametrize("out_dtype,inv_scale", [("f32", 1.0), ("bf16", 1.0), ("e4m3", 64.0)])
+@pytest.mark.parametrize("max_q", [4, 200])
+def test_outputs_that_are_16_byte_aligned_only(out_dtype, inv_scale, max_q):
+    """Rows of out on odd 16-byte boundaries: unsplit rows of either kernel, split ones through the combine; prompts."""
+    g = torch.Generator().manual_seed(3)
+    scale = 1 / math.sqrt(D)
+    sq, kv = ([1, 3], [300, 40]) if max_q == 4 else ([20, 200], [300, 210])
+    c, q, dq, cu = paged_case("bf16", sq, kv, 8, 2, 16, seed=3)
+    ref = c.reference(q, dq, cu, scale)
+    n, dev, pages = sum(sq), "cuda", b.kv_pages(c.k.cuda(), c.v.cuda())
+    esz = torch.tensor([], dtype=TORCH_OUT[out_dtype]).element_size()
+    for S in (1, 3):
+        plan = b.sdpa_paged_plan(2, 8, 2, D, "bf16", max_q, n, 300, force_splits=S)
+        ws = torch.empty(max(16, plan.workspace_bytes), dtype=torch.uint8, device=dev)
+        big = torch.full((16 // esz + n * 8 * D + 16 // esz,), 7, dtype=TORCH_OUT[out_dtype], device=dev)
+        out = big[16 // esz:-(16 // esz)].view(n, 8, D)
+        assert out.data_ptr() % 32 == 16
+        b.sdpa_paged(plan, n, q.to(dev), pages, c.table.to(dev), c.kv_lens.to(dev), cu.to(dev), None, None, None, scale,
+                     out_dtype, inv_scale, out, None, None, ws)
+        torch.cuda.synchronize()
+        status_clear()
+        check(out.cpu(), None, None, ref, "bf16", out_dtype, inv_scale)
+        assert torch.all(big[:16 // esz].float() == 7) and torch.all(big[-(16 // esz):].float() == 7)
+    k, v = (torch.randn((n, 2, D), generator=g).to(torch.bfloat16) for _ in range(2))
+    out.fill_(7)
+    b.sdpa_prompt(2, q.to(dev), k.to(dev), v.to(dev), cu.to(dev), cu.to(dev), None, None, None, scale,
+                  out_dtype, inv_scale, out)
+    torch.cuda.synchronize()
+    status_clear()
+    ref = op.prompt_attention(q.double().numpy(), k.double().numpy(), v.double().numpy(), cu.numpy(), cu.numpy(), scale)
+    check(out.cpu(), None, None, ref, "bf16", out_dtype, inv_scale)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
