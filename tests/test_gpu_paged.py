@@ -560,6 +560,31 @@ def test_waits_that_run_out_end_the_call_with_a_status(dtype, sq):
     check(*run_paged(c, q, dq, cu, 8), ref, dtype)
 
 
+def test_waits_that_run_out_in_an_equal_share():
+    """As above, in chunks over long e4m3 tables. (Few CTAs of the 16-row kernel have their loads in time: no wait of theirs
+    need run out.)"""
+    dtype, sq, kv = "e4m3", [40, 300, 70], [9000, 7000, 8000]
+    c, q, dq, cu = paged_case(dtype, sq, kv, 8, 2, 16, seed=3)
+    ref = c.reference(q, dq, cu, 1 / math.sqrt(D))
+    n = int(cu[-1])
+    plan = b.sdpa_paged_plan(len(sq), 8, 2, D, dtype, max(sq), n, 9000, num_sms=4)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+    out = torch.empty((n, 8, D), device="cuda")
+    args = [q.cuda(), b.kv_pages(c.k.cuda(), c.v.cuda()), c.table.cuda(), c.kv_lens.cuda(), cu.cuda()]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    try:
+        b.mla_set_wait_limit_ns(100)
+        flush.fill_(1)          # the keys are not in the cache
+        b.sdpa_paged(plan, n, *args, scalar(dq, dtype), scalar(c.dk, dtype), scalar(c.dv, dtype), 0.1, "f32", 1.0, out, None,
+                     None, ws)
+        torch.cuda.synchronize()
+        st, site = b.mla_get_status()
+        assert st & b.MLA_STATUS_TIMEOUT and site != 0
+    finally:
+        b.mla_set_wait_limit_ns(0)
+    check(*run_paged(c, q, dq, cu, 8, num_sms=4, max_kv=9000), ref, dtype)
+
+
 # ------------------------------------------------------------------------- prompt --
 
 def run_prompt(dtype, sq, kv, h_q, h_kv, seed=0, scale=1 / math.sqrt(D), out_dtype="f32", inv_scale=1.0, fused=False, pad=0,
