@@ -60,7 +60,7 @@ struct Cfg {
 };
 
 enum {
-  B_Q = 0, B_QDONE, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VFIX, B_END, B_DRAIN,
+  B_Q = 0, B_QDONE, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VLAND, B_END, B_DRAIN,
   B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_CLC, B_STAT,
   B_OREAD, B_KFULL,
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
@@ -407,13 +407,13 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       int tile_base = 0;     // tiles of earlier jobs
       int n = 0;             // this warp's products so far
       int with_tiles = 0;    // jobs that had any
-      int seen0 = 0, seen1 = 0, fixes = 0;
+      int seen0 = 0, seen1 = 0;
 #pragma unroll 1
       for (int job = 0; ok; ++job) {
         volatile int* w;
         ok = job_at(job, w);
         if (!ok || w[J_B] < 0) break;
-        const int tiles = w[J_TILES], cnt0 = w[J_CNT0], cnt1 = w[J_CNT1], tail = w[J_TAIL];
+        const int tiles = w[J_TILES], cnt0 = w[J_CNT0], cnt1 = w[J_CNT1];
         const bool one = w[J_ONE] != 0;
         job_read(job);
         if (tiles == 0) continue;
@@ -472,8 +472,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               const int t = tile_base + tile_at(i, u);
               if constexpr (kF8) ok = wait_for<kPoll>(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
               else
-                ok = wait_for<kPoll>(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit) &&
-                     (t - tile_base != tail || wait_for<kPoll>(bar(B_VFIX), fixes & 1, limit));
+                ok = wait_for<kPoll>(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit);
               // (the job's last two products have no later QK to follow; the turn is an order, P is the dependency)
               ok = ok && wait_for<kPoll>(bar(B_P0 + i), (i ? seen1 : seen0) & 1, limit) &&
                    (n + 2 > last || wait_for<kPoll>(bar(B_TURN_PV), (n + 2) & 1, limit));
@@ -501,7 +500,6 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
           if (ok && elect_one()) mma_commit(bar(B_END));
           __syncwarp();
-          if (tail >= 0) ++fixes;
         }
         tile_base += tiles;
         ++with_tiles;
@@ -523,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       const int boxes = kTile / page_rows;                 // of one tile (and column block)
       bool ok = true;
       int done = 0;                                        // tiles whose loads were started
-      int with_tiles = 0;
+      int with_tiles = 0, landed = 0;                      // jobs that had any; V tiles that went by B_VLAND
       AttnJobs jobs;
       // (in shared memory between the jobs: the loads' loop needs the registers)
       auto shares_at = reinterpret_cast<AttnShares<2, kTileHead>*>(smem + C::kOffShares);
@@ -662,17 +660,19 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
             if (lane == 0) misc[M_MASK + (done & (kMaskRing - 1))] = static_cast<int>(groups);
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar(full + sl), C::kItemBytes);
+          // (V's rows past the sequence's end are cleared before its tile counts as there)
+          const uint32_t there = bar(!kF8 && !is_k && t == tail ? static_cast<int>(B_VLAND) : full + sl);
+          if (lane == 0) mbar_arrive_expect_tx(there, C::kItemBytes);
           __syncwarp();
           if (lane < boxes) {
             const uint32_t dst = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
             if (kPaged && !kF8 && a.kv_wide != 0) {
               const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
               tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
-                          bar(full + sl));
+                          there);
             } else {
               for (int h = 0; h < C::kHalves; ++h)
-                tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, bar(full + sl));
+                tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, there);
             }
           }
           page = page_n;
@@ -697,7 +697,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         // the ragged end lies in the last tile: clear V's rows past it
         if (!kF8 && !is_k && tail >= 0) {
           const int sl = (done - 1) % C::kVSlots;
-          ok = wait_for<kPoll>(bar(B_VFULL + sl), ((done - 1) / C::kVSlots) & 1, limit);
+          ok = wait_for<kPoll>(bar(B_VLAND), landed & 1, limit);
+          if (!ok && !wait_drain(bar(B_VLAND), landed & 1, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+          ++landed;
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
             const bool wide = kPaged && a.kv_wide != 0;
@@ -707,9 +709,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               *reinterpret_cast<uint4*>(at + (wide ? 1024 : kTile * 128)) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_VFIX));
           }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_VFULL + sl));
         }
       }
       if (!ok) give_up(a, misc + M_ABORT, W_T_LOAD);
@@ -717,10 +719,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) {
         const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL;
-        bool landed = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
+        bool quiet = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
         for (int k = max(0, done - slots); k < done; ++k)
-          landed = wait_drain(bar(full + k % slots), (k / slots) & 1, a.drain_limit_ns) && landed;
-        if (!landed) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+          quiet = wait_drain(bar(full + k % slots), (k / slots) & 1, a.drain_limit_ns) && quiet;
+        if (!quiet) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
       }
     } else if (kF8 && warp >= 12) {
       // ================================================== V e4m3 -> f16 ===

@@ -628,6 +628,15 @@ def test_prompt(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [40, 100, 170])
+def test_many_short_jobs_a_cta(dtype, n):
+    """Several jobs a CTA, each of two row blocks over one or two key tiles of which the last ends in the sequence: the V
+    loads run ahead over more than one job's ragged end."""
+    run_prompt(dtype, [n] * 70, [n] * 70, 32, 8, seed=n)
+    go(dtype, [n] * 70, [n + 5] * 70, 32, 8, 16, seed=n, force_splits=1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (64, 1), (128, 1)])
 def test_prompt_groups(dtype, h_q, h_kv):
     run_prompt(dtype, [200, 3, 97], [200, 3, 97], h_q, h_kv, seed=h_q)
