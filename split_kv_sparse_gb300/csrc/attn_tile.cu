@@ -794,26 +794,27 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 
 // One warp per kHeads heads of a (token, KV head): M = max_s LSE_s, w_s = 2^(LSE_s -
 // M), O = sum_s w_s O_s / sum_s w_s. Lane (32 / kHeads) h + s holds the LSE of head h and
-// split s (mod 32 / kHeads), then every lane four columns of each head, several splits in
-// flight. A row has three loads in a chain, so many rows take four heads a warp
+// split s (mod 32 / kHeads), every lane four columns of each head, several splits in
+// flight, the first ones beside the LSE. A row has two loads in a chain (with three, 8 e4m3
+// sequences of 2,048 keys took 15.2 us, so 14.4), so many rows take four heads a warp
 // (measured on 47 thousand rows of 3 splits: 31 -> 14 us), few rows one, to spread over
 // the SMs (256 rows: 1.3 us less). A token whose job was not split is left alone.
 template <int kHeads>
 __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, const int rows_per_slot) {
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();
-  const int begin = max(a.cu_q[0], 0), end = min(max(a.cu_q[a.batch], 0), a.total_q);
+  const int begin = a.cu_q[0], end = a.cu_q[a.batch];   // (a token's map is on its way before these are there)
   float amax = 0.f;
   constexpr int kLanes = 32 / kHeads;            // lanes of a head: splits looked at together
   constexpr int kFlight = kHeads == 1 ? 8 : 4;   // splits of a head in flight
   const int parts = (a.group + kHeads - 1) / kHeads;
   const int64_t per_token = static_cast<int64_t>(a.h_kv) * parts;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); item < end * per_token;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); item < a.total_q * per_token;
        item += static_cast<int64_t>(gridDim.x) * 8) {
     const int tok = static_cast<int>(item / per_token), rest = static_cast<int>(item - tok * per_token);
     const int g = rest / parts, h0 = (rest - g * parts) * kHeads;
-    if (tok < begin) continue;
     const int2 map = a.row_map[static_cast<int64_t>(tok) * a.h_kv + g];
+    if (tok < begin || tok >= end) continue;
     const int S = map.y;
     // (a token of no job, which only offsets that decrease can leave, has no entry: nothing outside the partials is read)
     if (S < 1 || S > a.num_splits || map.x < 0 ||
@@ -831,6 +832,17 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
         const int s = s0 + sl;
         return hl < heads && s < S ? a.lse_part[row_of(s) + hl] : -INFINITY;
       };
+      float4 x[kHeads][kFlight];
+      auto load = [&](int s0) {
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+          for (int k = 0; k < kFlight; ++k) {
+            x[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (h < heads && s0 + k < S) x[h][k] = __ldcs(reinterpret_cast<const float4*>(a.o_part + (row_of(s0 + k) + h) * kD) + lane);
+          }
+      };
+      load(0);   // beside the LSE (the row of an empty split holds zeros)
       const float first = lse_at(0);
       float M = first, z = 0.f;
       for (int s0 = kLanes; s0 < S; s0 += kLanes) M = fmaxf(M, lse_at(s0));
@@ -844,27 +856,16 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
         const float w = l == -INFINITY ? 0.f : exp2f(l - M);
         z += w;
         for (int s1 = 0; s1 < kLanes && s0 + s1 < S; s1 += kFlight) {
-          float4 x[kHeads][kFlight];
-          float ws[kHeads][kFlight];
+          if (s0 + s1 > 0) load(s0 + s1);
 #pragma unroll
           for (int h = 0; h < kHeads; ++h)
 #pragma unroll
             for (int k = 0; k < kFlight; ++k) {
-              ws[h][k] = __shfl_sync(0xffffffffu, w, kLanes * h + s1 + k);
-              x[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (ws[h][k] != 0.f)
-                x[h][k] = __ldcs(reinterpret_cast<const float4*>(
-                                     a.o_part + (row_of(s0 + s1 + k) + h) * kD) + lane);
-            }
-#pragma unroll
-          for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              if (ws[h][k] == 0.f) continue;
-              acc[h].x = fmaf(ws[h][k], x[h][k].x, acc[h].x);
-              acc[h].y = fmaf(ws[h][k], x[h][k].y, acc[h].y);
-              acc[h].z = fmaf(ws[h][k], x[h][k].z, acc[h].z);
-              acc[h].w = fmaf(ws[h][k], x[h][k].w, acc[h].w);
+              const float ws = __shfl_sync(0xffffffffu, w, kLanes * h + s1 + k);
+              acc[h].x = fmaf(ws, x[h][k].x, acc[h].x);
+              acc[h].y = fmaf(ws, x[h][k].y, acc[h].y);
+              acc[h].z = fmaf(ws, x[h][k].z, acc[h].z);
+              acc[h].w = fmaf(ws, x[h][k].w, acc[h].w);
             }
         }
       }
