@@ -23,7 +23,7 @@
 // term at most, as much as the rounding of a bf16 result.
 // The tensor pipe bounds the bf16 kernel (prompt of 16,384 tokens, 32/8 heads: 1.10 ms, 2.0
 // PFLOP/s), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
-// 2,100; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
+// 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
 #include "attn_common.cuh"
 
