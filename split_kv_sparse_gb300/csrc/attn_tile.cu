@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL, empty = is_k ? B_KEMPTY : B_VEMPTY;
         const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t, ++done) {
+        for (int t = 0; t < tiles; ++t) {
           int page_n = 0, row_n = 0;
           bool have_n = false;
           if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
@@ -675,6 +675,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 tma_load_4d(dst + lane * page_rows * 128 + h * kTile * 128, tm, 64 * h, row, page, g, there);
             }
           }
+          ++done;   // at once: a wait below may run out, and what was started is drained by this count
           page = page_n;
           row = row_n;
           have = have_n;
