@@ -420,6 +420,30 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// P for e4m3 V is f16, which ends at 2^-25 below: its reference is therefore taken 2^kF16Shift under the running maximum, P
+// = 2^(s - m + kF16Shift), and the sums carry the same factor, so O / l needs nothing and the LSE a multiplication.
+// Weights down to 2^-32 of the largest then count (the numerator alone lost what fell below 2^-25: 32,768 keys of 2^-26
+// behind a key whose V is 0 gave O off by 92 %). At the top a reference that lags by kRescaleThreshold leaves P at
+// 2^15, finite in f16.
+constexpr float kF16Shift = 7.0f;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
+// Whether the maximum mx asks for a new reference. f16: mx and s - m are rounded to scores' own steps, which grow with them;
+// the lag allowed shrinks with |m| (8 at 0, none from 2^20 on), so that P stays in range.
+template <bool kF16>
+__device__ __forceinline__ bool new_reference(float mx, float m) {
+  if constexpr (kF16) return mx > fmaxf(m, fmaf(fabsf(m), -0x1p-17f, m + kRescaleThreshold));
+  return mx > m + kRescaleThreshold;
+}
+// The fp32 term of the exponent, and l without the shift's factor.
+template <bool kF16>
+__device__ __forceinline__ float minus_reference(float m) {
+  return m == -INFINITY ? 0.f : (kF16 ? kF16Shift : 0.f) - m;
+}
+template <bool kF16>
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return m + log2f(kF16 ? l * 0x1p-7f : l);
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -33,7 +33,6 @@ constexpr int kOffAbort = kOffStats + kWarps * 16 * 8;
 constexpr int kOffStage = kOffAbort + 16;               // int [kWarps]: the stage that holds a warp's result
 constexpr int kSmem = kOffStage + 16 + 1024;
 static_assert(16 * kD * 4 <= kStageBytes, "a warp's result goes through one stage");
-constexpr float kRescaleThreshold = 8.0f;
 // A piece's start and end, in key tiles of an equal share (128 sequences of 2,048 e4m3 keys: 0 97.9 us, 1 97.8, 2
 // 96.7; 8 of 8,192: 33.0, 32.8, 32.4).
 constexpr int kRowHead = 2;
@@ -334,7 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * esc;
     }
-    const bool need0 = mx[0] > m[0] + kRescaleThreshold, need1 = mx[1] > m[1] + kRescaleThreshold;
+    const bool need0 = new_reference<kF8>(mx[0], m[0]), need1 = new_reference<kF8>(mx[1], m[1]);
     if (__any_sync(0xffffffffu, need0 || need1)) {
       float al[2] = {1.f, 1.f};
       if (need0) {
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] *= al[k >> 1];
     }
-    const float nm0 = m[0] == -INFINITY ? 0.f : -m[0], nm1 = m[1] == -INFINITY ? 0.f : -m[1];
+    const float nm0 = minus_reference<kF8>(m[0]), nm1 = minus_reference<kF8>(m[1]);
 #pragma unroll
     for (int i = 0; i < kNt; ++i) {
 #pragma unroll
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   }
   const bool some = tot > 0.f || tot != tot;
   const float inv = some ? dv / tot : 0.f;
-  const float lse = some ? M + log2f(tot) : -INFINITY;
+  const float lse = some ? lse_of<kF8>(M, tot) : -INFINITY;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {

@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kD = kAttnDim;
 constexpr int kTile = kAttnKeyTile;
-constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
 // A piece's start and end, in halves of a key tile of an equal share (2 to 12 measure alike).
 constexpr int kTileHead = 4;
 
@@ -208,7 +207,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
       }
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
-      const bool need = mx > m_run + kRescaleThreshold;
+      const bool need = new_reference<kF8>(mx, m_run);
       // O_i's last product is done: P_i may be written again, O_i rescaled
       if (u > 0 && !wait_for<kPoll>(bar(B_O0 + i), (su + u - 1) & 1, limit)) {
         bad = true;
@@ -234,7 +233,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
         }
       }
-      const float nm = m_run == -INFINITY ? 0.f : -m_run;
+      const float nm = minus_reference<kF8>(m_run);
       const uint64_t esc2 = pair_f32(esc, esc), nm2 = pair_f32(nm, nm);
       uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -285,7 +284,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       if (!bad) {
         const bool some = l > 0.f || l != l;   // a NaN score stays a NaN result
         const float inv = some ? dv / l : 0.f;
-        const float lse = some ? m_run + log2f(l) : -INFINITY;
+        const float lse = some ? lse_of<kF8>(m_run, l) : -INFINITY;
         const int64_t orow = static_cast<int64_t>(q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
         const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
         const bool part = kPaged && slot0 >= 0;
