@@ -434,6 +434,14 @@ __device__ __forceinline__ bool new_reference(float mx, float m) {
   if constexpr (kF16) return mx > fmaxf(m, fmaf(fabsf(m), -0x1p-17f, m + kRescaleThreshold));
   return mx > m + kRescaleThreshold;
 }
+// l += x, compensated (Kahan, "Further remarks on reducing truncation errors", 1965): c is what l holds too much. A long
+// row's small terms would be lost behind a large one (16,384 keys of 2^-25 behind a sink: 4e-5 of the LSE by plain
+// sums). Under 1 % of the time (decode of 128 sequences of 2,048 e4m3 keys 95.0 -> 95.7 us, 7 ragged e4m3 prompts 233 -> 235).
+__device__ __forceinline__ void add_compensated(float& l, float& c, float x) {
+  const float y = x - c, s = l + y;
+  c = (s - l) - y;
+  l = s;
+}
 // The fp32 term of the exponent, and l without the shift's factor.
 template <bool kF16>
 __device__ __forceinline__ float minus_reference(float m) {

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
   for (int i = 0; i < 16; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, lc[2] = {0.f, 0.f};
   const uint32_t limit = wait_limit(a);
   bool ok = true;
   int n = 0;
@@ -346,6 +346,8 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       }
       l[0] *= al[0];
       l[1] *= al[1];
+      lc[0] *= al[0];
+      lc[1] *= al[1];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
@@ -356,9 +358,15 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     for (int i = 0; i < kNt; ++i) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[i][k] = ex2_approx(fmaf(s[i][k], esc, k < 2 ? nm0 : nm1));
-      l[0] += s[i][0] + s[i][1];
-      l[1] += s[i][2] + s[i][3];
     }
+    float more[2] = {s[0][0] + s[0][1], s[0][2] + s[0][3]};
+#pragma unroll
+    for (int i = 1; i < kNt; ++i) {
+      more[0] += s[i][0] + s[i][1];
+      more[1] += s[i][2] + s[i][3];
+    }
+    add_compensated(l[0], lc[0], more[0]);
+    add_compensated(l[1], lc[1], more[1]);
     if constexpr (kF8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                       // 16 keys

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     const int tok = tok0 + (one ? 0 : i * tokens) + rt;    // token of the sequence
     const bool live = rt < tokens && tok < sq;
     const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
-    float m_run = -INFINITY, l = 0.f;
+    float m_run = -INFINITY, l = 0.f, lc = 0.f;
     bool bad = false;
 #pragma unroll 1
     for (int u = 0; u < cnt; ++u) {
@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           al = m_run == -INFINITY ? 0.f : ex2_approx(m_run - mx);
           m_run = mx;
           l *= al;
+          lc *= al;
         }
         if (u > 0) {
 #pragma unroll
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar(B_P0 + i));
       float s0, s1;
       unpair_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])), s0, s1);
-      l += s0 + s1;
+      add_compensated(l, lc, s0 + s1);
     }
 
     // ---- epilogue

@@ -15,7 +15,7 @@ import pytest
 import torch
 
 import oracle.paged as op
-from _paged_util import D, cu_of, scalar, status_clear
+from _paged_util import D, LSE_ATOL, cu_of, scalar, status_clear
 from split_kv_sparse_gb300 import binding as b
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +116,24 @@ def test_rows_of_ones_at_scores_up_to_2_to_the_25(dtype, kind, unit):
     for S in ((1,) if kind == "prompt" else (1, 3)):
         out, lse = run(kind, dtype, q, k, v, unit * math.log(2), S)
         assert np.all(np.isfinite(lse)) and np.abs(out - 1).max() <= tol, np.abs(out - 1).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("keys,below", [(16384, 25.3), (100000, 25.3), (60000, 23.0), (100000, 31.3)])
+def test_lse_of_many_weights_below_the_sums_last_bit(dtype, kind, keys, below):
+    """Weights under half the last bit of a sum that a far larger one began: added one by one in fp32 none of them would
+    count. The library's 1e-5 on the LSE holds for any number of keys: the sums of a block or tile have at most 128 terms,
+    and their running sum is compensated, so its error is a few 2^-24, 4e-7 of the LSE, whatever their number."""
+    g = torch.Generator().manual_seed(keys)
+    n, h_q, h_kv = (1 if kind == "decode" else 40), 8, 2
+    q, k, v = torch.ones((n, h_q, D)), torch.zeros((keys, h_kv, D)), torch.ones((keys, h_kv, D))
+    k[:, :, 0] = torch.randint(-8, 9, (keys, h_kv), generator=g) / 8.0
+    k[0] = 1.5
+    q, k, v = (codes(x, dtype) for x in (q, k, v))
+    scale = below * math.log(2) / 192
+    _, L, _, _ = exact(q, k, v, scale, 0.0)
+    for S in ((1,) if kind == "prompt" else (1, 0)):
+        out, lse = run(kind, dtype, q, k, v, scale, S)
+        assert np.abs(lse - L).max() <= LSE_ATOL, (S, np.abs(lse - L).max())
+        assert np.abs(out - 1).max() <= half_step(dtype, kind) + 2.0 ** -12 + keys * 2.0 ** -24
