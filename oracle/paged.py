@@ -8,6 +8,9 @@ from . import codecs
 
 LN2 = float(np.log(2.0))
 
+# The weight below which the e4m3 kernels' P has an absolute error: they hold 2^(s - m + 7) in f16, subnormal below 2^-14.
+F16_FLOOR = 2.0 ** -21
+
 
 def pages(n: int, page_size: int, width: int) -> int:
     return min(max(0, -(-int(n) // page_size)), width)
@@ -48,10 +51,11 @@ def map_pages(page_size, held, new, cu_q, total_q, table, free_pages, free_in):
     return table, F, (n, short), slots, positions
 
 
-def attend(q, keys, values, seen, sm_scale):
+def attend(q, keys, values, seen, sm_scale, floor=F16_FLOOR):
     """One sequence: q [n, h_q, d] (fp64), keys and values [m, h_kv, d], seen bool [n, m]. Returns (O [n, h_q, d],
-    LSE2 [n, h_q], A [n, h_q, d]) with A = sum_j max(p_j, 2^-14) |v_j| / sum_j p_j, p_j = exp(s_j - max s), the scale of
-    rounding errors of P and of the sum: below 2^-14 an f16 p is subnormal and its error is u 2^-14, not u p."""
+    LSE2 [n, h_q], A [n, h_q, d]) with A = sum_j max(p_j, floor) |v_j| / sum_j p_j, p_j = exp(s_j - max s), the scale of
+    rounding errors of P and of the sum: below the floor an e4m3 kernel's p has an error of u floor, not of u p. floor = 0
+    for bf16, whose P has fp32's range, and for what is relative to the sum itself."""
     n, h_q, d = q.shape
     group = h_q // max(1, keys.shape[1])
     O, A = np.zeros((n, h_q, d)), np.zeros((n, h_q, d))
@@ -69,7 +73,7 @@ def attend(q, keys, values, seen, sm_scale):
         p = np.exp(s - m[:, None])
         z = np.where(has, p.sum(axis=1), 1.0)
         O[:, j] = (p @ V) / z[:, None]
-        A[:, j] = (np.where(seen, np.maximum(p, 2.0 ** -14), 0.0) @ np.abs(V)) / z[:, None]
+        A[:, j] = (np.where(seen, np.maximum(p, floor), 0.0) @ np.abs(V)) / z[:, None]
         L[:, j] = np.where(has, (m + np.log(z)) / LN2, -np.inf)
     return O, L, A
 
@@ -83,7 +87,7 @@ def decode_values(x, descale: float) -> np.ndarray:
     return codecs.e4m3_decode(x.contiguous().view(torch.uint8).numpy()) * descale
 
 
-def paged_attention(q, k_cache, v_cache, table, kv_lens, cu_q, sm_scale):
+def paged_attention(q, k_cache, v_cache, table, kv_lens, cu_q, sm_scale, floor=F16_FLOOR):
     """q [total_q, h_q, d], caches [num_pages, page_size, h_kv, d] as fp64 values; returns (O, LSE2, A); rows outside the
     sequences are NaN."""
     n_pages, ps = k_cache.shape[:2]
@@ -101,11 +105,11 @@ def paged_attention(q, k_cache, v_cache, table, kv_lens, cu_q, sm_scale):
         V = v_cache[np.where(ok, page, 0), pos % ps]
         at = m - (q1 - q0) + np.arange(q1 - q0)
         seen = (pos[None, :] <= at[:, None]) & ok[None, :]
-        O[q0:q1], L[q0:q1], A[q0:q1] = attend(q[q0:q1], K, V, seen, sm_scale)
+        O[q0:q1], L[q0:q1], A[q0:q1] = attend(q[q0:q1], K, V, seen, sm_scale, floor)
     return O, L, A
 
 
-def prompt_attention(q, k, v, cu_q, cu_kv, sm_scale):
+def prompt_attention(q, k, v, cu_q, cu_kv, sm_scale, floor=F16_FLOOR):
     total_q, h_q, d = q.shape
     O, A = np.full((total_q, h_q, d), np.nan), np.full((total_q, h_q, d), np.nan)
     L = np.full((total_q, h_q), np.nan)
@@ -113,5 +117,5 @@ def prompt_attention(q, k, v, cu_q, cu_kv, sm_scale):
         q0, q1, k0, k1 = int(cu_q[b]), int(cu_q[b + 1]), int(cu_kv[b]), int(cu_kv[b + 1])
         at = (k1 - k0) - (q1 - q0) + np.arange(q1 - q0)
         seen = np.arange(k1 - k0)[None, :] <= at[:, None]
-        O[q0:q1], L[q0:q1], A[q0:q1] = attend(q[q0:q1], k[k0:k1], v[k0:k1], seen, sm_scale)
+        O[q0:q1], L[q0:q1], A[q0:q1] = attend(q[q0:q1], k[k0:k1], v[k0:k1], seen, sm_scale, floor)
     return O, L, A
