@@ -383,10 +383,18 @@ def _on(stream, dev: int) -> int:
     return _t().raw_stream(dev) if stream is None else _stream(stream)
 
 
+def _pages(where: str, pages: KvPages, dev: int):
+    """The descriptor by reference; raises where kv_pages made it from tensors on another device than the current one."""
+    if getattr(pages, "device", dev) != dev:
+        _refuse(where, f"pages lie on CUDA device {pages.device}, the current one is {dev}")
+    return ctypes.byref(pages)
+
+
 def kv_pages(k_cache, v_cache) -> KvPages:
     """The C descriptor of a paged cache from views [num_pages, page_size, h_kv, d] of its tensors (bfloat16, or
     uint8 / float8_e4m3fn codes; any strides over a contiguous d, so a [num_pages, h_kv, page_size, d] cache is
-    passed as its permute(0, 2, 1, 3)). The descriptor keeps the tensors alive."""
+    passed as its permute(0, 2, 1, 3)). The descriptor keeps the tensors alive; calls that take it want their device to be
+    the current one."""
     where, t = "kv_pages", _t()
     dev = _device(where)
     k, v = (_dev(where, n, x, t.data, dev, contiguous=False) for n, x in (("k_cache", k_cache), ("v_cache", v_cache)))
@@ -396,7 +404,7 @@ def kv_pages(k_cache, v_cache) -> KvPages:
         _refuse(where, "k_cache and v_cache differ in shape, type or strides")
     n, ps, h, d = k_cache.shape
     pages = KvPages(k, v, dt, n, ps, h, d, 0, st[0], st[1], st[2])
-    pages.tensors = (k_cache, v_cache)
+    pages.tensors, pages.device = (k_cache, v_cache), dev
     return pages
 
 
@@ -434,7 +442,7 @@ def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, desca
     slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
     dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
     dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
-    _check(lib().kv_pages_write(ctypes.byref(pages), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev)), where)
+    _check(lib().kv_pages_write(_pages(where, pages, dev), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev)), where)
 
 
 def sdpa_paged_plan(batch: int, h_q: int, h_kv: int, d: int, dtype, max_q_per_seq: int, total_q_max: int, max_kv: int,
@@ -472,7 +480,7 @@ def sdpa_paged(plan: SdpaPagedPlan, total_q: int, q, pages: KvPages, block_table
         ws = _dev(where, "workspace", workspace, t.bytes, dev)
         if workspace.nbytes < plan.workspace_bytes:
             _refuse(where, "workspace is smaller than the plan's")
-    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, qp, st[0], st[1], ctypes.byref(pages), table, width, lens, cu, dq,
+    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, qp, st[0], st[1], _pages(where, pages, dev), table, width, lens, cu, dq,
                             dk, dv, sm_scale, od, out_inv_scale, o, lse, amax, ws, _on(stream, dev)), where)
 
 
