@@ -546,7 +546,8 @@ MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int 
  *   out  [total_q][h_q][128] contiguous, fp32 / bf16 / e4m3 (MLA_OUT_*); lse_out
  *      fp32 [total_q][h_q] or NULL; amax_out fp32 scalar or NULL.
  *   workspace  plan->workspace_bytes, 256-byte aligned. Calls that overlap on
- *      the GPU need workspaces of their own. */
+ *      the GPU need workspaces of their own. MLA_ERR_WORKSPACE without one, and for a
+ *      plan whose sizes and offsets are not those that the planner gave it. */
 MLA_API int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_t q_token_stride,
                int64_t q_head_stride, const kv_pages_t* pages, const int32_t* block_table, int table_width,
                const int32_t* kv_lens, const int32_t* cu_seqlens_q, const float* descale_q, const float* descale_k,

@@ -134,6 +134,28 @@ int64_t share_ctas(int wave, int h_kv) {
   return static_cast<int64_t>(wave / side) * side;
 }
 
+// The workspace of a plan with more than one split, from its other fields; false where its partial rows pass an int32.
+bool plan_layout(sdpa_paged_plan_t* p) {
+  if (p->num_sms > (1 << 24)) return false;   // (three waves' rows pass it, and twice the count would not be an int)
+  const int group = p->h_q / p->h_kv;
+  const bool rows16 = p->row_kernel != 0;
+  const int wave = rows16 ? p->num_sms * skv::kRowCtasPerSm : p->num_sms;
+  const int job_rows = rows16 ? skv::kRowRows : skv::kTileRows;
+  const int64_t unsplit = tiles_bound(p->total_q_max, p->batch, job_tokens(rows16, group)) * p->h_kv;
+  // split jobs: as many as forced; two pieces of cut jobs a CTA; at most so many waves (the rule keeps to that)
+  const int64_t slots = !p->adaptive_splits ? unsplit * p->num_splits
+                        : rows16            ? 2 * share_ctas(wave, p->h_kv)
+                                            : static_cast<int64_t>(wave) * skv::kTileSplitWaves;
+  if (slots * job_rows > 0x7FFFFFFFll) return false;
+  const uint64_t rows = static_cast<uint64_t>(slots) * job_rows;
+  p->o_acc_bytes = rows * kDim * 4;
+  p->lse_acc_offset = round_up(p->o_acc_bytes, 256);
+  p->lse_acc_bytes = rows * 4;
+  p->map_offset = round_up(p->lse_acc_offset + p->lse_acc_bytes, 256);
+  p->workspace_bytes = round_up(p->map_offset + static_cast<uint64_t>(p->total_q_max) * p->h_kv * 8, 256);
+  return true;
+}
+
 int shift_of(int pow2) {
   int s = 0;
   while ((1 << s) < pow2) ++s;
@@ -240,9 +262,6 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   }
   // few rows a sequence: the kernel of 16-row jobs, of which an SM holds two
   const bool rows16 = static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
-  const int wave = rows16 ? num_sms * skv::kRowCtasPerSm : num_sms;
-  const int job_rows = rows16 ? skv::kRowRows : skv::kTileRows;
-  const int64_t unsplit = tiles_bound(total_q_max, batch, job_tokens(rows16, group)) * h_kv;
   out->batch = batch;
   out->h_q = h_q;
   out->h_kv = h_kv;
@@ -255,21 +274,9 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->num_sms = num_sms;
   out->adaptive_splits = adaptive;
   out->row_kernel = rows16 ? 1 : 0;
-  if (S > 1) {
-    // split jobs: as many as forced; two pieces of cut jobs a CTA; at most so many waves (the rule keeps to that)
-    const int64_t slots = !adaptive ? unsplit * S
-                          : rows16  ? 2 * share_ctas(wave, h_kv)
-                                    : static_cast<int64_t>(wave) * skv::kTileSplitWaves;
-    if (slots * job_rows > 0x7FFFFFFFll) {
-      std::memset(out, 0, sizeof(*out));
-      return MLA_ERR_UNSUPPORTED;
-    }
-    const uint64_t rows = static_cast<uint64_t>(slots) * job_rows;
-    out->o_acc_bytes = rows * kDim * 4;
-    out->lse_acc_offset = round_up(out->o_acc_bytes, 256);
-    out->lse_acc_bytes = rows * 4;
-    out->map_offset = round_up(out->lse_acc_offset + out->lse_acc_bytes, 256);
-    out->workspace_bytes = round_up(out->map_offset + static_cast<uint64_t>(total_q_max) * h_kv * 8, 256);
+  if (S > 1 && !plan_layout(out)) {
+    std::memset(out, 0, sizeof(*out));
+    return MLA_ERR_UNSUPPORTED;
   }
   return MLA_OK;
 }
@@ -294,7 +301,15 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   const int e = elem_size(plan->dtype);
   if (!stride_ok(q_token_stride, e) || !stride_ok(q_head_stride, e)) return MLA_ERR_INVALID_ARG;
   if (!out_ok(out, out_dtype, out_inv_scale) || !std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
-  if (plan->workspace_bytes > 0 && (workspace == nullptr || !ptr_aligned(workspace, 256))) return MLA_ERR_WORKSPACE;
+  if (plan->num_splits > 1) {
+    // the kernels write where the plan says, so it has to be what the planner makes of its other fields
+    sdpa_paged_plan_t same = *plan;
+    if (!plan_layout(&same) || same.o_acc_bytes != plan->o_acc_bytes || same.lse_acc_offset != plan->lse_acc_offset ||
+        same.lse_acc_bytes != plan->lse_acc_bytes || same.map_offset != plan->map_offset ||
+        same.workspace_bytes != plan->workspace_bytes)
+      return MLA_ERR_WORKSPACE;
+    if (workspace == nullptr || !ptr_aligned(workspace, 256)) return MLA_ERR_WORKSPACE;
+  }
   skv::DeviceInfo dev;
   if ((st = skv::current_device(&dev)) != MLA_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
