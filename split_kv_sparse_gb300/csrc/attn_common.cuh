@@ -32,20 +32,18 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// Brings the lengths and this CTA's share of the block table towards L2, by one warp,
+// Pages: brings the lengths and this CTA's share of the block table towards L2, by one warp,
 // before grid_dependency_wait: a prefetch returns nothing, so it may run ahead of the
 // kernel that writes them, and the first loads after the wait are L2 hits.
 __device__ __forceinline__ void attn_prefetch(const AttnArgs& a, int lane) {
   for (int b = 32 * lane; b <= a.batch && b < 32 * 32; b += 32 * 32) {
     prefetch_l2_line(a.cu_q + b);
-    if (b < a.batch) prefetch_l2_line(a.table != nullptr ? a.kv_lens + b : a.cu_kv + b);
+    if (b < a.batch) prefetch_l2_line(a.kv_lens + b);
   }
-  if (a.table != nullptr) {
-    const int64_t lines = (static_cast<int64_t>(a.batch) * a.table_width + 31) / 32;
-    const int64_t each = (lines + gridDim.x - 1) / gridDim.x;
-    const int64_t first = each * blockIdx.x;
-    if (lane < each && each <= 32 && first + lane < lines) prefetch_l2_line(a.table + 32 * (first + lane));
-  }
+  const int64_t lines = (static_cast<int64_t>(a.batch) * a.table_width + 31) / 32;
+  const int64_t each = (lines + gridDim.x - 1) / gridDim.x;
+  const int64_t first = each * blockIdx.x;
+  if (lane < each && each <= 32 && first + lane < lines) prefetch_l2_line(a.table + 32 * (first + lane));
 }
 
 __device__ __forceinline__ int warp_scan_incl(int v, int lane) {
