@@ -405,9 +405,8 @@ __device__ __forceinline__ uint32_t wait_limit(const AttnArgs& a) {
   return a.wait_limit_ns < 4000000000ull ? static_cast<uint32_t>(a.wait_limit_ns) : 4000000000u;
 }
 // Records that a role's wait ran out.
-__device__ __forceinline__ void give_up(const AttnArgs& a, volatile int* abort_flag, uint32_t site) {
+__device__ __forceinline__ void give_up(const AttnArgs& a, uint32_t site) {
   if ((threadIdx.x & 31) == 0) {
-    *abort_flag = 1;
     atomicOr(&a.status[0], 1u);
     atomicCAS(&a.status[1], 0u, site);
   }

@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     __syncwarp();                                          // every lane has read the stage
   }
   if (!ok) {
-    give_up(a, abort_flag, W_R_FULL);
+    if (lane == 0) *abort_flag = 1;   // read at the merge
+    give_up(a, W_R_FULL);
     drain(loaded + n);
   }
 

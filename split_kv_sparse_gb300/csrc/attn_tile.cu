@@ -82,7 +82,7 @@ enum {
   J_TAIL,             // the local tile that holds the sequence's ragged end, or -1
   kJobWords
 };
-enum { M_TMEM = 0, M_ABORT, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
+enum { M_TMEM = 0, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
 static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
 // kPages: 0 packed K and V, jobs never split; 1 pages; 2 pages in equal shares (kernels of their
@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                                                    : 1;
       mbar_init(bar(i), n);
     }
-    misc[M_ABORT] = 0;
     mbar_init_fence();
   }
   if (warp == 8) {
@@ -375,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     ends += tiles > 0 ? 1 : 0;
     ones += one ? 1 : 0;
     if (bad) {
-      give_up(a, misc + M_ABORT, W_T_SOFTMAX);
+      give_up(a, W_T_SOFTMAX);
       break;
     }
     }
@@ -505,7 +504,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         ++with_tiles;
       }
       if (!ok) {
-        give_up(a, misc + M_ABORT, W_T_MMA);
+        give_up(a, W_T_MMA);
         const int drain = is_qk ? B_DRAIN : B_DRAIN2;
         if (elect_one()) mma_commit(bar(drain));
         __syncwarp();
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           if (lane == 0) mbar_arrive(bar(B_VFULL + sl));
         }
       }
-      if (!ok) give_up(a, misc + M_ABORT, W_T_LOAD);
+      if (!ok) give_up(a, W_T_LOAD);
       // nothing that was started may still be writing shared memory when the CTA ends
       __syncwarp();
       if (lane == 0) {
@@ -779,7 +778,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       }
       tile_base += tiles;
       }
-      if (!ok) give_up(a, misc + M_ABORT, W_T_CONVERT);
+      if (!ok) give_up(a, W_T_CONVERT);
     }
   }
 
