@@ -56,7 +56,9 @@ __device__ __forceinline__ int warp_scan_incl(int v, int lane) {
 }
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// ceil(x / y) for 0 <= x < 2^23, 1 <= y < 2^24 (exact: the float quotient is off by one at most).
+// ceil(x / y) for 0 <= x < 2^24 (a sequence's key tiles), y >= 1: x is a float, and below 2^23 the quotient's two last places
+// are less than one, so it is off by one at most and the remainder puts it right; above, the result may be off by one,
+// where a count of splits is cut to 64 anyway.
 __device__ __forceinline__ int ceil_div(int x, int y) {
   int q = __float2int_rz(__fdividef(static_cast<float>(x), static_cast<float>(y)));
   const int r = x - q * y;
