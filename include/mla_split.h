@@ -484,9 +484,10 @@ MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_
  *   [0, o_acc_bytes)                   fp32 partial rows [split job][R][128]
  *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][R]
  *   [map_offset, ...)                  per (token, KV head): its first partial row, its splits
- * so its size is bounded by the SMs and KV heads (two split jobs a CTA with row_kernel: 5 MB
- * on 152 SMs; three waves otherwise: 60 MB), not by the tokens, unless a split count is forced. 0
- * bytes with one split. It needs no clearing. */
+ * so the partials are bounded by the SMs (two split jobs a CTA with row_kernel: 5 MB on
+ * 152 SMs; three waves otherwise: 60 MB) unless a split count is forced, and the map adds 8
+ * bytes for each of total_q_max * h_kv (262,144 tokens of 8 KV heads: 17 MB). 0 bytes with one
+ * split. It needs no clearing. */
 typedef struct {
   int32_t batch;          /* sequences                                                  */
   int32_t h_q, h_kv;      /* query and KV heads; h_q % h_kv == 0, group = h_q / h_kv <= 128 */

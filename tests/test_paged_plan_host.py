@@ -45,3 +45,14 @@ def test_a_count_of_sms_past_an_int_is_refused():
         with pytest.raises(b.SplitKVError) as e:
             b.sdpa_paged_plan(2, 8, 2, 128, "bf16", max_q, 2 * max_q, 5000, num_sms=(1 << 31) - 1)
         assert e.value.status == 2
+
+
+@pytest.mark.parametrize("tokens,h_kv", [(96, 8), (262144, 8), (4096, 128)])
+@pytest.mark.parametrize("max_q", [1, 500])
+def test_the_workspace_is_what_the_header_says(tokens, h_kv, max_q):
+    """Partials bounded by the SMs, whatever the tokens, and 8 bytes of map a token and KV head."""
+    p = b.sdpa_paged_plan(96, 4 * h_kv, h_kv, 128, "bf16", max_q, tokens, 16384, num_sms=152)
+    assert p.row_kernel == (max_q == 1)
+    partials = 512 * (2 * 304 * 16 if p.row_kernel else 3 * 152 * 256)
+    assert p.o_acc_bytes <= partials and partials < (5.1e6 if p.row_kernel else 60.0e6)
+    assert 0 <= p.workspace_bytes - p.o_acc_bytes - p.lse_acc_bytes - 8 * tokens * h_kv <= 768
