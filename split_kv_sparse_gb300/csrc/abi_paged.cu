@@ -374,6 +374,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   // wave have no second one to even out (8 x 16 over 8,192 e4m3 keys: 40.5 -> 44.6 us); and the two cut jobs of
   // every CTA (256 rows each, and their combine) have to be small beside a sequence (e4m3, 2 x 2,048 tokens over 4,096 keys 145 ->
   // 157 us, 8,192 308 -> 296, 16,384 638 -> 579; 4 x 300 over 9,000 169 -> 129; 40 x 16 over 9,000 185 -> 144).
+  // The length is the plan's bound: 2 x 2,048 over 4,096 under a plan for 131,072 keys take 150 us instead of 139.
   constexpr int kLongKeys = 6144;
   if (plan->adaptive_splits) {
     const bool shares = rows16 || (plan->dtype == SDPA_E4M3 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);

@@ -224,7 +224,7 @@ struct AttnJobs {
 // one more; half as many where a job of the tile kernel has one row block only). Range r of R
 // takes the units [r U, (r + 1) U), by one CTA for each of the side heads: the heads of a row
 // lie side by side in memory, and read at one time they share DRAM rows (decode of 128 sequences of
-// 2,048 e4m3 keys, 8 KV heads: 98 us, with the heads one after the other on the line 141; one
+// 2,048 e4m3 keys, 8 KV heads: 97 us when it came, with the heads one after the other on the line 141; one
 // job a CTA 118). A job that crosses no boundary is written at once; the pieces of one
 // that does are partials. A CTA has at most one piece that begins a cut job (slot R side + h R +
 // r, h its head of the group) and one that goes on with one (slot h R + r), so the pieces of a
@@ -386,7 +386,7 @@ struct AttnShares {
 // a converged warp call it and leave it together (one barrier word, one timer). It
 // is kept this small because it is inlined at some thirty places: with the status
 // word and the CTA's abort flag handled in its loop, or with a vote behind it, these
-// kernels lose up to 40 % (e4m3 prompt of 16,384 tokens: 1.2 -> 2.0 ms). A role that gives up
+// kernels lose 30 to 40 % of their rate (e4m3 prompt of 16,384 tokens: 1.2 -> 2.0 ms). A role that gives up
 // says so once (give_up); the others run into their own limit.
 // kPoll: test_wait, for limits below kSuspendNs: the hardware suspends a try_wait for
 // longer than a load from memory takes, so such a limit could never run out. Limits

@@ -6,8 +6,8 @@
 // warp waits for another until the four results of a job are merged. Where the plan forces
 // no split count, a CTA takes an equal share of the batch's work (AttnShares): pieces of one or more
 // jobs, one after the other, the loads running ahead into the next. Measured with 32 query and 8
-// KV heads: 96 sequences of 100 to 12,000 bf16 keys 334 us (6.5 TB/s; one job a CTA 367),
-// 256 of 500 106 us (148), 8 of 65,536 e4m3 keys 167 us (6.4 TB/s), 8 of 1,024 to 16,384 35.5 us.
+// KV heads: 96 sequences of 100 to 12,000 bf16 keys 339 us (6.4 TB/s; with one job a CTA a tenth more),
+// 256 of 500 95 us, 8 of 65,536 e4m3 keys 166 us (6.5 TB/s), 8 of 1,024 to 16,384 34.5 us.
 //
 // The products are mma.sync with the 16 rows as M: a tcgen05 tile has at least 64, and
 // the tensor work of 16 rows is far below either pipe's rate. bf16: blocks of 16 keys

@@ -20,9 +20,10 @@
 // registers as soon as they are there), P_0, P_1 (64 each), O_0, O_1 (128 each).
 // P is rounded to V's MMA type (bf16; f16 for e4m3 V, whose values f16 holds exactly);
 // the sums are taken over the unrounded fp32 values. bf16 P costs 2^-8 relative a
-// term at most, as much as the rounding of a bf16 result.
-// The tensor pipe bounds the bf16 kernel (prompt of 16,384 tokens, 32/8 heads: 1.10 ms, 2.0
-// PFLOP/s), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
+// term at most, as much as the rounding of a bf16 result, and also where the result is fp32 (a pair as in the 16-row kernel
+// would double the PV products of a kernel that the tensor pipe bounds).
+// The tensor pipe bounds the bf16 kernel (prompt of 16,384 tokens, 32/8 heads: 1.13 ms, 1.95 PFLOP/s, a call of a burst
+// of 20; 1.28 ms, 1.71 PFLOP/s, one of 500, where the power cap takes the clock to 1.55 GHz), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
 // 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
 #include "attn_common.cuh"
