@@ -521,6 +521,11 @@ typedef struct {
  * one after the other), or more where the split jobs would not fit the workspace. An
  * unsplit sequence's rows are written at once, those of a split one by a combine kernel
  * launched behind. num_sms 0 = the current device's.
+ * The kernel and the rule follow from max_q_per_seq and max_kv, not from a call's lengths:
+ * any call is right under any plan, but decode steps under a plan for chunks take the 256-row
+ * jobs (8 sequences of 1,024 to 16,384 e4m3 keys 44 us for 34, 96 of bf16 396 for 353). So make a plan
+ * for each kind of step; their calls may share a workspace of the largest size where
+ * they do not overlap.
  * Errors as for mla_decode_plan (d must be 128, dtype SDPA_*, group <= 128). */
 MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_per_seq, int total_q_max,
                     int max_kv, int num_sms, int max_splits, int force_splits, sdpa_paged_plan_t* out);
@@ -532,12 +537,16 @@ MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int 
  * sits at position kv_lens[b] - s_b + i and sees keys 0 .. that position; query
  * head j reads KV head j / (h_q / h_kv). Key p of sequence b is row p % page_size
  * of page block_table[b][p / page_size]; the keys of an entry outside [0,
- * num_pages) are left out, like masked ones. A query that sees no key gives O = 0
+ * num_pages) are left out, like masked ones. total_q >= 1: a step without new tokens has no call. A query that sees no key gives O = 0
  * and LSE = -inf. Rows of out and lse_out at and past cu_seqlens_q[batch] are left as they
  * were, and nothing of the cache outside a sequence's keys reaches a result,
  * whatever it holds (a non-finite V element below kv_lens[b] may also reach
  * queries of that sequence before it). cu_seqlens_q starts at 0 and does not decrease;
  * offsets that do leave rows undefined, but nothing outside the buffers is touched.
+ * Scores, softmax statistics and O are fp32. The softmax weights that multiply V are
+ * rounded, whatever the output type: with e4m3 to f16 (2^-11 relative; 2^-32 of the row's largest
+ * weight below 2^-21 of it), with bf16 to a bf16 pair (2^-16) in the kernel of 16-row jobs and to
+ * bf16 (2^-8) in that of 256-row jobs, so a bf16 query's last bits depend on the plan's kernel.
  *   q  [total_q][h_q][128] of the plan's dtype, element (t, j, x) at t *
  *      q_token_stride + j * q_head_stride + x; 16-byte aligned, strides positive
  *      multiples of 16 bytes.
@@ -559,8 +568,8 @@ MLA_API int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q
  * queries cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 and the keys cu_seqlens_kv[b]
  * .. cu_seqlens_kv[b + 1] - 1 (as many for a prompt; more where a prefix precedes
  * it, fewer leave its first queries without a key), causal and grouped as in
- * sdpa_paged, same outputs. k and v share their strides; q, k and v may be slices
- * of one fused projection's output. total_q, total_kv are row counts of q and k/v; nothing
+ * sdpa_paged, same outputs, precision as its 256-row jobs. k and v share their strides; q, k and v may be slices
+ * of one fused projection's output. total_q and total_kv, both >= 1, are row counts of q and k/v; nothing
  * outside them is read, and rows of out and lse_out outside the sequences are left as they
  * were. Needs no workspace. Same alignment rules as sdpa_paged. */
 MLA_API int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,
