@@ -137,3 +137,17 @@ def test_lse_of_many_weights_below_the_sums_last_bit(dtype, kind, keys, below):
         out, lse = run(kind, dtype, q, k, v, scale, S)
         assert np.abs(lse - L).max() <= LSE_ATOL, (S, np.abs(lse - L).max())
         assert np.abs(out - 1).max() <= half_step(dtype, kind) + 2.0 ** -12 + keys * 2.0 ** -24
+
+
+@pytest.mark.parametrize("keys", [2, 5, 17, 60, 300])
+def test_decode_rounds_bf16_weights_to_a_pair(keys):
+    """The 16-row kernel's P is bf16 hi + lo: 2^-16 a term, where one bf16 costs 2^-8, which a few keys show. 2^-12 for fp32 as
+    above (the scores of N(0, 1) values: 128 products, 2^-13.6)."""
+    for seed in range(4):
+        g = torch.Generator().manual_seed(100 * keys + seed)
+        q, k, v = (codes(torch.randn((m, h, D), generator=g), "bf16") for m, h in ((1, 8), (keys, 2), (keys, 2)))
+        scale = 1 / math.sqrt(D)
+        O, L, _, A0 = exact(q, k, v, scale, 0.0)
+        out, lse = run("decode", "bf16", q, k, v, scale)
+        assert np.all(np.abs(out - O) <= (2.0 ** -16 + 2.0 ** -12) * A0), (np.abs(out - O) / A0).max()
+        assert np.abs(lse - L).max() <= LSE_ATOL
