@@ -422,7 +422,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // P for e4m3 V is f16, which ends at 2^-25 below: its reference is therefore taken 2^kF16Shift under the running maximum, P
 // = 2^(s - m + kF16Shift), and the sums carry the same factor, so O / l needs nothing and the LSE a multiplication.
 // Weights down to 2^-32 of the largest then count (the numerator alone lost what fell below 2^-25: 32,768 keys of 2^-26
-// behind a key whose V is 0 gave O off by 92 %). At the top a reference that lags by kRescaleThreshold leaves P at
+// behind a key whose V is 0 gave O = 0). At the top a reference that lags by kRescaleThreshold leaves P at
 // 2^15, finite in f16.
 constexpr float kF16Shift = 7.0f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units a row's reference may lag behind its maximum
