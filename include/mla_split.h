@@ -401,9 +401,13 @@ MLA_API int sdpa_fp8_decode(const sdpa_plan_t* plan, int total_q, int64_t total_
  * ======================================================================= */
 
 /* Element types of Q, K and V (the codes of MLA_OUT_*): bf16, or e4m3 codes that
- * stand for code * descale. Q, K and V of a call have one type. */
+ * stand for code * descale. Q, K and V of a call have one type. SDPA_E2M1 is a form of
+ * pages only, K and V in 4 bits beside a bf16 Q: 16 consecutive dims share a scale in
+ * e4m3, and each of them is an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) that
+ * stands for code * scale * descale. */
 #define SDPA_BF16 1
 #define SDPA_E4M3 2
+#define SDPA_E2M1 4
 
 /* A paged KV cache: num_pages pages of page_size rows; a row holds one token's
  * h_kv heads of d elements. Element (page p, row r, head g, dim x) of k and of v
@@ -411,17 +415,26 @@ MLA_API int sdpa_fp8_decode(const sdpa_plan_t* plan, int total_q, int64_t total_
  * base. A slot is p * page_size + r. Contiguous [num_pages][page_size][h_kv][d]
  * ("row before head") and [num_pages][h_kv][page_size][d] are both strides of
  * this form. k and v are 16-byte aligned, and the strides are positive multiples
- * of 16 bytes below 2^40 bytes. */
+ * of 16 bytes below 2^40 bytes.
+ *   SDPA_E2M1: a head of a row is 64 bytes, dim x in byte x / 2, even dims in its low
+ * four bits; the strides count bytes. Its 8 scales, dims 16 i .. 16 i + 15 in byte i, lie p *
+ * scale_page_stride + g * scale_head_stride + r * 8 bytes from k_scales and v_scales: the
+ * rows of a head of a page side by side, [num_pages][h_kv][page_size][8], page and head
+ * strides positive multiples of 16 bytes below 2^40, bases 16-byte aligned. Other types do
+ * not read the last four fields. 144 bytes a row and head of K and V together (bf16 512, e4m3 256). */
 typedef struct {
   void* k;
   void* v;
-  int32_t dtype;         /* SDPA_BF16 or SDPA_E4M3                          */
+  int32_t dtype;         /* SDPA_BF16, SDPA_E4M3 or SDPA_E2M1               */
   int32_t num_pages;
   int32_t page_size;     /* rows a page: a power of two, 16 .. 65536        */
   int32_t h_kv;
   int32_t d;             /* 128                                             */
   int32_t reserved;      /* 0                                               */
-  int64_t page_stride, row_stride, head_stride;   /* in elements            */
+  int64_t page_stride, row_stride, head_stride;   /* in elements; SDPA_E2M1: bytes */
+  void* k_scales;        /* SDPA_E2M1 only                                  */
+  void* v_scales;
+  int64_t scale_page_stride, scale_head_stride;   /* in bytes               */
 } kv_pages_t;
 
 /* Block tables and slot maps from request lengths, on the GPU, in place and
@@ -470,13 +483,54 @@ MLA_API int kv_pages_map(int batch, int page_size, const int32_t* held_lens, con
  * slot_map[r]; a bf16 cache takes the bits, an e4m3 cache
  *   code = e4m3_satfinite_rn(x / descale)      (fp32 division; NaN stays NaN)
  * with descale_k / descale_v fp32 device scalars (NULL = 1.0; ignored for bf16),
- * the ones that sdpa_paged multiplies back. A slot outside [0, num_pages *
+ * the ones that sdpa_paged multiplies back. A 4-bit cache takes, of each 16 dims,
+ *   y = x / descale, scale = e4m3_satfinite_rn(max |y| / 6), code = e2m1_satfinite_rn(y / scale)
+ * (fp32 divisions; ties of a code to the even one; codes of 0 under a scale of 0). A NaN
+ * makes the scale of its 16 dims NaN; what lies beyond 6 * 448 becomes that. A slot outside [0, num_pages *
  * page_size) is skipped. Two rows with the same slot leave some of each in it.
  * k_new and v_new are 16-byte aligned and their strides positive multiples of 8
  * elements, so K and V may be slices of a fused projection's output. rows >= 0. */
 MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, const void* v_new,
                    int64_t token_stride, int64_t head_stride, const int64_t* slot_map,
                    const float* descale_k, const float* descale_v, void* stream);
+
+/* The append with the position rotation on the way: kv_pages_write of the rotated rows of k_new (and
+ * of v_new as it is), and the rotated queries beside it, each byte read and written once. Row r
+ * stands at position p = positions[r]; of each head of q and k the first rotary_dim dims R
+ * are turned in pairs (i, j), i < j,
+ *   y_i = x_i c - x_j s,   y_j = x_j c + x_i s      (fp32, every operation rounded)
+ * by c = cos_sin[p][n], s = cos_sin[p][R / 2 + n], n = 0 .. R / 2 - 1: (i, j) = (n, n + R / 2), or
+ * (2 n, 2 n + 1) with interleaved = 1. The other dims pass. What a cache or q_out of fewer bits
+ * holds is rounded from the fp32 values at once.
+ *   q  bf16, element (r, j, x) at r * q_token_stride + j * q_head_stride + x; h_q may be 0 (no
+ *      queries; q and q_out are not looked at).
+ *   positions  int32 [rows]; a row whose position is outside [0, num_positions) is padding: nothing
+ *      of it is written. A row that only has no slot (slot_map as in kv_pages_write) is rotated
+ *      into q_out and k_out.
+ *   cos_sin  fp32 [num_positions][R], contiguous, 16-byte aligned; R a multiple of 32 up to 128
+ *      (else MLA_ERR_UNSUPPORTED).
+ *   q_out  SDPA_BF16, or SDPA_E4M3 codes of y / descale_q (fp32 device scalar, NULL = 1.0); may be
+ *      q itself with q's strides (bf16).
+ *   k_out  NULL, or the rotated rows of k in bf16 (for sdpa_prompt); may be k_new itself with its
+ *      strides. Outputs that overlap inputs or each other in another way are undefined.
+ * Pointers 16-byte aligned (slot_map 8, positions and scalars 4), strides positive multiples of 16
+ * bytes. rows >= 0. */
+MLA_API int kv_pages_write_rotary(const kv_pages_t* pages, int64_t rows, int h_q, const void* q,
+                   int64_t q_token_stride, int64_t q_head_stride, const void* k_new, const void* v_new,
+                   int64_t token_stride, int64_t head_stride, const int32_t* positions, const float* cos_sin,
+                   int64_t num_positions, int rotary_dim, int interleaved, const int64_t* slot_map,
+                   const float* descale_q, const float* descale_k, const float* descale_v, int q_out_dtype,
+                   void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                   int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+
+/* Rows of a cache of any type back as bf16: row r of k_out and v_out (element (r, g, x) at r * token_stride
+ * + g * head_stride + x) takes slot slot_map[r]: a bf16 cache's bits, else bf16_rn(value * descale), value =
+ * code (* scale), exact before the one fp32 product. A cached prefix becomes packed keys for
+ * sdpa_prompt this way. A row whose slot is outside [0, num_pages * page_size) is left as it was; the
+ * same slot may come in several rows. Alignment and strides as in kv_pages_write. rows >= 0. */
+MLA_API int kv_pages_read(const kv_pages_t* pages, int64_t rows, const int64_t* slot_map, const float* descale_k,
+                   const float* descale_v, void* k_out, void* v_out, int64_t token_stride, int64_t head_stride,
+                   void* stream);
 
 /* Plan of sdpa_paged: what its launches and workspace need, from bounds that the
  * host knows. A job is (sequence, KV head, up to R query rows, split), its rows

@@ -93,3 +93,23 @@ def e4m3_encode(y) -> np.ndarray:
     code = np.where(ar == 0, sign, code)
     code = np.where(np.isnan(y), 0x7F, code)
     return code.astype(np.uint8)
+
+
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_decode(codes) -> np.ndarray:
+    """4-bit codes (sign, two exponent bits of bias 1, one mantissa bit) -> float64 values."""
+    c = np.asarray(codes, dtype=np.int64)
+    return np.where(c & 8, -1.0, 1.0) * E2M1_VALUES[c & 7]
+
+
+def e2m1_encode(y) -> np.ndarray:
+    """Float64 -> 4-bit code: the nearest value, ties to the even code, saturating at 6 (NaN is not a value of the format)."""
+    y = np.asarray(y, dtype=np.float64)
+    a = np.abs(y)
+    code = np.zeros(y.shape, dtype=np.int64)
+    for k in range(1, 8):
+        middle = (E2M1_VALUES[k - 1] + E2M1_VALUES[k]) / 2
+        code = np.where((a > middle) | ((a == middle) & (k % 2 == 0)), k, code)
+    return (code | np.where(np.signbit(y), 8, 0)).astype(np.uint8)

@@ -119,3 +119,44 @@ def prompt_attention(q, k, v, cu_q, cu_kv, sm_scale, floor=F16_FLOOR):
         seen = np.arange(k1 - k0)[None, :] <= at[:, None]
         O[q0:q1], L[q0:q1], A[q0:q1] = attend(q[q0:q1], k[k0:k1], v[k0:k1], seen, sm_scale, floor)
     return O, L, A
+
+
+GROUP4 = 16     # dims of a 4-bit cache that share a scale
+
+
+def four_bit_encode(y):
+    """y [..., 128], the values over the descale: (codes [..., 64], scales [..., 8]) as bytes. The quotients are those of y's own
+    type, so fp32 values give the codes of fp32 divisions."""
+    y = np.asarray(y)
+    g = y.reshape(*y.shape[:-1], y.shape[-1] // GROUP4, GROUP4)
+    amax = np.abs(g).max(-1)
+    with np.errstate(all="ignore"):
+        scales = codecs.e4m3_encode((amax / y.dtype.type(6)).astype(np.float64))
+        s = codecs.e4m3_decode(scales).astype(y.dtype)[..., None]
+        q = np.where(s > 0, g / s, np.copysign(y.dtype.type(0), g))
+    c = codecs.e2m1_encode(np.clip(q, -1e6, 1e6).astype(np.float64)).reshape(y.shape)
+    return (c[..., 0::2] | (c[..., 1::2] << 4)).astype(np.uint8), scales
+
+
+def four_bit_decode(codes, scales) -> np.ndarray:
+    """fp64 values (without the descale) of codes [..., 64] and scales [..., 8]."""
+    codes = np.asarray(codes)
+    v = np.empty((*codes.shape[:-1], 2 * codes.shape[-1]))
+    v[..., 0::2], v[..., 1::2] = codecs.e2m1_decode(codes & 15), codecs.e2m1_decode(codes >> 4)
+    return v * np.repeat(codecs.e4m3_decode(scales), GROUP4, axis=-1)
+
+
+def rotate(x, cos_sin, positions, interleaved=False):
+    """x [rows, heads, 128] turned by the angles of its rows' positions, cos_sin [positions, R]; in x's own type, every
+    product and sum rounded. Rows without a position are left."""
+    x = np.array(x)
+    R = cos_sin.shape[1]
+    for r, p in enumerate(positions):
+        if p < 0 or p >= len(cos_sin):
+            continue
+        c, s = cos_sin[p, :R // 2].astype(x.dtype), cos_sin[p, R // 2:].astype(x.dtype)
+        i, j = (slice(0, R, 2), slice(1, R, 2)) if interleaved else (slice(0, R // 2), slice(R // 2, R))
+        a, b = x[r, :, i].copy(), x[r, :, j].copy()
+        x[r, :, i] = a * c - b * s
+        x[r, :, j] = b * c + a * s
+    return x

@@ -12,6 +12,6 @@ from .binding import (  # noqa: F401
     mla_set_index_checks,
     mla_sparse_decode_direct, mla_sparse_decode_split, mla_split_combine, sdpa_fp8_decode,
     sdpa_fp8_decode_direct, sdpa_fp8_decode_plan, sdpa_fp8_decode_split, sdpa_split_combine,
-    SDPA_BF16, SDPA_E4M3, KvPages, SdpaPagedPlan, kv_pages, kv_pages_map, kv_pages_write, sdpa_paged, sdpa_paged_plan,
-    sdpa_prompt,
+    SDPA_BF16, SDPA_E2M1, SDPA_E4M3, KvPages, SdpaPagedPlan, kv_pages, kv_pages_map, kv_pages_read, kv_pages_write,
+    kv_pages_write_rotary, sdpa_paged, sdpa_paged_plan, sdpa_prompt,
 )

@@ -23,7 +23,7 @@ MLA_STATUS_BAD_INDEX = 0x10
 MLA_STATUS_BAD_ALIGN = 0x4
 MLA_MAX_SPLITS = 64
 MLA_FORCE_BALANCED = -1
-SDPA_BF16, SDPA_E4M3 = 1, 2
+SDPA_BF16, SDPA_E4M3, SDPA_E2M1 = 1, 2, 4
 KV_PAGES_MAX_BATCH = 16384
 MLA_ERR_INVALID_ARG = 1
 OUT_DTYPES = {"f32": MLA_OUT_F32, "bf16": MLA_OUT_BF16, "e4m3": MLA_OUT_E4M3}
@@ -35,7 +35,8 @@ EXPORTS = [
     "sdpa_split_combine", "sdpa_fp8_decode_direct", "sdpa_fp8_decode", "mla_get_status",
     "mla_selftest_wait_timeout", "mla_status_string", "mla_abi_version", "mla_sparse_decode_noalloc",
     "mla_workspace_init", "mla_set_wait_limit_ns", "mla_plan_set_partials_bf16", "mla_set_index_checks",
-    "kv_pages_map", "kv_pages_write", "sdpa_paged_plan", "sdpa_paged", "sdpa_prompt",
+    "kv_pages_map", "kv_pages_write", "sdpa_paged_plan", "sdpa_paged", "sdpa_prompt", "kv_pages_write_rotary",
+    "kv_pages_read",
 ]
 
 
@@ -68,7 +69,8 @@ class KvPages(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("reserved", ctypes.c_int32), ("page_stride", ctypes.c_int64),
-                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+                ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("scale_page_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64)]
 
 
 class SdpaPagedPlan(ctypes.Structure):
@@ -113,6 +115,9 @@ _SIGS = {
     "mla_plan_set_partials_bf16": [ctypes.POINTER(MlaPlan), _I],
     "kv_pages_map": [_I, _I, _P, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P],
     "kv_pages_write": [ctypes.POINTER(KvPages), _I64, _P, _P, _I64, _I64, _P, _P, _P, _P],
+    "kv_pages_write_rotary": [ctypes.POINTER(KvPages), _I64, _I, _P, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I, _I, _P,
+                              _P, _P, _P, _I, _P, _I64, _I64, _P, _I64, _I64, _P],
+    "kv_pages_read": [ctypes.POINTER(KvPages), _I64, _P, _P, _P, _P, _P, _I64, _I64, _P],
     "sdpa_paged_plan": [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(SdpaPagedPlan)],
     "sdpa_paged": [ctypes.POINTER(SdpaPagedPlan), _I, _P, _I64, _I64, ctypes.POINTER(KvPages), _P, _I, _P, _P, _P, _P,
                    _P, _F, _I, _F, _P, _P, _P, _P, _P],
@@ -285,7 +290,7 @@ def mla_sparse_decode_noalloc(s_q: int, topk: int, q, kv, n_kv: int, idx, sm_sca
 
 # -------------------------------------------- paged KV cache, prompt attention --
 
-_SDPA_DTYPES = {"bf16": SDPA_BF16, "e4m3": SDPA_E4M3}
+_SDPA_DTYPES = {"bf16": SDPA_BF16, "e4m3": SDPA_E4M3, "e2m1": SDPA_E2M1}
 
 
 class _Types:
@@ -296,6 +301,7 @@ class _Types:
         self.i32, self.i64, self.f32, self.bf16 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
         self.codes = (torch.uint8, torch.float8_e4m3fn)
         self.data = self.bf16 + self.codes
+        self.bytes4 = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
         self.bytes = (torch.uint8, torch.float32)
         self.sdpa = {torch.bfloat16: SDPA_BF16, torch.uint8: SDPA_E4M3, torch.float8_e4m3fn: SDPA_E4M3}
         self.out = {MLA_OUT_F32: self.f32, MLA_OUT_BF16: self.bf16, MLA_OUT_E4M3: self.codes}
@@ -390,21 +396,40 @@ def _pages(where: str, pages: KvPages, dev: int):
     return ctypes.byref(pages)
 
 
-def kv_pages(k_cache, v_cache) -> KvPages:
+def kv_pages(k_cache, v_cache, k_scales=None, v_scales=None) -> KvPages:
     """The C descriptor of a paged cache from views [num_pages, page_size, h_kv, d] of its tensors (bfloat16, or
     uint8 / float8_e4m3fn codes; any strides over a contiguous d, so a [num_pages, h_kv, page_size, d] cache is
-    passed as its permute(0, 2, 1, 3)). The descriptor keeps the tensors alive; calls that take it want their device to be
-    the current one."""
+    passed as its permute(0, 2, 1, 3)). A cache in 4 bits has views [num_pages, page_size, h_kv, d / 2] of bytes (two e2m1
+    codes each, the first in the low half) and, with them, its scales: views [num_pages, page_size, h_kv, d / 16] of e4m3 bytes
+    in which the rows of a page and head lie side by side, the permute(0, 2, 1, 3) of [num_pages, h_kv, page_size, d / 16].
+    The descriptor keeps the tensors alive; calls that take it want their device to be the current one."""
     where, t = "kv_pages", _t()
     dev = _device(where)
-    k, v = (_dev(where, n, x, t.data, dev, contiguous=False) for n, x in (("k_cache", k_cache), ("v_cache", v_cache)))
+    four = k_scales is not None or v_scales is not None
+    k, v = (_dev(where, n, x, t.bytes4 if four else t.data, dev, contiguous=False)
+            for n, x in (("k_cache", k_cache), ("v_cache", v_cache)))
     st = _strided(where, "k_cache", k_cache, 4)
-    dt = t.sdpa[k_cache.dtype]
-    if v_cache.shape != k_cache.shape or t.sdpa[v_cache.dtype] != dt or _strided(where, "v_cache", v_cache, 4) != st:
+    dt = SDPA_E2M1 if four else t.sdpa[k_cache.dtype]
+    if (v_cache.shape != k_cache.shape or (not four and t.sdpa[v_cache.dtype] != dt)
+            or _strided(where, "v_cache", v_cache, 4) != st):
         _refuse(where, "k_cache and v_cache differ in shape, type or strides")
     n, ps, h, d = k_cache.shape
-    pages = KvPages(k, v, dt, n, ps, h, d, 0, st[0], st[1], st[2])
-    pages.tensors, pages.device = (k_cache, v_cache), dev
+    if not four:
+        pages = KvPages(k, v, dt, n, ps, h, d, 0, st[0], st[1], st[2])
+        pages.tensors, pages.device = (k_cache, v_cache), dev
+        return pages
+    d *= 2
+    ks, vs = (_dev(where, name, x, t.codes, dev, contiguous=False) for name, x in (("k_scales", k_scales), ("v_scales", v_scales)))
+    ss = _strided(where, "k_scales", k_scales, 4)
+    if tuple(k_scales.shape) != (n, ps, h, d // 16) or v_scales.shape != k_scales.shape or _strided(where, "v_scales", v_scales, 4) != ss:
+        _refuse(where, f"k_scales and v_scales must be [{n}, {ps}, {h}, {d // 16}], with the same strides")
+    if ps > 1 and ss[1] != d // 16:
+        _refuse(where, "the scales of a page and head must lie side by side: the permute(0, 2, 1, 3) of [num_pages, h_kv, page_size, d / 16]")
+    # (a dimension of one element, whose stride says nothing, counts as packed behind the rows)
+    sh = ss[2] if h > 1 else ps * (d // 16)
+    sp = ss[0] if n > 1 else ps * (d // 16) * h
+    pages = KvPages(k, v, dt, n, ps, h, d, 0, st[0], st[1], st[2], ks, vs, sp, sh)
+    pages.tensors, pages.device = (k_cache, v_cache, k_scales, v_scales), dev
     return pages
 
 
@@ -445,6 +470,74 @@ def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, desca
     _check(lib().kv_pages_write(_pages(where, pages, dev), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev)), where)
 
 
+def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, slot_map, q_out=None, k_out=None, *,
+                          interleaved: bool = False, descale_q=None, descale_k=None, descale_v=None, stream=None):
+    """kv_pages_write with the rows' rotation on the way: q (or None) and k_new turned by the angles of their positions, q into
+    q_out (bfloat16, or uint8 / float8_e4m3fn codes; None: in place), k_new into its slots and, rotated, into k_out
+    (bfloat16, or None). cos_sin is float32 [num_positions, rotary_dim], cosines then sines."""
+    where, t = "kv_pages_write_rotary", _t()
+    dev = _device(where)
+    k = _dev(where, "k_new", k_new, t.bf16, dev, contiguous=False)
+    v = _dev(where, "v_new", v_new, t.bf16, dev, contiguous=False)
+    st = _strided(where, "k_new", k_new, 3)
+    if v_new.shape != k_new.shape or _strided(where, "v_new", v_new, 3) != st:
+        _refuse(where, "k_new and v_new differ in shape or strides")
+    rows, h, d = k_new.shape
+    if h != pages.h_kv or d != pages.d:
+        _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
+    pos = _dev(where, "positions", positions, t.i32, dev, rows)
+    cs = _dev(where, "cos_sin", cos_sin, t.f32, dev, 1)
+    if cos_sin.dim() != 2:
+        _refuse(where, "cos_sin must be [num_positions, rotary_dim]")
+    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
+    h_q, qp, qs, qo, qo_dt, os_ = 0, None, (0, 0), None, SDPA_BF16, (0, 0)
+    if q is not None:
+        qp = _dev(where, "q", q, t.bf16, dev, contiguous=False)
+        qs = _strided(where, "q", q, 3)
+        h_q = q.shape[1]
+        if q.shape[0] != rows or q.shape[2] != d:
+            _refuse(where, f"q must be [{rows}, h_q, {d}]")
+        if q_out is None:
+            qo, os_ = qp, qs
+        else:
+            qo = _dev(where, "q_out", q_out, t.data, dev, contiguous=False)
+            os_, qo_dt = _strided(where, "q_out", q_out, 3), t.sdpa[q_out.dtype]
+            if q_out.shape != q.shape:
+                _refuse(where, "q_out must have q's shape")
+    elif q_out is not None:
+        _refuse(where, "q_out without q")
+    ko, ks = None, (0, 0)
+    if k_out is not None:
+        ko = _dev(where, "k_out", k_out, t.bf16, dev, contiguous=False)
+        ks = _strided(where, "k_out", k_out, 3)
+        if k_out.shape != k_new.shape:
+            _refuse(where, "k_out must have k_new's shape")
+    dq = _opt(where, "descale_q", descale_q, t.f32, dev, 1)
+    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    _check(lib().kv_pages_write_rotary(_pages(where, pages, dev), rows, h_q, qp, qs[0], qs[1], k, v, st[0], st[1], pos, cs,
+                                       cos_sin.shape[0], cos_sin.shape[1], int(interleaved), slots, dq, dk, dv, qo_dt, qo, os_[0],
+                                       os_[1], ko, ks[0], ks[1], _on(stream, dev)), where)
+
+
+def kv_pages_read(pages: KvPages, slot_map, k_out, v_out, descale_k=None, descale_v=None, stream=None):
+    """Rows of a cache of any type into k_out and v_out (bfloat16 [rows, h_kv, d], any strides over a contiguous d)."""
+    where, t = "kv_pages_read", _t()
+    dev = _device(where)
+    k = _dev(where, "k_out", k_out, t.bf16, dev, contiguous=False)
+    v = _dev(where, "v_out", v_out, t.bf16, dev, contiguous=False)
+    st = _strided(where, "k_out", k_out, 3)
+    if v_out.shape != k_out.shape or _strided(where, "v_out", v_out, 3) != st:
+        _refuse(where, "k_out and v_out differ in shape or strides")
+    rows, h, d = k_out.shape
+    if h != pages.h_kv or d != pages.d:
+        _refuse(where, f"k_out and v_out must be [rows, {pages.h_kv}, {pages.d}]")
+    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
+    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    _check(lib().kv_pages_read(_pages(where, pages, dev), rows, slots, dk, dv, k, v, st[0], st[1], _on(stream, dev)), where)
+
+
 def sdpa_paged_plan(batch: int, h_q: int, h_kv: int, d: int, dtype, max_q_per_seq: int, total_q_max: int, max_kv: int,
                     *, num_sms: int = 0, max_splits: int = 0, force_splits: int = 0) -> SdpaPagedPlan:
     plan = SdpaPagedPlan()
@@ -462,7 +555,7 @@ def sdpa_paged(plan: SdpaPagedPlan, total_q: int, q, pages: KvPages, block_table
     where, t = "sdpa_paged", _t()
     dev = _device(where)
     batch, h_q, d = plan.batch, plan.h_q, plan.d
-    qp = _dev(where, "q", q, t.bf16 if plan.dtype == SDPA_BF16 else t.codes, dev, contiguous=False)
+    qp = _dev(where, "q", q, t.codes if plan.dtype == SDPA_E4M3 else t.bf16, dev, contiguous=False)
     st = _strided(where, "q", q, 3)
     n, h, x = q.shape
     if h != h_q or x != d or n < total_q:

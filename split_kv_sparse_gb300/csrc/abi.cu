@@ -70,7 +70,7 @@ int device_state(DeviceState** out) {
     }
     if (skv::prepare_mla_kernels() != cudaSuccess || skv::prepare_sdpa_kernels() != cudaSuccess ||
         skv::prepare_paged_kernels() != cudaSuccess || skv::prepare_attn_tile() != cudaSuccess ||
-        skv::prepare_attn_row() != cudaSuccess) {
+        skv::prepare_attn_row() != cudaSuccess || skv::prepare_attn_row4() != cudaSuccess) {
       cudaGetLastError();
       return MLA_ERR_CUDA;
     }

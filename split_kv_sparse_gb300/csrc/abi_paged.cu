@@ -16,6 +16,8 @@ constexpr int kDim = 128;
 
 uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 
+// Bytes of an element of Q, and of a stride's unit of K and V.
+int q_size(int dtype) { return dtype == SDPA_E4M3 ? 1 : 2; }
 int elem_size(int dtype) { return dtype == SDPA_BF16 ? 2 : 1; }
 
 // An element stride that TMA and 16-byte loads can take.
@@ -36,7 +38,7 @@ bool words_ok(std::initializer_list<const void*> ps) {
 
 int check_heads(int batch, int h_q, int h_kv, int d, int dtype) {
   if (d != kDim) return MLA_ERR_UNSUPPORTED;
-  if (dtype != SDPA_BF16 && dtype != SDPA_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (dtype != SDPA_BF16 && dtype != SDPA_E4M3 && dtype != SDPA_E2M1) return MLA_ERR_UNSUPPORTED;
   if (batch < 1 || h_kv < 1 || h_q < 1 || h_q % h_kv != 0) return MLA_ERR_INVALID_ARG;
   if (h_q / h_kv > 128) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
@@ -44,7 +46,7 @@ int check_heads(int batch, int h_q, int h_kv, int d, int dtype) {
 
 int check_pages(const kv_pages_t* p) {
   if (p == nullptr) return MLA_ERR_INVALID_ARG;
-  if (p->dtype != SDPA_BF16 && p->dtype != SDPA_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (p->dtype != SDPA_BF16 && p->dtype != SDPA_E4M3 && p->dtype != SDPA_E2M1) return MLA_ERR_UNSUPPORTED;
   if (p->d != kDim) return MLA_ERR_UNSUPPORTED;
   if (p->k == nullptr || p->v == nullptr || !ptr_aligned(p->k, 16) || !ptr_aligned(p->v, 16)) return MLA_ERR_INVALID_ARG;
   if (p->num_pages < 1 || p->h_kv < 1) return MLA_ERR_INVALID_ARG;
@@ -52,6 +54,11 @@ int check_pages(const kv_pages_t* p) {
   const int e = elem_size(p->dtype);
   if (!stride_ok(p->page_stride, e) || !stride_ok(p->row_stride, e) || !stride_ok(p->head_stride, e))
     return MLA_ERR_INVALID_ARG;
+  if (p->dtype == SDPA_E2M1) {
+    if (p->k_scales == nullptr || p->v_scales == nullptr || !ptr_aligned(p->k_scales, 16) || !ptr_aligned(p->v_scales, 16))
+      return MLA_ERR_INVALID_ARG;
+    if (!stride_ok(p->scale_page_stride, 1) || !stride_ok(p->scale_head_stride, 1)) return MLA_ERR_INVALID_ARG;
+  }
   return MLA_OK;
 }
 
@@ -116,11 +123,44 @@ int encode_kv_wide(CUtensorMap* m, const kv_pages_t* p, const void* base, int wi
              : MLA_ERR_CUDA;
 }
 
+// K or V codes of 4-bit pages in boxes of `box_rows` rows of one page and head, and their scales, two words a row.
+int encode_kv4(CUtensorMap* m, const kv_pages_t* p, const void* base, int box_rows) {
+  auto enc = skv::tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t dims[4] = {kDim / 2, static_cast<cuuint64_t>(p->page_size), static_cast<cuuint64_t>(p->num_pages),
+                              static_cast<cuuint64_t>(p->h_kv)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p->row_stride), static_cast<cuuint64_t>(p->page_stride),
+                                 static_cast<cuuint64_t>(p->head_stride)};
+  const cuuint32_t box[4] = {kDim / 2, static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+int encode_scales(CUtensorMap* m, const kv_pages_t* p, const void* base, int box_rows) {
+  auto enc = skv::tensor_map_encoder();
+  if (enc == nullptr) return MLA_ERR_CUDA;
+  const cuuint64_t page = static_cast<cuuint64_t>(p->scale_page_stride);
+  const cuuint64_t dims[4] = {2 * static_cast<cuuint64_t>(p->page_size), 1, static_cast<cuuint64_t>(p->num_pages),
+                              static_cast<cuuint64_t>(p->h_kv)};
+  const cuuint64_t strides[3] = {page, page, static_cast<cuuint64_t>(p->scale_head_stride)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(2 * box_rows), 1, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), dims, strides, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? MLA_OK
+             : MLA_ERR_CUDA;
+}
+
 // The most (sequence, query tile) pairs of `tokens` tokens that total_q rows of `batch` sequences can make.
 int64_t tiles_bound(int total_q, int batch, int tokens) { return total_q / tokens + std::min(total_q, batch); }
 
-// Tokens of one job's rows.
-int job_tokens(bool rows16, int group) { return rows16 ? skv::kRowRows / group : 2 * (128 / group); }
+// Query rows of a job, and the tokens in them (row_kernel: as in the plan).
+int job_rows(int row_kernel) { return row_kernel == 2 ? 8 : row_kernel == 1 ? skv::kRowRows : skv::kTileRows; }
+int job_tokens(int row_kernel, int group) { return row_kernel ? job_rows(row_kernel) / group : 2 * (128 / group); }
 
 // Equal shares: of a wave's CTAs as many for each of `side` KV heads, the largest divisor of h_kv that leaves at most
 // one in sixteen without work.
@@ -140,14 +180,14 @@ bool plan_layout(sdpa_paged_plan_t* p) {
   const int group = p->h_q / p->h_kv;
   const bool rows16 = p->row_kernel != 0;
   const int wave = rows16 ? p->num_sms * skv::kRowCtasPerSm : p->num_sms;
-  const int job_rows = rows16 ? skv::kRowRows : skv::kTileRows;
-  const int64_t unsplit = tiles_bound(p->total_q_max, p->batch, job_tokens(rows16, group)) * p->h_kv;
+  const int slot_rows = rows16 ? skv::kRowRows : skv::kTileRows;
+  const int64_t unsplit = tiles_bound(p->total_q_max, p->batch, job_tokens(p->row_kernel, group)) * p->h_kv;
   // split jobs: as many as forced; two pieces of cut jobs a CTA; at most so many waves (the rule keeps to that)
   const int64_t slots = !p->adaptive_splits ? unsplit * p->num_splits
                         : rows16            ? 2 * share_ctas(wave, p->h_kv)
                                             : static_cast<int64_t>(wave) * skv::kTileSplitWaves;
-  if (slots * job_rows > 0x7FFFFFFFll) return false;
-  const uint64_t rows = static_cast<uint64_t>(slots) * job_rows;
+  if (slots * slot_rows > 0x7FFFFFFFll) return false;
+  const uint64_t rows = static_cast<uint64_t>(slots) * slot_rows;
   p->o_acc_bytes = rows * kDim * 4;
   p->lse_acc_offset = round_up(p->o_acc_bytes, 256);
   p->lse_acc_bytes = rows * 4;
@@ -160,6 +200,22 @@ int shift_of(int pow2) {
   int s = 0;
   while ((1 << s) < pow2) ++s;
   return s;
+}
+
+// What the append and the read-back take of a cache.
+void set_pages(skv::PagesAppendArgs* a, const kv_pages_t* p) {
+  a->k = p->k;
+  a->v = p->v;
+  a->k_scales = static_cast<uint8_t*>(p->k_scales);
+  a->v_scales = static_cast<uint8_t*>(p->v_scales);
+  a->page_stride = p->page_stride;
+  a->row_stride = p->row_stride;
+  a->cache_head_stride = p->head_stride;
+  a->scale_page_stride = p->scale_page_stride;
+  a->scale_head_stride = p->scale_head_stride;
+  a->num_slots = static_cast<int64_t>(p->num_pages) * p->page_size;
+  a->page_shift = shift_of(p->page_size);
+  a->h_kv = p->h_kv;
 }
 
 }  // namespace
@@ -217,6 +273,19 @@ int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, con
   skv::DeviceInfo dev;
   st = skv::current_device(&dev);
   if (st != MLA_OK) return st;
+  if (pages->dtype == SDPA_E2M1) {
+    skv::PagesAppendArgs a{};
+    set_pages(&a, pages);
+    a.k_new = static_cast<const uint16_t*>(k_new);
+    a.v_new = static_cast<const uint16_t*>(v_new);
+    a.token_stride = token_stride;
+    a.head_stride = head_stride;
+    a.slots = slot_map;
+    a.rows = rows;
+    a.descale_k = descale_k;
+    a.descale_v = descale_v;
+    return cuda_status(skv::launch_pages_append(a, pages->dtype, static_cast<cudaStream_t>(stream)));
+  }
   skv::PagesWriteArgs a{};
   a.k_new = static_cast<const uint16_t*>(k_new);
   a.v_new = static_cast<const uint16_t*>(v_new);
@@ -235,6 +304,94 @@ int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, con
   a.descale_k = descale_k;
   a.descale_v = descale_v;
   return cuda_status(skv::launch_pages_write(a, pages->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pages_write_rotary(const kv_pages_t* pages, int64_t rows, int h_q, const void* q, int64_t q_token_stride,
+                          int64_t q_head_stride, const void* k_new, const void* v_new, int64_t token_stride, int64_t head_stride,
+                          const int32_t* positions, const float* cos_sin, int64_t num_positions, int rotary_dim, int interleaved,
+                          const int64_t* slot_map, const float* descale_q, const float* descale_k, const float* descale_v,
+                          int q_out_dtype, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                          int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream) {
+  int st = check_pages(pages);
+  if (st != MLA_OK) return st;
+  if (rows < 0 || rows > 0x7FFFFFFFll || h_q < 0) return MLA_ERR_INVALID_ARG;
+  if (rotary_dim < 32 || rotary_dim > kDim || rotary_dim % 32 != 0) return MLA_ERR_UNSUPPORTED;
+  if (interleaved != 0 && interleaved != 1) return MLA_ERR_INVALID_ARG;
+  if (num_positions < 1 || num_positions > (int64_t{1} << 31)) return MLA_ERR_INVALID_ARG;
+  if (rows == 0) return MLA_OK;
+  if (k_new == nullptr || v_new == nullptr || slot_map == nullptr || positions == nullptr || cos_sin == nullptr)
+    return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(k_new, 16) || !ptr_aligned(v_new, 16) || !ptr_aligned(slot_map, 8) || !ptr_aligned(cos_sin, 16))
+    return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(token_stride, 2) || !stride_ok(head_stride, 2)) return MLA_ERR_INVALID_ARG;
+  if (!words_ok({positions, descale_q, descale_k, descale_v})) return MLA_ERR_INVALID_ARG;
+  if (h_q > 0) {
+    if (q == nullptr || q_out == nullptr || !ptr_aligned(q, 16) || !ptr_aligned(q_out, 16)) return MLA_ERR_INVALID_ARG;
+    if (q_out_dtype != SDPA_BF16 && q_out_dtype != SDPA_E4M3) return MLA_ERR_INVALID_ARG;
+    const int e = q_size(q_out_dtype);
+    if (!stride_ok(q_token_stride, 2) || !stride_ok(q_head_stride, 2) || !stride_ok(q_out_token_stride, e) ||
+        !stride_ok(q_out_head_stride, e))
+      return MLA_ERR_INVALID_ARG;
+  }
+  if (k_out != nullptr && (!ptr_aligned(k_out, 16) || !stride_ok(k_out_token_stride, 2) || !stride_ok(k_out_head_stride, 2)))
+    return MLA_ERR_INVALID_ARG;
+  if (rows * (h_q + 2ll * pages->h_kv) > (int64_t{1} << 35)) return MLA_ERR_INVALID_ARG;
+  skv::DeviceInfo dev;
+  if ((st = skv::current_device(&dev)) != MLA_OK) return st;
+  skv::PagesAppendArgs a{};
+  set_pages(&a, pages);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.token_stride = token_stride;
+  a.head_stride = head_stride;
+  a.slots = slot_map;
+  a.rows = rows;
+  a.h_q = h_q;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.num_positions = num_positions;
+  a.rot = rotary_dim;
+  a.interleaved = interleaved;
+  a.q_out = q_out;
+  a.q_out_e4m3 = q_out_dtype == SDPA_E4M3;
+  a.qo_ts = q_out_token_stride;
+  a.qo_hs = q_out_head_stride;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.ko_ts = k_out_token_stride;
+  a.ko_hs = k_out_head_stride;
+  a.descale_q = descale_q;
+  a.descale_k = descale_k;
+  a.descale_v = descale_v;
+  return cuda_status(skv::launch_pages_append(a, pages->dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int kv_pages_read(const kv_pages_t* pages, int64_t rows, const int64_t* slot_map, const float* descale_k, const float* descale_v,
+                  void* k_out, void* v_out, int64_t token_stride, int64_t head_stride, void* stream) {
+  int st = check_pages(pages);
+  if (st != MLA_OK) return st;
+  if (rows < 0 || rows > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (rows == 0) return MLA_OK;
+  if (k_out == nullptr || v_out == nullptr || slot_map == nullptr) return MLA_ERR_INVALID_ARG;
+  if (!ptr_aligned(k_out, 16) || !ptr_aligned(v_out, 16) || !ptr_aligned(slot_map, 8)) return MLA_ERR_INVALID_ARG;
+  if (!stride_ok(token_stride, 2) || !stride_ok(head_stride, 2)) return MLA_ERR_INVALID_ARG;
+  if (!words_ok({descale_k, descale_v})) return MLA_ERR_INVALID_ARG;
+  if (rows * pages->h_kv > (int64_t{1} << 35)) return MLA_ERR_INVALID_ARG;
+  skv::DeviceInfo dev;
+  if ((st = skv::current_device(&dev)) != MLA_OK) return st;
+  skv::PagesAppendArgs a{};
+  set_pages(&a, pages);
+  a.slots = slot_map;
+  a.rows = rows;
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.v_out = static_cast<uint16_t*>(v_out);
+  a.ko_ts = token_stride;
+  a.ko_hs = head_stride;
+  a.descale_k = descale_k;
+  a.descale_v = descale_v;
+  return cuda_status(skv::launch_pages_read(a, pages->dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_per_seq, int total_q_max, int max_kv,
@@ -261,7 +418,9 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
     adaptive = S > 1 ? 1 : 0;
   }
   // few rows a sequence: the kernel of 16-row jobs, of which an SM holds two
-  const bool rows16 = static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
+  const bool four = dtype == SDPA_E2M1;
+  if (four && group > skv::kRowRows) return MLA_ERR_UNSUPPORTED;
+  const bool rows16 = four || static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
   out->batch = batch;
   out->h_q = h_q;
   out->h_kv = h_kv;
@@ -273,7 +432,7 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->num_splits = S;
   out->num_sms = num_sms;
   out->adaptive_splits = adaptive;
-  out->row_kernel = rows16 ? 1 : 0;
+  out->row_kernel = !rows16 ? 0 : four && static_cast<int64_t>(max_q_per_seq) * group <= 8 ? 2 : 1;
   if (S > 1 && !plan_layout(out)) {
     std::memset(out, 0, sizeof(*out));
     return MLA_ERR_UNSUPPORTED;
@@ -293,12 +452,14 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if (pages->dtype != plan->dtype || pages->h_kv != plan->h_kv || pages->d != plan->d) return MLA_ERR_INVALID_ARG;
   if (plan->num_splits < 1 || plan->num_splits > MLA_MAX_SPLITS || plan->num_sms < 1) return MLA_ERR_INVALID_ARG;
   if (plan->adaptive_splits != 0 && plan->num_splits < 2) return MLA_ERR_INVALID_ARG;
-  if (plan->row_kernel != 0 && plan->h_q / plan->h_kv > skv::kRowRows) return MLA_ERR_INVALID_ARG;
+  if (plan->dtype == SDPA_E2M1 && plan->row_kernel == 0) return MLA_ERR_INVALID_ARG;
+  if (plan->row_kernel < 0 || plan->row_kernel > (plan->dtype == SDPA_E2M1 ? 2 : 1)) return MLA_ERR_INVALID_ARG;
+  if (plan->row_kernel != 0 && plan->h_q / plan->h_kv > job_rows(plan->row_kernel)) return MLA_ERR_INVALID_ARG;
   if (total_q < 1 || total_q > plan->total_q_max || table_width < 1) return MLA_ERR_INVALID_ARG;
   if (q == nullptr || block_table == nullptr || kv_lens == nullptr || cu_seqlens_q == nullptr) return MLA_ERR_INVALID_ARG;
   if (!ptr_aligned(q, 16) || !words_ok({block_table, kv_lens, cu_seqlens_q, descale_q, descale_k, descale_v, lse_out, amax_out}))
     return MLA_ERR_INVALID_ARG;
-  const int e = elem_size(plan->dtype);
+  const int e = q_size(plan->dtype);
   if (!stride_ok(q_token_stride, e) || !stride_ok(q_head_stride, e)) return MLA_ERR_INVALID_ARG;
   if (!out_ok(out, out_dtype, out_inv_scale) || !std::isfinite(sm_scale)) return MLA_ERR_INVALID_ARG;
   if (plan->num_splits > 1) {
@@ -351,14 +512,18 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.status = dev.status;
   a.wait_limit_ns = skv::wait_limit_ns();
   a.drain_limit_ns = skv::drain_limit_ns();
-  CUtensorMap tq, tk, tv;
-  const int box = rows16 ? skv::attn_row_box(plan->dtype, pages->page_size) : std::min(pages->page_size, 128);
+  CUtensorMap tq, tk, tv, tks, tvs;
+  const bool four = plan->dtype == SDPA_E2M1;
+  const int box = !rows16 ? std::min(pages->page_size, 128)
+                  : four  ? skv::attn_row4_box(pages->page_size)
+                          : skv::attn_row_box(plan->dtype, pages->page_size);
   if (!rows16 && plan->dtype == SDPA_BF16) {
     // (with one head its stride says nothing)
     if (pages->h_kv == 1 || pages->head_stride == kDim) a.kv_wide = 1;
     else if (pages->head_stride == pages->page_size * pages->row_stride) a.kv_wide = 2;
   }
   auto encode = [&](CUtensorMap* m, const void* base) {
+    if (four) return encode_kv4(m, pages, base, box);
     if (a.kv_wide) return encode_kv_wide(m, pages, base, a.kv_wide, box);
     return encode_kv(m, plan->dtype, base, pages->page_size, pages->row_stride, pages->num_pages, pages->page_stride,
                      pages->h_kv, pages->head_stride, box);
@@ -366,7 +531,10 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if (!rows16 && (st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK)
     return st;
   if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
-  const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(rows16, a.group)) * a.h_kv;
+  if (four && ((st = encode_scales(&tks, pages, pages->k_scales, box)) != MLA_OK ||
+               (st = encode_scales(&tvs, pages, pages->v_scales, box)) != MLA_OK))
+    return st;
+  const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(plan->row_kernel, a.group)) * a.h_kv;
   int64_t grid = unsplit * a.num_splits;
   // Equal shares balance best, but let query tiles of one sequence read the same keys at different times. Decode has one
   // query tile a sequence. With more rows, the keys of e4m3 still come from DRAM fast enough (32 KB a tile and SM in
@@ -391,8 +559,9 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     grid = share_ctas(a.num_sms, a.h_kv);
     a.part_gap = static_cast<int>(grid) * (rows16 ? skv::kRowRows : skv::kTileRows);
   }
-  st = cuda_status(rows16 ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
-                          : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
+  st = cuda_status(rows16 && four ? skv::launch_attn_row4(tk, tv, tks, tvs, a, job_rows(plan->row_kernel), grid, cs)
+                   : rows16       ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
+                                  : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;
   return cuda_status(skv::launch_attn_combine(a, rows16 ? skv::kRowRows : skv::kTileRows, cs));
 }
@@ -403,6 +572,7 @@ int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int
                 const float* descale_q, const float* descale_k, const float* descale_v, float sm_scale, int out_dtype,
                 float out_inv_scale, void* out, float* lse_out, float* amax_out, void* stream) {
   int st = check_heads(batch, h_q, h_kv, d, dtype);
+  if (st == MLA_OK && dtype == SDPA_E2M1) st = MLA_ERR_UNSUPPORTED;   // (a form of caches; kv_pages_read gives bf16 rows)
   if (st != MLA_OK) return st;
   if (total_q < 1 || total_kv < 1 || total_kv > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(total_q) * h_q > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;

@@ -197,6 +197,11 @@ cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, c
 cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
                             int64_t grid, cudaStream_t stream);
 int attn_row_box(int dtype, int page_size);
+// 4-bit pages; rows: of a job, 8 or 16. tm_k / tm_v: codes, box {64 bytes, attn_row4_box(page size) rows, 1, 1}, 64-byte
+// swizzle; tm_ks / tm_vs: scales as 4-D {rows * 2 words, 1, pages, heads}, box {2 attn_row4_box words, 1, 1, 1}.
+cudaError_t launch_attn_row4(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
+                             const AttnArgs& a, int rows, int64_t grid, cudaStream_t stream);
+int attn_row4_box(int page_size);
 // CTAs of the row kernel that an SM holds.
 constexpr int kRowCtasPerSm = 2;
 // Folds the partial rows of every split token; a.num_splits > 1. rows_per_slot: kTileRows or kRowRows.
@@ -235,8 +240,45 @@ struct PagesWriteArgs {
 };
 cudaError_t launch_pages_write(const PagesWriteArgs& a, int dtype, cudaStream_t stream);
 
+// Rows with arithmetic on the way: the append that rotates, the append into 4-bit pages, the read-back.
+struct PagesAppendArgs {
+  const uint16_t* q;            // [rows][h_q][128] (h_q may be 0)
+  int64_t q_ts, q_hs;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  int64_t token_stride, head_stride;
+  const int64_t* slots;
+  int64_t rows;
+  int h_q, h_kv;
+  const int32_t* positions;     // null: no rotation
+  const float* cos_sin;         // [num_positions][rot]: rot / 2 cosines, then the sines
+  int64_t num_positions;
+  int rot, interleaved;
+  void* q_out;                  // bf16, or e4m3 codes
+  int q_out_e4m3;
+  int64_t qo_ts, qo_hs;
+  uint16_t* k_out;              // append: rotated rows of k, or null; read: rows of k
+  uint16_t* v_out;              // read: rows of v, of k_out's strides
+  int64_t ko_ts, ko_hs;
+  void* k;
+  void* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  int64_t page_stride, row_stride, cache_head_stride;   // (4-bit pages: in bytes)
+  int64_t scale_page_stride, scale_head_stride;
+  int64_t num_slots;
+  int page_shift;
+  const float* descale_q;
+  const float* descale_k;
+  const float* descale_v;
+};
+// dtype: of the cache.
+cudaError_t launch_pages_append(const PagesAppendArgs& a, int dtype, cudaStream_t stream);
+cudaError_t launch_pages_read(const PagesAppendArgs& a, int dtype, cudaStream_t stream);
+
 cudaError_t prepare_paged_kernels();
 cudaError_t prepare_attn_tile();
 cudaError_t prepare_attn_row();
+cudaError_t prepare_attn_row4();
 
 }  // namespace skv

@@ -1,11 +1,11 @@
 // The paged KV cache's bookkeeping and append: block tables and slot maps from
 // request lengths, and the copy (or e4m3 cast) of new K/V rows into their slots.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include <algorithm>
 
 #include "attn_common.cuh"
+#include "quant.cuh"
 
 namespace skv {
 namespace {
@@ -173,26 +173,6 @@ __global__ void __launch_bounds__(256) pages_slots_kernel(const PagesMapArgs a) 
 
 // --------------------------------------------------------------- the append --
 
-// x / d for many x by one d, rounded to nearest as a division: with y = RN(1 / d) and q =
-// RN(x y), the residual x - q d is exact in an FMA and q + (x - q d) y rounds to the quotient
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000", 1990; a
-// zero keeps q's sign). Where y is not a normal number, or a q leaves the range, the
-// eight values are divided one by one (in a loop of its own: sixteen divisions
-// inlined here cost 24.2 us where this takes 20.1, 16,001 rows of 8 heads into e4m3).
-struct Divider {
-  float d, y;
-  bool plain;
-};
-__device__ __forceinline__ Divider divider(float d) {
-  Divider by;
-  by.d = d;
-  by.y = __fdiv_rn(1.f, d);
-  by.plain = !(fabsf(by.y) >= 1.17549435e-38f && fabsf(by.y) <= 3.40282347e38f);
-  return by;
-}
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
 __device__ __forceinline__ uint2 e4m3x8_of(const uint4& x, const Divider& by) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t c[4];
