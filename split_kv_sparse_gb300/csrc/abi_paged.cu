@@ -72,13 +72,13 @@ int cuda_status(cudaError_t e) {
 int encode_q(CUtensorMap* m, int dtype, const void* q, int64_t ts, int64_t hs, int h_q, int group, int total_q) {
   auto enc = skv::tensor_map_encoder();
   if (enc == nullptr) return MLA_ERR_CUDA;
-  const cuuint64_t e = elem_size(dtype);
+  const cuuint64_t e = q_size(dtype);
   const cuuint64_t dims[3] = {kDim, static_cast<cuuint64_t>(h_q), static_cast<cuuint64_t>(total_q)};
   const cuuint64_t strides[2] = {hs * e, ts * e};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / e), static_cast<cuuint32_t>(group),
                              static_cast<cuuint32_t>(128 / group)};
   const cuuint32_t one[3] = {1, 1, 1};
-  return enc(m, dtype == SDPA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+  return enc(m, e == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
              const_cast<void*>(q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? MLA_OK
@@ -418,9 +418,7 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
     adaptive = S > 1 ? 1 : 0;
   }
   // few rows a sequence: the kernel of 16-row jobs, of which an SM holds two
-  const bool four = dtype == SDPA_E2M1;
-  if (four && group > skv::kRowRows) return MLA_ERR_UNSUPPORTED;
-  const bool rows16 = four || static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
+  const bool rows16 = static_cast<int64_t>(max_q_per_seq) * group <= skv::kRowRows;
   out->batch = batch;
   out->h_q = h_q;
   out->h_kv = h_kv;
@@ -432,7 +430,7 @@ int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int max_q_pe
   out->num_splits = S;
   out->num_sms = num_sms;
   out->adaptive_splits = adaptive;
-  out->row_kernel = !rows16 ? 0 : four && static_cast<int64_t>(max_q_per_seq) * group <= 8 ? 2 : 1;
+  out->row_kernel = !rows16 ? 0 : dtype == SDPA_E2M1 && static_cast<int64_t>(max_q_per_seq) * group <= 8 ? 2 : 1;
   if (S > 1 && !plan_layout(out)) {
     std::memset(out, 0, sizeof(*out));
     return MLA_ERR_UNSUPPORTED;
@@ -452,7 +450,6 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if (pages->dtype != plan->dtype || pages->h_kv != plan->h_kv || pages->d != plan->d) return MLA_ERR_INVALID_ARG;
   if (plan->num_splits < 1 || plan->num_splits > MLA_MAX_SPLITS || plan->num_sms < 1) return MLA_ERR_INVALID_ARG;
   if (plan->adaptive_splits != 0 && plan->num_splits < 2) return MLA_ERR_INVALID_ARG;
-  if (plan->dtype == SDPA_E2M1 && plan->row_kernel == 0) return MLA_ERR_INVALID_ARG;
   if (plan->row_kernel < 0 || plan->row_kernel > (plan->dtype == SDPA_E2M1 ? 2 : 1)) return MLA_ERR_INVALID_ARG;
   if (plan->row_kernel != 0 && plan->h_q / plan->h_kv > job_rows(plan->row_kernel)) return MLA_ERR_INVALID_ARG;
   if (total_q < 1 || total_q > plan->total_q_max || table_width < 1) return MLA_ERR_INVALID_ARG;
@@ -545,7 +542,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   // The length is the plan's bound: 2 x 2,048 over 4,096 under a plan for 131,072 keys take 150 us instead of 139.
   constexpr int kLongKeys = 6144;
   if (plan->adaptive_splits) {
-    const bool shares = rows16 || (plan->dtype == SDPA_E4M3 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);
+    const bool shares = rows16 || (plan->dtype != SDPA_BF16 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);
     a.adaptive = shares ? skv::kShares : skv::kByLength;
   }
   if (a.adaptive == skv::kByLength) {
@@ -561,6 +558,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   }
   st = cuda_status(rows16 && four ? skv::launch_attn_row4(tk, tv, tks, tvs, a, job_rows(plan->row_kernel), grid, cs)
                    : rows16       ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
+                   : four         ? skv::launch_attn_tile4(tq, tk, tv, tks, tvs, a, grid, cs)
                                   : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;
   return cuda_status(skv::launch_attn_combine(a, rows16 ? skv::kRowRows : skv::kTileRows, cs));

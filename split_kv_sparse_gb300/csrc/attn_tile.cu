@@ -27,6 +27,7 @@
 // 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
 #include "attn_common.cuh"
+#include "quant.cuh"
 
 namespace skv {
 namespace {
@@ -36,36 +37,50 @@ constexpr int kTile = kAttnKeyTile;
 // A piece's start and end, in halves of a key tile of an equal share (2 to 12 measure alike).
 constexpr int kTileHead = 4;
 
-template <bool kF8>
+// kType: of the pages (1 bf16, 2 e4m3, 4 in 4 bits).
+template <int kType>
 struct Cfg {
-  static constexpr int kThreads = kF8 ? 512 : 384;
-  static constexpr int kEsz = kF8 ? 1 : 2;
-  static constexpr int kQBytes = 128 * kD * kEsz;        // one row block
-  static constexpr int kItemBytes = kTile * kD * kEsz;   // one K or V tile
-  static constexpr int kHalves = kF8 ? 1 : 2;            // 128-byte column blocks of a row
+  static constexpr bool kF8 = kType == 2, kF4 = kType == 4;
+  static constexpr int kThreads = kF8 || kF4 ? 512 : 384;
+  static constexpr int kQBytes = 128 * kD * (kF8 ? 1 : 2);   // one row block
+  static constexpr int kCodeBytes = kTile * kD / 2;          // 4 bits: the codes of a tile, its scales behind them
+  static constexpr int kItemBytes = kF4 ? kCodeBytes + kTile * 8 : kTile * kD * (kF8 ? 1 : 2);   // one K or V tile
+  static constexpr int kHalves = kF8 ? 1 : 2;            // 128-byte column blocks of a row of Q (bf16: of K and V)
   static constexpr int kKSlots = kF8 ? 4 : 3;            // K(t) in slot t % kKSlots of its ring, V(t) in t % kVSlots
-  static constexpr int kVSlots = kF8 ? 4 : 2;
-  static constexpr int kV16Bytes = kF8 ? kTile * kD * 2 : 0;
+  static constexpr int kVSlots = kF8 ? 4 : kF4 ? 0 : 2;  // (4 bits: both in one ring, K(t) before V(t))
+  static constexpr int kWideBytes = kF8 || kF4 ? kTile * kD * 2 : 0;   // a tile in f16
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = 2 * kQBytes;
-  static constexpr int kOffV = kOffK + kKSlots * kItemBytes;
-  static constexpr int kOffV16 = kOffV + kVSlots * kItemBytes;
-  static constexpr int kOffBars = kOffV16 + 2 * kV16Bytes;
+  static constexpr int kOffK16 = 2 * kQBytes;
+  static constexpr int kOffK = kOffK16 + (kF4 ? 2 * kWideBytes : 0);
+  static constexpr int kOffV = kOffK + (kF4 ? 0 : kKSlots * kItemBytes);
+  static constexpr int kOffV16 = kOffV + (kF4 ? kKSlots : kVSlots) * kItemBytes;
+  static constexpr int kOffBars = kOffV16 + 2 * kWideBytes;
   static constexpr int kOffMisc = kOffBars + 352;
   static constexpr int kOffStats = kOffMisc + 384;       // float2 [128 rows]: m, l of stream 1
   static constexpr int kOffShares = kOffStats + 1024;
-  static constexpr int kSmem = kOffShares + 128 + 1024;
+  static constexpr int kOffRow = kOffShares + 128;       // 4 bits: float [2 jobs][256 rows], what undoes a row's power of two
+  static constexpr int kSmem = kOffRow + (kF4 ? 2048 : 0) + 1024;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static constexpr int kConsumers = kF8 ? 16 : 12;       // warps that read a job's description
+  static_assert(kOffV16 % 1024 == 0 && kOffK % 1024 == 0, "swizzle atoms");
+  static constexpr int kConsumers = kF8 || kF4 ? 16 : 12;   // warps that read a job's description
+};
+// Tensor maps of the scales of 4-bit pages; no bytes for other types.
+template <int kType>
+struct ScaleMaps {};
+template <>
+struct ScaleMaps<4> {
+  CUtensorMap k, v;
 };
 
 enum {
   B_Q = 0, B_QDONE, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VLAND, B_END, B_DRAIN,
   B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_CLC, B_STAT,
-  B_OREAD, B_KFULL,
+  B_OREAD, B_Q16, B_KFULL,
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
 static_assert(kNumBars * 8 <= 352, "barrier area");
+// 4 bits: K tiles in f16, written and free (the places of the V ring's barriers, which has no ring of its own)
+constexpr int B_K16F0 = B_VFULL, B_K16E0 = B_VEMPTY;
 
 enum : uint32_t { W_T_SOFTMAX = 201, W_T_MMA, W_T_LOAD, W_T_CONVERT, W_T_DRAIN };   // whose wait ran out
 
@@ -88,11 +103,13 @@ static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
 
 // kPages: 0 packed K and V, jobs never split; 1 pages; 2 pages in equal shares (kernels of their
 // own, since the loops' code has to stay near in the instruction caches).
-template <bool kF8, int kPages, bool kPoll>
-__global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
+template <int kType, int kPages, bool kPoll>
+__global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
-  using C = Cfg<kF8>;
+                     const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const __grid_constant__ ScaleMaps<kType> tm_s) {
+  using C = Cfg<kType>;
+  constexpr bool kF8 = C::kF8, kF4 = C::kF4;
+  constexpr bool kF16 = kF8 || kF4;   // P and V are multiplied in f16
   constexpr bool kPaged = kPages > 0;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -106,8 +123,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
   const int tokens = 128 / a.group;   // of one row block
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const int n = i == B_STAT || i == B_OREAD || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 ||
-                            (kF8 && i >= B_VEMPTY)   // a V tile of codes is freed by its four converter warps
+      const int n = i == B_STAT || i == B_OREAD || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 || i == B_Q16 ||
+                            (kF8 && i >= B_VEMPTY) ||   // a tile of codes is freed by its four converter warps
+                            (kF4 && ((i >= B_KEMPTY && i < B_KEMPTY + 4) || i == B_K16F0 || i == B_K16F0 + 1))
                         ? 4
                     : i == B_READ0 || i == B_READ1 ? C::kConsumers
                                                    : 1;
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 
   if (warp < 8) {
     // ================================================= softmax + epilogue ===
-    if constexpr (kF8) regs_inc<192>();
+    if constexpr (kF16) regs_inc<192>();
     else regs_inc<208>();
     const int i = warp >> 2;
     const int row = 32 * (warp & 3) + lane;
@@ -150,7 +168,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 dv = a.descale_v ? *a.descale_v : 1.f;
     const float sc = dq * dk * a.scale_log2;
     const bool raw_ok = sc > 0.f;      // then the scale commutes with the maximum and goes into the exponent's FMA
-    const float esc = raw_ok ? sc : 1.f;
+    const float unit = raw_ok ? sc : 1.f;
     int su = 0, ends = 0, ones = 0, mask0 = 0;   // this stream's tiles, jobs with tiles, jobs of one row block, all tiles
 #pragma unroll 1
     for (int job = 0;; ++job) {
@@ -166,8 +184,14 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
     float m_run = -INFINITY, l = 0.f, lc = 0.f;
     bool bad = false;
+    float esc = unit, row_sc = sc;     // (4 bits: of this row of the job, with what undoes its power of two)
+    if constexpr (kF4) {
+      if (tiles > 0) bad = !wait_for<kPoll>(bar(B_Q16), ends & 1, limit);
+      row_sc = sc * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
+      if (raw_ok) esc = row_sc = fmaxf(row_sc, 1.17549435e-38f);   // (0 times a masked score's infinity would be a NaN)
+    }
 #pragma unroll 1
-    for (int u = 0; u < cnt; ++u) {
+    for (int u = 0; u < (kF4 && bad ? 0 : cnt); ++u) {
       const int t = one ? 2 * u + i : u;
       if (!wait_for<kPoll>(bar(B_S0 + i), (su + u) & 1, limit)) {
         bad = true;
@@ -187,7 +211,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[c][k] *= sc;
+          for (int k = 0; k < 32; ++k) x[c][k] *= row_sc;
       }
       const int kmax = lim - (tile0 + t) * kTile;          // last visible key of the tile
       if (__any_sync(0xffffffffu, kmax < kTile - 1)) {
@@ -207,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
       }
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
-      const bool need = new_reference<kF8>(mx, m_run);
+      const bool need = new_reference<kF16>(mx, m_run);
       // O_i's last product is done: P_i may be written again, O_i rescaled
       if (u > 0 && !wait_for<kPoll>(bar(B_O0 + i), (su + u - 1) & 1, limit)) {
         bad = true;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           }
         }
       }
-      const float nm = minus_reference<kF8>(m_run);
+      const float nm = minus_reference<kF16>(m_run);
       const uint64_t esc2 = pair_f32(esc, esc), nm2 = pair_f32(nm, nm);
       uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -247,7 +271,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           e0 = ex2_approx(e0);
           e1 = ex2_approx(e1);
           sum[k & 3] = add_f32x2(sum[k & 3], pair_f32(e0, e1));
-          p[k] = kF8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
+          p[k] = kF16 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
         }
         tmem_st_32x32b_x16(tp + 16 * c, p);
       }
@@ -285,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       if (!bad) {
         const bool some = l > 0.f || l != l;   // a NaN score stays a NaN result
         const float inv = some ? dv / l : 0.f;
-        const float lse = some ? lse_of<kF8>(m_run, l) : -INFINITY;
+        const float lse = some ? lse_of<kF16>(m_run, l) : -INFINITY;
         const int64_t orow = static_cast<int64_t>(q0 + tok) * a.h_q + g * a.group + (row - rt * a.group);
         const int64_t prow = static_cast<int64_t>(slot0) * kTileRows + (one ? 0 : 128 * i) + row;
         const bool part = kPaged && slot0 >= 0;
@@ -380,7 +404,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
     }
     }
   } else {
-    if constexpr (kF8) regs_dec<64>();
+    if constexpr (kF16) regs_dec<64>();
     else regs_dec<88>();
     if (warp == 8 || warp == 10) {
       // ====================================================== MMA issuers ===
@@ -392,17 +416,17 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
       // 128-byte-swizzled operands with 1024-byte atoms: one high word for all but V's leading stride (its low word)
       const uint32_t hi = static_cast<uint32_t>(sdesc_sw128(sbase, 16, 1024) >> 32);
       const bool is_qk = warp == 8;
-      constexpr uint32_t kIdescQK = idesc_make(128, 128, kF8 ? 0 : 1, false, false);
-      constexpr uint32_t kIdescPV = idesc_make(128, 128, kF8 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
+      constexpr uint32_t kIdescQK = idesc_make(128, 128, kF16 ? 0 : 1, false, false);
+      constexpr uint32_t kIdescPV = idesc_make(128, 128, kF16 ? 0 : 1, false, true);   // f16 or bf16; V is MN-major
       const uint32_t q_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffQ, 16, 1024));
-      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffK, 16, 1024));
+      const uint32_t k_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF4 ? C::kOffK16 : C::kOffK), 16, 1024));
       // K and V tiles: the 64-dim column blocks one after the other (8-row atoms 1024 bytes apart), or with kv_wide
       // beside one another (atoms 2048 bytes apart, the second block 1024 bytes on)
-      const bool wide = kPaged && !kF8 && a.kv_wide != 0;
+      const bool wide = kPaged && !kF16 && a.kv_wide != 0;
       const uint32_t block = wide ? 1024 : kTile * 128;
       const uint32_t kv_hi = wide ? static_cast<uint32_t>(sdesc_sw128(sbase, 16, 2048) >> 32) : hi;
       const uint32_t v_step = (wide ? 4096 : 2048) >> 4;   // 16 keys
-      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF8 ? C::kOffV16 : C::kOffV), block, 1024));
+      const uint32_t v_lo = static_cast<uint32_t>(sdesc_sw128(sbase + (kF16 ? C::kOffV16 : C::kOffV), block, 1024));
       bool ok = true;
       int tile_base = 0;     // tiles of earlier jobs
       int n = 0;             // this warp's products so far
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           const uint32_t d = tmem + kTmemS;
           const int first = n;   // (a job's first products have none of its own to follow)
           // (the last job's products are all done, so the turns below start afresh; its rows may still be on their way out)
-          ok = wait_for<kPoll>(bar(B_Q), with_tiles & 1, limit) &&
+          ok = wait_for<kPoll>(bar(kF4 ? B_Q16 : B_Q), with_tiles & 1, limit) &&
                (with_tiles == 0 || wait_for<kPoll>(bar(B_END), (with_tiles - 1) & 1, limit));
 #pragma unroll 1
           for (int u = 0; ok && u < steps; ++u) {
@@ -431,7 +455,8 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             for (int i = 0; i < 2; ++i) {
               if (!ok || u >= (i ? cnt1 : cnt0)) continue;
               const int t = tile_base + tile_at(i, u);
-              ok = wait_for<kPoll>(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, limit) &&
+              ok = (kF4 ? wait_for<kPoll>(bar(B_K16F0 + (t & 1)), (t >> 1) & 1, limit)
+                        : wait_for<kPoll>(bar(B_KFULL + t % C::kKSlots), (t / C::kKSlots) & 1, limit)) &&
                    (n < first + 3 || wait_for<kPoll>(bar(B_TURN_QK), (n - 3) & 1, limit)) &&
                    (n == 0 || wait_for<kPoll>(bar(B_SFREE), (n - 1) & 1, limit));
               if (!ok) break;
@@ -439,7 +464,8 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               tc_fence_after();
               if (elect_one()) {
                 const uint32_t qa = q_lo + (one ? 0 : i) * (C::kQBytes >> 4);
-                const uint32_t kb = k_lo + static_cast<uint32_t>(t % C::kKSlots) * (C::kItemBytes >> 4);
+                const uint32_t kb = k_lo + (kF4 ? static_cast<uint32_t>(t & 1) * (C::kWideBytes >> 4)
+                                                : static_cast<uint32_t>(t % C::kKSlots) * (C::kItemBytes >> 4));
                 if constexpr (kF8) {
                   mma_f8_wc<0>(d, qa, kb, hi, kIdescQK);
                   mma_f8_wc<1>(d, qa + 2, kb + 2, hi, kIdescQK);
@@ -455,7 +481,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 }
                 mbar_arrive(bar(B_TURN_PV));
                 mma_commit(bar(B_S0 + i));
-                if (one || i == 1) mma_commit(bar(B_KEMPTY + t % C::kKSlots));
+                if (one || i == 1) mma_commit(bar(kF4 ? B_K16E0 + (t & 1) : B_KEMPTY + t % C::kKSlots));
               }
               __syncwarp();
             }
@@ -470,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             for (int i = 0; i < 2; ++i) {
               if (!ok || u >= (i ? cnt1 : cnt0)) continue;
               const int t = tile_base + tile_at(i, u);
-              if constexpr (kF8) ok = wait_for<kPoll>(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
+              if constexpr (kF16) ok = wait_for<kPoll>(bar(B_V16F0 + (t & 1)), (t >> 1) & 1, limit);
               else
                 ok = wait_for<kPoll>(bar(B_VFULL + t % C::kVSlots), (t / C::kVSlots) & 1, limit);
               // (the job's last two products have no later QK to follow; the turn is an order, P is the dependency)
@@ -482,8 +508,9 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
               else ++seen0;
               tc_fence_after();
               if (elect_one()) {
-                const uint32_t vb = v_lo + (kF8 ? static_cast<uint32_t>(t & 1) * (C::kV16Bytes >> 4)
-                                                : static_cast<uint32_t>(t % C::kVSlots) * (C::kItemBytes >> 4));
+                uint32_t vb = v_lo;
+                if constexpr (kF16) vb += static_cast<uint32_t>(t & 1) * (C::kWideBytes >> 4);
+                else vb += static_cast<uint32_t>(t % C::kVSlots) * (C::kItemBytes >> 4);
                 const uint32_t pa = tmem + kTmemP + 64 * i, d = tmem + kTmemO + 128 * i;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)   // 16 keys an MMA: 8 columns of P, two 8-row atoms of V
@@ -491,7 +518,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                 mbar_arrive(bar(B_TURN_QK));
                 mma_commit(bar(B_O0 + i));
                 if (one || i == 1) {
-                  if constexpr (kF8) mma_commit(bar(B_V16E0 + (t & 1)));
+                  if constexpr (kF16) mma_commit(bar(B_V16E0 + (t & 1)));
                   else mma_commit(bar(B_VEMPTY + t % C::kVSlots));
                 }
               }
@@ -546,6 +573,10 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
           tma_prefetch_desc(&tm_q);
           tma_prefetch_desc(&tm_k);
           tma_prefetch_desc(&tm_v);
+          if constexpr (kF4) {
+            tma_prefetch_desc(&tm_s.k);
+            tma_prefetch_desc(&tm_s.v);
+          }
         }
         if constexpr (shared) {
           AttnShares<2, kTileHead> shares;
@@ -622,6 +653,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
                   tiles = w[J_TILES], tail = w[J_TAIL];
         const bool one = w[J_ONE] != 0;
         job_read(job);
+        if (kF4 && !is_k) continue;                        // (warp 9 loads both)
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
           const int key = (tile0 + t) * kTile + lane * page_rows;
@@ -640,33 +672,43 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         };
         int page = 0, row = 0;
         bool have = tiles > 0 && lookup(0, page, row);
+        constexpr int kParts = kF4 ? 2 : 1;                // of a tile that this warp loads: K, then V
         const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL, empty = is_k ? B_KEMPTY : B_VEMPTY;
         const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
+        int page_n = 0, row_n = 0;
+        bool have_n = false;
 #pragma unroll 1
-        for (int t = 0; t < tiles; ++t) {
-          int page_n = 0, row_n = 0;
-          bool have_n = false;
-          if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
+        for (int it = 0; it < kParts * tiles; ++it) {
+          const int t = it / kParts;
+          const bool is_v = kF4 && (it & 1);
+          if (!is_v) {
+            page_n = row_n = 0;
+            have_n = t + 1 < tiles && lookup(t + 1, page_n, row_n);
+          }
           const int sl = done % slots;
           if (done >= slots && !wait_for<kPoll>(bar(empty + sl), ((done / slots) - 1) & 1, limit)) {
             ok = false;
             break;
           }
-          if (kPaged && is_k) {
+          if (kPaged && is_k && !is_v) {
             // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
             const unsigned got = __ballot_sync(0xffffffffu, have);
             unsigned groups = 0;
             for (int i = 0; i < 8; ++i)
               if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
-            if (lane == 0) misc[M_MASK + (done & (kMaskRing - 1))] = static_cast<int>(groups);
+            if (lane == 0) misc[M_MASK + ((done / kParts) & (kMaskRing - 1))] = static_cast<int>(groups);
           }
           // (V's rows past the sequence's end are cleared before its tile counts as there)
-          const uint32_t there = bar(!kF8 && !is_k && t == tail ? static_cast<int>(B_VLAND) : full + sl);
+          const uint32_t there = bar(!kF16 && !is_k && t == tail ? static_cast<int>(B_VLAND) : full + sl);
           if (lane == 0) mbar_arrive_expect_tx(there, C::kItemBytes);
           __syncwarp();
           if (lane < boxes) {
             const uint32_t dst = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
-            if (kPaged && !kF8 && a.kv_wide != 0) {
+            if constexpr (kF4) {
+              const CUtensorMap *codes = is_v ? &tm_v : &tm_k, *scales = is_v ? &tm_s.v : &tm_s.k;
+              tma_load_4d(dst + lane * page_rows * 64, codes, 0, row, page, g, there);
+              tma_load_4d(dst + C::kCodeBytes + lane * page_rows * 8, scales, 2 * row, 0, page, g, there);
+            } else if (kPaged && !kF8 && a.kv_wide != 0) {
               const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
               tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
                           there);
@@ -676,10 +718,12 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
             }
           }
           ++done;   // at once: a wait below may run out, and what was started is drained by this count
-          page = page_n;
-          row = row_n;
-          have = have_n;
-          if (is_k && t == 0) {
+          if (!kF4 || is_v) {
+            page = page_n;
+            row = row_n;
+            have = have_n;
+          }
+          if (is_k && it == 0) {
             // Q once the products of the job before have read its place
             ok = with_tiles == 0 || wait_for<kPoll>(bar(B_QDONE), (with_tiles - 1) & 1, limit);
             if (!ok) break;
@@ -696,7 +740,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         }
         if (!ok) break;
         // the ragged end lies in the last tile: clear V's rows past it
-        if (!kF8 && !is_k && tail >= 0) {
+        if (!kF16 && !is_k && tail >= 0) {
           const int sl = (done - 1) % C::kVSlots;
           ok = wait_for<kPoll>(bar(B_VLAND), landed & 1, limit);
           if (!ok && !wait_drain(bar(B_VLAND), landed & 1, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
@@ -746,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
              (t < 2 || wait_for<kPoll>(bar(B_V16E0 + (t & 1)), ((t >> 1) - 1) & 1, limit));
         if (!ok) break;
         const uint8_t* src = smem + C::kOffV + sl * C::kItemBytes + key * 128;
-        uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kV16Bytes + key * 128;
+        uint8_t* dst = smem + C::kOffV16 + (t & 1) * C::kWideBytes + key * 128;
         const bool in = (tile0 + tl) * kTile + key < kv;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {               // 64 dims
@@ -775,6 +819,95 @@ __global__ void __launch_bounds__(Cfg<kF8>::kThreads, 1)
         if (lane == 0) {
           mbar_arrive(bar(B_V16F0 + (t & 1)));
           mbar_arrive(bar(B_VEMPTY + sl));
+        }
+      }
+      tile_base += tiles;
+      }
+      if (!ok) give_up(a, W_T_CONVERT);
+    } else if (kF4 && warp >= 12) {
+      // ================================ Q bf16 -> f16; K and V codes x scales -> f16 ===
+      // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own
+      // (largest element in [2^14, 2^15)): exact down to 2^-28 of that element, smaller ones are off by 2^-39 of it at most. A
+      // code times its scale is exact in f16. Rows of V past the end become 0 (K's scores there are masked).
+      const int key = threadIdx.x - 32 * 12;
+      const int r8 = key & 7, r4 = (key >> 1) & 3;
+      int tile_base = 0, with_tiles = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int job = 0; ok; ++job) {
+      volatile int* jw;
+      ok = job_at(job, jw);
+      if (!ok || jw[J_B] < 0) break;
+      const int kv = jw[J_KV], tile0 = jw[J_TILE0], tiles = jw[J_TILES];
+      const int blocks = jw[J_ONE] != 0 ? 1 : 2;
+      job_read(job);
+      if (tiles == 0) continue;
+      ok = wait_for<kPoll>(bar(B_Q), with_tiles & 1, limit);
+      if (!ok) break;
+#pragma unroll 1
+      for (int i = 0; i < blocks; ++i) {
+        uint8_t* q = smem + C::kOffQ + i * C::kQBytes + key * 128;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint4 v = *reinterpret_cast<const uint4*>(q + (c >> 3) * 128 * 128 + (((c & 7) ^ r8) << 4));
+          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max(ws[k] & 0x7fffu, (ws[k] >> 16) & 0x7fffu));
+        }
+        const int e = static_cast<int>(top >> 7);          // the largest element's exponent
+        const float up = __int_as_float(min(268 - e, 254) << 23);
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * 128 * 128 + (((c & 7) ^ r8) << 4));
+          const uint4 v = *at;
+          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
+          uint32_t h[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(__uint_as_float(ws[k] << 16) * up, __uint_as_float(ws[k] & 0xffff0000u) * up);
+          *at = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+        reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (with_tiles & 1) + 128 * i + key] =
+            e > 14 ? __int_as_float((e - 14) << 23) : __int_as_float(1 << 22);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_Q16));
+      ++with_tiles;
+#pragma unroll 1
+      for (int it = 0; it < 2 * tiles; ++it) {
+        const int t = tile_base + (it >> 1), item = 2 * tile_base + it;
+        const bool is_v = it & 1;
+        const int sl = item % C::kKSlots;
+        ok = wait_for<kPoll>(bar(B_KFULL + sl), (item / C::kKSlots) & 1, limit) &&
+             (t < 2 || wait_for<kPoll>(bar((is_v ? B_V16E0 : B_K16E0) + (t & 1)), ((t >> 1) - 1) & 1, limit));
+        if (!ok) break;
+        const uint8_t* src = smem + C::kOffK + sl * C::kItemBytes;
+        uint8_t* dst = smem + (is_v ? C::kOffV16 : C::kOffK16) + (t & 1) * C::kWideBytes + key * 128;
+        uint2 sc = *reinterpret_cast<const uint2*>(src + C::kCodeBytes + key * 8);
+        if (is_v && (tile0 + (it >> 1)) * kTile + key >= kv) sc = make_uint2(0, 0);
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + key * 64 + ((c ^ r4) << 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {                        // 32 dims, two scales
+          const uint32_t two = f16x2_of_e4m3((c < 2 ? sc.x : sc.y) >> (16 * (c & 1)));
+          const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {                      // 8 dims: one piece of 16 bytes
+            const uint32_t by = __byte_perm(two, 0, k < 2 ? 0x1010 : 0x3232);
+            uint32_t h[4];
+            f16_of_e2m1x8(ws[k], h);
+            const int piece = 4 * c + k;
+            *reinterpret_cast<uint4*>(dst + (piece >> 3) * kTile * 128 + (((piece & 7) ^ r8) << 4)) =
+                make_uint4(mul_f16x2(h[0], by), mul_f16x2(h[1], by), mul_f16x2(h[2], by), mul_f16x2(h[3], by));
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar((is_v ? B_V16F0 : B_K16F0) + (t & 1)));
+          mbar_arrive(bar(B_KEMPTY + sl));
         }
       }
       tile_base += tiles;
@@ -902,37 +1035,58 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
 }  // namespace
 
 namespace {
-using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
-// [e4m3][pages][polling waits]; bf16 takes no equal shares
-constexpr TileKernel kTileKernels[2][3][2] = {
-    {{attn_tile_kernel<false, 0, false>, attn_tile_kernel<false, 0, true>},
-     {attn_tile_kernel<false, 1, false>, attn_tile_kernel<false, 1, true>},
-     {nullptr, nullptr}},
-    {{attn_tile_kernel<true, 0, false>, attn_tile_kernel<true, 0, true>},
-     {attn_tile_kernel<true, 1, false>, attn_tile_kernel<true, 1, true>},
-     {attn_tile_kernel<true, 2, false>, attn_tile_kernel<true, 2, true>}}};
+template <int kType>
+using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs, ScaleMaps<kType>);
+// [pages][polling waits]; bf16 takes no equal shares, and 4 bits are a form of pages
+template <int kType>
+constexpr TileKernel<kType> kTileKernels[3][2] = {{attn_tile_kernel<kType, 0, false>, attn_tile_kernel<kType, 0, true>},
+                                                  {attn_tile_kernel<kType, 1, false>, attn_tile_kernel<kType, 1, true>},
+                                                  {attn_tile_kernel<kType, 2, false>, attn_tile_kernel<kType, 2, true>}};
+template <>
+constexpr TileKernel<1> kTileKernels<1>[3][2] = {{attn_tile_kernel<1, 0, false>, attn_tile_kernel<1, 0, true>},
+                                                 {attn_tile_kernel<1, 1, false>, attn_tile_kernel<1, 1, true>},
+                                                 {nullptr, nullptr}};
+template <>
+constexpr TileKernel<4> kTileKernels<4>[3][2] = {{nullptr, nullptr},
+                                                 {attn_tile_kernel<4, 1, false>, attn_tile_kernel<4, 1, true>},
+                                                 {attn_tile_kernel<4, 2, false>, attn_tile_kernel<4, 2, true>}};
+
+template <int kType>
+cudaError_t prepare() {
+  for (int k = 0; k < 6; ++k) {
+    if (kTileKernels<kType>[k >> 1][k & 1] == nullptr) continue;
+    const cudaError_t e = cudaFuncSetAttribute(kTileKernels<kType>[k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Cfg<kType>::kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+template <int kType>
+cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
+                   const ScaleMaps<kType>& tm_s, int64_t grid, cudaStream_t stream) {
+  const int pages = a.table == nullptr ? 0 : a.adaptive == kShares ? 2 : 1;
+  const TileKernel<kType> kernel = kTileKernels<kType>[pages][a.wait_limit_ns < kSuspendNs];
+  if (kernel == nullptr || grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
+  return launch_pdl(kernel, static_cast<unsigned>(grid), Cfg<kType>::kThreads, Cfg<kType>::kSmem, stream, tm_q, tm_k, tm_v, a, tm_s);
+}
 }  // namespace
 
 cudaError_t prepare_attn_tile() {
-  for (int f8 = 0; f8 < 2; ++f8)
-    for (int k = 0; k < 6; ++k) {
-      if (kTileKernels[f8][k >> 1][k & 1] == nullptr) continue;
-      const cudaError_t e = cudaFuncSetAttribute(kTileKernels[f8][k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem);
-      if (e != cudaSuccess) return e;
-    }
-  return cudaSuccess;
+  cudaError_t e = prepare<1>();
+  if (e == cudaSuccess) e = prepare<2>();
+  if (e == cudaSuccess) e = prepare<4>();
+  return e;
 }
 
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream) {
-  if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
-  const bool f8 = dtype == 2;
-  const int pages = a.table == nullptr ? 0 : a.adaptive == kShares ? 2 : 1;
-  if (kTileKernels[f8][pages][0] == nullptr) return cudaErrorInvalidValue;
-  return launch_pdl(kTileKernels[f8][pages][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid),
-                    f8 ? Cfg<true>::kThreads : Cfg<false>::kThreads, f8 ? Cfg<true>::kSmem : Cfg<false>::kSmem, stream, tm_q,
-                    tm_k, tm_v, a);
+  if (dtype == 2) return launch<2>(tm_q, tm_k, tm_v, a, {}, grid, stream);
+  return launch<1>(tm_q, tm_k, tm_v, a, {}, grid, stream);
+}
+
+cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks,
+                              const CUtensorMap& tm_vs, const AttnArgs& a, int64_t grid, cudaStream_t stream) {
+  return launch<4>(tm_q, tm_k, tm_v, a, {tm_ks, tm_vs}, grid, stream);
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream) {

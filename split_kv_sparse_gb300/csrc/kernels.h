@@ -193,6 +193,9 @@ constexpr int kTileSplitWaves = 3;
 // kv_wide as 5-D {64, 8 rows, column blocks, row groups, pages}, box {64, 8, 2, min(page, 128) / 8, 1}.
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
+// 4-bit pages: boxes of min(page, 128) rows, codes and scales as in launch_attn_row4.
+cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks,
+                              const CUtensorMap& tm_vs, const AttnArgs& a, int64_t grid, cudaStream_t stream);
 // Box of tm_k / tm_v: {128 bytes, attn_row_box(dtype, page size) rows, 1, 1}.
 cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
                             int64_t grid, cudaStream_t stream);

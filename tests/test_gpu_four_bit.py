@@ -49,7 +49,7 @@ def test_chunk(page, sq, kv):
     go(sq, kv, 8, 2, page, seed=page + len(sq))
 
 
-@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (24, 2), (9, 1), (7, 1)])
+@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (24, 2), (9, 1), (7, 1), (64, 1), (128, 1), (100, 1)])
 def test_group_sizes(h_q, h_kv):
     go([1, 1, 1], [100, 257, 33], h_q, h_kv, 32, seed=h_q)
     go([3, 17, 70], [100, 257, 70], h_q, h_kv, 32, seed=h_q + 1)
@@ -176,7 +176,7 @@ def test_strided_queries_on_a_stream_of_their_own():
     check(out.cpu(), lse.cpu(), None, ref, P_TYPE)
 
 
-@pytest.mark.parametrize("sq,kv", [([1] * 40, 3000)])
+@pytest.mark.parametrize("sq,kv", [([1] * 40, 3000), ([200] * 6, 900), ([64] * 200, 300)])
 def test_waits_that_run_out(sq, kv):
     """Limits below a load's latency: the call ends, the status says so, and the next call is right."""
     kv = [kv] * len(sq)
