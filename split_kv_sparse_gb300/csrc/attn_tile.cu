@@ -79,6 +79,11 @@ enum {
   B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
 };
 static_assert(kNumBars * 8 <= 352, "barrier area");
+// 4 bits: the place of a tile in the order in which a job's K and V tiles are loaded and widened, K a tile ahead (K_0, K_1, V_0,
+// K_2, V_1, .., V_n-2, V_n-1): V_t has to wait for the product of V_t-2, and the scores of later tiles not for that.
+__device__ __forceinline__ int item_of(int t, int tiles, bool is_v) {
+  return is_v ? (t == tiles - 1 ? 2 * tiles - 1 : 2 * t + 2) : (t == 0 ? 0 : 2 * t - 1);
+}
 // 4 bits: K tiles in f16, written and free (the places of the V ring's barriers, which has no ring of its own)
 constexpr int B_K16F0 = B_VFULL, B_K16E0 = B_VEMPTY;
 
@@ -98,8 +103,8 @@ enum {
   J_TAIL,             // the local tile that holds the sequence's ragged end, or -1
   kJobWords
 };
-enum { M_TMEM = 0, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16 };
-static_assert((M_MASK + kMaskRing) * 4 <= 384, "misc area");
+enum { M_TMEM = 0, M_CLC = 4, M_JOBS = 8, M_MASK = M_JOBS + 2 * kJobWords, kMaskRing = 16, M_LAST = M_MASK + kMaskRing };
+static_assert((M_LAST + 6) * 4 <= 384, "misc area");
 
 // kPages: 0 packed K and V, jobs never split; 1 pages; 2 pages in equal shares (kernels of their
 // own, since the loops' code has to stay near in the instruction caches).
@@ -549,6 +554,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       bool ok = true;
       int done = 0;                                        // tiles whose loads were started
       int with_tiles = 0, landed = 0;                      // jobs that had any; V tiles that went by B_VLAND
+      int tile_base = 0, older[3] = {-1, -1, -1};          // 4 bits: tiles of earlier jobs, this warp's last items
       AttnJobs jobs;
       // (in shared memory between the jobs: the loads' loop needs the registers)
       auto shares_at = reinterpret_cast<AttnShares<2, kTileHead>*>(smem + C::kOffShares);
@@ -653,7 +659,6 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
                   tiles = w[J_TILES], tail = w[J_TAIL];
         const bool one = w[J_ONE] != 0;
         job_read(job);
-        if (kF4 && !is_k) continue;                        // (warp 9 loads both)
         // this lane's page of tile t: (page, row), page = num_pages (zeros) where there is none
         auto lookup = [&](int t, int& page, int& row) {
           const int key = (tile0 + t) * kTile + lane * page_rows;
@@ -672,42 +677,37 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         };
         int page = 0, row = 0;
         bool have = tiles > 0 && lookup(0, page, row);
-        constexpr int kParts = kF4 ? 2 : 1;                // of a tile that this warp loads: K, then V
-        const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL, empty = is_k ? B_KEMPTY : B_VEMPTY;
+        const int slots = is_k || kF4 ? C::kKSlots : C::kVSlots, full = is_k || kF4 ? B_KFULL : B_VFULL,
+                  empty = is_k || kF4 ? B_KEMPTY : B_VEMPTY;
         const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
-        int page_n = 0, row_n = 0;
-        bool have_n = false;
 #pragma unroll 1
-        for (int it = 0; it < kParts * tiles; ++it) {
-          const int t = it / kParts;
-          const bool is_v = kF4 && (it & 1);
-          if (!is_v) {
-            page_n = row_n = 0;
-            have_n = t + 1 < tiles && lookup(t + 1, page_n, row_n);
-          }
-          const int sl = done % slots;
-          if (done >= slots && !wait_for<kPoll>(bar(empty + sl), ((done / slots) - 1) & 1, limit)) {
+        for (int t = 0; t < tiles; ++t) {
+          int page_n = 0, row_n = 0;
+          bool have_n = false;
+          if (t + 1 < tiles) have_n = lookup(t + 1, page_n, row_n);
+          const int item = kF4 ? 2 * tile_base + item_of(t, tiles, !is_k) : done;
+          const int sl = item % slots;
+          if (item >= slots && !wait_for<kPoll>(bar(empty + sl), ((item / slots) - 1) & 1, limit)) {
             ok = false;
             break;
           }
-          if (kPaged && is_k && !is_v) {
+          if (kPaged && is_k) {
             // the tile's 16-key groups that have a page (those past the sequence's end are masked anyway)
             const unsigned got = __ballot_sync(0xffffffffu, have);
             unsigned groups = 0;
             for (int i = 0; i < 8; ++i)
               if ((got >> (i * 16 / page_rows)) & 1u) groups |= 1u << i;
-            if (lane == 0) misc[M_MASK + ((done / kParts) & (kMaskRing - 1))] = static_cast<int>(groups);
+            if (lane == 0) misc[M_MASK + (done & (kMaskRing - 1))] = static_cast<int>(groups);
           }
           // (V's rows past the sequence's end are cleared before its tile counts as there)
           const uint32_t there = bar(!kF16 && !is_k && t == tail ? static_cast<int>(B_VLAND) : full + sl);
           if (lane == 0) mbar_arrive_expect_tx(there, C::kItemBytes);
           __syncwarp();
           if (lane < boxes) {
-            const uint32_t dst = sbase + (is_k ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
+            const uint32_t dst = sbase + (is_k || kF4 ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
             if constexpr (kF4) {
-              const CUtensorMap *codes = is_v ? &tm_v : &tm_k, *scales = is_v ? &tm_s.v : &tm_s.k;
-              tma_load_4d(dst + lane * page_rows * 64, codes, 0, row, page, g, there);
-              tma_load_4d(dst + C::kCodeBytes + lane * page_rows * 8, scales, 2 * row, 0, page, g, there);
+              tma_load_4d(dst + lane * page_rows * 64, tm, 0, row, page, g, there);
+              tma_load_4d(dst + C::kCodeBytes + lane * page_rows * 8, is_k ? &tm_s.k : &tm_s.v, 2 * row, 0, page, g, there);
             } else if (kPaged && !kF8 && a.kv_wide != 0) {
               const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
               tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
@@ -718,12 +718,15 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
             }
           }
           ++done;   // at once: a wait below may run out, and what was started is drained by this count
-          if (!kF4 || is_v) {
-            page = page_n;
-            row = row_n;
-            have = have_n;
+          if constexpr (kF4) {
+            older[2] = older[1];
+            older[1] = older[0];
+            older[0] = item;
           }
-          if (is_k && it == 0) {
+          page = page_n;
+          row = row_n;
+          have = have_n;
+          if (is_k && t == 0) {
             // Q once the products of the job before have read its place
             ok = with_tiles == 0 || wait_for<kPoll>(bar(B_QDONE), (with_tiles - 1) & 1, limit);
             if (!ok) break;
@@ -739,6 +742,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           }
         }
         if (!ok) break;
+        tile_base += tiles;
         // the ragged end lies in the last tile: clear V's rows past it
         if (!kF16 && !is_k && tail >= 0) {
           const int sl = (done - 1) % C::kVSlots;
@@ -763,8 +767,12 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       // nothing that was started may still be writing shared memory when the CTA ends
       __syncwarp();
       if (lane == 0) {
-        const int slots = is_k ? C::kKSlots : C::kVSlots, full = is_k ? B_KFULL : B_VFULL;
+        const int slots = is_k ? C::kKSlots : kF4 ? 1 : C::kVSlots, full = is_k ? B_KFULL : B_VFULL;
         bool quiet = with_tiles == 0 || wait_drain(bar(B_Q), (with_tiles - 1) & 1, a.drain_limit_ns);
+        if constexpr (kF4) {           // (two warps' tiles in one ring: drained behind the last barrier)
+          done = 0;
+          for (int k = 0; k < 3; ++k) misc[M_LAST + (is_k ? 0 : 3) + k] = older[k];
+        }
         for (int k = max(0, done - slots); k < done; ++k)
           quiet = wait_drain(bar(full + k % slots), (k / slots) & 1, a.drain_limit_ns) && quiet;
         if (!quiet) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
@@ -876,19 +884,23 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       ++with_tiles;
 #pragma unroll 1
       for (int it = 0; it < 2 * tiles; ++it) {
-        const int t = tile_base + (it >> 1), item = 2 * tile_base + it;
-        const bool is_v = it & 1;
+        const bool is_v = it == 2 * tiles - 1 || (it > 0 && !(it & 1));
+        const int tl = is_v ? it == 2 * tiles - 1 ? tiles - 1 : (it >> 1) - 1 : (it + 1) >> 1;   // (inverse of item_of)
+        const int t = tile_base + tl, item = 2 * tile_base + it;
         const int sl = item % C::kKSlots;
-        ok = wait_for<kPoll>(bar(B_KFULL + sl), (item / C::kKSlots) & 1, limit) &&
-             (t < 2 || wait_for<kPoll>(bar((is_v ? B_V16E0 : B_K16E0) + (t & 1)), ((t >> 1) - 1) & 1, limit));
+        ok = wait_for<kPoll>(bar(B_KFULL + sl), (item / C::kKSlots) & 1, limit);
         if (!ok) break;
         const uint8_t* src = smem + C::kOffK + sl * C::kItemBytes;
         uint8_t* dst = smem + (is_v ? C::kOffV16 : C::kOffK16) + (t & 1) * C::kWideBytes + key * 128;
         uint2 sc = *reinterpret_cast<const uint2*>(src + C::kCodeBytes + key * 8);
-        if (is_v && (tile0 + (it >> 1)) * kTile + key >= kv) sc = make_uint2(0, 0);
+        if (is_v && (tile0 + tl) * kTile + key >= kv) sc = make_uint2(0, 0);
         uint4 w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + key * 64 + ((c ^ r4) << 4));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_KEMPTY + sl));
+        ok = t < 2 || wait_for<kPoll>(bar((is_v ? B_V16E0 : B_K16E0) + (t & 1)), ((t >> 1) - 1) & 1, limit);
+        if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {                        // 32 dims, two scales
           const uint32_t two = f16x2_of_e4m3((c < 2 ? sc.x : sc.y) >> (16 * (c & 1)));
@@ -905,10 +917,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar((is_v ? B_V16F0 : B_K16F0) + (t & 1)));
-          mbar_arrive(bar(B_KEMPTY + sl));
-        }
+        if (lane == 0) mbar_arrive(bar((is_v ? B_V16F0 : B_K16F0) + (t & 1)));
       }
       tile_base += tiles;
       }
@@ -918,6 +927,17 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (kF4 && warp == 9 && lane == 0) {
+    // each slot's last tile, of whichever warp loaded it (a warp's last three hold all of its own among the ring's last three)
+    bool quiet = true;
+    for (int sl = 0; sl < C::kKSlots; ++sl) {
+      int last = -1;
+      for (int k = 0; k < 6; ++k)
+        if (misc[M_LAST + k] >= 0 && misc[M_LAST + k] % C::kKSlots == sl) last = max(last, misc[M_LAST + k]);
+      if (last >= 0) quiet = wait_drain(bar(B_KFULL + sl), (last / C::kKSlots) & 1, a.drain_limit_ns) && quiet;
+    }
+    if (!quiet) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+  }
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
