@@ -839,7 +839,8 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       // code times its scale is exact in f16. Rows of V past the end become 0 (K's scores there are masked).
       const int key = threadIdx.x - 32 * 12;
       const int r8 = key & 7, r4 = (key >> 1) & 3;
-      int tile_base = 0, with_tiles = 0;
+      int tile_base = 0, with_tiles = 0, slot = 0;
+      uint32_t phase = 0;
       bool ok = true;
 #pragma unroll 1
       for (int job = 0; ok; ++job) {
@@ -882,42 +883,49 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_Q16));
       ++with_tiles;
-#pragma unroll 1
-      for (int it = 0; it < 2 * tiles; ++it) {
-        const bool is_v = it == 2 * tiles - 1 || (it > 0 && !(it & 1));
-        const int tl = is_v ? it == 2 * tiles - 1 ? tiles - 1 : (it >> 1) - 1 : (it + 1) >> 1;   // (inverse of item_of)
-        const int t = tile_base + tl, item = 2 * tile_base + it;
-        const int sl = item % C::kKSlots;
-        ok = wait_for<kPoll>(bar(B_KFULL + sl), (item / C::kKSlots) & 1, limit);
-        if (!ok) break;
-        const uint8_t* src = smem + C::kOffK + sl * C::kItemBytes;
-        uint8_t* dst = smem + (is_v ? C::kOffV16 : C::kOffK16) + (t & 1) * C::kWideBytes + key * 128;
-        uint2 sc = *reinterpret_cast<const uint2*>(src + C::kCodeBytes + key * 8);
-        if (is_v && (tile0 + tl) * kTile + key >= kv) sc = make_uint2(0, 0);
-        uint4 w[4];
+      // A tile's codes come to registers while the wait for a free place of its values runs: their slot is free at once.
+      uint32_t w[4][4], sc[2];
+      auto kind = [&](int it) { return it == 2 * tiles - 1 || (it > 0 && !(it & 1)); };                             // V?
+      auto tile_of = [&](int it) { return it == 2 * tiles - 1 ? tiles - 1 : it & 1 ? (it + 1) >> 1 : max((it >> 1) - 1, 0); };   // (inverse of item_of)
+      auto take = [&](int it) {
+        ok = wait_for<kPoll>(bar(B_KFULL + slot), phase, limit);
+        if (!ok) return;
+        const uint32_t src = sbase + C::kOffK + slot * C::kItemBytes;
+        lds64(src + C::kCodeBytes + key * 8, sc);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(src + key * 64 + ((c ^ r4) << 4));
+        for (int c = 0; c < 4; ++c) lds128((src + key * 64 + (r4 << 4)) ^ (c << 4), w[c]);
+        if (kind(it) && (tile0 + tile_of(it)) * kTile + key >= kv) sc[0] = sc[1] = 0;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_KEMPTY + sl));
+        if (lane == 0) mbar_arrive(bar(B_KEMPTY + slot));
+        slot = slot == C::kKSlots - 1 ? 0 : slot + 1;
+        phase ^= slot == 0 ? 1u : 0u;
+      };
+      take(0);
+#pragma unroll 1
+      for (int it = 0; ok && it < 2 * tiles; ++it) {
+        const bool is_v = kind(it);
+        const int t = tile_base + tile_of(it);
         ok = t < 2 || wait_for<kPoll>(bar((is_v ? B_V16E0 : B_K16E0) + (t & 1)), ((t >> 1) - 1) & 1, limit);
         if (!ok) break;
+        const uint32_t dst = sbase + (is_v ? C::kOffV16 : C::kOffK16) + (t & 1) * C::kWideBytes + key * 128 + (r8 << 4);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {                        // 32 dims, two scales
-          const uint32_t two = f16x2_of_e4m3((c < 2 ? sc.x : sc.y) >> (16 * (c & 1)));
-          const uint32_t ws[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          const uint32_t two = f16x2_of_e4m3(sc[c >> 1] >> (16 * (c & 1)));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {                      // 8 dims: one piece of 16 bytes
             const uint32_t by = __byte_perm(two, 0, k < 2 ? 0x1010 : 0x3232);
             uint32_t h[4];
-            f16_of_e2m1x8(ws[k], h);
+            f16_of_e2m1x8(w[c][k], h);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], by);
             const int piece = 4 * c + k;
-            *reinterpret_cast<uint4*>(dst + (piece >> 3) * kTile * 128 + (((piece & 7) ^ r8) << 4)) =
-                make_uint4(mul_f16x2(h[0], by), mul_f16x2(h[1], by), mul_f16x2(h[2], by), mul_f16x2(h[3], by));
+            sts128((dst ^ ((piece & 7) << 4)) + (piece >> 3) * kTile * 128, h);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar((is_v ? B_V16F0 : B_K16F0) + (t & 1)));
+        if (it + 1 < 2 * tiles) take(it + 1);
       }
       tile_base += tiles;
       }
