@@ -511,9 +511,8 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   a.drain_limit_ns = skv::drain_limit_ns();
   CUtensorMap tq, tk, tv, tks, tvs;
   const bool four = plan->dtype == SDPA_E2M1;
-  const int box = !rows16 ? std::min(pages->page_size, 128)
-                  : four  ? skv::attn_row4_box(pages->page_size)
-                          : skv::attn_row_box(plan->dtype, pages->page_size);
+  const int box = rows16 && !four ? skv::attn_row_box(plan->dtype, pages->page_size)
+                                  : std::min(pages->page_size, rows16 ? skv::kRow4Box : 128);
   if (!rows16 && plan->dtype == SDPA_BF16) {
     // (with one head its stride says nothing)
     if (pages->h_kv == 1 || pages->head_stride == kDim) a.kv_wide = 1;

@@ -5,8 +5,9 @@
 // or dims as M and 8 query rows as N: K and V are widened once, straight into the registers of the A operand, and a
 // group of 4 or 8 heads wastes half as many products as with 16 rows as M.
 //
-// Everything else is that kernel's: four warps a CTA, two CTAs an SM, each warp with key blocks (64 keys), a TMA ring, a
-// running maximum and a sum of its own, merged at a job's end; equal shares of the batch's key tiles (AttnShares).
+// Two CTAs an SM, each with four warps that compute and four that load: every computing warp walks key blocks (64 keys, every
+// fourth of a job's) of its own with a running maximum and a sum of its own, merged at a job's end; a loading warp fills
+// its ring by TMA, page by page, ahead into the next job. Equal shares of the batch's key tiles (AttnShares).
 //
 // Widening: a byte of two e2m1 codes is one conversion to an f16 pair, times its e4m3 scale in f16: exact (6
 // significant bits, 2^-10 to 2688). The order of the contracted dims of S is free as long as Q has the same, so a lane takes
@@ -23,64 +24,71 @@ namespace {
 
 constexpr int kD = kAttnDim;
 constexpr int kTile = kAttnKeyTile;
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                               // that compute; as many load
+constexpr int kThreads = 64 * kWarps;
 constexpr int kStages = 3;
 constexpr int kBlock = 64;                              // keys of a block
+constexpr int kTiles = kBlock / 16;
 constexpr int kCodes = kBlock * kD / 2;                 // bytes of its K or V codes
 constexpr int kScales = kBlock * 8;
 constexpr int kOffV = kCodes, kOffKs = 2 * kCodes, kOffVs = kOffKs + kScales;
 constexpr int kStageBytes = 2 * (kCodes + kScales);
 constexpr int kWarpBytes = kStages * kStageBytes;
-constexpr int kOffBars = kWarps * kWarpBytes;
-constexpr int kOffStats = kOffBars + kWarps * kStages * 8;   // float2 [kWarps][16]: m, l
+constexpr int kOffFull = kWarps * kWarpBytes;           // barriers [kWarps][kStages]: a block is there; its place is free
+constexpr int kOffEmpty = kOffFull + kWarps * kStages * 8;
+constexpr int kOffHave = kOffEmpty + kWarps * kStages * 8;   // int [kWarps][kStages]: a bit for each box that has a page
+constexpr int kOffStats = kOffHave + kWarps * kStages * 8;   // float2 [kWarps][16]: m, l
 constexpr int kOffAbort = kOffStats + kWarps * 16 * 8;
 constexpr int kOffStage = kOffAbort + 16;               // int [kWarps]: the stage that holds a warp's result
 constexpr int kSmem = kOffStage + 16 + 1024;
-static_assert(16 * kD * 4 <= kStageBytes && kStageBytes % 512 == 0, "a warp's result goes through one stage; 64-byte swizzle");
+static_assert(16 * kD * 4 <= kStageBytes, "a warp's result goes through one stage");
 static_assert(kRowCtasPerSm * (kSmem + 1024) <= 233472, "two CTAs an SM");
+// Registers of a thread that loads, and that computes: 256 of two threads of a launch (jobs of 8 rows, 4 x 100,000 to 131,072 keys,
+// 64 / 8 heads: 40 + 216 108.4 us, 56 + 200 105.2, 72 + 184 102.7, 88 + 168 103.5; of 16 rows 48 + 208 is best).
+template <int kN>
+constexpr int kLoadRegs = kN == 1 ? 72 : 48;
+template <int kN>
+constexpr int kRegs = 256 - kLoadRegs<kN>;
 // A piece's start and end, in key tiles of an equal share.
 constexpr int kRowHead = 2;
 
-enum : uint32_t { W_R_FULL = 301, W_R_DRAIN };
+enum : uint32_t { W_R_FULL = 301, W_R_DRAIN, W_R_EMPTY };
 
 // Row i of a tile's eight is key kPerm(i) = 0, 3, 1, 2, 4, 7, 5, 6.
 __device__ __forceinline__ int perm8(int i) { return static_cast<int>((0x65742130u >> (4 * i)) & 7u); }
 
 __device__ __forceinline__ void mma_f16_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
+
 // kN: query rows of a job in eights.
 template <int kN, bool kPoll>
-__global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
     attn_row4_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs, const AttnArgs a,
-                     const int box_rows) {
+                     const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, q4 = lane & 3;
-  const uint32_t ring = sbase + warp * kWarpBytes;
-  auto bar = [&](int st) -> uint32_t { return sbase + kOffBars + (warp * kStages + st) * 8; };
+  auto full = [&](int w, int st) -> uint32_t { return sbase + kOffFull + (w * kStages + st) * 8; };
+  auto empty = [&](int w, int st) -> uint32_t { return sbase + kOffEmpty + (w * kStages + st) * 8; };
+  volatile int* have = reinterpret_cast<volatile int*>(smem + kOffHave);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffAbort);
-  if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bar(st), 1);
-    if (warp == 0) *abort_flag = 0;
+  if (threadIdx.x < kWarps * kStages) {
+    for (int k = 0; k < 2; ++k) mbar_init(sbase + kOffFull + 8 * (threadIdx.x + k * kWarps * kStages), 1);
+    if (threadIdx.x == 0) *abort_flag = 0;
     mbar_init_fence();
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_ks);
-    tma_prefetch_desc(&tm_vs);
   }
   if (warp == 1) attn_prefetch(a, lane);
   __syncthreads();
@@ -99,97 +107,91 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     next = jobs.find<true>(a, blockIdx.x, lane);
   }
   grid_launch_dependents();
-
-  // ---- this warp's loads: they run ahead of its products, into the next piece
-  const int box_shift = box_rows == 64 ? 6 : box_rows == 32 ? 5 : 4;
-  const int boxes = kBlock >> box_shift;                 // pages (or parts of one) of a block: 1, 2 or 4
-  struct Loads {                      // a piece: the warp's first key, its blocks, the sequence's keys, KV head, table
-    int key, cnt, kv, g;
-    const int32_t* table;
-  };
-  auto loads_of = [&](const AttnPiece& p) {
-    const AttnSeq seq = attn_seq(a, p.b);
+  const uint32_t limit = wait_limit(a);
+  // a piece's blocks of keys: up to the last token's keys
+  auto blocks_of = [&](const AttnPiece& p, const AttnSeq& seq) {
     const int key0 = p.tile0 * kTile;
-    // up to the last token's keys
-    const int key_end = static_cast<int>(min(key0 + static_cast<int64_t>(p.tiles) * kTile,
-                                             static_cast<int64_t>(seq.kv - seq.sq + min((p.j + 1) * tokens, seq.sq))));
-    const int blocks = key_end > key0 ? (key_end - key0 + kBlock - 1) / kBlock : 0;
-    Loads x;
-    x.key = key0 + warp * kBlock;
-    x.cnt = blocks > warp ? (blocks - warp + kWarps - 1) / kWarps : 0;
-    x.kv = seq.kv;
-    x.g = p.g;
-    x.table = a.table + static_cast<size_t>(p.b) * a.table_width;
-    return x;
+    const int end = static_cast<int>(min(key0 + static_cast<int64_t>(p.tiles) * kTile,
+                                         static_cast<int64_t>(seq.kv - seq.sq + min((p.j + 1) * tokens, seq.sq))));
+    return end > key0 ? (end - key0 + kBlock - 1) / kBlock : 0;
   };
-  // lane's (block, box) of a group of 32: the page, or num_pages (zeros) where there is none
-  auto lookup = [&](const Loads& x, int first) {
-    const int e = first + lane;
-    const int key = x.key + kWarps * kBlock * (e / boxes) + (e & (boxes - 1)) * box_rows;
-    int page = a.num_pages;
-    if (e < x.cnt * boxes && key < x.kv) {
-      const int p = x.table[key >> a.page_shift];
-      if (p >= 0 && p < a.num_pages) page = p;
-    }
-    return page;
-  };
-  int loaded = 0, issued = 0;         // blocks of earlier pieces; blocks whose loads were started
-  uint32_t have = 0;                  // four bits a block in flight: its boxes' pages exist
-  Loads in = {0, 0, 0, 0, nullptr}, then = in;   // the piece that the loads are in, the next one
-  bool more = false;                  // `then` is there and not entered yet
-  int at = 0, group0 = 0;             // next block of `in`; first (block, box) of `pages`
-  int pages = 0, pages_next = 0, pages_then = 0;
-  auto announce = [&](const AttnPiece& p) {   // `then` = p
-    more = p.b >= 0;
-    if (more) {
-      then = loads_of(p);
-      pages_then = lookup(then, 0);
-    }
-  };
-  auto load_ahead = [&](int seen) {   // until every stage is in flight
-    while (issued - seen < kStages) {
-      if (at == in.cnt) {
-        if (!more) break;
-        more = false;
-        in = then;
-        at = group0 = 0;
-        pages = pages_then;
-        pages_next = lookup(in, 32);
-        continue;
+
+  if (warp >= kWarps) {
+    // ============================================================ loads ===
+    regs_dec<kLoadRegs<kN>>();
+    const int w = warp - kWarps;                           // whose
+    const uint32_t ring = sbase + w * kWarpBytes;
+    // A lane loads a box (a page's rows, or 64 of one) of K's or V's codes or scales. Rows without a page become zeros.
+    const int box_shift = min(a.page_shift, 6);
+    const int boxes = kBlock >> box_shift;                 // of a block: 1, 2 or 4
+    const int box = lane & (boxes - 1), which = lane >> (6 - box_shift);
+    const bool is_v = which & 1, is_scale = which >= 2;
+    const uint32_t dst = ring + (is_scale ? (is_v ? kOffVs : kOffKs) + (box << (box_shift + 3)) : (is_v ? kOffV : 0) + (box << (box_shift + 6)));
+    const CUtensorMap* tm = is_scale ? (is_v ? &tm_vs : &tm_ks) : (is_v ? &tm_v : &tm_k);
+    const int row_mask = (1 << a.page_shift) - 1;
+    if (lane < 4) tma_prefetch_desc(lane == 0 ? &tm_k : lane == 1 ? &tm_v : lane == 2 ? &tm_ks : &tm_vs);
+    int used = 0, st = 0;                                  // blocks so far, the next one's stage and parity
+    uint32_t parity = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && next.b >= 0) {
+      const AttnSeq seq = attn_seq(a, next.b);
+      const int key0 = next.tile0 * kTile + w * kBlock, all = blocks_of(next, seq);
+      const int cnt = all > w ? (all - w + kWarps - 1) / kWarps : 0;   // this warp's blocks
+      const int32_t* table = a.table + static_cast<size_t>(next.b) * a.table_width;
+      const int head = next.g;
+      // lane's box of a group of 32: the page, or num_pages (zeros) where there is none
+      auto lookup = [&](int first) {
+        const int e = first + lane;
+        const int key = key0 + kWarps * kBlock * (e / boxes) + ((e & (boxes - 1)) << box_shift);
+        int page = a.num_pages;
+        if (e < cnt * boxes && key < seq.kv) {
+          const int p = table[key >> a.page_shift];
+          if (p >= 0 && p < a.num_pages) page = p;
+        }
+        return page;
+      };
+      int group0 = 0, pages = lookup(0), pages_next = lookup(32);
+      next.b = -1;
+      if (a.adaptive == kShares) next = shares.next(a);
+#pragma unroll 1
+      for (int at = 0; at < cnt; ++at) {
+        if (at * boxes - group0 >= 32) {
+          pages = pages_next;
+          group0 += 32;
+          pages_next = lookup(group0 + 32);
+        }
+        ok = used < kStages || wait_for<kPoll>(empty(w, st), parity ^ 1u, limit);
+        if (!ok) break;
+        ++used;
+        const int page = __shfl_sync(0xffffffffu, pages, (at * boxes - group0 + box) & 31);
+        const unsigned got = __ballot_sync(0xffffffffu, lane < boxes && page != a.num_pages);
+        if (lane == 0) {
+          have[w * kStages + st] = static_cast<int>(got);
+          mbar_arrive_expect_tx(full(w, st), kStageBytes);
+        }
+        __syncwarp();
+        if (lane < 4 * boxes) {
+          const int row = (key0 + kWarps * kBlock * at + (box << box_shift)) & row_mask;
+          tma_load_4d(dst + st * kStageBytes, tm, is_scale ? 2 * row : 0, is_scale ? 0 : row, page, head, full(w, st));
+        }
+        st = st == kStages - 1 ? 0 : st + 1;
+        parity ^= st == 0 ? 1u : 0u;
       }
-      if (at * boxes - group0 >= 32) {
-        pages = pages_next;
-        group0 += 32;
-        pages_next = lookup(in, group0 + 32);
-      }
-      const int box = lane & (boxes - 1);
-      const int page = __shfl_sync(0xffffffffu, pages, (at * boxes - group0 + box) & 31);
-      const unsigned got = __ballot_sync(0xffffffffu, lane < boxes && page != a.num_pages);
-      have = (have & ~(15u << (4 * (issued & 7)))) | (got << (4 * (issued & 7)));
-      const int st = issued % kStages;
-      if (lane == 0) mbar_arrive_expect_tx(bar(st), kStageBytes);
-      __syncwarp();
-      if (lane < 4 * boxes) {          // a lane a box of K's or V's codes or scales
-        const int which = lane >> (6 - box_shift);
-        const int key = in.key + kWarps * kBlock * at + box * box_rows;
-        const int row = key & ((1 << a.page_shift) - 1);
-        const uint32_t dst = ring + st * kStageBytes;
-        if (which < 2)
-          tma_load_4d(dst + which * kOffV + box * box_rows * 64, which ? &tm_v : &tm_k, 0, row, page, in.g, bar(st));
-        else
-          tma_load_4d(dst + kOffKs + (which - 2) * kScales + box * box_rows * 8, which == 3 ? &tm_vs : &tm_ks, 2 * row, 0, page, in.g,
-                      bar(st));
-      }
-      ++at;
-      ++issued;
     }
-  };
-  auto drain = [&](int seen) {        // what was started may not be writing shared memory any more when the CTA ends
-    bool done = true;
-    for (int k = seen; k < issued; ++k)
-      done = wait_drain(bar(k % kStages), (k / kStages) & 1, a.drain_limit_ns) && done;
-    if (!done && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
-  };
+    if (!ok) give_up(a, W_R_EMPTY);
+    // what was started may not be writing shared memory any more when the CTA ends
+    bool quiet = true;
+    for (int k = max(0, used - kStages); k < used; ++k)
+      quiet = wait_drain(full(w, k % kStages), (k / kStages) & 1, a.drain_limit_ns) && quiet;
+    if (!quiet && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
+    return;
+  }
+
+  // ============================================================ products ===
+  regs_inc<kRegs<kN>>();
+  const int box_shift = min(a.page_shift, 6), boxes = kBlock >> box_shift;
+  const uint32_t ring = sbase + warp * kWarpBytes;
   // shared memory offsets of this lane's rows of a tile of 16 keys
   const int k_row = perm8(quad);                          // keys of tile rows quad, and 8 on
   const uint32_t k_off = k_row * 64 + ((q4 ^ ((k_row >> 1) & 3)) << 4), ks_off = kOffKs + k_row * 8 + 2 * q4;
@@ -200,18 +202,23 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     v_off[e] = kOffV + row * 64 + (((quad >> 1) ^ ((row >> 1) & 3)) << 4) + 8 * (quad & 1);
     vs_off[e] = kOffVs + row * 8 + quad;
   }
-  announce(next);
+  int loaded = 0;                     // blocks of earlier pieces
+  int st = 0;                         // the next block's stage, its barrier's parity, whether it was seen there
+  uint32_t parity = 0;
+  bool seen = false;
+  AttnSeq seq_next = {0, 0, 0, 0};
+  if (next.b >= 0) seq_next = attn_seq(a, next.b);
 #pragma unroll 1
   while (next.b >= 0) {
   const AttnPiece job = next;
-  const AttnSeq seq = attn_seq(a, job.b);
+  const AttnSeq seq = seq_next;
   const int tok0 = job.j * tokens;
   const int ntok = min(tokens, seq.sq - tok0);
-  load_ahead(loaded);                 // (every earlier block has been used, so the loads are in this piece now)
-  const int first_key = in.key, cnt = in.cnt;   // this warp's
+  const int first_key = job.tile0 * kTile + warp * kBlock;
+  const int all = blocks_of(job, seq), cnt = all > warp ? (all - warp + kWarps - 1) / kWarps : 0;   // this warp's
   next.b = -1;
   if (a.adaptive == kShares) next = shares.next(a);
-  announce(next);
+  if (next.b >= 0) seq_next = attn_seq(a, next.b);
 
   // ---- Q fragments: row 8 n + quad (token r / group, head r % group), dims 32 q4 .. + 31, four a step
   const float dq = a.descale_q ? *a.descale_q : 1.f, dk = a.descale_k ? *a.descale_k : 1.f,
@@ -273,67 +280,67 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       m[n][k] = -INFINITY;
       l[n][k] = lc[n][k] = 0.f;
     }
-  const uint32_t limit = wait_limit(a);
   bool ok = true;
   int nb = 0;
 #pragma unroll 1
   for (; nb < cnt; ++nb) {
-    load_ahead(loaded + nb);
-    const int st = (loaded + nb) % kStages;
-    if (!wait_for<kPoll>(bar(st), ((loaded + nb) / kStages) & 1, limit)) {
+    if (!seen && !wait_for<kPoll>(full(warp, st), parity, limit)) {
       ok = false;
       break;
     }
     const uint32_t stage = ring + st * kStageBytes;
     const int key = first_key + kWarps * kBlock * nb;
-    if (key + kBlock > seq.kv) {
-      // rows past the sequence's end: 0 * NaN would reach the result, and only a scale can be NaN
-      for (int r = seq.kv - key + lane; r < kBlock; r += 32)
-        *reinterpret_cast<uint2*>(smem + warp * kWarpBytes + st * kStageBytes + kOffVs + 8 * r) = make_uint2(0, 0);
-      fence_proxy_async_smem();        // (a later load writes the stage)
-      __syncwarp();
-    }
-    float s[4][kN][4];
+    const uint32_t there = static_cast<uint32_t>(have[warp * kStages + st]);   // a bit a box
+    float s[kTiles][kN][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t0 = 0; t0 < kTiles; t0 += 2) {               // two tiles side by side: their products do not wait for one another
+      uint32_t w[2][2][4], sc2[2][2];
 #pragma unroll
-      for (int n = 0; n < kN; ++n)
+      for (int e = 0; e < 2; ++e) {
+        const int t = t0 + e;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[t][n][k] = 0.f;
-      uint32_t lo[4], hi[4];
-      lds128(stage + k_off + t * 1024, lo);
-      lds128(stage + k_off + t * 1024 + 512, hi);
-      const uint32_t slo = f16x2_of_e4m3(lds16(stage + ks_off + t * 128)), shi = f16x2_of_e4m3(lds16(stage + ks_off + t * 128 + 64));
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[t][n][k] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          lds128(stage + k_off + t * 1024 + h * 512, w[e][h]);
+          sc2[e][h] = f16x2_of_e4m3(lds16(stage + ks_off + t * 128 + h * 64));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t bl = __byte_perm(slo, 0, j < 2 ? 0x1010 : 0x3232), bh = __byte_perm(shi, 0, j < 2 ? 0x1010 : 0x3232);
-        uint32_t x[4], y[4];
-        f16_of_e2m1x8(lo[j], x);
-        f16_of_e2m1x8(hi[j], y);
+        uint32_t x[2][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = mul_f16x2(x[i], bl);
-          y[i] = mul_f16x2(y[i], bh);
-        }
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          mma_f16_16x8(s[t][n], x[0], y[0], x[1], y[1], qf[n][2 * j][0], qf[n][2 * j][1]);
-          mma_f16_16x8(s[t][n], x[2], y[2], x[3], y[3], qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
-        }
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t by = __byte_perm(sc2[e][h], 0, j < 2 ? 0x1010 : 0x3232);
+            f16_of_e2m1x8(w[e][h][j], x[e][h]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[e][h][i] = mul_f16x2(x[e][h][i], by);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+              mma_f16_16x8(s[t0 + e][n], x[e][0][2 * i], x[e][1][2 * i], x[e][0][2 * i + 1], x[e][1][2 * i + 1], qf[n][2 * j + i][0],
+                           qf[n][2 * j + i][1]);
       }
     }
     if (!raw_ok) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[t][n][k] *= esc[n][k & 1];
     }
-    const uint32_t there = (have >> (4 * ((loaded + nb) & 7))) & 15u;
     if (key + kBlock - 1 > lim_min || there != (1u << boxes) - 1u) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int n = 0; n < kN; ++n)
 #pragma unroll
@@ -342,6 +349,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
             if (at_key > lim[n][k & 1] || !((there >> ((16 * t) >> box_shift)) & 1u)) s[t][n][k] = -INFINITY;
           }
     }
+    // a row's keys lie over the eight lanes of a column: their maximum is needed only where a lane's asks for a new reference
     float mx[kN][2];
     bool need = false;
 #pragma unroll
@@ -350,10 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       for (int k = 0; k < 2; ++k) {
         float x = fmaxf(s[0][n][k], s[0][n][k + 2]);
 #pragma unroll
-        for (int t = 1; t < 4; ++t) x = fmax3(x, s[t][n][k], s[t][n][k + 2]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        for (int t = 1; t < kTiles; ++t) x = fmax3(x, s[t][n][k], s[t][n][k + 2]);
         mx[n][k] = raw_ok ? x * esc[n][k] : x;
         need = need || new_reference<true>(mx[n][k], m[n][k]);
       }
@@ -361,10 +366,14 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
 #pragma unroll
       for (int n = 0; n < kN; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (new_reference<true>(mx[n][k], m[n][k])) {
-            const float al = m[n][k] == -INFINITY ? 0.f : ex2_approx(m[n][k] - mx[n][k]);
-            m[n][k] = mx[n][k];
+        for (int k = 0; k < 2; ++k) {
+          float x = mx[n][k];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          if (new_reference<true>(x, m[n][k])) {
+            const float al = m[n][k] == -INFINITY ? 0.f : ex2_approx(m[n][k] - x);
+            m[n][k] = x;
             l[n][k] *= al;
             lc[n][k] *= al;
 #pragma unroll
@@ -373,15 +382,16 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
               o[i][n][k + 2] *= al;
             }
           }
+        }
     }
-    uint32_t pf[4][kN][2];                                 // P^T: keys 2 q4, 2 q4 + 1 (and + 8) of row quad
+    uint32_t pf[kTiles][kN][2];                                 // P^T: keys 2 q4, 2 q4 + 1 (and + 8) of row quad
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       const float nm0 = minus_reference<true>(m[n][0]), nm1 = minus_reference<true>(m[n][1]);
       const float e0 = raw_ok ? esc[n][0] : 1.f, e1 = raw_ok ? esc[n][1] : 1.f;
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int t = 0; t < kTiles; ++t) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) s[t][n][k] = ex2_approx(fmaf(s[t][n][k], k & 1 ? e1 : e0, k & 1 ? nm1 : nm0));
         sum[0] += s[t][n][0] + s[t][n][2];
@@ -392,8 +402,18 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       add_compensated(l[n][0], lc[n][0], sum[0]);
       add_compensated(l[n][1], lc[n][1], sum[1]);
     }
+    const int st_next = st == kStages - 1 ? 0 : st + 1;
+    const uint32_t parity_next = parity ^ (st_next == 0 ? 1u : 0u);
+    seen = nb + 1 < cnt && mbar_test_wait(full(warp, st_next), parity_next);
+    if (key + kBlock > seq.kv) {
+      // rows past the sequence's end: 0 * NaN would reach the result, and only a scale can be NaN
+      for (int r = seq.kv - key + lane; r < kBlock; r += 32)
+        *reinterpret_cast<uint2*>(smem + warp * kWarpBytes + st * kStageBytes + kOffVs + 8 * r) = make_uint2(0, 0);
+      fence_proxy_async_smem();        // (a later load writes the stage)
+      __syncwarp();
+    }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
       uint32_t w[2][2][2];                                 // [key + 8][key of the pair][eight dims]
       uint32_t sv[2];
 #pragma unroll
@@ -424,20 +444,22 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
           mma_f16_16x8(o[i][n], x[0][0][i], x[0][1][i], x[1][0][i], x[1][1][i], pf[t][n][0], pf[t][n][1]);
     }
     __syncwarp();                                          // every lane has read the stage
+    if (lane == 0 && nb + 1 < cnt) mbar_arrive(empty(warp, st));   // (the last one holds the warp's result first)
+    st = st_next;
+    parity = parity_next;
   }
   if (!ok) {
     if (lane == 0) *abort_flag = 1;   // read at the merge
     give_up(a, W_R_FULL);
-    drain(loaded + nb);
   }
 
   // ---- merge of the four warps' results
-  // A warp's rows x 128 fp32 go through the stage that the next load will take (at most two are in flight now). Row r's
-  // 16-byte piece c lies at c ^ c / 8 ^ r / 2 within its eight: no bank conflicts on either side.
+  // A warp's rows x 128 fp32 go through the stage of its last block. Row r's 16-byte piece c lies at c ^ c / 8 ^ r / 2 within its eight: no bank conflicts on either side.
   auto piece_at = [](int row, int c) { return row * 512 + (((c & 24) | ((c ^ (c >> 3) ^ ((row >> 1) & 3)) & 7)) << 4); };
   volatile int* stage_of = reinterpret_cast<volatile int*>(smem + kOffStage);
-  uint8_t* mine = smem + warp * kWarpBytes + (issued % kStages) * kStageBytes;
-  if (lane == 0) stage_of[warp] = issued % kStages;
+  const int last = (loaded + max(cnt, 1) - 1) % kStages;
+  uint8_t* mine = smem + warp * kWarpBytes + last * kStageBytes;
+  if (lane == 0) stage_of[warp] = cnt > 0 ? last : -1;
   float2* stats = reinterpret_cast<float2*>(smem + kOffStats);
 #pragma unroll
   for (int n = 0; n < kN; ++n)
@@ -448,85 +470,82 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
       z += __shfl_xor_sync(0xffffffffu, z, 8);
       z += __shfl_xor_sync(0xffffffffu, z, 16);
       const int r = 8 * n + 2 * q4 + k;
+      if (cnt > 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)                          // dims 16 quad + 8 h ..
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           *reinterpret_cast<float4*>(mine + piece_at(r, 4 * quad + 2 * h + j)) =
               make_float4(o[4 * j][n][2 * h + k], o[4 * j + 1][n][2 * h + k], o[4 * j + 2][n][2 * h + k], o[4 * j + 3][n][2 * h + k]);
+      }
       if (quad == 0) stats[warp * 16 + r] = make_float2(m[n][k], z);
     }
-  __syncthreads();
-  if (*abort_flag) {
-    if (ok) drain(loaded + cnt);
-    return;
-  }
-  const int row = threadIdx.x >> 3, x0 = (threadIdx.x & 7) * 16;
-  const int rt = row / a.group;
-  const bool live = row < 8 * kN && rt < ntok;
+  named_bar_sync(1, 32 * kWarps);
+  if (*abort_flag) return;
+  const bool part = job.slot >= 0;
   float amax = 0.f;
-  if (live) {
+#pragma unroll 1
+  for (int row = warp; row < 8 * kN; row += kWarps) {     // a warp a row, four dims a lane
+    const int rt = row / a.group;
+    if (rt >= ntok) break;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stats[w * 16 + row].x);
-    float tot = 0.f, y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = 0.f;
+    float tot = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
+      if (stage_of[w] < 0) continue;
       const float2 st = stats[w * 16 + row];
       const float f = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
       tot = fmaf(st.y, f, tot);
-      const uint8_t* r = smem + w * kWarpBytes + stage_of[w] * kStageBytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(r + piece_at(row, (x0 >> 2) + i));
-        y[4 * i] = fmaf(v.x, f, y[4 * i]);
-        y[4 * i + 1] = fmaf(v.y, f, y[4 * i + 1]);
-        y[4 * i + 2] = fmaf(v.z, f, y[4 * i + 2]);
-        y[4 * i + 3] = fmaf(v.w, f, y[4 * i + 3]);
-      }
+      const float4 v = *reinterpret_cast<const float4*>(smem + w * kWarpBytes + stage_of[w] * kStageBytes + piece_at(row, lane));
+      y.x = fmaf(v.x, f, y.x);
+      y.y = fmaf(v.y, f, y.y);
+      y.z = fmaf(v.z, f, y.z);
+      y.w = fmaf(v.w, f, y.w);
     }
     const bool some = tot > 0.f || tot != tot;
     const float inv = some ? dv / tot : 0.f;
     const float lse = some ? lse_of<true>(M, tot) : -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      y[i] = some ? y[i] * inv : 0.f;
-      amax = fmaxf(amax, fabsf(y[i]));
-    }
-    const bool part = job.slot >= 0;
+    y = some ? make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
     const int64_t orow = static_cast<int64_t>(seq.q0 + tok0 + rt) * a.h_q + job.g * a.group + (row - rt * a.group);
     const int64_t prow = static_cast<int64_t>(job.slot) * kRowRows + row;
-    if (part) store_row(a.o_part, 0, prow * kD + x0, y, 1.f);
-    else store_row(a.out, a.out_dtype, orow * kD + x0, y, a.inv_scale);
-    if (x0 == 0) {
+    const int64_t to = (part ? prow : orow) * kD + 4 * lane;
+    if (part) *reinterpret_cast<float4*>(a.o_part + to) = y;
+    else if (a.out_dtype == 0) *reinterpret_cast<float4*>(static_cast<float*>(a.out) + to) = y;
+    else if (a.out_dtype == 1)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + to) =
+          pack_e4m3x4(y.x * a.inv_scale, y.y * a.inv_scale, y.z * a.inv_scale, y.w * a.inv_scale);
+    if (lane == 0) {
       if (part) a.lse_part[prow] = lse;
       else if (a.lse_out != nullptr) a.lse_out[orow] = lse;
       if (a.row_map != nullptr && (job.S > 0 || !part) && row == rt * a.group)
         a.row_map[static_cast<int64_t>(seq.q0 + tok0 + rt) * a.h_kv + job.g] = make_int2(static_cast<int>(prow), part ? job.S : 0);
     }
   }
-  if (job.slot < 0 && a.amax != nullptr) {
+  if (!part && a.amax != nullptr) {
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
     if (lane == 0) atomicMax(reinterpret_cast<int*>(a.amax), __float_as_int(amax));
   }
   if (next.b < 0) break;
+  fence_proxy_async_smem();            // the stages were read and written here; TMA writes them next
+  named_bar_sync(1, 32 * kWarps);      // the results have been read
+  if (lane == 0 && cnt > 0) mbar_arrive(empty(warp, last));
   loaded += cnt;
-  fence_proxy_async_smem();            // stages were read and written here; TMA writes them next
-  __syncthreads();
   }
 }
 
-using Row4Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs, int);
+using Row4Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs);
 // [rows / 8 - 1][polling waits]
 constexpr Row4Kernel kRow4Kernels[2][2] = {{attn_row4_kernel<1, false>, attn_row4_kernel<1, true>},
                                            {attn_row4_kernel<2, false>, attn_row4_kernel<2, true>}};
 
 }  // namespace
-
-int attn_row4_box(int page_size) { return page_size < kBlock ? page_size : kBlock; }
 
 cudaError_t prepare_attn_row4() {
   for (int k = 0; k < 4; ++k) {
@@ -539,8 +558,8 @@ cudaError_t prepare_attn_row4() {
 cudaError_t launch_attn_row4(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
                              const AttnArgs& a, int rows, int64_t grid, cudaStream_t stream) {
   if (grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(kRow4Kernels[rows > 8][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid), kWarps * 32, kSmem, stream,
-                    tm_k, tm_v, tm_ks, tm_vs, a, attn_row4_box(1 << a.page_shift));
+  return launch_pdl(kRow4Kernels[rows > 8][a.wait_limit_ns < kSuspendNs], static_cast<unsigned>(grid), kThreads, kSmem, stream, tm_k,
+                    tm_v, tm_ks, tm_vs, a);
 }
 
 }  // namespace skv

@@ -193,18 +193,18 @@ constexpr int kTileSplitWaves = 3;
 // kv_wide as 5-D {64, 8 rows, column blocks, row groups, pages}, box {64, 8, 2, min(page, 128) / 8, 1}.
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
-// 4-bit pages: boxes of min(page, 128) rows, codes and scales as in launch_attn_row4.
+// 4-bit pages. tm_k / tm_v: codes, box {64 bytes, min(page, 128) rows, 1, 1}, 64-byte swizzle; tm_ks / tm_vs: scales as 4-D {rows * 2
+// words, 1, pages, heads}, box {2 min(page, 128) words, 1, 1, 1}.
 cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks,
                               const CUtensorMap& tm_vs, const AttnArgs& a, int64_t grid, cudaStream_t stream);
 // Box of tm_k / tm_v: {128 bytes, attn_row_box(dtype, page size) rows, 1, 1}.
 cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
                             int64_t grid, cudaStream_t stream);
 int attn_row_box(int dtype, int page_size);
-// 4-bit pages; rows: of a job, 8 or 16. tm_k / tm_v: codes, box {64 bytes, attn_row4_box(page size) rows, 1, 1}, 64-byte
-// swizzle; tm_ks / tm_vs: scales as 4-D {rows * 2 words, 1, pages, heads}, box {2 attn_row4_box words, 1, 1, 1}.
+// 4-bit pages; rows: of a job, 8 or 16. Maps as in launch_attn_tile4, boxes of min(page, kRow4Box) rows.
 cudaError_t launch_attn_row4(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
                              const AttnArgs& a, int rows, int64_t grid, cudaStream_t stream);
-int attn_row4_box(int page_size);
+constexpr int kRow4Box = 64;
 // CTAs of the row kernel that an SM holds.
 constexpr int kRowCtasPerSm = 2;
 // Folds the partial rows of every split token; a.num_splits > 1. rows_per_slot: kTileRows or kRowRows.
