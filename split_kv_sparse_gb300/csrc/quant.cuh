@@ -35,27 +35,25 @@ __device__ __forceinline__ float quotient(float x, float d, float y) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
-// x = x / d, eight values.
-__device__ __forceinline__ void divide8(float (&x)[8], const Divider& by) {
-  float q[8], most = 0.f;
+// x / d by divisions, where a quotient leaves the range that the short way is good for (a function of its own, which keeps
+// the others' code short).
+static __device__ __noinline__ float4 divide4_far(float4 x, float d) {
+  return make_float4(__fdiv_rn(x.x, d), __fdiv_rn(x.y, d), __fdiv_rn(x.z, d), __fdiv_rn(x.w, d));
+}
+// x = x / d, four values.
+__device__ __forceinline__ void divide4(float (&x)[4], const Divider& by) {
+  float q[4], most = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    most = fmaxf(most, fabsf(__fmul_rn(x[i], by.y)));
+  for (int i = 0; i < 4; ++i) {
     q[i] = quotient(x[i], by.d, by.y);
+    most = fmaxf(most, fabsf(__fmul_rn(x[i], by.y)));
   }
   if (by.plain || most > 1e30f) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      float v = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v = i == k ? x[k] : v;
-      v = __fdiv_rn(v, by.d);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) q[k] = i == k ? v : q[k];
-    }
+    const float4 v = divide4_far(make_float4(x[0], x[1], x[2], x[3]), by.d);
+    q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = q[i];
+  for (int i = 0; i < 4; ++i) x[i] = q[i];
 }
 
 // max(a, |x|) that keeps a NaN of either.
@@ -66,8 +64,11 @@ __device__ __forceinline__ float max_abs_nan(float a, float x) {
 }
 
 // The scale of 16 dims whose largest magnitude (after the descale) is amax: e4m3(amax / 6), which takes the largest of
-// them to e2m1's largest value. A NaN among them makes the scale NaN, as e2m1 has none.
-__device__ __forceinline__ uint32_t scale_code(float amax) { return e4m3x2(__fdiv_rn(amax, 6.f), 0.f) & 0xffu; }
+// them to e2m1's largest value. A NaN among them makes the scale NaN, as e2m1 has none. (Past 448 * 6 every scale is 448.)
+__device__ __forceinline__ uint32_t scale_code(float amax) {
+  const float q = quotient(fminf(amax, 1e6f), 6.f, 0.166666671633720397949f);   // RN(1 / 6)
+  return e4m3x2(amax == amax ? q : amax, 0.f) & 0xffu;
+}
 __device__ __forceinline__ float e4m3_value(uint32_t code) {
   uint32_t h;
   asm("{\n  .reg .b16 lo, hi;\n  mov.b32 {lo, hi}, %1;\n  cvt.rn.f16x2.e4m3x2 %0, lo;\n}\n" : "=r"(h) : "r"(code));
@@ -75,25 +76,26 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   asm("{\n  .reg .b16 lo, hi;\n  mov.b32 {lo, hi}, %1;\n  cvt.f32.f16 %0, lo;\n}\n" : "=f"(f) : "r"(h));
   return f;
 }
-// The e2m1 codes of eight y / scale (ties to even, at most 6), the first in the lowest four bits. The quotient is the
-// rounded one, as e2m1 of a division. Where the scale is 0 or NaN every code is a zero with its value's sign. (Beyond
-// 6 * 448 every code is the largest; the clamp keeps infinities out of the quotient's residual.)
-__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[8], float scale) {
-  const float r = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float q[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float v = fminf(fmaxf(y[2 * i + k], -4096.f), 4096.f);
-      q[k] = scale > 0.f ? quotient(v, scale, r) : copysignf(0.f, y[2 * i + k]);
-    }
-    uint32_t c;
-    asm("{\n  .reg .b8 b;\n  cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n  cvt.u32.u8 %0, b;\n}\n" : "=r"(c) : "f"(q[0]), "f"(q[1]));
-    w |= c << (8 * i);
-  }
-  return w;
+// RN(1 / s) of an e4m3 value s > 0: one Newton step in FMAs takes every approximation within 1 ulp there (tried for all 126).
+__device__ __forceinline__ float reciprocal_e4m3(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
+}
+// The e2m1 codes of eight y / scale (ties to even, at most 6), the first in the lowest four bits; |y| <= 1e30. The quotient is
+// the rounded one, as e2m1 of a division. Where the scale is 0 or NaN every code is a zero with its value's sign.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&y)[2][4], float scale) {
+  // (the quotient by a reciprocal of 0 is a zero of y's sign)
+  const bool some = scale > 0.f;
+  const float r = some ? reciprocal_e4m3(scale) : 0.f, d = some ? scale : 0.f;
+  uint32_t c;
+  asm("{\n  .reg .b8 b0, b1, b2, b3;\n  cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n  cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      "  cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n  mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+      : "=r"(c)
+      : "f"(quotient(y[0][0], d, r)), "f"(quotient(y[0][1], d, r)), "f"(quotient(y[0][2], d, r)), "f"(quotient(y[0][3], d, r)),
+        "f"(quotient(y[1][0], d, r)), "f"(quotient(y[1][1], d, r)), "f"(quotient(y[1][2], d, r)), "f"(quotient(y[1][3], d, r)));
+  return c;
 }
 // Eight e2m1 codes as four f16 pairs (exact).
 __device__ __forceinline__ void f16_of_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
