@@ -299,6 +299,7 @@ class _Types:
     def __init__(self):
         import torch
         self.i32, self.i64, self.f32, self.bf16 = (torch.int32,), (torch.int64,), (torch.float32,), (torch.bfloat16,)
+        self.BF, self.I32, self.I64, self.F32 = torch.bfloat16, torch.int32, torch.int64, torch.float32
         self.codes = (torch.uint8, torch.float8_e4m3fn)
         self.data = self.bf16 + self.codes
         self.bytes4 = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
@@ -477,32 +478,44 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
     (bfloat16, or None). cos_sin is float32 [num_positions, rotary_dim], cosines then sines."""
     where, t = "kv_pages_write_rotary", _t()
     dev = _device(where)
-    k = _dev(where, "k_new", k_new, t.bf16, dev, contiguous=False)
-    v = _dev(where, "v_new", v_new, t.bf16, dev, contiguous=False)
+    BF = t.BF
+    try:   # (the checks of _dev in one go: the call of few rows is the host's time)
+        ok = (k_new.get_device() == dev and v_new.get_device() == dev and positions.get_device() == dev
+              and cos_sin.get_device() == dev and slot_map.get_device() == dev and k_new.dtype is BF and v_new.dtype is BF
+              and positions.dtype is t.I32 and cos_sin.dtype is t.F32 and slot_map.dtype is t.I64
+              and positions.is_contiguous() and cos_sin.is_contiguous() and slot_map.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        for n, x, dt, c in (("k_new", k_new, t.bf16, False), ("v_new", v_new, t.bf16, False), ("positions", positions, t.i32, True),
+                            ("cos_sin", cos_sin, t.f32, True), ("slot_map", slot_map, t.i64, True)):
+            _dev(where, n, x, dt, dev, contiguous=c)
     st = _strided(where, "k_new", k_new, 3)
-    if v_new.shape != k_new.shape or _strided(where, "v_new", v_new, 3) != st:
+    shape = k_new.shape
+    if v_new.shape != shape or _strided(where, "v_new", v_new, 3) != st:
         _refuse(where, "k_new and v_new differ in shape or strides")
-    rows, h, d = k_new.shape
+    rows, h, d = shape
     if h != pages.h_kv or d != pages.d:
         _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
-    pos = _dev(where, "positions", positions, t.i32, dev, rows)
-    cs = _dev(where, "cos_sin", cos_sin, t.f32, dev, 1)
-    if cos_sin.dim() != 2:
+    table = cos_sin.shape
+    if len(table) != 2:
         _refuse(where, "cos_sin must be [num_positions, rotary_dim]")
-    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
+    if positions.numel() < rows or slot_map.numel() < rows:
+        _refuse(where, f"positions and slot_map must have {rows} elements")
     h_q, qp, qs, qo, qo_dt, os_ = 0, None, (0, 0), None, SDPA_BF16, (0, 0)
     if q is not None:
         qp = _dev(where, "q", q, t.bf16, dev, contiguous=False)
         qs = _strided(where, "q", q, 3)
-        h_q = q.shape[1]
-        if q.shape[0] != rows or q.shape[2] != d:
+        q_shape = q.shape
+        h_q = q_shape[1]
+        if q_shape[0] != rows or q_shape[2] != d:
             _refuse(where, f"q must be [{rows}, h_q, {d}]")
         if q_out is None:
             qo, os_ = qp, qs
         else:
             qo = _dev(where, "q_out", q_out, t.data, dev, contiguous=False)
             os_, qo_dt = _strided(where, "q_out", q_out, 3), t.sdpa[q_out.dtype]
-            if q_out.shape != q.shape:
+            if q_out.shape != q_shape:
                 _refuse(where, "q_out must have q's shape")
     elif q_out is not None:
         _refuse(where, "q_out without q")
@@ -510,14 +523,17 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
     if k_out is not None:
         ko = _dev(where, "k_out", k_out, t.bf16, dev, contiguous=False)
         ks = _strided(where, "k_out", k_out, 3)
-        if k_out.shape != k_new.shape:
+        if k_out.shape != shape:
             _refuse(where, "k_out must have k_new's shape")
-    dq = _opt(where, "descale_q", descale_q, t.f32, dev, 1)
-    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
-    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
-    _check(lib().kv_pages_write_rotary(_pages(where, pages, dev), rows, h_q, qp, qs[0], qs[1], k, v, st[0], st[1], pos, cs,
-                                       cos_sin.shape[0], cos_sin.shape[1], int(interleaved), slots, dq, dk, dv, qo_dt, qo, os_[0],
-                                       os_[1], ko, ks[0], ks[1], _on(stream, dev)), where)
+    dq = None if descale_q is None else _dev(where, "descale_q", descale_q, t.f32, dev, 1)
+    dk = None if descale_k is None else _dev(where, "descale_k", descale_k, t.f32, dev, 1)
+    dv = None if descale_v is None else _dev(where, "descale_v", descale_v, t.f32, dev, 1)
+    status = (_lib or lib()).kv_pages_write_rotary(
+        _pages(where, pages, dev), rows, h_q, qp, qs[0], qs[1], k_new.data_ptr(), v_new.data_ptr(), st[0], st[1],
+        positions.data_ptr(), cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_map.data_ptr(), dq, dk, dv, qo_dt, qo,
+        os_[0], os_[1], ko, ks[0], ks[1], _on(stream, dev))
+    if status:
+        raise SplitKVError(status, where)
 
 
 def kv_pages_read(pages: KvPages, slot_map, k_out, v_out, descale_k=None, descale_v=None, stream=None):

@@ -527,7 +527,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   if (!rows16 && (st = encode_q(&tq, plan->dtype, q, q_token_stride, q_head_stride, a.h_q, a.group, total_q)) != MLA_OK)
     return st;
   if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
-  if (four && ((st = encode_scales(&tks, pages, pages->k_scales, box)) != MLA_OK ||
+  if (four && rows16 && ((st = encode_scales(&tks, pages, pages->k_scales, box)) != MLA_OK ||
                (st = encode_scales(&tvs, pages, pages->v_scales, box)) != MLA_OK))
     return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(plan->row_kernel, a.group)) * a.h_kv;
@@ -555,9 +555,11 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     grid = share_ctas(a.num_sms, a.h_kv);
     a.part_gap = static_cast<int>(grid) * (rows16 ? skv::kRowRows : skv::kTileRows);
   }
+  const skv::KvScales scales = {static_cast<const uint8_t*>(pages->k_scales), static_cast<const uint8_t*>(pages->v_scales),
+                                pages->scale_page_stride, pages->scale_head_stride};
   st = cuda_status(rows16 && four ? skv::launch_attn_row4(tk, tv, tks, tvs, a, job_rows(plan->row_kernel), grid, cs)
                    : rows16       ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
-                   : four         ? skv::launch_attn_tile4(tq, tk, tv, tks, tvs, a, grid, cs)
+                   : four         ? skv::launch_attn_tile4(tq, tk, tv, a, scales, grid, cs)
                                   : skv::launch_attn_tile(tq, tk, tv, a, plan->dtype, grid, cs));
   if (st != MLA_OK || a.num_splits == 1) return st;
   return cuda_status(skv::launch_attn_combine(a, rows16 ? skv::kRowRows : skv::kTileRows, cs));

@@ -64,12 +64,12 @@ struct Cfg {
   static_assert(kOffV16 % 1024 == 0 && kOffK % 1024 == 0, "swizzle atoms");
   static constexpr int kConsumers = kF8 || kF4 ? 16 : 12;   // warps that read a job's description
 };
-// Tensor maps of the scales of 4-bit pages; no bytes for other types.
+// Where the scales of 4-bit pages lie; nothing for other types.
 template <int kType>
-struct ScaleMaps {};
+struct ScalesOf {};
 template <>
-struct ScaleMaps<4> {
-  CUtensorMap k, v;
+struct ScalesOf<4> {
+  KvScales at;
 };
 
 enum {
@@ -111,7 +111,7 @@ static_assert((M_LAST + 6) * 4 <= 384, "misc area");
 template <int kType, int kPages, bool kPoll>
 __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const __grid_constant__ ScaleMaps<kType> tm_s) {
+                     const __grid_constant__ CUtensorMap tm_v, const AttnArgs a, const ScalesOf<kType> scales) {
   using C = Cfg<kType>;
   constexpr bool kF8 = C::kF8, kF4 = C::kF4;
   constexpr bool kF16 = kF8 || kF4;   // P and V are multiplied in f16
@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
                             (kF8 && i >= B_VEMPTY) ||   // a tile of codes is freed by its four converter warps
                             (kF4 && ((i >= B_KEMPTY && i < B_KEMPTY + 4) || i == B_K16F0 || i == B_K16F0 + 1))
                         ? 4
+                    : kF4 && i >= B_KFULL && i < B_KEMPTY ? 33   // the codes' bytes, and each lane's copies of scales
                     : i == B_READ0 || i == B_READ1 ? C::kConsumers
                                                    : 1;
       mbar_init(bar(i), n);
@@ -579,10 +580,6 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           tma_prefetch_desc(&tm_q);
           tma_prefetch_desc(&tm_k);
           tma_prefetch_desc(&tm_v);
-          if constexpr (kF4) {
-            tma_prefetch_desc(&tm_s.k);
-            tma_prefetch_desc(&tm_s.v);
-          }
         }
         if constexpr (shared) {
           AttnShares<2, kTileHead> shares;
@@ -701,13 +698,29 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           }
           // (V's rows past the sequence's end are cleared before its tile counts as there)
           const uint32_t there = bar(!kF16 && !is_k && t == tail ? static_cast<int>(B_VLAND) : full + sl);
-          if (lane == 0) mbar_arrive_expect_tx(there, C::kItemBytes);
+          if (lane == 0) mbar_arrive_expect_tx(there, kF4 ? C::kCodeBytes : C::kItemBytes);
           __syncwarp();
+          if constexpr (kF4) {
+            // scales by cp.async, a lane those of rows 2 l, 2 l + 1 and of 64 on; 0 past the sequence's end and without a page (a
+            // box of TMA would bring 128 bytes of a page of 16, at about 90 clocks of this warp: ragged chunks 374 us)
+            const KvScales& from = scales.at;
+            const uint8_t* base = is_k ? from.k : from.v;
+            const uint32_t to = sbase + C::kOffK + sl * C::kItemBytes + C::kCodeBytes + 16 * lane;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r = 64 * h + 2 * lane, key = (tile0 + t) * kTile + r;
+              const int p = __shfl_sync(0xffffffffu, page, r / page_rows);
+              const bool there_is = p != a.num_pages;
+              const int64_t off = static_cast<int64_t>(there_is ? p : 0) * from.page_stride + g * from.head_stride +
+                                  8 * (key & ((1 << a.page_shift) - 1));
+              cp_async_16(to + 512 * h, base + off, there_is ? 8 * min(max(kv - key, 0), 2) : 0);
+            }
+            cp_async_arrive_noinc(there);
+          }
           if (lane < boxes) {
             const uint32_t dst = sbase + (is_k || kF4 ? C::kOffK : C::kOffV) + sl * C::kItemBytes;
             if constexpr (kF4) {
               tma_load_4d(dst + lane * page_rows * 64, tm, 0, row, page, g, there);
-              tma_load_4d(dst + C::kCodeBytes + lane * page_rows * 8, is_k ? &tm_s.k : &tm_s.v, 2 * row, 0, page, g, there);
             } else if (kPaged && !kF8 && a.kv_wide != 0) {
               const int groups = a.kv_wide == 2 ? g << (a.page_shift - 3) : 0;
               tma_load_5d(dst + lane * page_rows * 256, tm, 0, 0, a.kv_wide == 1 ? 2 * g : 0, groups + (row >> 3), page,
@@ -764,6 +777,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         }
       }
       if (!ok) give_up(a, W_T_LOAD);
+      if constexpr (kF4) cp_async_wait_all();
       // nothing that was started may still be writing shared memory when the CTA ends
       __syncwarp();
       if (lane == 0) {
@@ -836,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       // ================================ Q bf16 -> f16; K and V codes x scales -> f16 ===
       // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own
       // (largest element in [2^14, 2^15)): exact down to 2^-28 of that element, smaller ones are off by 2^-39 of it at most. A
-      // code times its scale is exact in f16. Rows of V past the end become 0 (K's scores there are masked).
+      // code times its scale is exact in f16.
       const int key = threadIdx.x - 32 * 12;
       const int r8 = key & 7, r4 = (key >> 1) & 3;
       int tile_base = 0, with_tiles = 0, slot = 0;
@@ -847,8 +861,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       volatile int* jw;
       ok = job_at(job, jw);
       if (!ok || jw[J_B] < 0) break;
-      const int kv = jw[J_KV], tile0 = jw[J_TILE0], tiles = jw[J_TILES];
-      const int blocks = jw[J_ONE] != 0 ? 1 : 2;
+      const int tiles = jw[J_TILES], blocks = jw[J_ONE] != 0 ? 1 : 2;
       job_read(job);
       if (tiles == 0) continue;
       ok = wait_for<kPoll>(bar(B_Q), with_tiles & 1, limit);
@@ -894,7 +907,6 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         lds64(src + C::kCodeBytes + key * 8, sc);
 #pragma unroll
         for (int c = 0; c < 4; ++c) lds128((src + key * 64 + (r4 << 4)) ^ (c << 4), w[c]);
-        if (kind(it) && (tile0 + tile_of(it)) * kTile + key >= kv) sc[0] = sc[1] = 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KEMPTY + slot));
         slot = slot == C::kKSlots - 1 ? 0 : slot + 1;
@@ -1064,7 +1076,7 @@ __global__ void __launch_bounds__(256, 2) attn_combine_kernel(const AttnArgs a, 
 
 namespace {
 template <int kType>
-using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs, ScaleMaps<kType>);
+using TileKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, AttnArgs, ScalesOf<kType>);
 // [pages][polling waits]; bf16 takes no equal shares, and 4 bits are a form of pages
 template <int kType>
 constexpr TileKernel<kType> kTileKernels[3][2] = {{attn_tile_kernel<kType, 0, false>, attn_tile_kernel<kType, 0, true>},
@@ -1091,11 +1103,11 @@ cudaError_t prepare() {
 }
 template <int kType>
 cudaError_t launch(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
-                   const ScaleMaps<kType>& tm_s, int64_t grid, cudaStream_t stream) {
+                   const ScalesOf<kType>& scales, int64_t grid, cudaStream_t stream) {
   const int pages = a.table == nullptr ? 0 : a.adaptive == kShares ? 2 : 1;
   const TileKernel<kType> kernel = kTileKernels<kType>[pages][a.wait_limit_ns < kSuspendNs];
   if (kernel == nullptr || grid < 1 || grid > 0x7fffffff) return cudaErrorInvalidValue;
-  return launch_pdl(kernel, static_cast<unsigned>(grid), Cfg<kType>::kThreads, Cfg<kType>::kSmem, stream, tm_q, tm_k, tm_v, a, tm_s);
+  return launch_pdl(kernel, static_cast<unsigned>(grid), Cfg<kType>::kThreads, Cfg<kType>::kSmem, stream, tm_q, tm_k, tm_v, a, scales);
 }
 }  // namespace
 
@@ -1112,9 +1124,9 @@ cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, c
   return launch<1>(tm_q, tm_k, tm_v, a, {}, grid, stream);
 }
 
-cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks,
-                              const CUtensorMap& tm_vs, const AttnArgs& a, int64_t grid, cudaStream_t stream) {
-  return launch<4>(tm_q, tm_k, tm_v, a, {tm_ks, tm_vs}, grid, stream);
+cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
+                              const KvScales& scales, int64_t grid, cudaStream_t stream) {
+  return launch<4>(tm_q, tm_k, tm_v, a, {scales}, grid, stream);
 }
 
 cudaError_t launch_attn_combine(const AttnArgs& a, int rows_per_slot, cudaStream_t stream) {

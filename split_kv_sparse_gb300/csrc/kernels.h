@@ -193,15 +193,19 @@ constexpr int kTileSplitWaves = 3;
 // kv_wide as 5-D {64, 8 rows, column blocks, row groups, pages}, box {64, 8, 2, min(page, 128) / 8, 1}.
 cudaError_t launch_attn_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const AttnArgs& a, int dtype, int64_t grid, cudaStream_t stream);
-// 4-bit pages. tm_k / tm_v: codes, box {64 bytes, min(page, 128) rows, 1, 1}, 64-byte swizzle; tm_ks / tm_vs: scales as 4-D {rows * 2
-// words, 1, pages, heads}, box {2 min(page, 128) words, 1, 1, 1}.
-cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks,
-                              const CUtensorMap& tm_vs, const AttnArgs& a, int64_t grid, cudaStream_t stream);
+// 4-bit pages. tm_k / tm_v: codes, box {64 bytes, min(page, 128) rows, 1, 1}, 64-byte swizzle.
+struct KvScales {
+  const uint8_t *k, *v;
+  int64_t page_stride, head_stride;   // bytes; a row is 8
+};
+cudaError_t launch_attn_tile4(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a,
+                              const KvScales& scales, int64_t grid, cudaStream_t stream);
 // Box of tm_k / tm_v: {128 bytes, attn_row_box(dtype, page size) rows, 1, 1}.
 cudaError_t launch_attn_row(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const AttnArgs& a, int dtype,
                             int64_t grid, cudaStream_t stream);
 int attn_row_box(int dtype, int page_size);
-// 4-bit pages; rows: of a job, 8 or 16. Maps as in launch_attn_tile4, boxes of min(page, kRow4Box) rows.
+// 4-bit pages; rows: of a job, 8 or 16. tm_k / tm_v as in launch_attn_tile4, boxes of min(page, kRow4Box) rows; tm_ks / tm_vs: scales
+// as 4-D {rows * 2 words, 1, pages, heads}, boxes of as many rows.
 cudaError_t launch_attn_row4(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
                              const AttnArgs& a, int rows, int64_t grid, cudaStream_t stream);
 constexpr int kRow4Box = 64;
