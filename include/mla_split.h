@@ -534,7 +534,7 @@ MLA_API int kv_pages_read(const kv_pages_t* pages, int64_t rows, const int64_t* 
 
 /* Plan of sdpa_paged: what its launches and workspace need, from bounds that the
  * host knows. A job is (sequence, KV head, up to R query rows, split), its rows
- * tokens x the heads of one group, R = 16 with row_kernel, else 256. Workspace layout (256-byte aligned):
+ * tokens x the heads of one group, R = 16 with row_kernel (its jobs of 8 rows too), else 256. Workspace layout (256-byte aligned):
  *   [0, o_acc_bytes)                   fp32 partial rows [split job][R][128]
  *   [lse_acc_offset, + lse_acc_bytes)  their fp32 log2 LSE [split job][R]
  *   [map_offset, ...)                  per (token, KV head): its first partial row, its splits
@@ -546,7 +546,7 @@ typedef struct {
   int32_t batch;          /* sequences                                                  */
   int32_t h_q, h_kv;      /* query and KV heads; h_q % h_kv == 0, group = h_q / h_kv <= 128 */
   int32_t d;              /* 128                                                        */
-  int32_t dtype;          /* SDPA_BF16 or SDPA_E4M3                                     */
+  int32_t dtype;          /* SDPA_BF16, SDPA_E4M3 or SDPA_E2M1 (of K and V; Q is bf16 then) */
   int32_t max_q_per_seq;  /* expected bound on new tokens of one sequence (chooses the kernel) */
   int32_t total_q_max;    /* bound on new tokens of the batch                           */
   int32_t max_kv;         /* expected bound on keys of one sequence (sizes the split count
@@ -555,7 +555,8 @@ typedef struct {
   int32_t num_sms;
   int32_t adaptive_splits; /* 1: each sequence's split count follows from the lengths, on the GPU */
   int32_t row_kernel;     /* 1: max_q_per_seq * group <= 16: the kernel of 16-row jobs, two
-                             of them an SM; else the one of 256-row jobs. Either takes any number of tokens */
+                             of them an SM (2: SDPA_E2M1 with at most 8: of 8-row jobs); else the
+                             one of 256-row jobs. Each takes any number of tokens */
   uint64_t o_acc_bytes;
   uint64_t lse_acc_offset;
   uint64_t lse_acc_bytes;
@@ -566,7 +567,7 @@ typedef struct {
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
  * max_kv) for each sequence, from the lengths, on the GPU. With row_kernel (two CTAs an SM), and
- * for e4m3 where the unsplit jobs pass one wave (num_sms jobs) and max_kv >= 6144, one wave of
+ * for e4m3 and 4 bits where the unsplit jobs pass one wave (num_sms jobs) and max_kv >= 6144, one wave of
  * CTAs takes equal shares of the key tiles of all jobs, laid one after the other, and a job
  * is split where a share ends (shares are larger where it would be split into more than the
  * bound). Otherwise, with T = the key tiles a job should walk, a sequence gets
@@ -598,10 +599,12 @@ MLA_API int sdpa_paged_plan(int batch, int h_q, int h_kv, int d, int dtype, int 
  * queries of that sequence before it). cu_seqlens_q starts at 0 and does not decrease;
  * offsets that do leave rows undefined, but nothing outside the buffers is touched.
  * Scores, softmax statistics and O are fp32. The softmax weights that multiply V are
- * rounded, whatever the output type: with e4m3 to f16 (2^-11 relative; 2^-32 of the row's largest
+ * rounded, whatever the output type: with e4m3 and 4 bits to f16 (2^-11 relative; 2^-32 of the row's largest
  * weight below 2^-21 of it), with bf16 to a bf16 pair (2^-16) in the kernel of 16-row jobs and to
  * bf16 (2^-8) in that of 256-row jobs, so a bf16 query's last bits depend on the plan's kernel.
- *   q  [total_q][h_q][128] of the plan's dtype, element (t, j, x) at t *
+ * A 4-bit cache's values code * scale are exact; Q (bf16) is held in f16 at a power of two of its row, which
+ * rounds elements below 2^-28 of the row's largest by at most 2^-39 of that. A scale that is NaN makes its 16 dims NaN.
+ *   q  [total_q][h_q][128] of the plan's dtype (SDPA_E2M1: bf16), element (t, j, x) at t *
  *      q_token_stride + j * q_head_stride + x; 16-byte aligned, strides positive
  *      multiples of 16 bytes.
  *   block_table  int32 [batch][table_width]; kv_lens int32 [batch] (taken as 0
@@ -625,7 +628,8 @@ MLA_API int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q
  * sdpa_paged, same outputs, precision as its 256-row jobs. k and v share their strides; q, k and v may be slices
  * of one fused projection's output. total_q and total_kv, both >= 1, are row counts of q and k/v; nothing
  * outside them is read, and rows of out and lse_out outside the sequences are left as they
- * were. Needs no workspace. Same alignment rules as sdpa_paged. */
+ * were. Needs no workspace. Same alignment rules as sdpa_paged. dtype is SDPA_BF16 or SDPA_E4M3
+ * (kv_pages_read gives the rows of a 4-bit cache in bf16). */
 MLA_API int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int total_q, int64_t total_kv, const void* q,
                 int64_t q_token_stride, int64_t q_head_stride, const void* k, const void* v,
                 int64_t kv_token_stride, int64_t kv_head_stride, const int32_t* cu_seqlens_q,
@@ -714,7 +718,7 @@ MLA_API const char* mla_status_string(int status);
 
 /* ABI version of this header (bumped on any signature or layout change). */
 MLA_API int mla_abi_version(void);
-#define MLA_ABI_VERSION 2
+#define MLA_ABI_VERSION 3
 
 #ifdef __cplusplus
 }

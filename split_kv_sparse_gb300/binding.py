@@ -371,6 +371,14 @@ def _strided(where: str, name: str, x, dims: int):
     return tuple(st)
 
 
+def _strided_pair(where: str, names, x, y, dims: int):
+    """The strides of two tensors that have to share shape and strides."""
+    st = _strided(where, names[0], x, dims)
+    if y.shape != x.shape or (y.stride() != x.stride() and _strided(where, names[1], y, dims) != st):
+        _refuse(where, f"{names[0]} and {names[1]} differ in shape or strides")
+    return st
+
+
 def _table(where: str, block_table, batch: int, dev: int):
     p = _dev(where, "block_table", block_table, _t().i32, dev, 1)
     if block_table.dim() != 2 or block_table.shape[0] < batch:
@@ -459,9 +467,7 @@ def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, desca
     dev = _device(where)
     k = _dev(where, "k_new", k_new, t.bf16, dev, contiguous=False)
     v = _dev(where, "v_new", v_new, t.bf16, dev, contiguous=False)
-    st = _strided(where, "k_new", k_new, 3)
-    if v_new.shape != k_new.shape or _strided(where, "v_new", v_new, 3) != st:
-        _refuse(where, "k_new and v_new differ in shape or strides")
+    st = _strided_pair(where, ("k_new", "v_new"), k_new, v_new, 3)
     rows, h, d = k_new.shape
     if h != pages.h_kv or d != pages.d:
         _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
@@ -490,10 +496,8 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
         for n, x, dt, c in (("k_new", k_new, t.bf16, False), ("v_new", v_new, t.bf16, False), ("positions", positions, t.i32, True),
                             ("cos_sin", cos_sin, t.f32, True), ("slot_map", slot_map, t.i64, True)):
             _dev(where, n, x, dt, dev, contiguous=c)
-    st = _strided(where, "k_new", k_new, 3)
+    st = _strided_pair(where, ("k_new", "v_new"), k_new, v_new, 3)
     shape = k_new.shape
-    if v_new.shape != shape or _strided(where, "v_new", v_new, 3) != st:
-        _refuse(where, "k_new and v_new differ in shape or strides")
     rows, h, d = shape
     if h != pages.h_kv or d != pages.d:
         _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
@@ -542,9 +546,7 @@ def kv_pages_read(pages: KvPages, slot_map, k_out, v_out, descale_k=None, descal
     dev = _device(where)
     k = _dev(where, "k_out", k_out, t.bf16, dev, contiguous=False)
     v = _dev(where, "v_out", v_out, t.bf16, dev, contiguous=False)
-    st = _strided(where, "k_out", k_out, 3)
-    if v_out.shape != k_out.shape or _strided(where, "v_out", v_out, 3) != st:
-        _refuse(where, "k_out and v_out differ in shape or strides")
+    st = _strided_pair(where, ("k_out", "v_out"), k_out, v_out, 3)
     rows, h, d = k_out.shape
     if h != pages.h_kv or d != pages.d:
         _refuse(where, f"k_out and v_out must be [rows, {pages.h_kv}, {pages.d}]")

@@ -49,7 +49,7 @@ def test_chunk(page, sq, kv):
     go(sq, kv, 8, 2, page, seed=page + len(sq))
 
 
-@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (24, 2), (9, 1), (7, 1), (64, 1), (128, 1), (100, 1)])
+@pytest.mark.parametrize("h_q,h_kv", [(1, 1), (8, 8), (5, 1), (14, 2), (16, 1), (24, 2), (9, 1), (7, 1), (8, 1), (64, 1), (128, 1), (100, 1)])
 def test_group_sizes(h_q, h_kv):
     go([1, 1, 1], [100, 257, 33], h_q, h_kv, 32, seed=h_q)
     go([3, 17, 70], [100, 257, 70], h_q, h_kv, 32, seed=h_q + 1)
@@ -300,3 +300,135 @@ def test_a_prefix_read_back_for_packed_attention():
     kk, vv = kk.reshape(-1, 2, D)[sel], vv.reshape(-1, 2, D)[sel]
     assert np.all(np.abs(k.cpu().double().numpy() - kk) <= 2.0 ** -8 * np.abs(kk) * (1 + 2.0 ** -8))
     assert np.all(np.abs(v.cpu().double().numpy() - vv) <= 2.0 ** -8 * np.abs(vv) * (1 + 2.0 ** -8))
+
+
+# --------------------------------------------------------------- what else a caller may do --
+
+def test_a_scale_of_the_queries_applies():
+    sq = [1, 3]
+    c, q, cu = Paged4([200, 90], 2, 16, seed=17), queries(4, 8, 18), cu_of(sq)
+    ref = c.reference((q.float() * 0.5).to(torch.bfloat16), cu, 1 / math.sqrt(D))     # (exact: a power of two)
+    check(*run4(c, q, cu, 8, descale_q=0.5), ref, P_TYPE)
+
+
+@pytest.mark.parametrize("max_q", [1, 4, 40])
+def test_pages_that_sequences_share(max_q):
+    """Five requests over one prefix of 10 pages, and a page that stands twice in one table."""
+    c = Paged4([300, 64, 64, 64, 64], 2, 16, seed=19)
+    c.table[1:, :10] = c.table[0, :10]
+    c.table[4, 7] = c.table[4, 2]
+    c.kv_lens[1:] = 160
+    sq = [1] * 5 if max_q < 40 else [1, 30, 1, 40, 7]
+    q, cu = queries(sum(sq), 8, 20), cu_of(sq)
+    check(*run4(c, q, cu, 8, max_q=max_q), c.reference(q, cu, 1 / math.sqrt(D)), P_TYPE)
+
+
+@pytest.mark.parametrize("max_q,max_kv", [(1, 60), (2, 500), (4, 500), (40, 60), (40, 9000)])
+def test_hundreds_of_short_sequences(max_q, max_kv):
+    rng = np.random.default_rng(max_q + max_kv)
+    sq = [int(x) for x in rng.integers(0, 4, 500)]
+    kv = [int(x) for x in rng.integers(0, 60, 500)]
+    sq[300], kv[300] = (3, 400) if max_q < 40 else (150, 480)
+    go(sq, kv, 8, 2, 16, seed=7, max_q=max_q, max_kv=max_kv)
+
+
+@pytest.mark.parametrize("page,h_q,h_kv", [(1024, 8, 1), (65536, 4, 2), (16, 32, 8)])
+def test_pages_of_any_size(page, h_q, h_kv):
+    go([1, 2, 1], [1500, 700, 64], h_q, h_kv, page, seed=page)
+    go([50, 2, 1], [1500, 700, 64], h_q, h_kv, page, seed=page)
+
+
+@pytest.mark.parametrize("max_q", [1, 3, 100])
+def test_repeated_calls_give_the_same_bits(max_q):
+    sq = [1, 1, 1] if max_q < 100 else [20, 70, 1]
+    c, q, cu = Paged4([1500, 300, 64], 2, 16, seed=3), queries(sum(sq), 8, 4), cu_of(sq)
+    a, z = (run4(c, q, cu, 8, max_q=max_q) for _ in range(2))
+    assert torch.equal(a[0], z[0]) and torch.equal(a[1], z[1]) and a[2] == z[2]
+
+
+@pytest.mark.parametrize("S", [0, 2])
+@pytest.mark.parametrize("cu", [[0, 5, 3, 8], [4, 9, 2, 12], [0, 200, 10, 250], [-5, 7, 1 << 20, 3], [0, 0, 0, 0]])
+@pytest.mark.parametrize("max_q", [1, 4, 100])
+def test_offsets_that_decrease_touch_nothing_outside(cu, S, max_q):
+    """Rows are undefined then, but every write stays inside the buffers and every wait ends."""
+    c, total = Paged4([500, 300, 64], 2, 16, seed=6), 260
+    plan = b.sdpa_paged_plan(3, 8, 2, D, "e2m1", max_q, total, 500, force_splits=S)
+    ws = torch.empty(max(16, plan.workspace_bytes) + 4096, dtype=torch.uint8, device="cuda")
+    ws.fill_(0x5A)
+    out = torch.full((total + 8, 8, D), 7.0, device="cuda")
+    b.sdpa_paged(plan, total, queries(total, 8, 7).cuda(), c.pages(), c.table.cuda(), c.kv_lens.cuda(),
+                 torch.tensor(cu, dtype=torch.int32, device="cuda"), None, f32(c.dk), f32(c.dv), 0.1, "f32", 1.0, out, None, None, ws)
+    torch.cuda.synchronize()
+    status_clear()
+    assert torch.all(out[total:] == 7.0) and torch.all(ws[-4096:] == 0x5A)
+
+
+def test_calls_on_two_streams_at_once():
+    """Four calls of different kinds in flight together, five times over, each with a workspace of its own."""
+    cases, state = [], []
+    for i, sq in enumerate(([1] * 12, [4] * 5, [90, 200, 1], [1, 1])):
+        kv = [int(x) for x in np.random.default_rng(i).integers(max(sq), 2500, len(sq))]
+        c, q, cu = Paged4(kv, 2, 32, seed=30 + i), queries(sum(sq), 8, 40 + i), cu_of(sq)
+        plan = b.sdpa_paged_plan(len(sq), 8, 2, D, "e2m1", max(sq), sum(sq), max(kv))
+        ws = torch.full((max(1, plan.workspace_bytes),), 0xFF, dtype=torch.uint8, device="cuda")
+        out, lse = torch.zeros((sum(sq), 8, D), device="cuda"), torch.zeros((sum(sq), 8), device="cuda")
+        cases.append((c, q, cu))
+        state.append((plan, sum(sq), q.cuda(), c.pages(), c.table.cuda(), c.kv_lens.cuda(), cu.cuda(), None, f32(c.dk), f32(c.dv),
+                      1 / math.sqrt(D), "f32", 1.0, out, lse, None, ws))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, s in enumerate(state):
+            b.sdpa_paged(*s, stream=streams[i & 1])
+    torch.cuda.synchronize()
+    status_clear()
+    for (c, q, cu), s in zip(cases, state):
+        check(s[13].cpu(), s[14].cpu(), None, c.reference(q, cu, 1 / math.sqrt(D)), P_TYPE)
+
+
+def test_graphs_of_two_plans_share_a_workspace():
+    """Decode and chunk captured apart over one workspace of the larger size, replayed in turn with other lengths."""
+    c = Paged4([900, 700, 64], 2, 16, seed=50)
+    plans = [b.sdpa_paged_plan(3, 8, 2, D, "e2m1", n, 3 * n, 1000) for n in (1, 50)]
+    ws = torch.full((max(p.workspace_bytes for p in plans),), 0xFF, dtype=torch.uint8, device="cuda")
+    pages, table, lens = c.pages(), c.table.cuda(), torch.zeros(3, dtype=torch.int32, device="cuda")
+    graphs = []
+    for p, n in zip(plans, (1, 50)):
+        q = queries(3 * n, 8, 60 + n)
+        dev, cu, out = q.cuda(), cu_of([n] * 3).cuda(), torch.zeros((3 * n, 8, D), device="cuda")
+        args = (p, 3 * n, dev, pages, table, lens, cu, None, f32(c.dk), f32(c.dv), 1 / math.sqrt(D), "f32", 1.0, out, None, None, ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.sdpa_paged(*args)
+        graphs.append((g, args, q, n, out))
+    for kv in ([900, 700, 64], [60, 650, 50], [800, 51, 64]):
+        lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        c.kv_lens = torch.tensor(kv, dtype=torch.int32)
+        for g, _, q, n, out in graphs + graphs[::-1]:
+            g.replay()
+            torch.cuda.synchronize()
+            status_clear()
+            check(out.cpu(), None, None, c.reference(q, cu_of([n] * 3), 1 / math.sqrt(D)), P_TYPE)
+
+
+def test_codes_behind_32_bit_offsets():
+    """Pages of codes and scales that lie more than 2^32 bytes from their bases."""
+    page, stride = 16, (1 << 31) + 4096
+    big = torch.zeros(3 * stride, dtype=torch.uint8, device="cuda")
+    view = lambda last, at: big.as_strided((3, page, 1, last), (stride, last, page * last, 1), at)
+    k, v, ks, vs = view(D // 2, 0), view(D // 2, 1024), view(8, 2048), view(8, 2048 + 128)
+    c = Paged4([40], 1, page, seed=70, spare=0)
+    for dst, src in ((k, c.k), (v, c.v), (ks, c.ks), (vs, c.vs)):
+        dst.copy_(src)
+    for sq in ([2], [30]):
+        q, cu = queries(sum(sq), 4, 71), cu_of(sq)
+        plan = b.sdpa_paged_plan(1, 4, 1, D, "e2m1", sq[0], sq[0], 40, force_splits=1)
+        out = torch.empty((sq[0], 4, D), device="cuda")
+        b.sdpa_paged(plan, sq[0], q.cuda(), b.kv_pages(k, v, ks, vs), c.table.cuda(), c.kv_lens.cuda(), cu.cuda(), None, f32(c.dk), f32(c.dv),
+                     0.1, "f32", 1.0, out)
+        torch.cuda.synchronize()
+        status_clear()
+        check(out.cpu(), None, None, c.reference(q, cu, 0.1), P_TYPE)
+    del big, k, v, ks, vs
+    torch.cuda.empty_cache()

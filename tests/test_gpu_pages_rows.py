@@ -268,7 +268,7 @@ def test_read(dtype, rows, h_kv, page, layout):
 
 
 def test_rows_behind_32_bit_offsets():
-    """Pages of codes that lie more than 2^32 bytes from the base; a table of rotations of more than 2^31 entries is read at its end."""
+    """Pages of codes that lie more than 2^32 bytes from the base."""
     page, stride = 16, (1 << 31) + 4096
     big = torch.zeros(3 * stride, dtype=torch.uint8, device="cuda")
     k = big.as_strided((3, page, 1, D // 2), (stride, D, D, 1))
@@ -287,4 +287,21 @@ def test_rows_behind_32_bit_offsets():
         c, s = held(x[:, i:i + 1].float().numpy(), 0.004, "e2m1")
         assert torch.equal(out[i].cpu(), bf16_bytes(op.four_bit_decode(c.numpy(), s.numpy()).astype(np.float32) * np.float32(0.004)))
     del big, k, v, ks, vs
+    torch.cuda.empty_cache()
+
+
+def test_positions_behind_32_bit_offsets():
+    """A table of rotations of more than 2^31 entries, read at its end: a quarter turn there takes a head's halves into one another."""
+    n = (1 << 24) + 6
+    cs = torch.zeros((n, D), device="cuda")
+    cs[n - 1, D // 2:] = 1
+    x = torch.randn((1, 3, D), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    k, v = caches("bf16", 1, 16, 1, device="cuda")[:2]
+    dev, out = x.cuda(), torch.zeros((1, 1, D), dtype=torch.bfloat16, device="cuda")
+    b.kv_pages_write_rotary(b.kv_pages(k, v), dev[:, :1], dev[:, 1:2], dev[:, 2:], torch.tensor([n - 1], dtype=torch.int32, device="cuda"), cs,
+                            torch.tensor([3], device="cuda"), out)
+    torch.cuda.synchronize()
+    turn = lambda y: torch.cat([-y[..., D // 2:], y[..., :D // 2]], -1)
+    assert torch.equal(out.cpu(), turn(x[:, :1])) and torch.equal(k[0, 3].cpu(), turn(x[0, 1:2])) and torch.equal(v[0, 3].cpu(), x[0, 2:])
+    del cs
     torch.cuda.empty_cache()
