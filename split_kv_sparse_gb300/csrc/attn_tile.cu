@@ -191,19 +191,20 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
     float m_run = -INFINITY, l = 0.f, lc = 0.f;
     bool bad = false;
     float esc = unit, row_sc = sc;     // (4 bits: of this row of the job, with what undoes its power of two)
-    if constexpr (kF4) {
-      if (tiles > 0) bad = !wait_for<kPoll>(bar(B_Q16), ends & 1, limit);
-      row_sc = sc * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
-      if (raw_ok) esc = row_sc = fmaxf(row_sc, 1.17549435e-38f);   // (0 times a masked score's infinity would be a NaN)
-    }
 #pragma unroll 1
-    for (int u = 0; u < (kF4 && bad ? 0 : cnt); ++u) {
+    for (int u = 0; u < cnt; ++u) {
       const int t = one ? 2 * u + i : u;
       if (!wait_for<kPoll>(bar(B_S0 + i), (su + u) & 1, limit)) {
         bad = true;
         break;
       }
       tc_fence_after();
+      if (kF4 && u == 0) {
+        // (written before the scores' product was issued. No wait for Q's own barrier here: behind a long epilogue it may be two jobs
+        // further on, and its parity would say nothing)
+        row_sc = sc * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
+        if (raw_ok) esc = row_sc = fmaxf(row_sc, 1.17549435e-38f);   // (0 times a masked score's infinity would be a NaN)
+      }
       uint32_t r[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, r[c]);

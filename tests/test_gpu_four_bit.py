@@ -332,6 +332,19 @@ def test_hundreds_of_short_sequences(max_q, max_kv):
     go(sq, kv, 8, 2, 16, seed=7, max_q=max_q, max_kv=max_kv)
 
 
+@pytest.mark.parametrize("max_kv", [200, 9000])
+@pytest.mark.parametrize("S", [0, 1])
+@pytest.mark.parametrize("each", [[(64, 200), (3, 40), (2, 9)], [(64, 64), (40, 50), (1, 1), (9, 130)], [(50, 90), (33, 33)]])
+def test_short_jobs_behind_long_ones(each, S, max_kv):
+    """Several jobs a CTA, those of one key tile and one or two row blocks behind jobs with rows to write for long: what a job's
+    rows were scaled by has to be its own."""
+    sq, kv = ([x[k] for x in each] * 40 for k in (0, 1))
+    c, q, cu = Paged4(kv, 8, 16, seed=len(each)), queries(sum(sq), 32, 21), cu_of(sq)
+    x = (q.float() * 2.0 ** torch.randint(-12, 12, (len(q), 32, 1), generator=torch.Generator().manual_seed(1))).to(torch.bfloat16)
+    x /= x.float().abs().amax(-1, keepdim=True).clamp(min=1).to(torch.bfloat16)
+    check(*run4(c, x, cu, 32, force_splits=S, max_kv=max_kv), c.reference(x, cu, 1 / math.sqrt(D)), P_TYPE)
+
+
 @pytest.mark.parametrize("page,h_q,h_kv", [(1024, 8, 1), (65536, 4, 2), (16, 32, 8)])
 def test_pages_of_any_size(page, h_q, h_kv):
     go([1, 2, 1], [1500, 700, 64], h_q, h_kv, page, seed=page)
