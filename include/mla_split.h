@@ -514,7 +514,7 @@ MLA_API int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_
  *   k_out  NULL, or the rotated rows of k in bf16 (for sdpa_prompt); may be k_new itself with its
  *      strides. Outputs that overlap inputs or each other in another way are undefined.
  * Pointers 16-byte aligned (slot_map 8, positions and scalars 4), strides positive multiples of 16
- * bytes. rows >= 0. */
+ * bytes. rows >= 0; at most 2^24 heads of q and of pages, 2^35 rows x heads. */
 MLA_API int kv_pages_write_rotary(const kv_pages_t* pages, int64_t rows, int h_q, const void* q,
                    int64_t q_token_stride, int64_t q_head_stride, const void* k_new, const void* v_new,
                    int64_t token_stride, int64_t head_stride, const int32_t* positions, const float* cos_sin,

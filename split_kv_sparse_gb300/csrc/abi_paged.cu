@@ -13,6 +13,7 @@ namespace {
 using skv::ptr_aligned;
 
 constexpr int kDim = 128;
+constexpr int kMaxHeads = 1 << 24;   // of the append that rotates, the read-back and 4-bit pages: heads are counted in int32
 
 uint64_t round_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
 
@@ -58,6 +59,7 @@ int check_pages(const kv_pages_t* p) {
     if (p->k_scales == nullptr || p->v_scales == nullptr || !ptr_aligned(p->k_scales, 16) || !ptr_aligned(p->v_scales, 16))
       return MLA_ERR_INVALID_ARG;
     if (!stride_ok(p->scale_page_stride, 1) || !stride_ok(p->scale_head_stride, 1)) return MLA_ERR_INVALID_ARG;
+    if (p->h_kv > kMaxHeads) return MLA_ERR_INVALID_ARG;
   }
   return MLA_OK;
 }
@@ -314,7 +316,7 @@ int kv_pages_write_rotary(const kv_pages_t* pages, int64_t rows, int h_q, const 
                           int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream) {
   int st = check_pages(pages);
   if (st != MLA_OK) return st;
-  if (rows < 0 || rows > 0x7FFFFFFFll || h_q < 0) return MLA_ERR_INVALID_ARG;
+  if (rows < 0 || rows > 0x7FFFFFFFll || h_q < 0 || h_q > kMaxHeads || pages->h_kv > kMaxHeads) return MLA_ERR_INVALID_ARG;
   if (rotary_dim < 32 || rotary_dim > kDim || rotary_dim % 32 != 0) return MLA_ERR_UNSUPPORTED;
   if (interleaved != 0 && interleaved != 1) return MLA_ERR_INVALID_ARG;
   if (num_positions < 1 || num_positions > (int64_t{1} << 31)) return MLA_ERR_INVALID_ARG;
@@ -372,7 +374,7 @@ int kv_pages_read(const kv_pages_t* pages, int64_t rows, const int64_t* slot_map
                   void* k_out, void* v_out, int64_t token_stride, int64_t head_stride, void* stream) {
   int st = check_pages(pages);
   if (st != MLA_OK) return st;
-  if (rows < 0 || rows > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (rows < 0 || rows > 0x7FFFFFFFll || pages->h_kv > kMaxHeads) return MLA_ERR_INVALID_ARG;
   if (rows == 0) return MLA_OK;
   if (k_out == nullptr || v_out == nullptr || slot_map == nullptr) return MLA_ERR_INVALID_ARG;
   if (!ptr_aligned(k_out, 16) || !ptr_aligned(v_out, 16) || !ptr_aligned(slot_map, 8)) return MLA_ERR_INVALID_ARG;
@@ -528,7 +530,7 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     return st;
   if ((st = encode(&tk, pages->k)) != MLA_OK || (st = encode(&tv, pages->v)) != MLA_OK) return st;
   if (four && rows16 && ((st = encode_scales(&tks, pages, pages->k_scales, box)) != MLA_OK ||
-               (st = encode_scales(&tvs, pages, pages->v_scales, box)) != MLA_OK))
+                         (st = encode_scales(&tvs, pages, pages->v_scales, box)) != MLA_OK))
     return st;
   const int64_t unsplit = tiles_bound(total_q, a.batch, job_tokens(plan->row_kernel, a.group)) * a.h_kv;
   int64_t grid = unsplit * a.num_splits;
@@ -550,8 +552,8 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     // the units of all jobs have to add up to an int32
     const int64_t tiles = std::min<int64_t>((static_cast<int64_t>(table_width) << a.page_shift) / 128, 1 << 24);
     a.side = heads_side(a.num_sms, a.h_kv);
-    // (4 bits: 256 keys are a block for each of a CTA's four warps; cut at 128, two of them idle at a piece's end: 8 ragged sequences
-    // 28.4 -> 26.8 us, 96 149 -> 145)
+    // (4 bits: 256 keys are a block for each of a CTA's four warps; cut at 128, two of them idle at a piece's end: 8 ragged
+    // sequences 28.4 us, 26.8 so, 96 149 and 145)
     if (four && rows16) a.share_shift = 1;
     while (unsplit / a.side * (2 * (tiles >> a.share_shift) + 32) > 0x7FFFFFFFll)
       if (++a.share_shift > 16) return MLA_ERR_UNSUPPORTED;   // (four million jobs)

@@ -77,8 +77,8 @@ __global__ void __launch_bounds__(kThreads, kCache == 1 && !kQ8 ? 4 : 3) pages_a
   float4(&mine)[4][8] = angles[threadIdx.x >> 5];                  // cosines of this thread's first and last four pairs, sines
   if (kTurn != 0 && turning && sub < 2) {
     const float* row = a.cos_sin + pos * a.rot + 8 * t + (sub ? a.rot >> 1 : 0);
-    mine[2 * sub][t] = __ldg(reinterpret_cast<const float4*>(row));
-    mine[2 * sub + 1][t] = __ldg(reinterpret_cast<const float4*>(row) + 1);
+    mine[2 * sub][t] = reinterpret_cast<const float4*>(row)[0];
+    mine[2 * sub + 1][t] = reinterpret_cast<const float4*>(row)[1];
   }
   __syncwarp();
   auto pair = [](float& u, float& v, float cs, float sn) {
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, kCache == 1 && !kQ8 ? 4 : 3) pages_a
   }
 }
 
-// The way back: 16 dims a thread, code x scale x descale rounded once to bf16 (a bf16 cache's bits as they are).
+// The way back: 16 dims a thread, code x scale (exact) x descale in fp32, rounded to bf16 (a bf16 cache's bits as they are).
 template <int kCache, int kFlight>
 __global__ void __launch_bounds__(kThreads) pages_read_kernel(const PagesAppendArgs a) {
   const int lane = threadIdx.x & 31, p = lane & 7;
@@ -213,15 +213,15 @@ __global__ void __launch_bounds__(kThreads) pages_read_kernel(const PagesAppendA
     const int64_t src = page * a.page_stride + at * a.row_stride + g * a.cache_head_stride;
     if constexpr (kCache == 1) {
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + src + 16 * p);
-      x[k][0] = __ldg(from);
-      x[k][1] = __ldg(from + 1);
+      x[k][0] = from[0];
+      x[k][1] = from[1];
     } else if constexpr (kCache == 2) {
-      x[k][0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + src + 16 * p));
+      x[k][0] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(cache) + src + 16 * p);
     } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + src + 8 * p));
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + src + 8 * p);
       x[k][0].x = v.x;
       x[k][0].y = v.y;
-      scale[k] = __ldg((is_k ? a.k_scales : a.v_scales) + page * a.scale_page_stride + g * a.scale_head_stride + 8 * at + p);
+      scale[k] = (is_k ? a.k_scales : a.v_scales)[page * a.scale_page_stride + g * a.scale_head_stride + 8 * at + p];
     }
   }
   const float dk = a.descale_k ? *a.descale_k : 1.f, dv = a.descale_v ? *a.descale_v : 1.f;

@@ -215,3 +215,14 @@ def test_rotation_is_a_complex_product(inter, R):
     assert np.allclose(pair(y), pair(x) * np.exp(1j * a[[7, 12, 0]])[:, None])
     assert np.allclose(op.rotate(y, cs, [n, n, n], inter), op.rotate(x, cs, [7 + n, 12 + n, n], inter))
     assert np.array_equal(op.rotate(x, cs, [-1, 2 * n, 1 << 30], inter), x)
+
+
+def test_head_counts_beyond_int32_arithmetic():
+    most, p = 1 << 24, pages(h_kv=(1 << 24) + 1)
+    assert status_of("kv_pages_write", ctypes.byref(p), 1, FAKE, FAKE, 256, 128, FAKE, None, None, None) == 1
+    assert status_of("kv_pages_read", ctypes.byref(p), 1, FAKE, None, None, FAKE, FAKE, 256, 128, None) == 1
+    for h_q, h_kv in ((most + 1, 2), ((1 << 31) - 1, 2), (4, most + 1), (4, (1 << 31) - 1)):
+        p = pages(dtype=1, page_stride=4096, row_stride=256, head_stride=128, h_kv=h_kv)
+        assert status_of("kv_pages_write_rotary", *(ROTARY | dict(p=ctypes.byref(p), h_q=h_q)).values()) == 1
+        if h_kv > most:
+            assert status_of("kv_pages_read", ctypes.byref(p), 1, FAKE, None, None, FAKE, FAKE, 256, 128, None) == 1
