@@ -373,6 +373,9 @@ def _strided(where: str, name: str, x, dims: int):
 
 def _strided_pair(where: str, names, x, y, dims: int):
     """The strides of two tensors that have to share shape and strides."""
+    st, shape = x.stride(), x.shape
+    if len(shape) == dims and 1 not in shape and st[-1] == 1 and y.stride() == st and y.shape == shape:
+        return st
     st = _strided(where, names[0], x, dims)
     if y.shape != x.shape or (y.stride() != x.stride() and _strided(where, names[1], y, dims) != st):
         _refuse(where, f"{names[0]} and {names[1]} differ in shape or strides")
@@ -484,18 +487,28 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
     (bfloat16, or None). cos_sin is float32 [num_positions, rotary_dim], cosines then sines."""
     where, t = "kv_pages_write_rotary", _t()
     dev = _device(where)
-    BF = t.BF
+    BF, F32 = t.BF, t.F32
     try:   # (the checks of _dev in one go: the call of few rows is the host's time)
         ok = (k_new.get_device() == dev and v_new.get_device() == dev and positions.get_device() == dev
               and cos_sin.get_device() == dev and slot_map.get_device() == dev and k_new.dtype is BF and v_new.dtype is BF
-              and positions.dtype is t.I32 and cos_sin.dtype is t.F32 and slot_map.dtype is t.I64
-              and positions.is_contiguous() and cos_sin.is_contiguous() and slot_map.is_contiguous())
+              and positions.dtype is t.I32 and cos_sin.dtype is F32 and slot_map.dtype is t.I64
+              and positions.is_contiguous() and cos_sin.is_contiguous() and slot_map.is_contiguous()
+              and (q is None or (q.get_device() == dev and q.dtype is BF))
+              and (q_out is None or (q_out.get_device() == dev and q_out.dtype in t.sdpa))
+              and (descale_q is None or (descale_q.get_device() == dev and descale_q.dtype is F32 and descale_q.numel() == 1))
+              and (descale_k is None or (descale_k.get_device() == dev and descale_k.dtype is F32 and descale_k.numel() == 1))
+              and (descale_v is None or (descale_v.get_device() == dev and descale_v.dtype is F32 and descale_v.numel() == 1)))
     except AttributeError:
         ok = False
     if not ok:
         for n, x, dt, c in (("k_new", k_new, t.bf16, False), ("v_new", v_new, t.bf16, False), ("positions", positions, t.i32, True),
                             ("cos_sin", cos_sin, t.f32, True), ("slot_map", slot_map, t.i64, True)):
             _dev(where, n, x, dt, dev, contiguous=c)
+        for n, x, dt in (("q", q, t.bf16), ("q_out", q_out, t.data)):
+            if x is not None:
+                _dev(where, n, x, dt, dev, contiguous=False)
+        for n, x in (("descale_q", descale_q), ("descale_k", descale_k), ("descale_v", descale_v)):
+            _opt(where, n, x, t.f32, dev, 1)
     st = _strided_pair(where, ("k_new", "v_new"), k_new, v_new, 3)
     shape = k_new.shape
     rows, h, d = shape
@@ -508,19 +521,21 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
         _refuse(where, f"positions and slot_map must have {rows} elements")
     h_q, qp, qs, qo, qo_dt, os_ = 0, None, (0, 0), None, SDPA_BF16, (0, 0)
     if q is not None:
-        qp = _dev(where, "q", q, t.bf16, dev, contiguous=False)
-        qs = _strided(where, "q", q, 3)
-        q_shape = q.shape
+        qp = q.data_ptr()
+        q_shape, qs = q.shape, q.stride()
+        if len(q_shape) != 3 or 1 in q_shape or qs[2] != 1:
+            qs = _strided(where, "q", q, 3)
         h_q = q_shape[1]
         if q_shape[0] != rows or q_shape[2] != d:
             _refuse(where, f"q must be [{rows}, h_q, {d}]")
         if q_out is None:
             qo, os_ = qp, qs
         else:
-            qo = _dev(where, "q_out", q_out, t.data, dev, contiguous=False)
-            os_, qo_dt = _strided(where, "q_out", q_out, 3), t.sdpa[q_out.dtype]
+            qo, qo_dt, os_ = q_out.data_ptr(), t.sdpa[q_out.dtype], q_out.stride()
             if q_out.shape != q_shape:
                 _refuse(where, "q_out must have q's shape")
+            if 1 in q_shape or os_[2] != 1:
+                os_ = _strided(where, "q_out", q_out, 3)
     elif q_out is not None:
         _refuse(where, "q_out without q")
     ko, ks = None, (0, 0)
@@ -529,9 +544,9 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
         ks = _strided(where, "k_out", k_out, 3)
         if k_out.shape != shape:
             _refuse(where, "k_out must have k_new's shape")
-    dq = None if descale_q is None else _dev(where, "descale_q", descale_q, t.f32, dev, 1)
-    dk = None if descale_k is None else _dev(where, "descale_k", descale_k, t.f32, dev, 1)
-    dv = None if descale_v is None else _dev(where, "descale_v", descale_v, t.f32, dev, 1)
+    dq = None if descale_q is None else descale_q.data_ptr()
+    dk = None if descale_k is None else descale_k.data_ptr()
+    dv = None if descale_v is None else descale_v.data_ptr()
     status = (_lib or lib()).kv_pages_write_rotary(
         _pages(where, pages, dev), rows, h_q, qp, qs[0], qs[1], k_new.data_ptr(), v_new.data_ptr(), st[0], st[1],
         positions.data_ptr(), cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_map.data_ptr(), dq, dk, dv, qo_dt, qo,

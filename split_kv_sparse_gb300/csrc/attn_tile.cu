@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr int kItemBytes = kF4 ? kCodeBytes + kTile * 8 : kTile * kD * (kF8 ? 1 : 2);   // one K or V tile
   static constexpr int kHalves = kF8 ? 1 : 2;            // 128-byte column blocks of a row of Q (bf16: of K and V)
   static constexpr int kKSlots = kF8 ? 4 : 3;            // K(t) in slot t % kKSlots of its ring, V(t) in t % kVSlots
-  static constexpr int kVSlots = kF8 ? 4 : kF4 ? 0 : 2;  // (4 bits: both in one ring, K(t) before V(t))
+  static constexpr int kVSlots = kF8 ? 4 : kF4 ? 1 : 2;  // (4 bits: none, V lies in the ring of K, in the order item_of)
   static constexpr int kWideBytes = kF8 || kF4 ? kTile * kD * 2 : 0;   // a tile in f16
   static constexpr int kOffQ = 0;
   static constexpr int kOffK16 = 2 * kQBytes;
