@@ -382,6 +382,33 @@ def _strided_pair(where: str, names, x, y, dims: int):
     return st
 
 
+def _rows(where: str, pages: KvPages, names, x, y, slot_map, descale_k, descale_v, dev: int):
+    """What kv_pages_write and kv_pages_read take of their tensors: addresses, strides, the row count."""
+    t = _t()
+    F32 = t.F32
+    try:   # (the checks of _dev in one go: the call of few rows is the host's time)
+        ok = (x.get_device() == dev and y.get_device() == dev and slot_map.get_device() == dev and x.dtype is t.BF and y.dtype is t.BF
+              and slot_map.dtype is t.I64 and slot_map.is_contiguous()
+              and (descale_k is None or (descale_k.get_device() == dev and descale_k.dtype is F32 and descale_k.numel() == 1))
+              and (descale_v is None or (descale_v.get_device() == dev and descale_v.dtype is F32 and descale_v.numel() == 1)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        for n, z in zip(names, (x, y)):
+            _dev(where, n, z, t.bf16, dev, contiguous=False)
+        _dev(where, "slot_map", slot_map, t.i64, dev)
+        _opt(where, "descale_k", descale_k, t.f32, dev, 1)
+        _opt(where, "descale_v", descale_v, t.f32, dev, 1)
+    st = _strided_pair(where, names, x, y, 3)
+    rows, h, d = x.shape
+    if h != pages.h_kv or d != pages.d:
+        _refuse(where, f"{names[0]} and {names[1]} must be [rows, {pages.h_kv}, {pages.d}]")
+    if slot_map.numel() < rows:
+        _refuse(where, f"slot_map has {slot_map.numel()} elements, fewer than {rows}")
+    return (rows, x.data_ptr(), y.data_ptr(), st, slot_map.data_ptr(), None if descale_k is None else descale_k.data_ptr(),
+            None if descale_v is None else descale_v.data_ptr())
+
+
 def _table(where: str, block_table, batch: int, dev: int):
     p = _dev(where, "block_table", block_table, _t().i32, dev, 1)
     if block_table.dim() != 2 or block_table.shape[0] < batch:
@@ -466,18 +493,12 @@ def kv_pages_map(page_size: int, held_lens, new_lens, cu_seqlens_q, total_q: int
 
 def kv_pages_write(pages: KvPages, k_new, v_new, slot_map, descale_k=None, descale_v=None, stream=None):
     """Rows of k_new and v_new (bfloat16 [rows, h_kv, d], any strides over a contiguous d) into their slots."""
-    where, t = "kv_pages_write", _t()
+    where = "kv_pages_write"
     dev = _device(where)
-    k = _dev(where, "k_new", k_new, t.bf16, dev, contiguous=False)
-    v = _dev(where, "v_new", v_new, t.bf16, dev, contiguous=False)
-    st = _strided_pair(where, ("k_new", "v_new"), k_new, v_new, 3)
-    rows, h, d = k_new.shape
-    if h != pages.h_kv or d != pages.d:
-        _refuse(where, f"k_new and v_new must be [rows, {pages.h_kv}, {pages.d}]")
-    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
-    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
-    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
-    _check(lib().kv_pages_write(_pages(where, pages, dev), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev)), where)
+    rows, k, v, st, slots, dk, dv = _rows(where, pages, ("k_new", "v_new"), k_new, v_new, slot_map, descale_k, descale_v, dev)
+    status = (_lib or lib()).kv_pages_write(_pages(where, pages, dev), rows, k, v, st[0], st[1], slots, dk, dv, _on(stream, dev))
+    if status:
+        raise SplitKVError(status, where)
 
 
 def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, slot_map, q_out=None, k_out=None, *,
@@ -557,18 +578,12 @@ def kv_pages_write_rotary(pages: KvPages, q, k_new, v_new, positions, cos_sin, s
 
 def kv_pages_read(pages: KvPages, slot_map, k_out, v_out, descale_k=None, descale_v=None, stream=None):
     """Rows of a cache of any type into k_out and v_out (bfloat16 [rows, h_kv, d], any strides over a contiguous d)."""
-    where, t = "kv_pages_read", _t()
+    where = "kv_pages_read"
     dev = _device(where)
-    k = _dev(where, "k_out", k_out, t.bf16, dev, contiguous=False)
-    v = _dev(where, "v_out", v_out, t.bf16, dev, contiguous=False)
-    st = _strided_pair(where, ("k_out", "v_out"), k_out, v_out, 3)
-    rows, h, d = k_out.shape
-    if h != pages.h_kv or d != pages.d:
-        _refuse(where, f"k_out and v_out must be [rows, {pages.h_kv}, {pages.d}]")
-    slots = _dev(where, "slot_map", slot_map, t.i64, dev, rows)
-    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
-    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
-    _check(lib().kv_pages_read(_pages(where, pages, dev), rows, slots, dk, dv, k, v, st[0], st[1], _on(stream, dev)), where)
+    rows, k, v, st, slots, dk, dv = _rows(where, pages, ("k_out", "v_out"), k_out, v_out, slot_map, descale_k, descale_v, dev)
+    status = (_lib or lib()).kv_pages_read(_pages(where, pages, dev), rows, slots, dk, dv, k, v, st[0], st[1], _on(stream, dev))
+    if status:
+        raise SplitKVError(status, where)
 
 
 def sdpa_paged_plan(batch: int, h_q: int, h_kv: int, d: int, dtype, max_q_per_seq: int, total_q_max: int, max_kv: int,
