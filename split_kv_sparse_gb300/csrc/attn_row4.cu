@@ -7,7 +7,8 @@
 //
 // Two CTAs an SM, each with four warps that compute and four that load: every computing warp walks key blocks (64 keys, every
 // fourth of a job's) of its own with a running maximum and a sum of its own, merged at a job's end; a loading warp fills
-// its ring by TMA, page by page, ahead into the next job. Equal shares of the batch's key tiles (AttnShares).
+// its ring by TMA, page by page, ahead into the next job. Equal shares of the batch's key tiles (AttnShares). 4 x 100,000 to
+// 131,072 keys, 64 / 8 heads: 102 us, 5.1 TB/s (91 us of loads alone); 96 x 100 to 12,000, 32 / 8 heads, pages of 16: 144 us, 4.6 TB/s.
 //
 // Widening: a byte of two e2m1 codes is one conversion to an f16 pair, times its e4m3 scale in f16: exact (6
 // significant bits, 2^-10 to 2688). The order of the contracted dims of S is free as long as Q has the same, so a lane takes
@@ -60,9 +61,9 @@ __device__ __forceinline__ int perm8(int i) { return static_cast<int>((0x6574213
 __device__ __forceinline__ void mma_f16_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-               "{%0, %1, %2, %3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
@@ -454,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
   }
 
   // ---- merge of the four warps' results
-  // A warp's rows x 128 fp32 go through the stage of its last block. Row r's 16-byte piece c lies at c ^ c / 8 ^ r / 2 within its eight: no bank conflicts on either side.
+  // A warp's rows x 128 fp32 go through the stage of its last block. Row r's 16-byte piece c lies at c ^ c / 8 ^ r / 2 within its
+  // eight: no bank conflicts on either side.
   auto piece_at = [](int row, int c) { return row * 512 + (((c & 24) | ((c ^ (c >> 3) ^ ((row >> 1) & 3)) & 7)) << 4); };
   volatile int* stage_of = reinterpret_cast<volatile int*>(smem + kOffStage);
   const int last = (loaded + max(cnt, 1) - 1) % kStages;
@@ -472,11 +474,11 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
       const int r = 8 * n + 2 * q4 + k;
       if (cnt > 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)                          // dims 16 quad + 8 h ..
+        for (int h = 0; h < 2; ++h)                        // dims 16 quad + 8 h ..
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float4*>(mine + piece_at(r, 4 * quad + 2 * h + j)) =
-              make_float4(o[4 * j][n][2 * h + k], o[4 * j + 1][n][2 * h + k], o[4 * j + 2][n][2 * h + k], o[4 * j + 3][n][2 * h + k]);
+          for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<float4*>(mine + piece_at(r, 4 * quad + 2 * h + j)) =
+                make_float4(o[4 * j][n][2 * h + k], o[4 * j + 1][n][2 * h + k], o[4 * j + 2][n][2 * h + k], o[4 * j + 3][n][2 * h + k]);
       }
       if (quad == 0) stats[warp * 16 + r] = make_float2(m[n][k], z);
     }

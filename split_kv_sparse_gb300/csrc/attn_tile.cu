@@ -15,10 +15,11 @@
 //   warps 9, 11     TMA: Q and the K tiles, the V tiles, each into a ring of slots, page by page;
 //                   warp 11 also looks for the CTA's jobs and (bf16) clears the V rows past
 //                   a sequence's end (0 * NaN would reach a result).
-//   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0.
+//   warps 12-15     e4m3: convert each V tile to f16 (exact), rows past the end to 0. 4 bits: convert Q's rows, and
+//                   widen each K and V tile, to f16.
 // TMEM: S (128 columns, one buffer for both streams: a stream's scores leave it for
 // registers as soon as they are there), P_0, P_1 (64 each), O_0, O_1 (128 each).
-// P is rounded to V's MMA type (bf16; f16 for e4m3 V, whose values f16 holds exactly);
+// P is rounded to V's MMA type (bf16; f16 for V in e4m3 or 4 bits, whose values f16 holds exactly);
 // the sums are taken over the unrounded fp32 values. bf16 P costs 2^-8 relative a
 // term at most, as much as the rounding of a bf16 result, and also where the result is fp32 (a pair as in the 16-row kernel
 // would double the PV products of a kernel that the tensor pipe bounds).
@@ -26,6 +27,8 @@
 // of 20; 1.28 ms, 1.71 PFLOP/s, one of 500, where the power cap takes the clock to 1.55 GHz), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
 // 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
+// 4 bits: the same pace (2,048 tokens over 32,768 keys 687 us, 1.55 PFLOP/s; ragged chunks over pages of 16 367 us). Widening does not bound
+// it (694 and 357 us without), but where the roles' code lies does: the converting warps' ahead of the softmax 818 and 390 us.
 #include "attn_common.cuh"
 #include "quant.cuh"
 
