@@ -2,7 +2,7 @@
 // pages, and the way back from pages of any type to bf16 rows.
 //
 // Both kernels are copies: every byte is read and written once and HBM bounds them, latency a call of few rows. 16,001 rows of 32 + 2 x 8
-// heads into bf16: 59 us of back-to-back calls, 6.7 TB/s; 8,192 into 4 bits 48 (4.7 TB/s: the codes' arithmetic beside the loads); 20,000 rows
+// heads into bf16: 59 us of back-to-back calls, 6.7 TB/s; 8,192 into 4 bits 40 (4.5 TB/s: the codes' arithmetic beside the loads); 20,000 rows
 // of 4 bits back 17.4 (6.0 TB/s).
 #include "attn_common.cuh"
 #include "quant.cuh"
