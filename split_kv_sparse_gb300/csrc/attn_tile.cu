@@ -27,8 +27,9 @@
 // of 20; 1.28 ms, 1.71 PFLOP/s, one of 500, where the power cap takes the clock to 1.55 GHz), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
 // 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
-// 4 bits: the same pace (2,048 tokens over 32,768 keys 687 us, 1.55 PFLOP/s; ragged chunks over pages of 16 367 us). Widening does not bound
-// it (694 and 357 us without), but where the roles' code lies does: the converting warps' ahead of the softmax 818 and 390 us.
+// 4 bits: much the same (2,048 tokens over 32,768 keys 634 to 660 us, 1.6 PFLOP/s; ragged chunks over pages of 16 360 us). Widening does not
+// bound it (no gain without), the softmax and its code do: with a mask for the last keys, one for pages and a path for negative scales of their
+// own, as the other types have them, 685 and 367 us; with the converting warps' code ahead of the softmax 818 and 390.
 #include "attn_common.cuh"
 #include "quant.cuh"
 
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
   constexpr bool kF8 = C::kF8, kF4 = C::kF4;
   constexpr bool kF16 = kF8 || kF4;   // P and V are multiplied in f16
   constexpr bool kPaged = kPages > 0;
+  constexpr int kRescaleUnroll = kF4 ? 2 : 8;   // (of O's rare rescaling; 4 bits: for its code's size)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
     const int lim = live ? kv - sq + tok : kv - 1;   // last key the row sees (a dead row's result goes nowhere)
     float m_run = -INFINITY, l = 0.f, lc = 0.f;
     bool bad = false;
-    float esc = unit, row_sc = sc;     // (4 bits: of this row of the job, with what undoes its power of two)
+    float esc = unit;                  // (4 bits: of this row of the job, with what undoes its power of two; the sign is in Q)
 #pragma unroll 1
     for (int u = 0; u < cnt; ++u) {
       const int t = one ? 2 * u + i : u;
@@ -205,8 +207,8 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       if (kF4 && u == 0) {
         // (written before the scores' product was issued. No wait for Q's own barrier here: behind a long epilogue it may be two jobs
         // further on, and its parity would say nothing)
-        row_sc = sc * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
-        if (raw_ok) esc = row_sc = fmaxf(row_sc, 1.17549435e-38f);   // (0 times a masked score's infinity would be a NaN)
+        const float x = fabsf(sc) * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
+        esc = x == x ? fmaxf(x, 1.17549435e-38f) : x;   // (0 times a masked score's infinity would be a NaN)
       }
       uint32_t r[4][32];
 #pragma unroll
@@ -217,28 +219,44 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_SFREE));   // the other stream's scores may come
       float(&x)[4][32] = reinterpret_cast<float(&)[4][32]>(r);
-      if (!raw_ok) {
+      if (!kF4 && !raw_ok) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 32; ++k) x[c][k] *= row_sc;
+          for (int k = 0; k < 32; ++k) x[c][k] *= sc;
       }
       const int kmax = lim - (tile0 + t) * kTile;          // last visible key of the tile
-      if (__any_sync(0xffffffffu, kmax < kTile - 1)) {
+      if constexpr (kF4) {
+        // (both masks in one block: rarely run, but the loop's code that it parts has to be fetched around it)
+        const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
+        if (__any_sync(0xffffffffu, kmax < kTile - 1 || pages != 0xffu)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int last = kmax - 32 * c;
+            const uint32_t seen = (last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u) &
+                                  (((pages >> (2 * c)) & 1u ? 0xffffu : 0u) | ((pages >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (32 * c + k > kmax) x[c][k] = -INFINITY;
-      }
-      const uint32_t pages = !kPaged ? 0xffu : static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
-      if (pages != 0xffu) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (!((pages >> c) & 1u)) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) x[c >> 1][16 * (c & 1) + k] = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if (!((seen >> k) & 1u)) x[c][k] = -INFINITY;
           }
+        }
+      } else {
+        if (__any_sync(0xffffffffu, kmax < kTile - 1)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * c + k > kmax) x[c][k] = -INFINITY;
+        }
+        const uint32_t pages = !kPaged ? 0xffu : static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
+        if (pages != 0xffu) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (!((pages >> c) & 1u)) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[c >> 1][16 * (c & 1) + k] = -INFINITY;
+            }
+        }
       }
       const float mx = fmaxf(fmaxf(max32(x[0]), max32(x[1])), fmaxf(max32(x[2]), max32(x[3]))) * esc;
       const bool need = new_reference<kF16>(mx, m_run);
@@ -257,7 +275,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           lc *= al;
         }
         if (u > 0) {
-#pragma unroll
+#pragma unroll kRescaleUnroll
           for (int c = 0; c < 8; ++c) {
             uint32_t o[16];
             tmem_ld_32x32b_x16(to + 16 * c, o);
@@ -852,11 +870,12 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       if (!ok) give_up(a, W_T_CONVERT);
     } else if (kF4 && warp >= 12) {
       // ================================ Q bf16 -> f16; K and V codes x scales -> f16 ===
-      // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own
-      // (largest element in [2^14, 2^15)): exact down to 2^-28 of that element, smaller ones are off by 2^-39 of it at most. A
+      // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own (largest
+      // element in [2^14, 2^15)) with the sign of the scores' scale: exact down to 2^-28 of that element, smaller ones are off by 2^-39 of it at most. A
       // code times its scale is exact in f16.
       const int key = threadIdx.x - 32 * 12;
       const int r8 = key & 7, r4 = (key >> 1) & 3;
+      const float sign = (a.descale_q ? *a.descale_q : 1.f) * (a.descale_k ? *a.descale_k : 1.f) * a.scale_log2;   // of the scores' scale
       int tile_base = 0, with_tiles = 0, slot = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -882,7 +901,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           for (int k = 0; k < 4; ++k) top = max(top, max(ws[k] & 0x7fffu, (ws[k] >> 16) & 0x7fffu));
         }
         const int e = static_cast<int>(top >> 7);          // the largest element's exponent
-        const float up = __int_as_float(min(268 - e, 254) << 23);
+        const float up = copysignf(__int_as_float(min(268 - e, 254) << 23), sign);
 #pragma unroll 4
         for (int c = 0; c < 16; ++c) {
           uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * 128 * 128 + (((c & 7) ^ r8) << 4));

@@ -109,6 +109,14 @@ def test_scales_that_are_not_positive(sq, scale):
     go(sq, [200, 90], 8, 2, 16, scale=scale)
 
 
+@pytest.mark.parametrize("sq", [[1, 1], [4, 2], [2, 50]])
+def test_a_descale_that_is_not_a_number(sq):
+    c, q, cu = Paged4([200, 90], 2, 16, seed=5), queries(sum(sq), 8, 6), cu_of(sq)
+    c.dk = float("nan")
+    out, lse, _ = run4(c, q, cu, 8)
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 @pytest.mark.parametrize("sq", [[1, 1, 1], [2, 50, 1]])
 def test_queries_of_any_size(sq):
     """Q is held in f16 at a power of two of its row: rows near bf16's ends, rows of zeros, and elements far below their row's largest."""
