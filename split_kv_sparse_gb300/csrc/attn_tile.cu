@@ -27,7 +27,7 @@
 // of 20; 1.28 ms, 1.71 PFLOP/s, one of 500, where the power cap takes the clock to 1.55 GHz), the softmax's latency the e4m3 one (2,900 clocks a tile of two streams, of which the products take
 // 1,560; 7 ragged prompts: 234 us, 1.56 PFLOP/s). Between two jobs the pipe waits for the first one's epilogue
 // (2.2 us into bf16 rows, 4 us into fp32 partials).
-// 4 bits: much the same (2,048 tokens over 32,768 keys 634 to 660 us, 1.6 PFLOP/s; ragged chunks over pages of 16 360 us). Widening does not
+// 4 bits: much the same (2,048 tokens over 32,768 keys 612 to 640 us, 1.7 PFLOP/s; ragged chunks over pages of 16 358 us). Widening does not
 // bound it (no gain without), the softmax and its code do: with a mask for the last keys, one for pages and a path for negative scales of their
 // own, as the other types have them, 685 and 367 us; with the converting warps' code ahead of the softmax 818 and 390.
 #include "attn_common.cuh"
@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         const float x = fabsf(sc) * reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (ends & 1) + (one ? 0 : 128 * i) + row];
         esc = x == x ? fmaxf(x, 1.17549435e-38f) : x;   // (0 times a masked score's infinity would be a NaN)
       }
+      uint32_t pages4 = 0xffu;           // 4 bits: 16-key groups with a page (read here, not behind the scores: 655 -> 634 us)
+      if constexpr (kF4) pages4 = static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);
       uint32_t r[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, r[c]);
@@ -228,13 +230,12 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       const int kmax = lim - (tile0 + t) * kTile;          // last visible key of the tile
       if constexpr (kF4) {
         // (both masks in one block: rarely run, but the loop's code that it parts has to be fetched around it)
-        const uint32_t pages = static_cast<uint32_t>(misc[M_MASK + ((mask0 + t) & (kMaskRing - 1))]);   // 16-key groups with a page
-        if (__any_sync(0xffffffffu, kmax < kTile - 1 || pages != 0xffu)) {
+        if (__any_sync(0xffffffffu, kmax < kTile - 1 || pages4 != 0xffu)) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int last = kmax - 32 * c;
             const uint32_t seen = (last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u) &
-                                  (((pages >> (2 * c)) & 1u ? 0xffffu : 0u) | ((pages >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
+                                  (((pages4 >> (2 * c)) & 1u ? 0xffffu : 0u) | ((pages4 >> (2 * c + 1)) & 1u ? 0xffff0000u : 0u));
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (!((seen >> k) & 1u)) x[c][k] = -INFINITY;
