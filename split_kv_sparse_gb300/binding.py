@@ -603,26 +603,51 @@ def sdpa_paged(plan: SdpaPagedPlan, total_q: int, q, pages: KvPages, block_table
     where, t = "sdpa_paged", _t()
     dev = _device(where)
     batch, h_q, d = plan.batch, plan.h_q, plan.d
-    qp = _dev(where, "q", q, t.codes if plan.dtype == SDPA_E4M3 else t.bf16, dev, contiguous=False)
-    st = _strided(where, "q", q, 3)
-    n, h, x = q.shape
-    if h != h_q or x != d or n < total_q:
+    q_types = t.codes if plan.dtype == SDPA_E4M3 else t.bf16
+    od, F32, I32 = _dtype(out_dtype), t.F32, t.I32
+    try:   # (the checks of _dev in one go: a short call is the host's time)
+        ok = (q.get_device() == dev and q.dtype in q_types and block_table.get_device() == dev and block_table.dtype is I32
+              and block_table.is_contiguous() and block_table.numel() > 0 and kv_lens.get_device() == dev and kv_lens.dtype is I32
+              and kv_lens.is_contiguous() and kv_lens.numel() >= batch and cu_seqlens_q.get_device() == dev and cu_seqlens_q.dtype is I32
+              and cu_seqlens_q.is_contiguous() and cu_seqlens_q.numel() > batch
+              and (descale_q is None or (descale_q.get_device() == dev and descale_q.dtype is F32 and descale_q.numel() == 1))
+              and (descale_k is None or (descale_k.get_device() == dev and descale_k.dtype is F32 and descale_k.numel() == 1))
+              and (descale_v is None or (descale_v.get_device() == dev and descale_v.dtype is F32 and descale_v.numel() == 1))
+              and out.get_device() == dev and out.dtype in t.out[od] and out.is_contiguous() and out.numel() >= total_q * h_q * d
+              and (lse_out is None or (lse_out.get_device() == dev and lse_out.dtype is F32 and lse_out.is_contiguous()
+                                       and lse_out.numel() >= total_q * h_q))
+              and (amax_out is None or (amax_out.get_device() == dev and amax_out.dtype is F32 and amax_out.numel() == 1)))
+    except (AttributeError, KeyError):
+        ok = False
+    if not ok:
+        _dev(where, "q", q, q_types, dev, contiguous=False)
+        _table(where, block_table, batch, dev)
+        _dev(where, "kv_lens", kv_lens, t.i32, dev, batch)
+        _dev(where, "cu_seqlens_q", cu_seqlens_q, t.i32, dev, batch + 1)
+        for n, x in (("descale_q", descale_q), ("descale_k", descale_k), ("descale_v", descale_v)):
+            _opt(where, n, x, t.f32, dev, 1)
+        _outputs(where, od, out, lse_out, amax_out, total_q * h_q, d, dev)
+    q_shape, st = q.shape, q.stride()
+    if len(q_shape) != 3 or 1 in q_shape or st[2] != 1:
+        st = _strided(where, "q", q, 3)
+    if q_shape[1] != h_q or q_shape[2] != d or q_shape[0] < total_q:
         _refuse(where, f"q must be [{total_q} or more, {h_q}, {d}]")
-    table, width = _table(where, block_table, batch, dev)
-    lens = _dev(where, "kv_lens", kv_lens, t.i32, dev, batch)
-    cu = _dev(where, "cu_seqlens_q", cu_seqlens_q, t.i32, dev, batch + 1)
-    dq = _opt(where, "descale_q", descale_q, t.f32, dev, 1)
-    dk = _opt(where, "descale_k", descale_k, t.f32, dev, 1)
-    dv = _opt(where, "descale_v", descale_v, t.f32, dev, 1)
-    od = _dtype(out_dtype)
-    o, lse, amax = _outputs(where, od, out, lse_out, amax_out, total_q * h_q, d, dev)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] < batch:
+        _refuse(where, "block_table must be [batch, table_width]")
     ws = None
     if plan.workspace_bytes:
         ws = _dev(where, "workspace", workspace, t.bytes, dev)
         if workspace.nbytes < plan.workspace_bytes:
             _refuse(where, "workspace is smaller than the plan's")
-    _check(lib().sdpa_paged(ctypes.byref(plan), total_q, qp, st[0], st[1], _pages(where, pages, dev), table, width, lens, cu, dq,
-                            dk, dv, sm_scale, od, out_inv_scale, o, lse, amax, ws, _on(stream, dev)), where)
+    status = (_lib or lib()).sdpa_paged(
+        ctypes.byref(plan), total_q, q.data_ptr(), st[0], st[1], _pages(where, pages, dev), block_table.data_ptr(), shape[1],
+        kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), None if descale_q is None else descale_q.data_ptr(),
+        None if descale_k is None else descale_k.data_ptr(), None if descale_v is None else descale_v.data_ptr(), sm_scale, od,
+        out_inv_scale, out.data_ptr(), None if lse_out is None else lse_out.data_ptr(),
+        None if amax_out is None else amax_out.data_ptr(), ws, _on(stream, dev))
+    if status:
+        raise SplitKVError(status, where)
 
 
 def sdpa_prompt(batch: int, q, k, v, cu_seqlens_q, cu_seqlens_kv, descale_q, descale_k, descale_v, sm_scale: float,
