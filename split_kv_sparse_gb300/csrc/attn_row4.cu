@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
     const int st_next = st == kStages - 1 ? 0 : st + 1;
     const uint32_t parity_next = parity ^ (st_next == 0 ? 1u : 0u);
     seen = nb + 1 < cnt && mbar_test_wait(full(warp, st_next), parity_next);
-    if (key + kBlock > seq.kv) {
+    if (seq.kv - key < kBlock) {
       // rows past the sequence's end: 0 * NaN would reach the result, and only a scale can be NaN
       for (int r = seq.kv - key + lane; r < kBlock; r += 32)
         *reinterpret_cast<uint2*>(smem + warp * kWarpBytes + st * kStageBytes + kOffVs + 8 * r) = make_uint2(0, 0);
