@@ -922,8 +922,11 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       ++with_tiles;
       // A tile's codes come to registers while the wait for a free place of its values runs: their slot is free at once.
       uint32_t w[4][4], sc[2];
-      auto kind = [&](int it) { return it == 2 * tiles - 1 || (it > 0 && !(it & 1)); };                             // V?
-      auto tile_of = [&](int it) { return it == 2 * tiles - 1 ? tiles - 1 : it & 1 ? (it + 1) >> 1 : max((it >> 1) - 1, 0); };   // (inverse of item_of)
+      // item `it` of the job (the inverse of item_of)
+      auto kind = [&](int it) { return it == 2 * tiles - 1 || (it > 0 && !(it & 1)); };   // V?
+      auto tile_of = [&](int it) {
+        return it == 2 * tiles - 1 ? tiles - 1 : it & 1 ? (it + 1) >> 1 : max((it >> 1) - 1, 0);
+      };
       auto take = [&](int it) {
         ok = wait_for<kPoll>(bar(B_KFULL + slot), phase, limit);
         if (!ok) return;
