@@ -567,7 +567,8 @@ typedef struct {
 /* Split counts: force_splits > 0 cuts the keys of every sequence into that many
  * near-equal runs of 128-key tiles. Automatic (0): up to min(max_splits or 64, tiles of
  * max_kv) for each sequence, from the lengths, on the GPU. With row_kernel (two CTAs an SM), and
- * for e4m3 and 4 bits where the unsplit jobs pass one wave (num_sms jobs) and max_kv >= 6144, one wave of
+ * for e4m3 and 4 bits where the unsplit jobs pass one wave (num_sms jobs) and max_kv >= 6144 (4 bits also where max_q_per_seq
+ * tokens fit one job and max_kv >= 1024), one wave of
  * CTAs takes equal shares of the key tiles of all jobs, laid one after the other, and a job
  * is split where a share ends (shares are larger where it would be split into more than the
  * bound). Otherwise, with T = the key tiles a job should walk, a sequence gets

@@ -542,8 +542,14 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
   // 157 us, 8,192 308 -> 296, 16,384 638 -> 579; 4 x 300 over 9,000 169 -> 129; 40 x 16 over 9,000 185 -> 144).
   // The length is the plan's bound: 2 x 2,048 over 4,096 under a plan for 131,072 keys take 150 us instead of 139.
   constexpr int kLongKeys = 6144;
+  // 4 bits, sequences of one query tile each, as decode: whole jobs leave too few pieces to even out (16 x 1 to 16 tokens over 1,024 to
+  // 16,384 keys by length 133 us, in shares 98; 8 x 8 over 8,192 55 and 52; 40 x 1 to 16 over 1,000 to 5,500 126 and 111; 8 of 256 to
+  // 1,024 23.9 and 24.1, 8 of 128 to 300 20.6 and 26.6). Chunks gain or lose with the keys an SM has (1 x 512 over 32,768 202 and 180,
+  // 2 x 300 over 16,384 72 and 88), which the host does not know, and keep to the rule of e4m3.
+  constexpr int kFewKeys = 1024;
   if (plan->adaptive_splits) {
-    const bool shares = rows16 || (plan->dtype != SDPA_BF16 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);
+    const bool one_tile = four && plan->max_q_per_seq <= job_tokens(0, a.group) && plan->max_kv >= kFewKeys;
+    const bool shares = rows16 || one_tile || (plan->dtype != SDPA_BF16 && unsplit > a.num_sms && plan->max_kv >= kLongKeys);
     a.adaptive = shares ? skv::kShares : skv::kByLength;
   }
   if (a.adaptive == skv::kByLength) {

@@ -73,6 +73,17 @@ def test_shares_that_cross_sequences(num_sms, page, max_q):
     go(sq[:9], kv[:9], 10, 5, page, seed=num_sms, num_sms=num_sms, max_q=max_q)
 
 
+@pytest.mark.parametrize("num_sms", [1, 3, 20, 152])
+@pytest.mark.parametrize("page", [16, 128])
+def test_few_tokens_in_equal_shares(num_sms, page):
+    """Sequences of one query tile in the kernel of 256-row jobs, cut where a CTA's share ends."""
+    rng = np.random.default_rng(num_sms + page)
+    kv = [int(x) for x in rng.integers(0, 1500, 30)]
+    sq = [int(x) for x in rng.integers(0, 17, 30)]
+    go(sq, kv, 8, 2, page, seed=num_sms, num_sms=num_sms, max_q=16, max_kv=2000)
+    go(sq[:4], kv[:4], 32, 2, page, seed=num_sms, num_sms=num_sms, max_q=16, max_kv=1024)
+
+
 @pytest.mark.parametrize("S", [0, 1, 3])
 def test_rows_without_keys_and_empty_sequences(S):
     """More new tokens than keys (the first queries see nothing), no keys at all, no new tokens."""
