@@ -79,8 +79,9 @@ struct ScalesOf<4> {
 enum {
   B_Q = 0, B_QDONE, B_S0, B_S1, B_SFREE, B_P0, B_P1, B_O0, B_O1, B_TURN_QK, B_TURN_PV, B_VLAND, B_END, B_DRAIN,
   B_DRAIN2, B_V16F0, B_V16F1, B_V16E0, B_V16E1, B_JOB0, B_JOB1, B_READ0, B_READ1, B_CLC, B_STAT,
-  B_OREAD, B_Q16, B_KFULL,
-  B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4, kNumBars = B_VEMPTY + 4
+  B_OREAD, B_KFULL,
+  B_KEMPTY = B_KFULL + 4, B_VFULL = B_KEMPTY + 4, B_VEMPTY = B_VFULL + 4,
+  B_Q16 = B_VEMPTY + 4, kNumBars   // (the last one: 4 bits alone, Q's rows are f16)
 };
 static_assert(kNumBars * 8 <= 352, "barrier area");
 // 4 bits: the place of a tile in the order in which a job's K and V tiles are loaded and widened, K a tile ahead (K_0, K_1, V_0,
@@ -132,12 +133,19 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
 
   const int tokens = 128 / a.group;   // of one row block
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      const int n = i == B_STAT || i == B_OREAD || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 || i == B_Q16 ||
-                            (kF8 && i >= B_VEMPTY) ||   // a tile of codes is freed by its four converter warps
-                            (kF4 && ((i >= B_KEMPTY && i < B_KEMPTY + 4) || i == B_K16F0 || i == B_K16F0 + 1))
+    // Arrivals: of four warps, of a tile's converting warps, of all that read a job's description; of 4-bit codes' bytes and each lane's
+    // copies of scales. (An expression for each kind: with Q16 among the barriers of e4m3 too its kernels' loops lay elsewhere in
+    // the code, and ragged chunks over pages of 16 took 141.3 us instead of 139, 1 to 16 tokens 40.6 instead of 39.6.)
+    for (int i = 0; i < (kF4 ? kNumBars : B_Q16); ++i) {
+      const int n = kF4 ? (i == B_STAT || i == B_OREAD || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 ||
+                                   i == B_Q16 || (i >= B_KEMPTY && i < B_KEMPTY + 4) || i == B_K16F0 || i == B_K16F0 + 1
+                               ? 4
+                           : i >= B_KFULL && i < B_KEMPTY       ? 33
+                           : i == B_READ0 || i == B_READ1       ? C::kConsumers
+                                                                : 1)
+                    : i == B_STAT || i == B_OREAD || i == B_SFREE || i == B_P0 || i == B_P1 || i == B_V16F0 || i == B_V16F1 ||
+                            (kF8 && i >= B_VEMPTY)
                         ? 4
-                    : kF4 && i >= B_KFULL && i < B_KEMPTY ? 33   // the codes' bytes, and each lane's copies of scales
                     : i == B_READ0 || i == B_READ1 ? C::kConsumers
                                                    : 1;
       mbar_init(bar(i), n);
