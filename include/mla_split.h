@@ -644,7 +644,8 @@ MLA_API int sdpa_prompt(int batch, int h_q, int h_kv, int d, int dtype, int tota
 
 /* Synchronises the current device, then reads and clears its status word
  * (MLA_STATUS_* bits set by kernels whose bounded waits ran out). *site_out,
- * if not NULL, receives the code of the first wait that ran out (0 = none). */
+ * if not NULL, receives the code of the first wait that ran out (0 = none), or of an aborting
+ * CTA's wait for its own copies and MMAs if that ran out too. */
 MLA_API int mla_get_status(uint32_t* status_out, uint32_t* site_out);
 
 /* Launches a one-CTA kernel that waits on an mbarrier nothing ever arrives on,

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, kRowCtasPerSm)
     bool done = true;
     for (int k = seen; k < issued; ++k)
       done = wait_drain(bar(k % kStages), (k / kStages) & 1, a.drain_limit_ns) && done;
-    if (!done && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
+    if (!done && lane == 0) atomicExch(&a.status[1], W_R_DRAIN);
   };
   announce(next);
 #pragma unroll 1

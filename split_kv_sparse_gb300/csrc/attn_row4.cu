@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
     bool quiet = true;
     for (int k = max(0, used - kStages); k < used; ++k)
       quiet = wait_drain(full(w, k % kStages), (k / kStages) & 1, a.drain_limit_ns) && quiet;
-    if (!quiet && lane == 0) atomicCAS(&a.status[1], 0u, W_R_DRAIN);
+    if (!quiet && lane == 0) atomicExch(&a.status[1], W_R_DRAIN);
     return;
   }
 

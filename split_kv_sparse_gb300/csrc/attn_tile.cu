@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         const int drain = is_qk ? B_DRAIN : B_DRAIN2;
         if (elect_one()) mma_commit(bar(drain));
         __syncwarp();
-        if (!wait_drain(bar(drain), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+        if (!wait_drain(bar(drain), 0, a.drain_limit_ns)) atomicExch(&a.status[1], W_T_DRAIN);
       }
     } else if (warp == 9 || warp == 11) {
       // ============================================ loads (K and Q; V) and jobs ===
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         if (!kF16 && !is_k && tail >= 0) {
           const int sl = (done - 1) % C::kVSlots;
           ok = wait_for<kPoll>(bar(B_VLAND), landed & 1, limit);
-          if (!ok && !wait_drain(bar(B_VLAND), landed & 1, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+          if (!ok && !wait_drain(bar(B_VLAND), landed & 1, a.drain_limit_ns)) atomicExch(&a.status[1], W_T_DRAIN);
           ++landed;
           if (ok) {
             uint8_t* v = smem + C::kOffV + sl * C::kItemBytes;
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         }
         for (int k = max(0, done - slots); k < done; ++k)
           quiet = wait_drain(bar(full + k % slots), (k / slots) & 1, a.drain_limit_ns) && quiet;
-        if (!quiet) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+        if (!quiet) atomicExch(&a.status[1], W_T_DRAIN);
       }
     } else if (kF8 && warp >= 12) {
       // ================================================== V e4m3 -> f16 ===
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
         if (misc[M_LAST + k] >= 0 && misc[M_LAST + k] % C::kKSlots == sl) last = max(last, misc[M_LAST + k]);
       if (last >= 0) quiet = wait_drain(bar(B_KFULL + sl), (last / C::kKSlots) & 1, a.drain_limit_ns) && quiet;
     }
-    if (!quiet) atomicCAS(&a.status[1], 0u, W_T_DRAIN);
+    if (!quiet) atomicExch(&a.status[1], W_T_DRAIN);
   }
   if (warp == 8) {
     tc_fence_after();

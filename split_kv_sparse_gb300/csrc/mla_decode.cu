@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // previous one was consumed, so it is the only one that can be in flight;
       // already landed, unless the CTA is aborting).
       if (issued > 0 && !wait_drain(bar(B_QFULL), (issued - 1) & 1, a.drain_limit_ns))
-        atomicCAS(&a.status[1], 0u, W_DRAIN_Q);
+        atomicExch(&a.status[1], W_DRAIN_Q);
     }
   } else if (warp == 3) {
     // ========================================================= MMA issuer ===
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         // no MMA may still be reading shared memory or writing TMEM when the CTA exits
         mma_commit(bar(B_DRAIN));
-        if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_DRAIN_MMA);
+        if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicExch(&a.status[1], W_DRAIN_MMA);
       }
     }
   } else {

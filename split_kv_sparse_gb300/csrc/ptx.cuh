@@ -80,7 +80,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // a per-CTA abort flag in shared memory that lets one stuck role stop the others.
 struct WaitCtx {
   uint64_t limit_ns;
-  uint32_t* status;         // global: [0] = MLA_STATUS_* bits, [1] = first site that timed out
+  uint32_t* status;         // global: [0] = MLA_STATUS_* bits, [1] = first site that timed out (or a drain's)
   volatile int* abort_flag; // shared
 };
 

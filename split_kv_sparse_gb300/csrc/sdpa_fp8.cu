@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // already, unless the CTA is aborting).
       for (int st = 0; st < kStages; ++st)
         if (last[st] >= 0 && !wait_drain(bar(B_SFULL_STAGE0 + st), (last[st] / kStages) & 1, a.drain_limit_ns))
-          atomicCAS(&a.status[1], 0u, W_DRAIN_TMA2);
-      if (!wait_drain(bar(B_QFULL), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_DRAIN_TMA2);
+          atomicExch(&a.status[1], W_DRAIN_TMA2);
+      if (!wait_drain(bar(B_QFULL), 0, a.drain_limit_ns)) atomicExch(&a.status[1], W_DRAIN_TMA2);
     }
   } else if (warp == 1) {
     // ========================================================= MMA issuer ===
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) mma_commit(bar(B_FINAL));
       if (!ok) {
         mma_commit(bar(B_DRAIN));
-        if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicCAS(&a.status[1], 0u, W_DRAIN_MMA2);
+        if (!wait_drain(bar(B_DRAIN), 0, a.drain_limit_ns)) atomicExch(&a.status[1], W_DRAIN_MMA2);
       }
     }
   } else if (warp >= kFirstConverter) {

@@ -32,7 +32,8 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
   return fmaxf(fmax3(b0, b1, b2), fmaxf(a[9], a[10]));
 }
 
-// Waits without looking at the abort flag (used to drain in-flight copies on abort).
+// Waits without looking at the abort flag (used to drain in-flight copies on abort). A drain that runs out replaces the recorded site by its
+// own: a CTA that ends with copies in flight is more than a wait that ran out.
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
