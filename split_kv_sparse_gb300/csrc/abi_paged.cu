@@ -208,13 +208,15 @@ int shift_of(int pow2) {
 void set_pages(skv::PagesAppendArgs* a, const kv_pages_t* p) {
   a->k = p->k;
   a->v = p->v;
-  a->k_scales = static_cast<uint8_t*>(p->k_scales);
-  a->v_scales = static_cast<uint8_t*>(p->v_scales);
   a->page_stride = p->page_stride;
   a->row_stride = p->row_stride;
   a->cache_head_stride = p->head_stride;
-  a->scale_page_stride = p->scale_page_stride;
-  a->scale_head_stride = p->scale_head_stride;
+  if (p->dtype == SDPA_E2M1) {   // (other types: the descriptor may end before these)
+    a->k_scales = static_cast<uint8_t*>(p->k_scales);
+    a->v_scales = static_cast<uint8_t*>(p->v_scales);
+    a->scale_page_stride = p->scale_page_stride;
+    a->scale_head_stride = p->scale_head_stride;
+  }
   a->num_slots = static_cast<int64_t>(p->num_pages) * p->page_size;
   a->page_shift = shift_of(p->page_size);
   a->h_kv = p->h_kv;
@@ -566,8 +568,10 @@ int sdpa_paged(const sdpa_paged_plan_t* plan, int total_q, const void* q, int64_
     grid = share_ctas(a.num_sms, a.h_kv);
     a.part_gap = static_cast<int>(grid) * (rows16 ? skv::kRowRows : skv::kTileRows);
   }
-  const skv::KvScales scales = {static_cast<const uint8_t*>(pages->k_scales), static_cast<const uint8_t*>(pages->v_scales),
-                                pages->scale_page_stride, pages->scale_head_stride};
+  skv::KvScales scales = {};
+  if (four)
+    scales = {static_cast<const uint8_t*>(pages->k_scales), static_cast<const uint8_t*>(pages->v_scales), pages->scale_page_stride,
+              pages->scale_head_stride};
   st = cuda_status(rows16 && four ? skv::launch_attn_row4(tk, tv, tks, tvs, a, job_rows(plan->row_kernel), grid, cs)
                    : rows16       ? skv::launch_attn_row(tk, tv, a, plan->dtype, grid, cs)
                    : four         ? skv::launch_attn_tile4(tq, tk, tv, a, scales, grid, cs)
