@@ -14,9 +14,11 @@ namespace skv {
 // x / d for many x by one d, rounded to nearest as a division: with y = RN(1 / d) and q =
 // RN(x y), the residual x - q d is exact in an FMA and q + (x - q d) y rounds to the quotient
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000", 1990; a
-// zero keeps q's sign). Where y is not a normal number, or a q leaves the range, the
-// eight values are divided one by one (in a loop of its own: sixteen divisions
-// inlined here cost 24.2 us where this takes 20.1, 16,001 rows of 8 heads into e4m3).
+// zero keeps q's sign). The residual has to be a multiple of 2^-149: with d from 2^-90 up it is one for every q that a code
+// tells from 0 (2^-11 and more, 24 bits each). Below that (a descale of 2^-116 gave codes one off), where y is not a
+// normal number, or where a q leaves the range, the values are divided one by one, those of divide4 in a function of its own,
+// the eight that pages.cu takes at a time in a loop (sixteen divisions inlined there cost 24.2 us where this takes 20.1, 16,001 rows
+// of 8 heads into e4m3).
 struct Divider {
   float d, y;
   bool plain;
@@ -25,7 +27,7 @@ __device__ __forceinline__ Divider divider(float d) {
   Divider by;
   by.d = d;
   by.y = __fdiv_rn(1.f, d);
-  by.plain = !(fabsf(by.y) >= 1.17549435e-38f && fabsf(by.y) <= 3.40282347e38f);
+  by.plain = !(fabsf(by.y) >= 1.17549435e-38f && fabsf(by.y) <= 0x1p90f);
   return by;
 }
 __device__ __forceinline__ float quotient(float x, float d, float y) {
