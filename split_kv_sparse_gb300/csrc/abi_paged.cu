@@ -280,6 +280,7 @@ int kv_pages_write(const kv_pages_t* pages, int64_t rows, const void* k_new, con
   if (pages->dtype == SDPA_E2M1) {
     skv::PagesAppendArgs a{};
     set_pages(&a, pages);
+  a.num_sms = dev.num_sms;
     a.k_new = static_cast<const uint16_t*>(k_new);
     a.v_new = static_cast<const uint16_t*>(v_new);
     a.token_stride = token_stride;
@@ -344,6 +345,7 @@ int kv_pages_write_rotary(const kv_pages_t* pages, int64_t rows, int h_q, const 
   if ((st = skv::current_device(&dev)) != MLA_OK) return st;
   skv::PagesAppendArgs a{};
   set_pages(&a, pages);
+  a.num_sms = dev.num_sms;
   a.q = static_cast<const uint16_t*>(q);
   a.q_ts = q_token_stride;
   a.q_hs = q_head_stride;
@@ -387,6 +389,7 @@ int kv_pages_read(const kv_pages_t* pages, int64_t rows, const int64_t* slot_map
   if ((st = skv::current_device(&dev)) != MLA_OK) return st;
   skv::PagesAppendArgs a{};
   set_pages(&a, pages);
+  a.num_sms = dev.num_sms;
   a.slots = slot_map;
   a.rows = rows;
   a.k_out = static_cast<uint16_t*>(k_out);

@@ -275,6 +275,7 @@ struct PagesAppendArgs {
   int64_t scale_page_stride, scale_head_stride;
   int64_t num_slots;
   int page_shift;
+  int num_sms;
   const float* descale_q;
   const float* descale_k;
   const float* descale_v;

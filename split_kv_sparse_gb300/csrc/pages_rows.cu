@@ -4,6 +4,8 @@
 // Both kernels are copies: every byte is read and written once and HBM bounds them, latency a call of few rows. 16,001 rows of 32 + 2 x 8
 // heads into bf16: 59 us of back-to-back calls, 6.7 TB/s; 8,192 into 4 bits 40 (4.5 TB/s: the codes' arithmetic beside the loads); 20,000 rows
 // of 4 bits back 17.4 (6.0 TB/s).
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "quant.cuh"
 
@@ -269,8 +271,8 @@ __global__ void __launch_bounds__(kThreads) pages_read_kernel(const PagesAppendA
   }
 }
 
-// Warps that fill the SMs: with fewer a call takes the smallest pieces.
-constexpr int64_t kFullWarps = 16ll * 152;
+// Warps of an SM that keep HBM busy: where a call has fewer it takes the smallest pieces.
+constexpr int64_t kSmWarps = 16;
 
 unsigned blocks_of(int64_t warps) {
   const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
@@ -279,18 +281,25 @@ unsigned blocks_of(int64_t warps) {
 
 template <int kCache>
 cudaError_t launch_rows(const PagesAppendArgs& a, bool read, cudaStream_t stream) {
+  const int64_t full = kSmWarps * a.num_sms;
   if (read) {
-    const bool many = a.rows * 2 * a.h_kv >= 16 * kFullWarps;
+    const bool many = a.rows * 2 * a.h_kv >= 16 * full;
     const int64_t each = many ? 16 : 4;
     const unsigned grid = blocks_of(a.rows * ((2ll * a.h_kv + each - 1) / each));
     if (grid == 0) return cudaErrorInvalidValue;
     return launch_pdl(many ? pages_read_kernel<kCache, 4> : pages_read_kernel<kCache, 1>, grid, kThreads, 0, stream, a);
   }
   const int chunks = (a.h_q + 3) / 4 + (a.h_kv + 1) / 2;
-  // A warp's start waits for the position and then the angles: it takes many chunks where the rows fill the SMs. (16,001 rows
-  // of 32 + 2 x 8 heads, bf16: 6 chunks 63.4 us, all 12 65.4, 1 122; 8,192 into 4 bits: 6 48.3, all 42.5, 1 98.)
-  const int most = kCache == 1 && chunks > 6 ? 6 : chunks;
-  const int per = a.rows * chunks >= 12 * kFullWarps ? most : 1;
+  // A warp's start waits for the position and then the angles: it takes many chunks where the rows fill the SMs, in bf16 at most six
+  // (16,001 rows of 32 + 2 x 8 heads in bf16, graphs: 6 chunks 61.0 us, all 12 65.4, 1 122; 8,192 into 4 bits: all 40, 6 48.3, 1 98).
+  // A row's warps take even parts, and no more than leaves every SM its warps (parts of six and a rest: bf16, 28 + 2 x 4 heads 49.8
+  // us, even 48.6; 40 + 2 x 8 74.9 and 72.4; 20 + 2 x 4 44.1 and 39.8; whole rows in 4 bits: 1,000 of 64 + 2 x 64 heads 33.6, so 28.7).
+  int per = 1;
+  if (a.rows * chunks >= 12 * full) {
+    const int64_t most = std::min<int64_t>(kCache == 1 ? 6 : chunks, a.rows * chunks / full);
+    const int64_t parts = (chunks + most - 1) / most;
+    per = static_cast<int>((chunks + parts - 1) / parts);
+  }
   const unsigned grid = blocks_of(a.rows * ((chunks + per - 1) / per));
   if (grid == 0) return cudaErrorInvalidValue;
   if (a.positions == nullptr) return launch_pdl(pages_append_kernel<kCache, 0, false>, grid, kThreads, 0, stream, a, per);
