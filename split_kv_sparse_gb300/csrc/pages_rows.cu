@@ -12,7 +12,6 @@
 namespace skv {
 namespace {
 
-constexpr int kD = kAttnDim;
 constexpr int kThreads = 256;
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[2][4]) {
@@ -302,7 +301,9 @@ cudaError_t launch_rows(const PagesAppendArgs& a, bool read, cudaStream_t stream
   }
   const unsigned grid = blocks_of(a.rows * ((chunks + per - 1) / per));
   if (grid == 0) return cudaErrorInvalidValue;
-  if (a.positions == nullptr) return launch_pdl(pages_append_kernel<kCache, 0, false>, grid, kThreads, 0, stream, a, per);
+  if constexpr (kCache == 4) {   // (the other types' append without a turn is pages_write_kernel)
+    if (a.positions == nullptr) return launch_pdl(pages_append_kernel<4, 0, false>, grid, kThreads, 0, stream, a, per);
+  }
   const bool q8 = a.h_q > 0 && a.q_out_e4m3;
   return launch_pdl(a.interleaved ? (q8 ? pages_append_kernel<kCache, 2, true> : pages_append_kernel<kCache, 2, false>)
                                   : (q8 ? pages_append_kernel<kCache, 1, true> : pages_append_kernel<kCache, 1, false>),
