@@ -45,9 +45,11 @@ constexpr int kSmem = kOffStage + 16 + 1024;
 static_assert(16 * kD * 4 <= kStageBytes, "a warp's result goes through one stage");
 static_assert(kRowCtasPerSm * (kSmem + 1024) <= 233472, "two CTAs an SM");
 // Registers of a thread that loads, and that computes: 256 of two threads of a launch (jobs of 8 rows, 4 x 100,000 to 131,072 keys,
-// 64 / 8 heads: 40 + 216 108.4 us, 56 + 200 105.2, 72 + 184 102.7, 88 + 168 103.5; of 16 rows 48 + 208 is best).
+// 64 / 8 heads: 40 + 216 108.4 us, 56 + 200 105.2, 72 + 184 102.7, 88 + 168 103.5; of 16 rows, 32 x 3 tokens over 4,096 to 8,192 keys, 32 / 8
+// heads: 40 + 216 75.7, 48 + 208 77.0, 56 + 200 77.7, 72 + 184 83.5). With 16 rows the compiler spills all the same (448 bytes of stores, 376
+// of loads; none with 8), and e4m3 pages of the same lengths are quicker, 71.3 us.
 template <int kN>
-constexpr int kLoadRegs = kN == 1 ? 72 : 48;
+constexpr int kLoadRegs = kN == 1 ? 72 : 40;
 template <int kN>
 constexpr int kRegs = 256 - kLoadRegs<kN>;
 // A piece's start and end, in units of an equal share (256 keys; 96 sequences of 100 to 12,000 keys: 0 150.6 us, 1 148.4, 2 145.1, 3 146.4).
