@@ -15,8 +15,7 @@
 // 32 consecutive dims of a key (16 bytes: one load); for O a lane has 16 dims of four keys, and a pair of one dim of two
 // keys is made by putting their codes into one byte before the conversion. Keys are taken in the order kPerm within
 // eight, which keeps the loads of K and of V free of bank conflicts under the 64-byte swizzle.
-// Q is held in f16 at a power of two of its row (largest element in [2^14, 2^15)): exact down to 2^-28 of that element, whose
-// smaller ones are rounded by at most 2^-39 of it.
+// Q is held in f16 at a power of two of its row (f16_row_up).
 #include "attn_common.cuh"
 #include "quant.cuh"
 
@@ -254,11 +253,11 @@ __global__ void __launch_bounds__(kThreads, kRowCtasPerSm)
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = static_cast<int>(top >> 7);             // the largest element's exponent
-    const float up = __int_as_float(min(268 - e, 254) << 23);
+    const float up = f16_row_up(e);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       qf[n][i >> 1][i & 1] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-    const float down = e > 14 ? __int_as_float((e - 14) << 23) : __int_as_float(1 << 22);
+    const float down = f16_row_down(e);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       lim[n][k] = __shfl_sync(0xffffffffu, last, 8 * q4 + 4 * k);

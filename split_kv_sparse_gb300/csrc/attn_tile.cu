@@ -879,9 +879,8 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
       if (!ok) give_up(a, W_T_CONVERT);
     } else if (kF4 && warp >= 12) {
       // ================================ Q bf16 -> f16; K and V codes x scales -> f16 ===
-      // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own (largest
-      // element in [2^14, 2^15)) with the sign of the scores' scale: exact down to 2^-28 of that element, smaller ones are off by 2^-39 of it at most. A
-      // code times its scale is exact in f16.
+      // A thread is a row of Q, then a key of every tile. Q's rows are taken to f16 in place at a power of two of their own (f16_row_up) with
+      // the sign of the scores' scale. A code times its scale is exact in f16.
       const int key = threadIdx.x - 32 * 12;
       const int r8 = key & 7, r4 = (key >> 1) & 3;
       const float sign = (a.descale_q ? *a.descale_q : 1.f) * (a.descale_k ? *a.descale_k : 1.f) * a.scale_log2;   // of the scores' scale
@@ -910,7 +909,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           for (int k = 0; k < 4; ++k) top = max(top, max(ws[k] & 0x7fffu, (ws[k] >> 16) & 0x7fffu));
         }
         const int e = static_cast<int>(top >> 7);          // the largest element's exponent
-        const float up = copysignf(__int_as_float(min(268 - e, 254) << 23), sign);
+        const float up = copysignf(f16_row_up(e), sign);
 #pragma unroll 4
         for (int c = 0; c < 16; ++c) {
           uint4* at = reinterpret_cast<uint4*>(q + (c >> 3) * 128 * 128 + (((c & 7) ^ r8) << 4));
@@ -921,8 +920,7 @@ __global__ void __launch_bounds__(Cfg<kType>::kThreads, 1)
           for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(__uint_as_float(ws[k] << 16) * up, __uint_as_float(ws[k] & 0xffff0000u) * up);
           *at = make_uint4(h[0], h[1], h[2], h[3]);
         }
-        reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (with_tiles & 1) + 128 * i + key] =
-            e > 14 ? __int_as_float((e - 14) << 23) : __int_as_float(1 << 22);
+        reinterpret_cast<volatile float*>(smem + C::kOffRow)[256 * (with_tiles & 1) + 128 * i + key] = f16_row_down(e);
       }
       fence_proxy_async_smem();
       __syncwarp();

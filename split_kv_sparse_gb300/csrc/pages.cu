@@ -180,10 +180,8 @@ __device__ __forceinline__ uint2 e4m3x8_of(const uint4& x, const Divider& by) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xffff0000u);
-    const float q0 = __fmul_rn(x0, by.y), q1 = __fmul_rn(x1, by.y);
-    most = fmax3(most, fabsf(q0), fabsf(q1));
-    c[i] = e4m3x2(copysignf(__fmaf_rn(__fmaf_rn(-q0, by.d, x0), by.y, q0), q0),
-                  copysignf(__fmaf_rn(__fmaf_rn(-q1, by.d, x1), by.y, q1), q1));
+    most = fmax3(most, fabsf(__fmul_rn(x0, by.y)), fabsf(__fmul_rn(x1, by.y)));
+    c[i] = e4m3x2(quotient(x0, by.d, by.y), quotient(x1, by.d, by.y));
   }
   if (by.plain || most > 1e30f) {
 #pragma unroll 1

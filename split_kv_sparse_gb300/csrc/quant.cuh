@@ -112,6 +112,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// A bf16 row of Q in f16 beside 4-bit pages: times 2^(141 - e) with e the exponent field of its largest element, which comes to lie in
+// [2^14, 2^15) (rows below 2^-113 times 2^127), so the row is exact down to 2^-28 of that element and smaller ones are off by 2^-39
+// of it at most. The second factor undoes the first.
+__device__ __forceinline__ float f16_row_up(int e) { return __int_as_float(min(268 - e, 254) << 23); }
+__device__ __forceinline__ float f16_row_down(int e) { return e > 14 ? __int_as_float((e - 14) << 23) : __int_as_float(1 << 22); }
+
 // Two e4m3 codes (the low half of w) as an f16 pair (exact).
 __device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t w) {
   uint32_t h;
