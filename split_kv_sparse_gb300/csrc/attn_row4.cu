@@ -7,8 +7,8 @@
 //
 // Two CTAs an SM, each with four warps that compute and four that load: every computing warp walks key blocks (64 keys, every
 // fourth of a job's) of its own with a running maximum and a sum of its own, merged at a job's end; a loading warp fills
-// its ring by TMA, page by page, ahead into the next job. Equal shares of the batch's key tiles (AttnShares). 4 x 100,000 to
-// 131,072 keys, 64 / 8 heads: 102 us, 5.1 TB/s (91 us of loads alone); 96 x 100 to 12,000, 32 / 8 heads, pages of 16: 144 us, 4.6 TB/s.
+// its ring by TMA, page by page, ahead into the next job. Equal shares of the batch's key tiles (AttnShares). Back-to-back calls: 4 x 100,000 to
+// 131,072 keys, 64 / 8 heads, 99 us, 5.3 TB/s; 96 x 100 to 12,000, 32 / 8 heads, pages of 16, 142 us, 4.7 TB/s.
 //
 // Widening: a byte of two e2m1 codes is one conversion to an f16 pair, times its e4m3 scale in f16: exact (6
 // significant bits, 2^-10 to 2688). The order of the contracted dims of S is free as long as Q has the same, so a lane takes

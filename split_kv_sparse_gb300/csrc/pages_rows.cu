@@ -1,9 +1,9 @@
 // Rows of the paged cache with arithmetic on the way: the append that rotates by position, the append into 4-bit
 // pages, and the way back from pages of any type to bf16 rows.
 //
-// Both kernels are copies: every byte is read and written once and HBM bounds them, latency a call of few rows. 16,001 rows of 32 + 2 x 8
-// heads into bf16: 59 us of back-to-back calls, 6.7 TB/s; 8,192 into 4 bits 40 (4.5 TB/s: the codes' arithmetic beside the loads); 20,000 rows
-// of 4 bits back 17.4 (6.0 TB/s).
+// Both kernels are copies: every byte is read and written once and HBM bounds them, latency a call of few rows. Back-to-back calls of 16,001
+// rows of 32 + 2 x 8 heads: into bf16 60 us (6.6 TB/s), q and cache into e4m3 63 (4.8), into 4 bits 69 (5.1; 8,192 rows 40), K and V alone
+// 30.5 (2.8): the codes' arithmetic beside the loads. 20,000 rows back: of 4 bits 17.8 (5.9), of e4m3 20.5 (6.0), of bf16 26.4 (6.2).
 #include <algorithm>
 
 #include "attn_common.cuh"
